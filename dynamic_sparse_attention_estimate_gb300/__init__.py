@@ -8,6 +8,7 @@ load the library; the first call does, and fails loudly if it has not been built
 """
 from .binding import (  # noqa: F401
     DSVError,
+    RopeTable,
     dsv_adaln_bwd,
     dsv_adaln_bwd_workspace,
     dsv_adaln_fwd,
@@ -15,6 +16,12 @@ from .binding import (  # noqa: F401
     dsv_estimate_topk,
     dsv_estimate_topk_csr,
     dsv_estimate_topk_workspace,
+    dsv_qk_norm_rope_bwd,
+    dsv_qk_norm_rope_bwd_workspace,
+    dsv_qk_norm_rope_fwd,
+    dsv_rope3d_bwd,
+    dsv_rope3d_fwd,
+    dsv_rope3d_table,
     dsv_sparse_attn_bwd,
     dsv_sparse_attn_bwd_csr,
     dsv_sparse_attn_bwd_prepare,

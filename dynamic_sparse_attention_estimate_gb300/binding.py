@@ -8,8 +8,9 @@ computation runs in the library's CUDA kernels; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
@@ -30,6 +31,8 @@ EXPORTED = (
     "dsv_sparse_attn_bwd_csr_workspace", "dsv_sparse_attn_bwd_csr", "dsv_csr_launch_order",
     "dsv_adaln_fwd", "dsv_adaln_bwd_workspace", "dsv_adaln_bwd",
     "dsv_sparse_attn_bwd_prepare", "dsv_sparse_attn_bwd_prepared", "dsv_sparse_attn_fwd_workspace",
+    "dsv_rope3d_table_bytes", "dsv_rope3d_table", "dsv_rope3d_fwd", "dsv_rope3d_bwd",
+    "dsv_qk_norm_rope_fwd", "dsv_qk_norm_rope_bwd_workspace", "dsv_qk_norm_rope_bwd",
 )
 
 
@@ -47,6 +50,20 @@ class Dims(ctypes.Structure):
 
 class AdalnDims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("N", ctypes.c_int64), ("D", ctypes.c_int64), ("eps", ctypes.c_float)]
+
+
+class RopeDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("H", ctypes.c_int64), ("N", ctypes.c_int64), ("d", ctypes.c_int64),
+                ("rot", ctypes.c_int64 * 3), ("len", ctypes.c_int64 * 3), ("pairing", ctypes.c_int32),
+                ("pos_batched", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class ViewStrides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("n", ctypes.c_int64)]
+
+
+# dsv_view_strides[2] and [3]: sample, head and token strides of each tensor in turn
+_Strides6, _Strides9 = ctypes.c_int64 * 6, ctypes.c_int64 * 9
 
 
 def library_path() -> str:
@@ -112,6 +129,20 @@ def load_library(path: Optional[str] = None):
     lib.dsv_adaln_bwd_workspace.restype = sz
     lib.dsv_adaln_bwd.argtypes = [ap, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.dsv_adaln_bwd.restype = st
+    rp, vs = ctypes.POINTER(RopeDims), ctypes.POINTER(ViewStrides)
+    lib.dsv_rope3d_table_bytes.argtypes = [rp]
+    lib.dsv_rope3d_table_bytes.restype = sz
+    lib.dsv_rope3d_table.argtypes = [rp, ctypes.POINTER(ctypes.c_double), vp, vp]
+    lib.dsv_rope3d_table.restype = st
+    for f in (lib.dsv_rope3d_fwd, lib.dsv_rope3d_bwd):
+        f.argtypes = [rp, vp, vs, vp, vp, vp, vs, vp]
+        f.restype = st
+    lib.dsv_qk_norm_rope_fwd.argtypes = [rp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.dsv_qk_norm_rope_fwd.restype = st
+    lib.dsv_qk_norm_rope_bwd_workspace.argtypes = [rp]
+    lib.dsv_qk_norm_rope_bwd_workspace.restype = sz
+    lib.dsv_qk_norm_rope_bwd.argtypes = [rp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.dsv_qk_norm_rope_bwd.restype = st
     lib.dsv_profile_enable.argtypes = [st]
     lib.dsv_profile_enable.restype = st
     lib.dsv_profile_read.argtypes = [ctypes.c_char_p, sz]
@@ -445,6 +476,212 @@ def dsv_adaln_bwd(x: torch.Tensor, scale: torch.Tensor, dy: torch.Tensor, eps: f
     _check(lib.dsv_adaln_bwd(ctypes.byref(dims), _ptr(x), _ptr(scale), _ptr(dy), _ptr(dx), _ptr(d_scale),
                              _ptr(d_shift), _ptr(workspace), workspace.numel(), _stream_ptr(x)), "dsv_adaln_bwd")
     return dx, d_scale, d_shift
+
+
+# ---------------------------------------------------------------- rotary positions, qk norm
+# The calls below take tens of microseconds on the GPU at most sizes, so their host side is kept lean:
+# what depends on sizes alone (the dims struct, workspace sizes) is made once per size.
+
+_PAIRINGS = {"interleaved": 0, "halves": 1}
+
+
+class RopeTable(NamedTuple):
+    """(cos, sin) of every axis' positions, as the rotation calls read them (layout in include/dsv.h).
+
+    data: fp32, flat, on the GPU; axes: rotated features of (time, height, width); lengths: positions of
+    each axis; pairing: "interleaved" (features 2j, 2j+1 turn together) or "halves" (j, j + R/2)."""
+    data: torch.Tensor
+    axes: Tuple[int, int, int]
+    lengths: Tuple[int, int, int]
+    pairing: str = "interleaved"
+
+
+@functools.lru_cache(maxsize=256)
+def _rope_dims(shape: Tuple[int, ...], axes: Tuple, lengths: Tuple, pairing: str, pos_batched: bool, eps: float):
+    """(dims struct, numbers its table holds) for tensors of `shape`."""
+    B, H, N, d = shape
+    if len(axes) != 3 or len(lengths) != 3:
+        raise ValueError("axes and lengths need three entries (time, height, width)")
+    if pairing not in _PAIRINGS:
+        raise ValueError(f"pairing must be one of {sorted(_PAIRINGS)}, got {pairing!r}")
+    dims = RopeDims(B, H, N, d, (ctypes.c_int64 * 3)(*axes), (ctypes.c_int64 * 3)(*lengths), _PAIRINGS[pairing],
+                    int(pos_batched), eps)
+    return dims, 2 * sum((r // 2) * n for r, n in zip(axes, lengths))
+
+
+@functools.lru_cache(maxsize=256)
+def _qk_norm_rope_ws(B: int, H: int, N: int, d: int) -> int:
+    return int(load_library().dsv_qk_norm_rope_bwd_workspace(ctypes.byref(RopeDims(B, H, N, d))))
+
+
+def _need_view(t: torch.Tensor, name: str, shape=None, device: Optional[int] = None):
+    """The strides of a bf16 CUDA [B, H, N, d] view whose features are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    strides = t.stride()
+    if t.dtype is torch.bfloat16 and len(strides) == 4 and strides[3] == 1 and t.is_cuda and \
+            (shape is None or (t.shape == shape and t.get_device() == device)):
+        return strides[:3]
+    raise ValueError(f"{name}: need a CUDA bfloat16 [B, H, N, d] tensor with contiguous features"
+                     + ("" if shape is None else f" of shape {tuple(shape)} on cuda:{device}")
+                     + f", got {t.dtype} {tuple(t.shape)} strides={strides} device={t.device}")
+
+
+def _need_on(t: torch.Tensor, name: str, dtype, shape, device: int):
+    """A contiguous CUDA tensor of this type and shape on this device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{device}, got "
+                         f"{t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} device={t.device}")
+
+
+def _rope_args(x: torch.Tensor, pos: Optional[torch.Tensor], rope: Optional[RopeTable], eps: float):
+    """(dims struct, pos pointer, table pointer) for x [B, H, N, d]."""
+    shape = x.shape
+    if rope is None:
+        if pos is not None:
+            raise ValueError("pos without a RopeTable")
+        return _rope_dims(shape, (0, 0, 0), (0, 0, 0), "interleaved", False, float(eps))[0], None, None
+    device = x.get_device()
+    if pos is None:
+        raise ValueError("a RopeTable needs pos")
+    batched = pos.dim() == 3
+    dims, numbers = _rope_dims(shape, tuple(rope.axes), tuple(rope.lengths), rope.pairing, batched, float(eps))
+    _need_on(pos, "pos", torch.int32, (shape[0], shape[2], 3) if batched else (shape[2], 3), device)
+    table = rope.data
+    if table.dtype != torch.float32 or table.numel() < numbers or not table.is_contiguous() or \
+            table.get_device() != device:
+        raise ValueError(f"rope.data: need a contiguous float32 tensor of {numbers} numbers on {x.device}, got "
+                         f"{table.dtype} {tuple(table.shape)} on {table.device}")
+    return dims, pos.data_ptr(), table.data_ptr()
+
+
+def _call(name: str, device: int, *args):
+    """One library call on this device's current stream, with the device made current for it."""
+    f = getattr(load_library(), name)
+    if torch.cuda.current_device() == device:
+        status = f(*args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, torch._C._cuda_getCurrentRawStream(device))
+    if status != DSV_OK:
+        _check(status, name)
+
+
+def dsv_rope3d_table(axes: Sequence[int], lengths: Sequence[int], theta: Union[float, Sequence[float]] = 10000.0,
+                     pairing: str = "interleaved", device: Union[str, torch.device] = "cuda") -> RopeTable:
+    """The (cos, sin) table of positions 0 .. lengths[a] - 1 of each axis: pair i of axis a turns by
+    p * theta_a^(-2 i / axes[a]) at position p (angles in fp64).  Made once per model."""
+    axes, lengths = tuple(int(r) for r in axes), tuple(int(n) for n in lengths)
+    dims, numbers = _rope_dims((1, 1, 1, 64 if sum(axes) <= 64 else 128), axes, lengths, pairing, False, 0.0)
+    theta = (float(theta),) * 3 if isinstance(theta, (int, float)) else tuple(float(t) for t in theta)
+    if len(theta) != 3:
+        raise ValueError("theta must be one number or three (time, height, width)")
+    data = torch.empty((max(numbers, 0),), dtype=torch.float32, device=device)
+    if not data.is_cuda:
+        raise ValueError(f"the table lives on a CUDA device, got {data.device}")
+    _call("dsv_rope3d_table", data.get_device(), dims, (ctypes.c_double * 3)(*theta), data.data_ptr())
+    return RopeTable(data, axes, lengths, pairing)
+
+
+def _rope3d(fn: str, name: str, x: torch.Tensor, pos: torch.Tensor, rope: RopeTable, out: Optional[torch.Tensor]):
+    xs = _need_view(x, name)
+    if rope is None:
+        raise ValueError("need a RopeTable")
+    dims, pos_ptr, table_ptr = _rope_args(x, pos, rope, 0.0)
+    device = x.get_device()
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    os_ = _need_view(out, "out", x.shape, device)
+    _call(fn, device, dims, x.data_ptr(), ViewStrides(*xs), pos_ptr, table_ptr, out.data_ptr(), ViewStrides(*os_))
+    return out
+
+
+def dsv_rope3d_fwd(x: torch.Tensor, pos: torch.Tensor, rope: RopeTable,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x [B, H, N, d] (any view with contiguous features) rotated at pos [N, 3] or [B, N, 3] (int32
+    (t, h, w) of each token); `out` defaults to a contiguous tensor and may be x itself (in place)."""
+    return _rope3d("dsv_rope3d_fwd", "x", x, pos, rope, out)
+
+
+def dsv_rope3d_bwd(dy: torch.Tensor, pos: torch.Tensor, rope: RopeTable,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dx of dsv_rope3d_fwd for the loss gradient dy: the rotation by the negative angles."""
+    return _rope3d("dsv_rope3d_bwd", "dy", dy, pos, rope, out)
+
+
+def dsv_qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], wq: Optional[torch.Tensor],
+                         wk: Optional[torch.Tensor], pos: Optional[torch.Tensor], rope: Optional[RopeTable],
+                         eps: float = 1e-6, out: Optional[Tuple] = None):
+    """(q, k, v) contiguous [B, H, N, d] for the attention calls: q and k RMS-normed for each head, times
+    wq / wk [d] (None: ones), rotated at pos; v copied (None: not part of the call).  The inputs are
+    [B, H, N, d] views with contiguous features, e.g. the three slices of a packed projection
+    [B, N, 3, H, d].  rope = pos = None: the norm alone.  out: the three outputs (v's None without v)."""
+    strides = _need_view(q, "q")
+    shape, device = q.shape, q.get_device()
+    strides += _need_view(k, "k", shape, device)
+    strides += (0, 0, 0) if v is None else _need_view(v, "v", shape, device)
+    dims, pos_ptr, table_ptr = _rope_args(q, pos, rope, eps)
+    for w, n in ((wq, "wq"), (wk, "wk")):
+        if w is not None:
+            _need_on(w, n, torch.bfloat16, shape[3:], device)
+    if out is None:
+        qo, ko = torch.empty(shape, dtype=q.dtype, device=q.device), torch.empty(shape, dtype=q.dtype, device=q.device)
+        vo = None if v is None else torch.empty(shape, dtype=q.dtype, device=q.device)
+    else:
+        qo, ko, vo = out
+        for t, n in ((qo, "q_out"), (ko, "k_out"), (vo, "v_out")):
+            if t is not None:
+                _need_on(t, n, torch.bfloat16, shape, device)
+    _call("dsv_qk_norm_rope_fwd", device, dims, q.data_ptr(), k.data_ptr(), _ptr(v), _Strides9(*strides), _ptr(wq),
+          _ptr(wk), pos_ptr, table_ptr, _ptr(qo), _ptr(ko), _ptr(vo))
+    return qo, ko, vo
+
+
+def dsv_qk_norm_rope_bwd_workspace(B: int, H: int, N: int, d: int) -> int:
+    return _qk_norm_rope_ws(int(B), int(H), int(N), int(d))
+
+
+def dsv_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, dv_out: Optional[torch.Tensor], q: torch.Tensor,
+                         k: torch.Tensor, wq: Optional[torch.Tensor], wk: Optional[torch.Tensor],
+                         pos: Optional[torch.Tensor], rope: Optional[RopeTable], eps: float = 1e-6,
+                         out: Optional[Tuple] = None, workspace: Optional[torch.Tensor] = None):
+    """(dq, dk, dv, dwq, dwk) of dsv_qk_norm_rope_fwd: dq, dk, dv bf16 [B, H, N, d] (by default views of
+    one packed [B, N, 3, H, d] gradient; `out` takes any three views with contiguous features), dwq, dwk
+    fp32 [d] (None where the weight is None).  q, k are the forward's inputs; dv_out = None: no values
+    (dv is None)."""
+    strides = _need_view(q, "q")
+    shape, device = q.shape, q.get_device()
+    strides += _need_view(k, "k", shape, device)
+    for t, n in ((dq_out, "dq_out"), (dk_out, "dk_out"), (dv_out, "dv_out")):
+        if t is not None or n != "dv_out":
+            _need_on(t, n, torch.bfloat16, shape, device)
+    dims, pos_ptr, table_ptr = _rope_args(q, pos, rope, eps)
+    for w, n in ((wq, "wq"), (wk, "wk")):
+        if w is not None:
+            _need_on(w, n, torch.bfloat16, shape[3:], device)
+    B, H, N, d = shape
+    if out is None:
+        packed = torch.empty((B, N, 2 if dv_out is None else 3, H, d), dtype=q.dtype, device=q.device)
+        dq, dk, dv = (*packed.permute(2, 0, 3, 1, 4).unbind(0), None)[:3]
+    else:
+        dq, dk, dv = out
+    dstrides = _need_view(dq, "dq", shape, device) + _need_view(dk, "dk", shape, device)
+    dstrides += (0, 0, 0) if dv is None else _need_view(dv, "dv", shape, device)
+    dwq, dwk = torch.empty((2, d), dtype=torch.float32, device=q.device).unbind(0)
+    dwq, dwk = None if wq is None else dwq, None if wk is None else dwk
+    if workspace is None:
+        nbytes = 0 if wq is None and wk is None else _qk_norm_rope_ws(B, H, N, d)
+        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=q.device) if nbytes else None
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+        if not workspace.is_contiguous() or workspace.get_device() != device:
+            raise ValueError(f"workspace: need a contiguous tensor on cuda:{device}")
+    _call("dsv_qk_norm_rope_bwd", device, dims, dq_out.data_ptr(), dk_out.data_ptr(), _ptr(dv_out), q.data_ptr(),
+          k.data_ptr(), _Strides6(*strides), _ptr(wq), _ptr(wk), pos_ptr, table_ptr, _ptr(dq), _ptr(dk), _ptr(dv),
+          _Strides9(*dstrides), _ptr(dwq), _ptr(dwk), _ptr(workspace), nbytes)
+    return dq, dk, dv, dwq, dwk
 
 
 def dsv_last_device_status(device: Optional[torch.device] = None) -> int:

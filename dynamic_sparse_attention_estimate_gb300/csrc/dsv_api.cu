@@ -8,6 +8,7 @@
 #include <atomic>
 #include <map>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "../../include/dsv.h"
@@ -616,9 +617,10 @@ dsv_status dsv_last_device_status(void* stream) {
   if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_dsv_status, &zero, sizeof(zero));
   if (e != cudaSuccess) return fail(DSV_ERR_CUDA, "status word: %s", cudaGetErrorString(e));
   if (v)
-    return fail(DSV_ERR_DEVICE_CHECK, "device status 0x%x:%s%s", v,
+    return fail(DSV_ERR_DEVICE_CHECK, "device status 0x%x:%s%s%s", v,
                 (v & 1u) ? " an out-of-range or repeated key index" : "",
-                (v & 2u) ? " a kernel gave up waiting on its own barrier" : "");
+                (v & 2u) ? " a kernel gave up waiting on its own barrier" : "",
+                (v & 4u) ? " a token position outside its axis' table" : "");
   return ok();
 }
 
@@ -690,6 +692,268 @@ dsv_status dsv_adaln_bwd(const dsv_adaln_dims* dims, const void* x, const void* 
   if ((s = status_word(&p.status)) != DSV_OK) return s;
   cudaError_t e = dsv::launch_adaln_bwd(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(DSV_ERR_CUDA, "adaln backward launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+// ---------------------------------------------------------------- rotary positions, qk norm
+static dsv_status check_rope(const dsv_rope_dims* d, dsv::RopeGeom* g) {
+  if (!d) return fail(DSV_ERR_INVALID_ARG, "dims is NULL");
+  constexpr int64_t kMax = 0x7fffffffLL;
+  if (d->B < 1 || d->H < 1 || d->N < 1) return fail(DSV_ERR_INVALID_ARG, "B, H, N must be >= 1");
+  if (d->B > kMax || d->H > kMax || d->N > kMax || d->B * d->H > kMax || d->B * d->H * d->N > kMax)
+    return fail(DSV_ERR_INVALID_ARG, "B*H*N must fit int32 row coordinates (split the heads over calls)");
+  if (d->d != 64 && d->d != 128)
+    return fail(DSV_ERR_UNSUPPORTED, "head dim d must be 64 or 128 (got %lld)", (long long)d->d);
+  if (d->pairing != DSV_PAIRS_INTERLEAVED && d->pairing != DSV_PAIRS_HALVES)
+    return fail(DSV_ERR_INVALID_ARG, "pairing must be DSV_PAIRS_INTERLEAVED or DSV_PAIRS_HALVES (got %d)", d->pairing);
+  int64_t rotated = 0, entries = 0;
+  for (int a = 0; a < 3; ++a) {
+    if (d->rot[a] < 0 || d->rot[a] % 2 || d->rot[a] > d->d)
+      return fail(DSV_ERR_INVALID_ARG, "rot[%d] must be even and in [0, d] (got %lld)", a, (long long)d->rot[a]);
+    if (d->rot[a] > 0 && (d->len[a] < 1 || d->len[a] > kMax))
+      return fail(DSV_ERR_INVALID_ARG, "len[%d] must be >= 1 and fit int32 (got %lld)", a, (long long)d->len[a]);
+    rotated += d->rot[a];
+    g->axis_pairs[a] = static_cast<int>(d->rot[a] / 2);
+    g->len[a] = d->rot[a] > 0 ? d->len[a] : 0;
+    g->table_off[a] = entries;
+    entries += g->len[a] * g->axis_pairs[a];
+  }
+  if (rotated > d->d) return fail(DSV_ERR_INVALID_ARG, "rot must sum to at most d (got %lld)", (long long)rotated);
+  if (entries > kMax) return fail(DSV_ERR_INVALID_ARG, "the table must hold at most 2^31 - 1 (cos, sin) pairs");
+  if (d->pairing == DSV_PAIRS_HALVES && rotated % 16)
+    return fail(DSV_ERR_UNSUPPORTED, "pairs in halves need rot to sum to a multiple of 16 (got %lld)",
+                (long long)rotated);
+  if (!(d->eps >= 0.f) || d->eps > 3.0e38f) return fail(DSV_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  g->B = d->B;
+  g->H = d->H;
+  g->N = d->N;
+  g->pos_batch = d->pos_batched ? d->N : 0;
+  g->pairs = static_cast<int>(rotated / 2);
+  return DSV_OK;
+}
+
+// A view's strides and the bytes it spans; an output's elements must be distinct.
+struct ViewSpan {
+  const char *lo, *hi;
+};
+static dsv_status check_view(const dsv_rope_dims* d, const char* name, const void* p, const dsv_view_strides* s,
+                             bool output, dsv::RopeView* view, ViewSpan* span) {
+  if (!p) return fail(DSV_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned16(p)) return fail(DSV_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+  const int64_t n[3] = {d->B, d->H, d->N};
+  int64_t st[3] = {s ? s->b : d->H * d->N * d->d, s ? s->h : d->N * d->d, s ? s->n : d->d};
+  int64_t last = d->d - 1;
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] == 1) st[i] = 0;   // a single entry: its stride is never used
+    if (st[i] < 0 || st[i] % 8 || st[i] > (1LL << 40))
+      return fail(DSV_ERR_INVALID_ARG, "%s: strides must be multiples of 8 elements in [0, 2^40] (got %lld)", name,
+                  (long long)st[i]);
+    last += (n[i] - 1) * (st[i] / 8) * 8;
+    if (n[i] > (1LL << 48) / (st[i] + 1) || last > (1LL << 48))
+      return fail(DSV_ERR_INVALID_ARG, "%s: the view spans too much memory", name);
+  }
+  if (output) {   // innermost to outermost: each stride must pass what the inner ones span
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < 2 - i; ++j)
+        if (st[order[j]] > st[order[j + 1]]) std::swap(order[j], order[j + 1]);
+    int64_t extent = d->d;
+    for (int i = 0; i < 3; ++i) {
+      const int a = order[i];
+      if (n[a] == 1) continue;
+      if (st[a] < extent) return fail(DSV_ERR_INVALID_ARG, "%s: the output's strides let its elements overlap", name);
+      extent += (n[a] - 1) * st[a];
+    }
+  }
+  view->p = static_cast<dsv::bf16*>(const_cast<void*>(p));
+  view->sb = st[0];
+  view->sh = st[1];
+  view->sn = st[2];
+  span->lo = static_cast<const char*>(p);
+  span->hi = span->lo + (last + 1) * 2;
+  return DSV_OK;
+}
+static bool apart(const ViewSpan& a, const ViewSpan& b) { return a.hi <= b.lo || b.hi <= a.lo; }
+
+static dsv_status check_rope_tables(const dsv::RopeGeom& g, const int32_t* pos, const float* table) {
+  if (!g.pairs) return DSV_OK;
+  DSV_NEED_PTR(pos);
+  DSV_NEED_PTR(table);
+  return DSV_OK;
+}
+
+size_t dsv_rope3d_table_bytes(const dsv_rope_dims* dims) {
+  dsv::RopeGeom g{};
+  if (check_rope(dims, &g) != DSV_OK) return 0;
+  size_t n = 0;
+  for (int a = 0; a < 3; ++a) n += static_cast<size_t>(g.len[a]) * g.axis_pairs[a];
+  return n * 2 * sizeof(float);
+}
+
+dsv_status dsv_rope3d_table(const dsv_rope_dims* dims, const double theta[3], float* table, void* stream) {
+  dsv::RopeGeom g{};
+  dsv_status s = check_rope(dims, &g);
+  if (s != DSV_OK) return s;
+  if (!g.pairs) return ok();
+  if (!theta) return fail(DSV_ERR_INVALID_ARG, "theta is NULL");
+  double th[3] = {1.0, 1.0, 1.0};
+  for (int a = 0; a < 3; ++a) {
+    if (!g.axis_pairs[a]) continue;
+    if (!(theta[a] > 0.0) || theta[a] > 1e300) return fail(DSV_ERR_INVALID_ARG, "theta[%d] must be finite and > 0", a);
+    th[a] = theta[a];
+  }
+  DSV_NEED_PTR(table);
+  cudaError_t e = dsv::launch_rope3d_table(g, th, table, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(DSV_ERR_CUDA, "rope table launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+static dsv_status rope3d_impl(const dsv_rope_dims* dims, const void* x, const dsv_view_strides* xs, const int32_t* pos,
+                              const float* table, void* y, const dsv_view_strides* ys, bool backward, void* stream) {
+  dsv::RopeParams p{};
+  dsv_status s = check_rope(dims, &p.g);
+  if (s != DSV_OK) return s;
+  ViewSpan a, b;
+  if ((s = check_view(dims, backward ? "dy" : "x", x, xs, false, &p.q, &a)) != DSV_OK) return s;
+  if ((s = check_view(dims, backward ? "dx" : "y", y, ys, true, &p.qo, &b)) != DSV_OK) return s;
+  const bool in_place = p.q.p == p.qo.p && p.q.sb == p.qo.sb && p.q.sh == p.qo.sh && p.q.sn == p.qo.sn;
+  if (!in_place && !apart(a, b))
+    return fail(DSV_ERR_INVALID_ARG, "the output overlaps the input (in place needs the same pointer and strides)");
+  if ((s = check_rope_tables(p.g, pos, table)) != DSV_OK) return s;
+  p.d = static_cast<int>(dims->d);
+  p.half = dims->pairing == DSV_PAIRS_HALVES;
+  p.backward = backward;
+  p.pos = pos;
+  p.table = table;
+  if ((s = status_word(&p.status)) != DSV_OK) return s;
+  cudaError_t e = dsv::launch_rope3d(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(DSV_ERR_CUDA, "rope3d launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+dsv_status dsv_rope3d_fwd(const dsv_rope_dims* dims, const void* x, const dsv_view_strides* x_strides,
+                          const int32_t* pos, const float* table, void* y, const dsv_view_strides* y_strides,
+                          void* stream) {
+  return rope3d_impl(dims, x, x_strides, pos, table, y, y_strides, false, stream);
+}
+
+dsv_status dsv_rope3d_bwd(const dsv_rope_dims* dims, const void* dy, const dsv_view_strides* dy_strides,
+                          const int32_t* pos, const float* table, void* dx, const dsv_view_strides* dx_strides,
+                          void* stream) {
+  return rope3d_impl(dims, dy, dy_strides, pos, table, dx, dx_strides, true, stream);
+}
+
+dsv_status dsv_qk_norm_rope_fwd(const dsv_rope_dims* dims, const void* q, const void* k, const void* v,
+                                const dsv_view_strides strides[3], const void* wq, const void* wk,
+                                const int32_t* pos, const float* table, void* q_out, void* k_out, void* v_out,
+                                void* stream) {
+  dsv::RopeParams p{};
+  dsv_status s = check_rope(dims, &p.g);
+  if (s != DSV_OK) return s;
+  if (!v != !v_out) return fail(DSV_ERR_INVALID_ARG, "v and v_out must both be given, or both be NULL");
+  const int nt = v ? 3 : 2;
+  const char* in_name[3] = {"q", "k", "v"};
+  const char* out_name[3] = {"q_out", "k_out", "v_out"};
+  const void* in[3] = {q, k, v};
+  void* out[3] = {q_out, k_out, v_out};
+  dsv::RopeView* iv[3] = {&p.q, &p.k, &p.v};
+  dsv::RopeView* ov[3] = {&p.qo, &p.ko, &p.vo};
+  ViewSpan is[3], os[3];
+  for (int i = 0; i < nt; ++i) {
+    if ((s = check_view(dims, in_name[i], in[i], strides ? strides + i : nullptr, false, iv[i], &is[i])) != DSV_OK)
+      return s;
+    if ((s = check_view(dims, out_name[i], out[i], nullptr, true, ov[i], &os[i])) != DSV_OK) return s;
+  }
+  for (int i = 0; i < nt; ++i)
+    for (int j = 0; j < nt; ++j) {
+      if (!apart(is[i], os[j])) return fail(DSV_ERR_INVALID_ARG, "%s overlaps %s", out_name[j], in_name[i]);
+      if (i < j && !apart(os[i], os[j])) return fail(DSV_ERR_INVALID_ARG, "%s overlaps %s", out_name[j], out_name[i]);
+    }
+  if (wq) DSV_NEED_PTR(wq);
+  if (wk) DSV_NEED_PTR(wk);
+  if ((s = check_rope_tables(p.g, pos, table)) != DSV_OK) return s;
+  p.d = static_cast<int>(dims->d);
+  p.half = dims->pairing == DSV_PAIRS_HALVES;
+  p.eps = dims->eps;
+  p.wq = static_cast<const dsv::bf16*>(wq);
+  p.wk = static_cast<const dsv::bf16*>(wk);
+  p.pos = pos;
+  p.table = table;
+  if ((s = status_word(&p.status)) != DSV_OK) return s;
+  cudaError_t e = dsv::launch_qk_norm_rope_fwd(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(DSV_ERR_CUDA, "qk_norm_rope forward launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+static size_t qk_norm_rope_ws(const dsv::RopeGeom& g, int64_t d) {
+  const dsv::RopeGeom plan = dsv::rope_plan(g, static_cast<int>(d));
+  return up(static_cast<size_t>(dsv::rope_bwd_ctas(plan)) * 2 * d * sizeof(float));
+}
+
+size_t dsv_qk_norm_rope_bwd_workspace(const dsv_rope_dims* dims) {
+  dsv::RopeGeom g{};
+  if (check_rope(dims, &g) != DSV_OK) return 0;
+  return qk_norm_rope_ws(g, dims->d);
+}
+
+dsv_status dsv_qk_norm_rope_bwd(const dsv_rope_dims* dims, const void* d_q_out, const void* d_k_out,
+                                const void* d_v_out, const void* q, const void* k, const dsv_view_strides strides[2],
+                                const void* wq, const void* wk, const int32_t* pos, const float* table, void* dq,
+                                void* dk, void* dv, const dsv_view_strides d_strides[3], float* dwq, float* dwk,
+                                void* ws, size_t ws_bytes, void* stream) {
+  dsv::RopeParams p{};
+  dsv_status s = check_rope(dims, &p.g);
+  if (s != DSV_OK) return s;
+  if (!d_v_out != !dv) return fail(DSV_ERR_INVALID_ARG, "d_v_out and dv must both be given, or both be NULL");
+  const int nt = dv ? 3 : 2;
+  const char* in_name[5] = {"d_q_out", "d_k_out", "q", "k", "d_v_out"};
+  const void* in[5] = {d_q_out, d_k_out, q, k, d_v_out};
+  dsv::RopeView* iv[5] = {&p.qo, &p.ko, &p.q, &p.k, &p.vo};
+  const char* out_name[3] = {"dq", "dk", "dv"};
+  void* out[3] = {dq, dk, dv};
+  dsv::RopeView* ov[3] = {&p.dq, &p.dk, &p.dv};
+  ViewSpan is[5], os[3];
+  const int ni = dv ? 5 : 4;
+  for (int i = 0; i < ni; ++i) {
+    const dsv_view_strides* st = (i == 2 || i == 3) && strides ? strides + (i - 2) : nullptr;
+    if ((s = check_view(dims, in_name[i], in[i], st, false, iv[i], &is[i])) != DSV_OK) return s;
+  }
+  for (int i = 0; i < nt; ++i)
+    if ((s = check_view(dims, out_name[i], out[i], d_strides ? d_strides + i : nullptr, true, ov[i], &os[i])) !=
+        DSV_OK)
+      return s;
+  for (int j = 0; j < nt; ++j) {
+    for (int i = 0; i < ni; ++i)
+      if (!apart(is[i], os[j])) return fail(DSV_ERR_INVALID_ARG, "%s overlaps %s", out_name[j], in_name[i]);
+    for (int i = 0; i < j; ++i)   // packed outputs interleave; the same base cannot
+      if (out[i] == out[j]) return fail(DSV_ERR_INVALID_ARG, "%s and %s are the same tensor", out_name[i], out_name[j]);
+  }
+  if (wq) DSV_NEED_PTR(wq);
+  if (wk) DSV_NEED_PTR(wk);
+  if (dwq) DSV_NEED_PTR(dwq);
+  if (dwk) DSV_NEED_PTR(dwk);
+  if ((s = check_rope_tables(p.g, pos, table)) != DSV_OK) return s;
+  if (dwq || dwk) {
+    const size_t need = qk_norm_rope_ws(p.g, dims->d);
+    if (!ws) return fail(DSV_ERR_WORKSPACE, "workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(ws) % kAlign)
+      return fail(DSV_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (ws_bytes < need)
+      return fail(DSV_ERR_WORKSPACE, "workspace of %zu bytes is below the %zu needed", ws_bytes, need);
+  }
+  p.d = static_cast<int>(dims->d);
+  p.half = dims->pairing == DSV_PAIRS_HALVES;
+  p.eps = dims->eps;
+  p.wq = static_cast<const dsv::bf16*>(wq);
+  p.wk = static_cast<const dsv::bf16*>(wk);
+  p.dwq = dwq;
+  p.dwk = dwk;
+  p.partial = static_cast<float*>(ws);
+  p.pos = pos;
+  p.table = table;
+  if ((s = status_word(&p.status)) != DSV_OK) return s;
+  cudaError_t e = dsv::launch_qk_norm_rope_bwd(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(DSV_ERR_CUDA, "qk_norm_rope backward launch: %s", cudaGetErrorString(e));
   return ok();
 }
 

@@ -139,4 +139,44 @@ cudaError_t launch_adaln_fwd(const AdalnParams& p, cudaStream_t stream);
 cudaError_t launch_adaln_bwd(const AdalnParams& p, cudaStream_t stream);
 cudaError_t launch_bwd_main_tc(const BwdParams& p, const BwdWave& w, int64_t W32, cudaStream_t stream);
 
+// ---------------------------------------------------------------- rotary positions, qk norm (dsv_rope.cu)
+// A [B][H][N][d] view: element strides of sample, head and token (features are contiguous).
+struct RopeView {
+  bf16* p = nullptr;
+  int64_t sb = 0, sh = 0, sn = 0;
+};
+struct RopeGeom {
+  int64_t B, H, N;
+  int64_t pos_batch;        // rows of pos between samples (0: shared)
+  int pairs;                // rotated pairs of a row
+  int axis_pairs[3];        // of them, each axis'
+  int64_t len[3];           // positions of each axis' table
+  int64_t table_off[3];     // first (cos, sin) of each axis
+  // launch plan (rope_plan)
+  int64_t tiles_per_b, heads_per_chunk, chunks, units;
+};
+struct RopeParams {
+  RopeGeom g;
+  int d;
+  bool half, backward;      // pairs (j, j + R/2) instead of (2j, 2j + 1); rope3d's direction
+  float eps;
+  RopeView q, k, v;         // inputs (rope3d: q alone)
+  RopeView qo, ko, vo;      // outputs of the forward; their gradients in the backward
+  RopeView dq, dk, dv;      // gradients of the inputs (backward)
+  const bf16 *wq, *wk;      // [d] or null (ones)
+  float *dwq, *dwk;         // [d] or null (backward)
+  float* partial;           // [rope_bwd_ctas][2][d] (backward)
+  const int32_t* pos;       // [N][3] or [B][N][3]
+  const float* table;
+  unsigned int* status;
+};
+constexpr int64_t kRopeWantCtas = 8 * 152;   // CTAs below which the heads of a token are split
+constexpr int64_t kRopeBwdCtas = 4 * 152;    // persistent CTAs of the backward (rows of partial sums)
+RopeGeom rope_plan(const RopeGeom& in, int d);
+int64_t rope_bwd_ctas(const RopeGeom& plan);
+cudaError_t launch_rope3d_table(const RopeGeom& g, const double (&theta)[3], float* table, cudaStream_t stream);
+cudaError_t launch_rope3d(const RopeParams& p, cudaStream_t stream);
+cudaError_t launch_qk_norm_rope_fwd(const RopeParams& p, cudaStream_t stream);
+cudaError_t launch_qk_norm_rope_bwd(const RopeParams& p, cudaStream_t stream);
+
 }  // namespace dsv

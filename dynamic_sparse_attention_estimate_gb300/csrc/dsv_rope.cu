@@ -1,0 +1,538 @@
+// Rotary positions with several axes (time, height, width), alone and behind the per-head RMS norm
+// of queries and keys, both directions.
+//
+// A head row of d features is d / 8 16-byte vectors, one per lane (LPR = 8 or 16 lanes a row).  Its
+// pairs (x0, x1) turn by the angle of their axis: y0 = x0 c - x1 s, y1 = x0 s + x1 c; the backward
+// turns by the negative angle.  The angles separate over the axes, so (cos, sin) come from one
+// small table per axis (rows = positions, a few KB in all, L1-resident) instead of a [N][d/2]
+// array of the clip (266 MB at 520,192 tokens and d = 128): a token costs its 12 bytes of
+// coordinates.  With the norm, n = x rstd w with rstd = 1 / sqrt(mean(x^2) + eps) before the
+// rotation; the backward recomputes rstd from x:
+//   g = rotation^T(dy),  dw = sum_rows g x rstd,  dx = rstd (g w - x rstd^2 mean(g w x)).
+//
+// Bound: HBM.  A group of LPR lanes owns one token and walks its heads, so a token's (cos, sin) and
+// the weights are read once for all its heads and both tensors; a packed token-major projection
+// is read front to back, and the head-major outputs get rows of consecutive tokens from
+// neighbouring groups.  Queries, keys and values go in one launch: the loads of several
+// rows are issued before the first is used, which is what keeps HBM busy (no staging is needed:
+// nothing is read twice).
+#include "dsv_common.cuh"
+#include "dsv_internal.h"
+
+namespace dsv {
+namespace {
+
+constexpr int kThreads = 128;
+// rows (heads) of each tensor that a group loads ahead
+constexpr int kRopeRows = 2, kNormRows = 2, kBackRows = 2;
+constexpr int kBackCtas = 4;   // of the backward, on an SM
+
+DSV_DEVICE uint32_t word(const uint4& u, int j) { return j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w; }
+
+DSV_DEVICE void unpack(const uint4& u, float (&f)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = bf16_lo(word(u, j));
+    f[2 * j + 1] = bf16_hi(word(u, j));
+  }
+}
+DSV_DEVICE uint4 pack(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+DSV_DEVICE uint4 shfl(const uint4& u, int src) {
+  return make_uint4(__shfl_sync(0xffffffffu, u.x, src), __shfl_sync(0xffffffffu, u.y, src),
+                    __shfl_sync(0xffffffffu, u.z, src), __shfl_sync(0xffffffffu, u.w, src));
+}
+
+// Sum over the LPR lanes of a row (every lane gets it; the order is fixed).
+template <int LPR>
+DSV_DEVICE float row_sum(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// The rotation of one lane's vector at one token: (cos, +-sin) of its pairs.
+//   interleaved: pair i of the vector is its elements (2i, 2i + 1); 4 pairs, those from `turned` on pass
+//   halves:      element e pairs with element e of the vector `partner` lanes hold; 8 pairs, all or none
+template <bool HALF>
+struct Turn {
+  static constexpr int P = HALF ? 8 : 4;
+  float c[P], s[P];
+  int turned;   // pairs of this vector that are rotated
+};
+
+// sign: +1 forward, -1 backward.  An axis whose position is outside its table leaves its pairs
+// unrotated (angle 0) and sets the status bit.
+template <bool HALF>
+DSV_DEVICE void load_turn(Turn<HALF>& t, const RopeGeom& g, const float2* __restrict__ table,
+                          const int32_t* __restrict__ pos, int64_t row, bool active, int vec, float sign,
+                          unsigned int* status) {
+  const int half_vecs = g.pairs / 8;   // HALF: vectors of a half (pairs is a multiple of 8)
+  int j0;
+  if (HALF) {
+    const bool second = vec >= half_vecs;
+    j0 = (second ? vec - half_vecs : vec) * 8;
+    t.turned = vec < 2 * half_vecs ? 8 : 0;
+    if (!second) sign = -sign;   // y0 = x0 c - x1 s; y1 = x1 c + x0 s
+  } else {
+    j0 = vec * 4;
+    const int left = g.pairs - j0;
+    t.turned = left < 0 ? 0 : left > 4 ? 4 : left;
+  }
+#pragma unroll
+  for (int i = 0; i < Turn<HALF>::P; ++i) {
+    t.c[i] = 1.f;
+    t.s[i] = 0.f;
+  }
+  if (!active || t.turned == 0) return;
+  int p[3];
+#pragma unroll
+  for (int a = 0; a < 3; ++a) {
+    p[a] = __ldg(pos + row * 3 + a);
+    if (g.axis_pairs[a] > 0 && static_cast<uint32_t>(p[a]) >= static_cast<uint32_t>(g.len[a])) {
+      flag_status(status, kStatusBadPosition);
+      p[a] = -1;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < Turn<HALF>::P; ++i) {
+    const int j = j0 + i;
+    if (i >= t.turned) continue;
+    int a = 0, first = 0;
+    if (j >= g.axis_pairs[0]) { a = 1; first = g.axis_pairs[0]; }
+    if (j >= g.axis_pairs[0] + g.axis_pairs[1]) { a = 2; first = g.axis_pairs[0] + g.axis_pairs[1]; }
+    const int pa = a == 0 ? p[0] : a == 1 ? p[1] : p[2];
+    const int np = a == 0 ? g.axis_pairs[0] : a == 1 ? g.axis_pairs[1] : g.axis_pairs[2];
+    const int64_t off = a == 0 ? 0 : a == 1 ? g.table_off[1] : g.table_off[2];
+    if (pa < 0) continue;
+    const float2 cs = __ldg(table + off + static_cast<int64_t>(pa) * np + (j - first));
+    t.c[i] = cs.x;
+    t.s[i] = sign * cs.y;
+  }
+}
+
+// f (this lane's 8 values) turned; fp: the partner vector's values (HALF only).
+template <bool HALF>
+DSV_DEVICE void turn(const Turn<HALF>& t, float (&f)[8], const float (&fp)[8]) {
+  if constexpr (HALF) {
+    if (t.turned) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = fmaf(f[e], t.c[e], fp[e] * t.s[e]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= t.turned) continue;   // features past the rotated ones pass, infinities too
+      const float a = f[2 * i], b = f[2 * i + 1];
+      f[2 * i] = fmaf(a, t.c[i], -(b * t.s[i]));
+      f[2 * i + 1] = fmaf(a, t.s[i], b * t.c[i]);
+    }
+  }
+}
+
+// HALF: the lane of this row that holds the partner vector (itself where nothing turns).
+template <int LPR>
+DSV_DEVICE int partner_lane(const RopeGeom& g, int lane, int vec) {
+  const int hv = g.pairs / 8;
+  const int p = vec < hv ? vec + hv : vec < 2 * hv ? vec - hv : vec;
+  return (lane & ~(LPR - 1)) | p;
+}
+
+struct Lane {
+  int lane, vec;
+  int64_t b, n, row;   // sample, token, row of pos
+  int64_t h0, h1;
+  bool active;
+};
+
+// blockIdx.x: token tile of a sample; blockIdx.y: head chunk
+template <int LPR>
+DSV_DEVICE Lane lane_of(const RopeGeom& g, int64_t unit) {
+  Lane l;
+  l.lane = threadIdx.x & 31;
+  l.vec = threadIdx.x & (LPR - 1);
+  constexpr int kTok = kThreads / LPR;
+  const int64_t chunk = unit % g.chunks, tile = unit / g.chunks;
+  l.b = tile / g.tiles_per_b;
+  l.n = (tile % g.tiles_per_b) * kTok + threadIdx.x / LPR;
+  l.active = l.n < g.N;
+  l.row = l.b * g.pos_batch + l.n;
+  l.h0 = chunk * g.heads_per_chunk;
+  l.h1 = l.h0 + g.heads_per_chunk < g.H ? l.h0 + g.heads_per_chunk : g.H;
+  return l;
+}
+
+// U rows of a view, heads h .. h + U - 1 of this group's token (zeros past its heads).
+template <int U>
+DSV_DEVICE void load_rows(uint4 (&v)[U], const bf16* p, int64_t stride, int64_t h, const Lane& l) {
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    v[u] = l.active && h + u < l.h1 ? *reinterpret_cast<const uint4*>(p + (h + u) * stride)
+                                    : make_uint4(0, 0, 0, 0);
+}
+DSV_DEVICE void store_row(bf16* p, const uint4& v) { *reinterpret_cast<uint4*>(p) = v; }
+
+// ---------------------------------------------------------------- rotation alone
+template <int D, bool HALF>
+__global__ void __launch_bounds__(kThreads)
+rope3d_kernel(RopeGeom g, RopeView x, RopeView y, const int32_t* __restrict__ pos, const float2* __restrict__ table,
+              float sign, unsigned int* status) {
+  constexpr int LPR = D / 8, U = kRopeRows;
+  const Lane l = lane_of<LPR>(g, blockIdx.x);
+  const bf16* xp = x.p + l.b * x.sb + l.n * x.sn + l.vec * 8;
+  bf16* yp = y.p + l.b * y.sb + l.n * y.sn + l.vec * 8;
+  uint4 next[U];
+  load_rows<U>(next, xp, x.sh, l.h0, l);   // on their way while the table is read
+  Turn<HALF> t;
+  load_turn<HALF>(t, g, table, pos, l.row, l.active, l.vec, sign, status);
+  const int partner = HALF ? partner_lane<LPR>(g, l.lane, l.vec) : 0;
+  for (int64_t h = l.h0; h < l.h1; h += U) {
+    uint4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = next[u];
+    load_rows<U>(next, xp, x.sh, h + U, l);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float f[8], fp[8];
+      unpack(v[u], f);
+      if constexpr (HALF) unpack(shfl(v[u], partner), fp);
+      turn<HALF>(t, f, fp);
+      if (l.active && h + u < l.h1) store_row(yp + (h + u) * y.sh, pack(f));
+    }
+  }
+}
+
+// ---------------------------------------------------------------- norm + rotation, forward
+template <int D, bool HALF>
+DSV_DEVICE uint4 norm_turn(const uint4& v, const uint4& w, const uint4& wp, const Turn<HALF>& t, int partner,
+                           float eps) {
+  constexpr int LPR = D / 8;
+  float f[8], fw[8], fp[8];
+  unpack(v, f);
+  float ss = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
+  const float rstd = rsqrtf(fmaf(row_sum<LPR>(ss), 1.f / D, eps));
+  unpack(w, fw);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * fw[e];
+  if constexpr (HALF) {
+    unpack(shfl(v, partner), fp);
+    unpack(wp, fw);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) fp[e] = fp[e] * rstd * fw[e];
+  }
+  turn<HALF>(t, f, fp);
+  return pack(f);
+}
+
+DSV_DEVICE uint4 load_weight(const bf16* w, int vec) {
+  // without a weight: ones (bf16 1.0 = 0x3f80)
+  return w ? __ldg(reinterpret_cast<const uint4*>(w) + vec)
+           : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+}
+
+template <int D, bool HALF>
+__global__ void __launch_bounds__(kThreads)
+qk_norm_rope_fwd_kernel(RopeGeom g, RopeView q, RopeView k, RopeView v, RopeView qo, RopeView ko, RopeView vo,
+                        const bf16* __restrict__ wq, const bf16* __restrict__ wk, const int32_t* __restrict__ pos,
+                        const float2* __restrict__ table, float eps, unsigned int* status) {
+  constexpr int LPR = D / 8, U = kNormRows;
+  const Lane l = lane_of<LPR>(g, blockIdx.x);
+  const bool has_v = v.p != nullptr;
+  const bf16* qp = q.p + l.b * q.sb + l.n * q.sn + l.vec * 8;
+  const bf16* kp = k.p + l.b * k.sb + l.n * k.sn + l.vec * 8;
+  const bf16* vp = has_v ? v.p + l.b * v.sb + l.n * v.sn + l.vec * 8 : nullptr;
+  bf16* qop = qo.p + l.b * qo.sb + l.n * qo.sn + l.vec * 8;
+  bf16* kop = ko.p + l.b * ko.sb + l.n * ko.sn + l.vec * 8;
+  bf16* vop = has_v ? vo.p + l.b * vo.sb + l.n * vo.sn + l.vec * 8 : nullptr;
+  uint4 na[U], nb[U], nc[U];
+  auto fetch = [&](int64_t h) {
+    load_rows<U>(na, qp, q.sh, h, l);
+    load_rows<U>(nb, kp, k.sh, h, l);
+    if (has_v) load_rows<U>(nc, vp, v.sh, h, l);
+  };
+  fetch(l.h0);   // on their way while the table and the weights are read
+  Turn<HALF> t;
+  load_turn<HALF>(t, g, table, pos, l.row, l.active, l.vec, 1.f, status);
+  const int partner = HALF ? partner_lane<LPR>(g, l.lane, l.vec) : 0;
+  const uint4 fq = load_weight(wq, l.vec), fk = load_weight(wk, l.vec);
+  uint4 fqp = fq, fkp = fk;
+  if constexpr (HALF) {
+    fqp = shfl(fq, partner);
+    fkp = shfl(fk, partner);
+  }
+  for (int64_t h = l.h0; h < l.h1; h += U) {
+    uint4 a[U], b[U], c[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      a[u] = na[u];
+      b[u] = nb[u];
+      c[u] = nc[u];
+    }
+    fetch(h + U);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool on = l.active && h + u < l.h1;
+      const uint4 ra = norm_turn<D, HALF>(a[u], fq, fqp, t, partner, eps);
+      const uint4 rb = norm_turn<D, HALF>(b[u], fk, fkp, t, partner, eps);
+      if (on) {
+        store_row(qop + (h + u) * qo.sh, ra);
+        store_row(kop + (h + u) * ko.sh, rb);
+        if (has_v) store_row(vop + (h + u) * vo.sh, c[u]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- norm + rotation, backward
+// dx of one vector; its part of the weight's gradient is added to dw.
+template <int D, bool HALF>
+DSV_DEVICE uint4 norm_turn_back(const uint4& dy, const uint4& x, const uint4& w, const Turn<HALF>& t, int partner,
+                                float eps, bool on, float (&dw)[8]) {
+  constexpr int LPR = D / 8;
+  float gr[8], f[8], fw[8], fp[8];
+  unpack(dy, gr);
+  if constexpr (HALF) unpack(shfl(dy, partner), fp);
+  turn<HALF>(t, gr, fp);
+  unpack(x, f);
+  unpack(w, fw);
+  float ss = 0.f, m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    ss = fmaf(f[e], f[e], ss);
+    m = fmaf(gr[e] * fw[e], f[e], m);
+  }
+  ss = row_sum<LPR>(ss);
+  m = row_sum<LPR>(m);
+  const float rstd = rsqrtf(fmaf(ss, 1.f / D, eps));
+  m *= rstd * (1.f / D);                       // mean(g w xhat)
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float xhat = f[e] * rstd;
+    if (on) dw[e] = fmaf(gr[e], xhat, dw[e]);   // a row of zeros past the heads has no finite xhat at eps = 0
+    f[e] = rstd * fmaf(-xhat, m, gr[e] * fw[e]);
+  }
+  return pack(f);
+}
+
+template <int D, bool HALF>
+__global__ void __launch_bounds__(kThreads, kBackCtas)
+qk_norm_rope_bwd_kernel(RopeGeom g, RopeView dqo, RopeView dko, RopeView dvo, RopeView q, RopeView k, RopeView dq,
+                        RopeView dk, RopeView dv, const bf16* __restrict__ wq, const bf16* __restrict__ wk,
+                        const int32_t* __restrict__ pos, const float2* __restrict__ table, float eps,
+                        float* __restrict__ partial, unsigned int* status) {
+  constexpr int LPR = D / 8, kTok = kThreads / LPR, U = kBackRows;
+  // the column sums may be scheduled once every CTA of this grid has started; they wait for its end
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  __shared__ float red[kTok][2 * D];
+  const int vec = threadIdx.x & (LPR - 1), grp = threadIdx.x / LPR;
+  const uint4 fq = load_weight(wq, vec), fk = load_weight(wk, vec);
+  float aq[8], ak[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) aq[e] = ak[e] = 0.f;
+  for (int64_t unit = blockIdx.x; unit < g.units; unit += gridDim.x) {
+    const Lane l = lane_of<LPR>(g, unit);
+    auto at = [&](const RopeView& r) { return r.p + l.b * r.sb + l.n * r.sn + vec * 8; };
+    Turn<HALF> t;
+    const int partner = HALF ? partner_lane<LPR>(g, l.lane, l.vec) : 0;
+    // one tensor's heads of this token, then the next tensor's (half the registers of both at once);
+    // values ride along: c = copied rows, if any
+    auto walk = [&](const RopeView& ry, const RopeView& rx, const RopeView& rd, const RopeView& rc,
+                    const RopeView& rcd, const uint4& w, float (&acc)[8], bool first) {
+      const bf16 *py = at(ry), *px = at(rx);
+      bf16* pd = at(rd);
+      const bool copy = rc.p != nullptr;
+      const bf16* pc = copy ? at(rc) : nullptr;
+      bf16* pcd = copy ? at(rcd) : nullptr;
+      uint4 ny[U], nx[U], nc[U];
+      auto fetch = [&](int64_t h) {
+        load_rows<U>(ny, py, ry.sh, h, l);
+        load_rows<U>(nx, px, rx.sh, h, l);
+        if (copy) load_rows<U>(nc, pc, rc.sh, h, l);
+      };
+      fetch(l.h0);
+      if (first) load_turn<HALF>(t, g, table, pos, l.row, l.active, l.vec, -1.f, status);
+      // a token's heads are summed first and its sum then added: two short chains of fp32
+      // additions instead of one as long as the clip
+      float tok[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) tok[e] = 0.f;
+      for (int64_t h = l.h0; h < l.h1; h += U) {
+        uint4 y[U], x[U], c[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          y[u] = ny[u];
+          x[u] = nx[u];
+          c[u] = nc[u];
+        }
+        fetch(h + U);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const bool on = l.active && h + u < l.h1;
+          const uint4 r = norm_turn_back<D, HALF>(y[u], x[u], w, t, partner, eps, on, tok);
+          if (on) {
+            store_row(pd + (h + u) * rd.sh, r);
+            if (copy) store_row(pcd + (h + u) * rcd.sh, c[u]);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += tok[e];
+    };
+    walk(dqo, q, dq, dvo, dv, fq, aq, true);
+    walk(dko, k, dk, RopeView(), RopeView(), fk, ak, false);
+  }
+  if (!partial) return;   // no weights: nothing to sum
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    red[grp][vec * 8 + e] = aq[e];
+    red[grp][D + vec * 8 + e] = ak[e];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    float s = 0.f;
+    for (int r = 0; r < kTok; ++r) s += red[r][i];
+    partial[static_cast<int64_t>(blockIdx.x) * 2 * D + i] = s;
+  }
+}
+
+// dw[i] = sum over the CTAs of partial[c][i], in a fixed order: 32 columns a CTA, 32 warps take
+// every 32nd row each, then the 32 sums in warp order.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(32 * kSumWarps)
+qk_norm_colsum_kernel(const float* __restrict__ partial, int rows, int D, float* __restrict__ dwq,
+                      float* __restrict__ dwk) {
+  __shared__ float red[kSumWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  float s0 = 0.f;
+#pragma unroll 8
+  for (int r = warp; r < rows; r += kSumWarps) s0 += partial[static_cast<int64_t>(r) * 2 * D + col];
+  red[warp][lane] = s0;
+  __syncthreads();
+  if (warp == 0) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSumWarps; ++w) s += red[w][lane];
+    float* out = col < D ? dwq : dwk;
+    if (out) out[col < D ? col : col - D] = s;
+  }
+}
+
+// ---------------------------------------------------------------- the table
+// (cos, sin) of angle p theta^(-2i / r) in double, rounded once: far positions keep their phase.
+__global__ void __launch_bounds__(kThreads)
+rope3d_table_kernel(RopeGeom g, double th0, double th1, double th2, int64_t total, float2* __restrict__ table) {
+  const int64_t e = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (e >= total) return;
+  const int a = e >= g.table_off[2] ? 2 : e >= g.table_off[1] ? 1 : 0;
+  const double theta = a == 0 ? th0 : a == 1 ? th1 : th2;
+  const int np = g.axis_pairs[a];
+  const int64_t local = e - g.table_off[a];
+  const int64_t p = local / np;
+  const int i = static_cast<int>(local % np);
+  const double ang = static_cast<double>(p) * pow(theta, -static_cast<double>(i) / np);
+  double s, c;
+  sincos(ang, &s, &c);
+  table[e] = make_float2(static_cast<float>(c), static_cast<float>(s));
+}
+
+// Head chunks: a CTA walks all heads of its tokens unless that leaves the card's 152 SMs short of
+// CTAs; then the heads are split.
+void split_heads(RopeGeom& g, int tok) {
+  g.tiles_per_b = (g.N + tok - 1) / tok;
+  const int64_t tiles = g.B * g.tiles_per_b;
+  int64_t chunks = (kRopeWantCtas + tiles - 1) / tiles;
+  if (chunks > g.H) chunks = g.H;
+  g.heads_per_chunk = (g.H + chunks - 1) / chunks;
+  g.chunks = (g.H + g.heads_per_chunk - 1) / g.heads_per_chunk;
+  g.units = tiles * g.chunks;
+}
+
+}  // namespace
+
+RopeGeom rope_plan(const RopeGeom& in, int d) {
+  RopeGeom g = in;
+  split_heads(g, kThreads / (d / 8));
+  return g;
+}
+
+int64_t rope_bwd_ctas(const RopeGeom& g) { return g.units < kRopeBwdCtas ? g.units : kRopeBwdCtas; }
+
+cudaError_t launch_rope3d_table(const RopeGeom& g, const double (&theta)[3], float* table, cudaStream_t stream) {
+  int64_t total = 0;
+  for (int a = 0; a < 3; ++a) total += g.len[a] * g.axis_pairs[a];
+  if (total == 0) return cudaSuccess;
+  ProfScope prof("rope3d_table", stream);
+  rope3d_table_kernel<<<static_cast<unsigned>((total + kThreads - 1) / kThreads), kThreads, 0, stream>>>(
+      g, theta[0], theta[1], theta[2], total, reinterpret_cast<float2*>(table));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rope3d(const RopeParams& p, cudaStream_t stream) {
+  const RopeGeom g = rope_plan(p.g, p.d);
+  const float2* table = reinterpret_cast<const float2*>(p.table);
+  const float sign = p.backward ? -1.f : 1.f;
+  const unsigned grid = static_cast<unsigned>(g.units);
+  ProfScope prof(p.backward ? "rope3d_bwd" : "rope3d_fwd", stream);
+  if (p.d == 128) {
+    if (p.half) rope3d_kernel<128, true><<<grid, kThreads, 0, stream>>>(g, p.q, p.qo, p.pos, table, sign, p.status);
+    else rope3d_kernel<128, false><<<grid, kThreads, 0, stream>>>(g, p.q, p.qo, p.pos, table, sign, p.status);
+  } else {
+    if (p.half) rope3d_kernel<64, true><<<grid, kThreads, 0, stream>>>(g, p.q, p.qo, p.pos, table, sign, p.status);
+    else rope3d_kernel<64, false><<<grid, kThreads, 0, stream>>>(g, p.q, p.qo, p.pos, table, sign, p.status);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_qk_norm_rope_fwd(const RopeParams& p, cudaStream_t stream) {
+  const RopeGeom g = rope_plan(p.g, p.d);
+  const float2* table = reinterpret_cast<const float2*>(p.table);
+  const unsigned grid = static_cast<unsigned>(g.units);
+  ProfScope prof("qk_norm_rope_fwd", stream);
+  auto go = [&](auto kernel) {
+    kernel<<<grid, kThreads, 0, stream>>>(g, p.q, p.k, p.v, p.qo, p.ko, p.vo, p.wq, p.wk, p.pos, table, p.eps,
+                                          p.status);
+  };
+  if (p.d == 128) p.half ? go(qk_norm_rope_fwd_kernel<128, true>) : go(qk_norm_rope_fwd_kernel<128, false>);
+  else p.half ? go(qk_norm_rope_fwd_kernel<64, true>) : go(qk_norm_rope_fwd_kernel<64, false>);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_qk_norm_rope_bwd(const RopeParams& p, cudaStream_t stream) {
+  const RopeGeom g = rope_plan(p.g, p.d);
+  const float2* table = reinterpret_cast<const float2*>(p.table);
+  const int64_t ctas = rope_bwd_ctas(g);
+  const unsigned grid = static_cast<unsigned>(ctas);
+  float* partial = p.dwq || p.dwk ? p.partial : nullptr;
+  {
+    ProfScope prof("qk_norm_rope_bwd", stream);
+    auto go = [&](auto kernel) {
+      kernel<<<grid, kThreads, 0, stream>>>(g, p.qo, p.ko, p.vo, p.q, p.k, p.dq, p.dk, p.dv, p.wq, p.wk, p.pos, table,
+                                            p.eps, partial, p.status);
+    };
+    if (p.d == 128) p.half ? go(qk_norm_rope_bwd_kernel<128, true>) : go(qk_norm_rope_bwd_kernel<128, false>);
+    else p.half ? go(qk_norm_rope_bwd_kernel<64, true>) : go(qk_norm_rope_bwd_kernel<64, false>);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (!partial) return cudaSuccess;
+  ProfScope prof("qk_norm_colsum", stream);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * p.d / 32));
+  cfg.blockDim = dim3(32 * kSumWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, qk_norm_colsum_kernel, static_cast<const float*>(partial), static_cast<int>(ctas),
+                            p.d, p.dwq, p.dwk);
+}
+
+}  // namespace dsv

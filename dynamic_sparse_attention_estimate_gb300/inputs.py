@@ -190,6 +190,13 @@ def make_inputs(wl: Workload, heads: Optional[Sequence[int]] = None, b: int = 0)
     return {key: torch.stack([s[key] for s in slices], 0).unsqueeze(0).contiguous() for key in slices[0]}
 
 
+def token_positions(latent: Sequence[int], block_shape: Optional[Sequence[int]]) -> torch.Tensor:
+    """int32 [N, 3]: the (t, h, w) of the token at each block-major position (what the rotary calls take)."""
+    T, Hh, W = latent
+    p = block_major_permutation(latent, block_shape)
+    return torch.from_numpy(np.stack([p // (Hh * W), p // W % Hh, p % W], 1).astype(np.int32))
+
+
 def sample_blocks(n_blocks_total: int, count: int, seed: int = 0) -> np.ndarray:
     """Seeded, sorted choice of `count` distinct query blocks (for sampled parity checks)."""
     rng = np.random.default_rng(seed + 31337)

@@ -254,9 +254,9 @@ const char* dsv_status_string(dsv_status status);
 const char* dsv_last_error_message(void);
 
 /* Synchronises `stream`, then reads and clears the current device's status word.
- * Returns DSV_ERR_DEVICE_CHECK if a kernel met a key index outside [0, N) since the
- * last read (the offending entry is skipped, never dereferenced), DSV_ERR_CUDA if
- * the synchronisation failed, DSV_OK otherwise. */
+ * Returns DSV_ERR_DEVICE_CHECK if a kernel met a key index outside [0, N), or a token
+ * position outside its axis' table, since the last read (the offending entry is skipped,
+ * never dereferenced), DSV_ERR_CUDA if the synchronisation failed, DSV_OK otherwise. */
 dsv_status dsv_last_device_status(void* stream);
 
 /*
@@ -309,6 +309,100 @@ size_t dsv_adaln_bwd_workspace(const dsv_adaln_dims* dims);
  * programmatic dependent of the first (it waits for the first to finish before reading). */
 dsv_status dsv_adaln_bwd(const dsv_adaln_dims* dims, const void* x, const void* scale, const void* dy, void* dx,
                          float* d_scale, float* d_shift, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------- rotary positions with several axes, qk norm
+ * What a video DiT block does between its Q/K/V projection and the attention above: the norm of
+ * queries and keys for each head, the rotation by the token's (time, height, width) position, and
+ * the move from the projection's layout to [B][H][N][d].  (The DSV pages take Q and K as given;
+ * these calls produce them.)
+ *
+ * Rotation.  Axis a (0 time, 1 height, 2 width) turns rot[a] features (even; 0: axis unused): its
+ * pair i < rot[a] / 2 by the angle p * theta[a]^(-2 i / rot[a]) at position p.  The R / 2 pairs
+ * (R = rot[0] + rot[1] + rot[2] <= d) are numbered through the axes in order; pair j is
+ *   DSV_PAIRS_INTERLEAVED: features (2 j, 2 j + 1);   DSV_PAIRS_HALVES: features (j, j + R / 2),
+ * and turns  y0 = x0 cos - x1 sin,  y1 = x0 sin + x1 cos  (the backward by the negative angle).
+ * Features from R on pass unchanged.  Angles separate over the axes, so the table holds one small
+ * part per axis instead of a row per token:
+ *   table: fp32 (cos, sin) pairs; axis a's part is [len[a]][rot[a] / 2][2], the parts one after
+ *     another (dsv_rope3d_table fills it from theta, angles in fp64; a caller with scaled
+ *     positions or frequencies fills its own);
+ *   pos: int32 [N][3] (pos_batched = 0, shared by the samples) or [B][N][3]: each token's
+ *     (t, h, w), 0 <= pos < len of that axis.  Tokens may be in any order (e.g. block-major).  An
+ *     axis whose position is outside its table is not rotated for that token, and the device status
+ *     word is set (dsv_last_device_status).
+ *   With R = 0 nothing is rotated (norm alone); pos and table may then be NULL.
+ *
+ * Views.  Tensors are bf16 [B][H][N][d] with contiguous features; dsv_view_strides gives the
+ * element strides of sample, head and token (each >= 0 and a multiple of 8; NULL: contiguous
+ * [B][H][N][d]).  A packed projection [B][N][3][H][d] is three such views.  Inputs may be broadcast
+ * (stride 0).  An output's elements must be distinct (its strides are checked), and outputs must
+ * not overlap inputs or each other, except that rope3d may run in place (the same pointer and
+ * strides); ranges that overlap an input's in any other way are refused, the packed outputs of one
+ * call may interleave.
+ *
+ * Validation before any launch: B, H, N >= 1; B*H*N < 2^31; d in {64, 128}; rot even, >= 0, sum
+ * <= d (a multiple of 16 for DSV_PAIRS_HALVES); len >= 1 for every axis in use, and at most 2^31
+ * (cos, sin) pairs in all; eps >= 0 and finite.  Any N: it need not be a multiple of the
+ * attention's block.
+ */
+typedef enum { DSV_PAIRS_INTERLEAVED = 0, DSV_PAIRS_HALVES = 1 } dsv_pairing;
+
+typedef struct {
+  int64_t B, H, N, d;
+  int64_t rot[3];        /* rotated features of time, height, width */
+  int64_t len[3];        /* positions of each axis' table */
+  int32_t pairing;       /* dsv_pairing */
+  int32_t pos_batched;   /* pos has a row per (sample, token) */
+  float eps;             /* of the norm (the rope3d calls do not read it) */
+} dsv_rope_dims;
+
+typedef struct {
+  int64_t b, h, n;       /* element strides of sample, head, token */
+} dsv_view_strides;
+
+/* Bytes of the table (0 for invalid dims, or with R = 0). */
+size_t dsv_rope3d_table_bytes(const dsv_rope_dims* dims);
+/* Fills the table; theta[a] > 0 and finite for every axis in use.  Once per model, not per step. */
+dsv_status dsv_rope3d_table(const dsv_rope_dims* dims, const double theta[3], float* table, void* stream);
+
+/* y = x rotated at each token's position. */
+dsv_status dsv_rope3d_fwd(const dsv_rope_dims* dims, const void* x, const dsv_view_strides* x_strides,
+                          const int32_t* pos, const float* table, void* y, const dsv_view_strides* y_strides,
+                          void* stream);
+/* dx for the loss gradient dy: the rotation by the negative angles. */
+dsv_status dsv_rope3d_bwd(const dsv_rope_dims* dims, const void* dy, const dsv_view_strides* dy_strides,
+                          const int32_t* pos, const float* table, void* dx, const dsv_view_strides* dx_strides,
+                          void* stream);
+
+/*
+ * Norm of queries and keys for each head and the rotation in one pass, with the layout change:
+ *   n = x / sqrt(mean_d(x^2) + eps) * w,  out = rotation(n)   for q (w = wq) and k (w = wk);
+ *   v_out = v  (v and v_out both NULL: no values in this call).
+ * wq, wk: bf16 [d] (NULL: ones).  strides: of q, k, v in this order (NULL: all contiguous).
+ * q_out, k_out, v_out: contiguous [B][H][N][d], as the attention calls take them.
+ * fp32 arithmetic, one rounding to bf16 at the end.
+ */
+dsv_status dsv_qk_norm_rope_fwd(const dsv_rope_dims* dims, const void* q, const void* k, const void* v,
+                                const dsv_view_strides strides[3], const void* wq, const void* wk,
+                                const int32_t* pos, const float* table, void* q_out, void* k_out, void* v_out,
+                                void* stream);
+/* Bytes of workspace dsv_qk_norm_rope_bwd needs (partial sums of the weights' gradients). */
+size_t dsv_qk_norm_rope_bwd_workspace(const dsv_rope_dims* dims);
+/*
+ * Gradients of the call above: with g = rotation^T(d_out) and xhat = x / sqrt(mean_d(x^2) + eps),
+ *   dx = rstd (g w - xhat mean_d(g w xhat)),   dw[d] = sum over B, H, N of g xhat,   dv = d_v_out.
+ * d_q_out, d_k_out, d_v_out: contiguous bf16 [B][H][N][d] (d_v_out NULL with dv: no values).
+ * q, k: the forward's inputs, strides[0], strides[1].  dq, dk, dv: bf16 views with d_strides[0..2]
+ * (NULL: contiguous).  dwq, dwk: fp32 [d], NULL where not wanted; bitwise reproducible (fixed
+ * summation order).  ws: at least dsv_qk_norm_rope_bwd_workspace(dims) bytes, 256-byte aligned
+ * (not needed, and not read, with both dwq and dwk NULL); one workspace must not serve two calls
+ * that can run at the same time.
+ */
+dsv_status dsv_qk_norm_rope_bwd(const dsv_rope_dims* dims, const void* d_q_out, const void* d_k_out,
+                                const void* d_v_out, const void* q, const void* k, const dsv_view_strides strides[2],
+                                const void* wq, const void* wk, const int32_t* pos, const float* table, void* dq,
+                                void* dk, void* dv, const dsv_view_strides d_strides[3], float* dwq, float* dwk,
+                                void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

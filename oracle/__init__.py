@@ -19,7 +19,10 @@ Pins (what ties each function to something other than itself) live in ``tests/``
   fused AdaLN      : torch fp64 layer_norm + modulation and its autograd, central finite
                      differences, closed forms (constant rows give y = shift, the per-row
                      invariants sum dx = 0 and sum dx * xhat = 0, d_shift = sum dy),
-                     planted mistakes rejected.
+                     planted mistakes rejected;
+  rotary, qk norm  : complex multiplication in torch fp64 and autograd through it, central
+                     finite differences, closed forms (norms kept, relative positions,
+                     position 0 is the identity).
 """
 from .dsv_oracle import (  # noqa: F401
     block_representatives,
@@ -37,3 +40,11 @@ from .dsv_oracle import (  # noqa: F401
     topk_select,
 )
 from .adaln_oracle import adaln_bwd, adaln_fwd, row_stats  # noqa: F401,E402
+from .rope_oracle import (  # noqa: F401,E402
+    pair_features,
+    qk_norm,
+    qk_norm_rope_bwd,
+    qk_norm_rope_fwd,
+    rope,
+    rope_angles,
+)

@@ -1,0 +1,159 @@
+"""Host validation of the rotary and qk-norm calls: refused before anything is launched (CPU only)."""
+import ctypes
+
+import pytest
+import torch
+
+import dynamic_sparse_attention_estimate_gb300 as pkg
+from dynamic_sparse_attention_estimate_gb300 import RopeTable
+from dynamic_sparse_attention_estimate_gb300.binding import RopeDims, ViewStrides
+
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from dynamic_sparse_attention_estimate_gb300.build import build
+    build()
+    return pkg.load_library()
+
+
+@pytest.fixture(autouse=True)
+def no_gpu():
+    """Made-up device addresses are only passed where no launch could follow."""
+    if torch.cuda.is_available():
+        pytest.skip("made-up device addresses are only passed where no GPU is visible")
+
+
+def dims(**over):
+    d = RopeDims(B=2, H=3, N=40, d=64, pairing=0, pos_batched=0, eps=1e-6)
+    d.rot[:] = (24, 20, 20)
+    d.len[:] = (4, 16, 16)
+    for k, v in over.items():
+        if k in ("rot", "len"):
+            getattr(d, k)[:] = v
+        else:
+            setattr(d, k, v)
+    return d
+
+
+X, Y, POS, TAB = 0x100000, 0x900000, 0x2000000, 0x3000000
+
+
+def rope(lib, d, x=X, xs=None, y=Y, ys=None, pos=POS, tab=TAB, fn="dsv_rope3d_fwd"):
+    return getattr(lib, fn)(d, x, xs, pos, tab, y, ys, None)
+
+
+@pytest.mark.parametrize("over,status,what", [
+    (dict(B=0), INVALID, b"B, H, N"), (dict(H=0), INVALID, b"B, H, N"), (dict(N=0), INVALID, b"B, H, N"),
+    (dict(N=-1), INVALID, b"B, H, N"), (dict(N=1 << 33), INVALID, b"int32"), (dict(N=1 << 30, H=4), INVALID, b"int32"),
+    (dict(d=96), UNSUPPORTED, b"64 or 128"), (dict(pairing=2), INVALID, b"pairing"),
+    (dict(rot=(3, 0, 0)), INVALID, b"even"), (dict(rot=(-2, 0, 0)), INVALID, b"even"),
+    (dict(rot=(32, 32, 2)), INVALID, b"at most d"), (dict(rot=(66, 0, 0)), INVALID, b"rot"),
+    (dict(len=(0, 4, 4)), INVALID, b"len"), (dict(len=(1 << 32, 4, 4)), INVALID, b"len"),
+    (dict(len=(1 << 30, 4, 4)), INVALID, b"table"),
+    (dict(pairing=1, rot=(4, 4, 4)), UNSUPPORTED, b"multiple of 16"),
+    (dict(eps=-1.0), INVALID, b"eps"), (dict(eps=float("nan")), INVALID, b"eps"), (dict(eps=float("inf")), INVALID, b"eps"),
+])
+def test_bad_dims(lib, over, status, what):
+    d = dims(**over)
+    for fn in ("dsv_rope3d_fwd", "dsv_rope3d_bwd"):
+        assert rope(lib, d, fn=fn) == status
+        assert what in lib.dsv_last_error_message()
+    assert lib.dsv_rope3d_table_bytes(d) == 0
+    assert lib.dsv_qk_norm_rope_bwd_workspace(d) == 0
+    assert lib.dsv_qk_norm_rope_fwd(d, X, X, None, None, None, None, POS, TAB, Y, 2 * Y, None, None) == status
+
+
+def test_null_dims_and_pointers(lib):
+    assert rope(lib, None) == INVALID
+    d = dims()
+    for kw in (dict(x=None), dict(y=None), dict(pos=None), dict(tab=None)):
+        assert rope(lib, d, **kw) == INVALID and b"NULL" in lib.dsv_last_error_message()
+    for kw in (dict(x=X + 8), dict(y=Y + 2), dict(pos=POS + 4), dict(tab=TAB + 8)):
+        assert rope(lib, d, **kw) == INVALID and b"aligned" in lib.dsv_last_error_message()
+
+
+def test_table_sizes_and_theta(lib):
+    d = dims()
+    assert lib.dsv_rope3d_table_bytes(d) == 8 * (12 * 4 + 10 * 16 + 10 * 16)
+    assert lib.dsv_rope3d_table_bytes(dims(rot=(0, 0, 0))) == 0
+    th = (ctypes.c_double * 3)(1e4, 0.0, 1e4)
+    assert lib.dsv_rope3d_table(d, th, TAB, None) == INVALID and b"theta[1]" in lib.dsv_last_error_message()
+    assert lib.dsv_rope3d_table(d, None, TAB, None) == INVALID
+    th[1] = float("inf")
+    assert lib.dsv_rope3d_table(d, th, TAB, None) == INVALID
+    th[1] = 1e4
+    assert lib.dsv_rope3d_table(d, th, None, None) == INVALID
+    # nothing rotated: nothing to fill
+    assert lib.dsv_rope3d_table(dims(rot=(0, 0, 0)), None, None, None) == OK
+
+
+def test_strides(lib):
+    d = dims()
+    for s in ((-8, 64, 192), (4, 2560, 64), (7680, 2560, 60), (1 << 41, 2560, 64)):
+        assert rope(lib, d, xs=ViewStrides(*s)) == INVALID and b"strides" in lib.dsv_last_error_message()
+    # elements of an output that fall on one another
+    for s in ((7680, 2560, 0), (0, 2560, 64), (7680, 64, 64), (7680, 2552, 64), (7672, 2560, 64), (7680, 64, 184)):
+        assert rope(lib, d, ys=ViewStrides(*s)) == INVALID and b"overlap" in lib.dsv_last_error_message()
+
+
+def test_outputs_over_inputs(lib):
+    d = dims()
+    size = 2 * 3 * 40 * 64 * 2
+    # shifted by a row, one past, a different layout in place
+    assert rope(lib, d, y=X + 128) == INVALID and b"overlaps" in lib.dsv_last_error_message()
+    assert rope(lib, d, y=X - size + 16) == INVALID
+    assert rope(lib, d, y=X, ys=ViewStrides(7680, 64, 192)) == INVALID
+    args = lambda qo, ko, vo: (d, X, X + size, X + 2 * size, None, None, None, POS, TAB, qo, ko, vo, None)
+    assert lib.dsv_qk_norm_rope_fwd(*args(X, Y, 2 * Y)) == INVALID
+    assert lib.dsv_qk_norm_rope_fwd(*args(Y, Y, 2 * Y)) == INVALID
+    assert lib.dsv_qk_norm_rope_fwd(*args(Y, Y + size - 16, 2 * Y)) == INVALID
+    assert lib.dsv_qk_norm_rope_fwd(*args(Y, Y + size, X + 3 * size - 16)) == INVALID
+    assert b"v_out overlaps v" in lib.dsv_last_error_message()
+
+
+def bwd(lib, d, **over):
+    size = 2 * 3 * 40 * 64 * 2
+    a = dict(dq_out=X, dk_out=X + size, dv_out=X + 2 * size, q=X + 3 * size, k=X + 4 * size, strides=None, wq=TAB, wk=TAB,
+             pos=POS, tab=TAB, dq=Y, dk=Y + size, dv=Y + 2 * size, ds=None, dwq=0x4000000, dwk=0x4001000, ws=0x5000000,
+             nbytes=1 << 30)
+    a.update(over)
+    return lib.dsv_qk_norm_rope_bwd(d, *a.values(), None)
+
+
+def test_backward_arguments(lib):
+    d = dims()
+    need = lib.dsv_qk_norm_rope_bwd_workspace(d)
+    assert need >= 2 * 64 * 4
+    for kw in (dict(dq_out=None), dict(dk_out=None), dict(q=None), dict(k=None), dict(dq=None), dict(dk=None)):
+        assert bwd(lib, d, **kw) == INVALID and b"NULL" in lib.dsv_last_error_message()
+    for kw in (dict(dv=None), dict(dv_out=None)):
+        assert bwd(lib, d, **kw) == INVALID and b"both" in lib.dsv_last_error_message()
+    for kw in (dict(wq=TAB + 2), dict(wk=TAB + 8), dict(dwq=0x4000004), dict(dwk=0x4000008)):
+        assert bwd(lib, d, **kw) == INVALID and b"aligned" in lib.dsv_last_error_message()
+    assert bwd(lib, d, ws=None) == WORKSPACE
+    assert bwd(lib, d, ws=0x5000010) == WORKSPACE
+    assert bwd(lib, d, nbytes=need - 1) == WORKSPACE
+    assert bwd(lib, d, dk=Y) == INVALID and b"same tensor" in lib.dsv_last_error_message()
+    assert bwd(lib, d, dq=X) == INVALID and b"overlaps" in lib.dsv_last_error_message()
+
+
+def test_python_refusals_without_a_gpu(lib):
+    x = torch.zeros(1, 2, 8, 64, dtype=torch.bfloat16)
+    pos = torch.zeros(8, 3, dtype=torch.int32)
+    table = RopeTable(torch.zeros(64 * 8), (24, 20, 20), (1, 1, 1))
+    with pytest.raises(ValueError, match="CUDA"):
+        pkg.dsv_rope3d_fwd(x, pos, table)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkg.dsv_qk_norm_rope_fwd(x, x, x, None, None, pos, table)
+    with pytest.raises(TypeError):
+        pkg.dsv_rope3d_bwd(None, pos, table)
+    with pytest.raises(ValueError, match="three"):
+        pkg.dsv_rope3d_table((24, 20), (4, 4), device="cpu")
+    with pytest.raises(ValueError, match="pairing"):
+        pkg.dsv_rope3d_table((24, 20, 20), (4, 4, 4), pairing="other", device="cpu")
+    with pytest.raises(ValueError, match="theta"):
+        pkg.dsv_rope3d_table((24, 20, 20), (4, 4, 4), theta=(1.0, 2.0), device="cpu")
+    with pytest.raises(ValueError, match="CUDA"):
+        pkg.dsv_rope3d_table((24, 20, 20), (4, 4, 4), device="cpu")
