@@ -627,8 +627,9 @@ def dsv_qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Ten
         if w is not None:
             _need_on(w, n, torch.bfloat16, shape[3:], device)
     if out is None:
-        qo, ko = torch.empty(shape, dtype=q.dtype, device=q.device), torch.empty(shape, dtype=q.dtype, device=q.device)
-        vo = None if v is None else torch.empty(shape, dtype=q.dtype, device=q.device)
+        # one allocation: the three live and die together
+        outs = torch.empty((2 if v is None else 3, *shape), dtype=q.dtype, device=q.device)
+        qo, ko, vo = (*outs.unbind(0), None)[:3]
     else:
         qo, ko, vo = out
         for t, n in ((qo, "q_out"), (ko, "k_out"), (vo, "v_out")):

@@ -885,15 +885,16 @@ dsv_status dsv_qk_norm_rope_fwd(const dsv_rope_dims* dims, const void* q, const 
   return ok();
 }
 
-static size_t qk_norm_rope_ws(const dsv::RopeGeom& g, int64_t d) {
-  const dsv::RopeGeom plan = dsv::rope_plan(g, static_cast<int>(d));
-  return up(static_cast<size_t>(dsv::rope_bwd_ctas(plan)) * 2 * d * sizeof(float));
+static size_t qk_norm_rope_ws(const dsv::RopeGeom& g, const dsv_rope_dims* d) {
+  const dsv::RopeGeom plan = dsv::rope_plan(g, static_cast<int>(d->d));
+  const int64_t rows = dsv::rope_bwd_ctas(plan);
+  return up(static_cast<size_t>(rows) * 2 * d->d * sizeof(float));
 }
 
 size_t dsv_qk_norm_rope_bwd_workspace(const dsv_rope_dims* dims) {
   dsv::RopeGeom g{};
   if (check_rope(dims, &g) != DSV_OK) return 0;
-  return qk_norm_rope_ws(g, dims->d);
+  return qk_norm_rope_ws(g, dims);
 }
 
 dsv_status dsv_qk_norm_rope_bwd(const dsv_rope_dims* dims, const void* d_q_out, const void* d_k_out,
@@ -934,7 +935,7 @@ dsv_status dsv_qk_norm_rope_bwd(const dsv_rope_dims* dims, const void* d_q_out, 
   if (dwk) DSV_NEED_PTR(dwk);
   if ((s = check_rope_tables(p.g, pos, table)) != DSV_OK) return s;
   if (dwq || dwk) {
-    const size_t need = qk_norm_rope_ws(p.g, dims->d);
+    const size_t need = qk_norm_rope_ws(p.g, dims);
     if (!ws) return fail(DSV_ERR_WORKSPACE, "workspace is NULL");
     if (reinterpret_cast<uintptr_t>(ws) % kAlign)
       return fail(DSV_ERR_WORKSPACE, "workspace must be 256-byte aligned");

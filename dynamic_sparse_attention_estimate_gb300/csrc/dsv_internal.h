@@ -171,7 +171,6 @@ struct RopeParams {
   unsigned int* status;
 };
 constexpr int64_t kRopeWantCtas = 8 * 152;   // CTAs below which the heads of a token are split
-constexpr int64_t kRopeBwdCtas = 4 * 152;    // persistent CTAs of the backward (rows of partial sums)
 RopeGeom rope_plan(const RopeGeom& in, int d);
 int64_t rope_bwd_ctas(const RopeGeom& plan);
 cudaError_t launch_rope3d_table(const RopeGeom& g, const double (&theta)[3], float* table, cudaStream_t stream);

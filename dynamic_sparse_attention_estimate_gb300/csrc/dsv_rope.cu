@@ -16,6 +16,8 @@
 // neighbouring groups.  Queries, keys and values go in one launch: the loads of several
 // rows are issued before the first is used, which is what keeps HBM busy (no staging is needed:
 // nothing is read twice).
+#include <type_traits>
+
 #include "dsv_common.cuh"
 #include "dsv_internal.h"
 
@@ -23,9 +25,7 @@ namespace dsv {
 namespace {
 
 constexpr int kThreads = 128;
-// rows (heads) of each tensor that a group loads ahead
-constexpr int kRopeRows = 2, kNormRows = 2, kBackRows = 2;
-constexpr int kBackCtas = 4;   // of the backward, on an SM
+constexpr int kBackCtas = 4;   // of the backward, on an SM (128 registers; 5 spill and take 389 us where 4 take 354)
 
 DSV_DEVICE uint32_t word(const uint4& u, int j) { return j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w; }
 
@@ -175,11 +175,11 @@ DSV_DEVICE void load_rows(uint4 (&v)[U], const bf16* p, int64_t stride, int64_t 
 DSV_DEVICE void store_row(bf16* p, const uint4& v) { *reinterpret_cast<uint4*>(p) = v; }
 
 // ---------------------------------------------------------------- rotation alone
-template <int D, bool HALF>
+template <int D, bool HALF, int U>
 __global__ void __launch_bounds__(kThreads)
 rope3d_kernel(RopeGeom g, RopeView x, RopeView y, const int32_t* __restrict__ pos, const float2* __restrict__ table,
               float sign, unsigned int* status) {
-  constexpr int LPR = D / 8, U = kRopeRows;
+  constexpr int LPR = D / 8;
   const Lane l = lane_of<LPR>(g, blockIdx.x);
   const bf16* xp = x.p + l.b * x.sb + l.n * x.sn + l.vec * 8;
   bf16* yp = y.p + l.b * y.sb + l.n * y.sn + l.vec * 8;
@@ -234,12 +234,14 @@ DSV_DEVICE uint4 load_weight(const bf16* w, int vec) {
            : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
 }
 
-template <int D, bool HALF>
-__global__ void __launch_bounds__(kThreads)
+// Pairs in halves need 143 registers: held to 128 a fourth CTA fits on the SM (mid clip 285 -> 252 us; the
+// interleaved form has 112, and any bound there costs it: 247 -> 268 us).
+template <int D, bool HALF, int U>
+__global__ void __launch_bounds__(kThreads, HALF ? 4 : 0)
 qk_norm_rope_fwd_kernel(RopeGeom g, RopeView q, RopeView k, RopeView v, RopeView qo, RopeView ko, RopeView vo,
                         const bf16* __restrict__ wq, const bf16* __restrict__ wk, const int32_t* __restrict__ pos,
                         const float2* __restrict__ table, float eps, unsigned int* status) {
-  constexpr int LPR = D / 8, U = kNormRows;
+  constexpr int LPR = D / 8;
   const Lane l = lane_of<LPR>(g, blockIdx.x);
   const bool has_v = v.p != nullptr;
   const bf16* qp = q.p + l.b * q.sb + l.n * q.sn + l.vec * 8;
@@ -318,13 +320,13 @@ DSV_DEVICE uint4 norm_turn_back(const uint4& dy, const uint4& x, const uint4& w,
   return pack(f);
 }
 
-template <int D, bool HALF>
+template <int D, bool HALF, int U>
 __global__ void __launch_bounds__(kThreads, kBackCtas)
 qk_norm_rope_bwd_kernel(RopeGeom g, RopeView dqo, RopeView dko, RopeView dvo, RopeView q, RopeView k, RopeView dq,
                         RopeView dk, RopeView dv, const bf16* __restrict__ wq, const bf16* __restrict__ wk,
                         const int32_t* __restrict__ pos, const float2* __restrict__ table, float eps,
                         float* __restrict__ partial, unsigned int* status) {
-  constexpr int LPR = D / 8, kTok = kThreads / LPR, U = kBackRows;
+  constexpr int LPR = D / 8, kTok = kThreads / LPR;
   // the column sums may be scheduled once every CTA of this grid has started; they wait for its end
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   __shared__ float red[kTok][2 * D];
@@ -461,7 +463,8 @@ RopeGeom rope_plan(const RopeGeom& in, int d) {
   return g;
 }
 
-int64_t rope_bwd_ctas(const RopeGeom& g) { return g.units < kRopeBwdCtas ? g.units : kRopeBwdCtas; }
+// Persistent CTAs of the backward (rows of its partial sums): as many as are resident at once.
+int64_t rope_bwd_ctas(const RopeGeom& g) { return g.units < 152 * kBackCtas ? g.units : 152 * kBackCtas; }
 
 cudaError_t launch_rope3d_table(const RopeGeom& g, const double (&theta)[3], float* table, cudaStream_t stream) {
   int64_t total = 0;
@@ -473,33 +476,42 @@ cudaError_t launch_rope3d_table(const RopeGeom& g, const double (&theta)[3], flo
   return cudaGetLastError();
 }
 
+// A group loads U = 2 heads of each tensor ahead.  Where it has only one or two heads to walk, half
+// of that would be loads of nothing or registers that keep other CTAs out: U = 1.  Measured with
+// U = 2 / U = 1: forward of 1 head 167 / 117 us (524,288 tokens, d = 64), 2 heads 99 / 82 us, 8 heads
+// 71 / 74 us; backward of 1 head 231 / 191 us, 2 heads 136 / 148 us; rope3d alone 66 / 60, 40 / 39, 29 / 33.
+template <class F>
+void pick(const RopeParams& p, bool one, F&& go) {
+  auto rows = [&](auto d, auto half) {
+    one ? go(d, half, std::integral_constant<int, 1>()) : go(d, half, std::integral_constant<int, 2>());
+  };
+  auto dim = [&](auto half) {
+    p.d == 128 ? rows(std::integral_constant<int, 128>(), half) : rows(std::integral_constant<int, 64>(), half);
+  };
+  p.half ? dim(std::true_type()) : dim(std::false_type());
+}
+
 cudaError_t launch_rope3d(const RopeParams& p, cudaStream_t stream) {
   const RopeGeom g = rope_plan(p.g, p.d);
   const float2* table = reinterpret_cast<const float2*>(p.table);
-  const float sign = p.backward ? -1.f : 1.f;
-  const unsigned grid = static_cast<unsigned>(g.units);
   ProfScope prof(p.backward ? "rope3d_bwd" : "rope3d_fwd", stream);
-  if (p.d == 128) {
-    if (p.half) rope3d_kernel<128, true><<<grid, kThreads, 0, stream>>>(g, p.q, p.qo, p.pos, table, sign, p.status);
-    else rope3d_kernel<128, false><<<grid, kThreads, 0, stream>>>(g, p.q, p.qo, p.pos, table, sign, p.status);
-  } else {
-    if (p.half) rope3d_kernel<64, true><<<grid, kThreads, 0, stream>>>(g, p.q, p.qo, p.pos, table, sign, p.status);
-    else rope3d_kernel<64, false><<<grid, kThreads, 0, stream>>>(g, p.q, p.qo, p.pos, table, sign, p.status);
-  }
+  pick(p, g.heads_per_chunk <= 2, [&](auto d, auto half, auto u) {
+    rope3d_kernel<decltype(d)::value, decltype(half)::value, decltype(u)::value>
+        <<<static_cast<unsigned>(g.units), kThreads, 0, stream>>>(g, p.q, p.qo, p.pos, table, p.backward ? -1.f : 1.f,
+                                                                  p.status);
+  });
   return cudaGetLastError();
 }
 
 cudaError_t launch_qk_norm_rope_fwd(const RopeParams& p, cudaStream_t stream) {
   const RopeGeom g = rope_plan(p.g, p.d);
   const float2* table = reinterpret_cast<const float2*>(p.table);
-  const unsigned grid = static_cast<unsigned>(g.units);
   ProfScope prof("qk_norm_rope_fwd", stream);
-  auto go = [&](auto kernel) {
-    kernel<<<grid, kThreads, 0, stream>>>(g, p.q, p.k, p.v, p.qo, p.ko, p.vo, p.wq, p.wk, p.pos, table, p.eps,
-                                          p.status);
-  };
-  if (p.d == 128) p.half ? go(qk_norm_rope_fwd_kernel<128, true>) : go(qk_norm_rope_fwd_kernel<128, false>);
-  else p.half ? go(qk_norm_rope_fwd_kernel<64, true>) : go(qk_norm_rope_fwd_kernel<64, false>);
+  pick(p, g.heads_per_chunk <= 2, [&](auto d, auto half, auto u) {
+    qk_norm_rope_fwd_kernel<decltype(d)::value, decltype(half)::value, decltype(u)::value>
+        <<<static_cast<unsigned>(g.units), kThreads, 0, stream>>>(g, p.q, p.k, p.v, p.qo, p.ko, p.vo, p.wq, p.wk,
+                                                                  p.pos, table, p.eps, p.status);
+  });
   return cudaGetLastError();
 }
 
@@ -507,16 +519,14 @@ cudaError_t launch_qk_norm_rope_bwd(const RopeParams& p, cudaStream_t stream) {
   const RopeGeom g = rope_plan(p.g, p.d);
   const float2* table = reinterpret_cast<const float2*>(p.table);
   const int64_t ctas = rope_bwd_ctas(g);
-  const unsigned grid = static_cast<unsigned>(ctas);
   float* partial = p.dwq || p.dwk ? p.partial : nullptr;
   {
     ProfScope prof("qk_norm_rope_bwd", stream);
-    auto go = [&](auto kernel) {
-      kernel<<<grid, kThreads, 0, stream>>>(g, p.qo, p.ko, p.vo, p.q, p.k, p.dq, p.dk, p.dv, p.wq, p.wk, p.pos, table,
-                                            p.eps, partial, p.status);
-    };
-    if (p.d == 128) p.half ? go(qk_norm_rope_bwd_kernel<128, true>) : go(qk_norm_rope_bwd_kernel<128, false>);
-    else p.half ? go(qk_norm_rope_bwd_kernel<64, true>) : go(qk_norm_rope_bwd_kernel<64, false>);
+    pick(p, g.heads_per_chunk == 1, [&](auto d, auto half, auto u) {
+      qk_norm_rope_bwd_kernel<decltype(d)::value, decltype(half)::value, decltype(u)::value>
+          <<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(g, p.qo, p.ko, p.vo, p.q, p.k, p.dq, p.dk, p.dv, p.wq,
+                                                                 p.wk, p.pos, table, p.eps, partial, p.status);
+    });
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
