@@ -16,6 +16,9 @@ from .binding import (  # noqa: F401
     dsv_estimate_topk,
     dsv_estimate_topk_csr,
     dsv_estimate_topk_workspace,
+    dsv_ffn_gated_bwd,
+    dsv_ffn_gated_bwd_workspace,
+    dsv_ffn_gated_fwd,
     dsv_qk_norm_rope_bwd,
     dsv_qk_norm_rope_bwd_workspace,
     dsv_qk_norm_rope_fwd,

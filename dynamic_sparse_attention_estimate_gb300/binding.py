@@ -33,6 +33,7 @@ EXPORTED = (
     "dsv_sparse_attn_bwd_prepare", "dsv_sparse_attn_bwd_prepared", "dsv_sparse_attn_fwd_workspace",
     "dsv_rope3d_table_bytes", "dsv_rope3d_table", "dsv_rope3d_fwd", "dsv_rope3d_bwd",
     "dsv_qk_norm_rope_fwd", "dsv_qk_norm_rope_bwd_workspace", "dsv_qk_norm_rope_bwd",
+    "dsv_ffn_gated_fwd", "dsv_ffn_gated_bwd_workspace", "dsv_ffn_gated_bwd",
 )
 
 
@@ -56,6 +57,10 @@ class RopeDims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("H", ctypes.c_int64), ("N", ctypes.c_int64), ("d", ctypes.c_int64),
                 ("rot", ctypes.c_int64 * 3), ("len", ctypes.c_int64 * 3), ("pairing", ctypes.c_int32),
                 ("pos_batched", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class FfnDims(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("D", ctypes.c_int64), ("F", ctypes.c_int64), ("act", ctypes.c_int32)]
 
 
 class ViewStrides(ctypes.Structure):
@@ -143,6 +148,13 @@ def load_library(path: Optional[str] = None):
     lib.dsv_qk_norm_rope_bwd_workspace.restype = sz
     lib.dsv_qk_norm_rope_bwd.argtypes = [rp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.dsv_qk_norm_rope_bwd.restype = st
+    fp = ctypes.POINTER(FfnDims)
+    lib.dsv_ffn_gated_fwd.argtypes = [fp, vp, vp, vp, vp, vp]
+    lib.dsv_ffn_gated_fwd.restype = st
+    lib.dsv_ffn_gated_bwd_workspace.argtypes = [fp]
+    lib.dsv_ffn_gated_bwd_workspace.restype = sz
+    lib.dsv_ffn_gated_bwd.argtypes = [fp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.dsv_ffn_gated_bwd.restype = st
     lib.dsv_profile_enable.argtypes = [st]
     lib.dsv_profile_enable.restype = st
     lib.dsv_profile_read.argtypes = [ctypes.c_char_p, sz]
@@ -683,6 +695,80 @@ def dsv_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, dv_out: Opt
           k.data_ptr(), _Strides6(*strides), _ptr(wq), _ptr(wk), pos_ptr, table_ptr, _ptr(dq), _ptr(dk), _ptr(dv),
           _Strides9(*dstrides), _ptr(dwq), _ptr(dwk), _ptr(workspace), nbytes)
     return dq, dk, dv, dwq, dwk
+
+
+# ---------------------------------------------------------------- gated feed-forward
+
+_ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
+
+
+@functools.lru_cache(maxsize=256)
+def _ffn_dims(M: int, D: int, F: int, act: str):
+    """(dims struct, workspace bytes of the backward)."""
+    if act not in _ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(_ACTIVATIONS)}, got {act!r}")
+    dims = FfnDims(M, D, F, _ACTIVATIONS[act])
+    return dims, int(load_library().dsv_ffn_gated_bwd_workspace(ctypes.byref(dims)))
+
+
+def _ffn_args(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: str):
+    """(dims struct, workspace bytes, h's shape) after the checks of the inputs."""
+    for t, n in ((x, "x"), (w_gate, "w_gate")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{n} must be a torch.Tensor")
+    if x.dtype is not torch.bfloat16 or x.dim() < 2 or not x.is_contiguous() or not x.is_cuda:
+        raise ValueError(f"x: need a contiguous CUDA bfloat16 [..., D] tensor with at least 2 dims, got {x.dtype} "
+                         f"{tuple(x.shape)} contiguous={x.is_contiguous()} device={x.device}")
+    if w_gate.dim() != 2:
+        raise ValueError(f"w_gate must be [F, D], got {tuple(w_gate.shape)}")
+    D, F, device = x.shape[-1], w_gate.shape[0], x.get_device()
+    _need_on(w_gate, "w_gate", torch.bfloat16, (F, D), device)
+    _need_on(w_up, "w_up", torch.bfloat16, (F, D), device)
+    dims, ws = _ffn_dims(x.numel() // D if D else 0, D, F, act)
+    return dims, ws, (*x.shape[:-1], F)
+
+
+def dsv_ffn_gated_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: str = "silu",
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """h [..., F] = act(x w_gate^T) * (x w_up^T) for x bf16 [..., D] and weights bf16 [F, D]
+    (act: "silu" or "gelu_tanh"; see include/dsv.h)."""
+    dims, _, shape = _ffn_args(x, w_gate, w_up, act)
+    device = x.get_device()
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    else:
+        _need_on(out, "out", torch.bfloat16, shape, device)
+    _call("dsv_ffn_gated_fwd", device, dims, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr())
+    return out
+
+
+def dsv_ffn_gated_bwd_workspace(M: int, D: int, F: int) -> int:
+    return _ffn_dims(int(M), int(D), int(F), "silu")[1]
+
+
+def dsv_ffn_gated_bwd(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: str = "silu",
+                      out: Optional[Tuple[torch.Tensor, torch.Tensor, torch.Tensor]] = None,
+                      workspace: Optional[torch.Tensor] = None):
+    """(dx [..., D], dw_gate [F, D], dw_up [F, D]), all bf16, for the loss gradient dh [..., F]; g and u are
+    recomputed from x (the forward keeps nothing)."""
+    dims, nbytes, shape = _ffn_args(x, w_gate, w_up, act)
+    device = x.get_device()
+    _need_on(dh, "dh", torch.bfloat16, shape, device)
+    if out is None:
+        dx, dwg, dwu = torch.empty_like(x), torch.empty_like(w_gate), torch.empty_like(w_up)
+    else:
+        dx, dwg, dwu = out
+        for t, n, like in ((dx, "dx", x), (dwg, "dw_gate", w_gate), (dwu, "dw_up", w_up)):
+            _need_on(t, n, torch.bfloat16, like.shape, device)
+    if workspace is None:
+        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=x.device)
+    else:
+        if not workspace.is_contiguous() or workspace.get_device() != device:
+            raise ValueError(f"workspace: need a contiguous tensor on cuda:{device}")
+        nbytes = workspace.numel() * workspace.element_size()
+    _call("dsv_ffn_gated_bwd", device, dims, dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+          dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), workspace.data_ptr(), nbytes)
+    return dx, dwg, dwu
 
 
 def dsv_last_device_status(device: Optional[torch.device] = None) -> int:

@@ -958,6 +958,106 @@ dsv_status dsv_qk_norm_rope_bwd(const dsv_rope_dims* dims, const void* d_q_out, 
   return ok();
 }
 
+// ---------------------------------------------------------------- gated feed-forward
+static dsv_status check_ffn(const dsv_ffn_dims* d) {
+  if (!d) return fail(DSV_ERR_INVALID_ARG, "dims is NULL");
+  if (d->M < 1 || d->M > 0x7fffffffLL - 256) return fail(DSV_ERR_INVALID_ARG, "M must be in [1, 2^31 - 257] (got %lld)", (long long)d->M);
+  if (d->D < 8 || d->D % 8 || d->D > (1 << 20) || d->F < 8 || d->F % 8 || d->F > (1 << 20))
+    return fail(DSV_ERR_INVALID_ARG, "D and F must be multiples of 8 in [8, 2^20] (got %lld, %lld)", (long long)d->D,
+                (long long)d->F);
+  if (d->act != DSV_ACT_SILU && d->act != DSV_ACT_GELU_TANH)
+    return fail(DSV_ERR_INVALID_ARG, "act must be DSV_ACT_SILU or DSV_ACT_GELU_TANH (got %d)", d->act);
+  return DSV_OK;
+}
+
+// Checks a call's tensors: not NULL, aligned, no output over an input or another output.
+struct NamedSpan {
+  const char* name;
+  const void* p;
+  int64_t elements;
+};
+static dsv_status check_spans(const NamedSpan* in, int n_in, const NamedSpan* out, int n_out) {
+  auto span = [](const NamedSpan& t) {
+    const char* lo = static_cast<const char*>(t.p);
+    return ViewSpan{lo, lo + 2 * t.elements};
+  };
+  for (int i = 0; i < n_in + n_out; ++i) {
+    const NamedSpan& t = i < n_in ? in[i] : out[i - n_in];
+    if (!t.p) return fail(DSV_ERR_INVALID_ARG, "%s is NULL", t.name);
+    if (!aligned16(t.p)) return fail(DSV_ERR_INVALID_ARG, "%s is not 16-byte aligned", t.name);
+  }
+  for (int j = 0; j < n_out; ++j)
+    for (int i = 0; i < n_in + j; ++i) {
+      const NamedSpan& t = i < n_in ? in[i] : out[i - n_in];
+      if (!apart(span(t), span(out[j]))) return fail(DSV_ERR_INVALID_ARG, "%s overlaps %s", out[j].name, t.name);
+    }
+  return DSV_OK;
+}
+
+dsv_status dsv_ffn_gated_fwd(const dsv_ffn_dims* dims, const void* x, const void* w_gate, const void* w_up, void* h,
+                             void* stream) {
+  dsv_status s = check_ffn(dims);
+  if (s != DSV_OK) return s;
+  const int64_t M = dims->M, D = dims->D, F = dims->F;
+  const NamedSpan in[3] = {{"x", x, M * D}, {"w_gate", w_gate, F * D}, {"w_up", w_up, F * D}};
+  const NamedSpan out[1] = {{"h", h, M * F}};
+  if ((s = check_spans(in, 3, out, 1)) != DSV_OK) return s;
+  dsv::FfnParams p{};
+  p.M = M;
+  p.D = D;
+  p.F = F;
+  p.act = dims->act;
+  p.x = static_cast<const dsv::bf16*>(x);
+  p.w_gate = static_cast<const dsv::bf16*>(w_gate);
+  p.w_up = static_cast<const dsv::bf16*>(w_up);
+  p.h = static_cast<dsv::bf16*>(h);
+  if ((s = status_word(&p.status)) != DSV_OK) return s;
+  cudaError_t e = dsv::launch_ffn_gated_fwd(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(DSV_ERR_CUDA, "ffn forward launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+static size_t ffn_half_bytes(const dsv_ffn_dims* d) { return up(sizeof(uint16_t) * static_cast<size_t>(d->M) * d->F); }
+
+size_t dsv_ffn_gated_bwd_workspace(const dsv_ffn_dims* dims) {
+  if (check_ffn(dims) != DSV_OK) return 0;
+  return 2 * ffn_half_bytes(dims);
+}
+
+dsv_status dsv_ffn_gated_bwd(const dsv_ffn_dims* dims, const void* dh, const void* x, const void* w_gate,
+                             const void* w_up, void* dx, void* dw_gate, void* dw_up, void* ws, size_t ws_bytes,
+                             void* stream) {
+  dsv_status s = check_ffn(dims);
+  if (s != DSV_OK) return s;
+  const int64_t M = dims->M, D = dims->D, F = dims->F;
+  const size_t need = 2 * ffn_half_bytes(dims);
+  const NamedSpan in[4] = {{"dh", dh, M * F}, {"x", x, M * D}, {"w_gate", w_gate, F * D}, {"w_up", w_up, F * D}};
+  const NamedSpan out[4] = {{"dx", dx, M * D}, {"dw_gate", dw_gate, F * D}, {"dw_up", dw_up, F * D},
+                            {"ws", ws, static_cast<int64_t>(need / 2)}};
+  if (!ws) return fail(DSV_ERR_WORKSPACE, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(ws) % kAlign) return fail(DSV_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (ws_bytes < need) return fail(DSV_ERR_WORKSPACE, "workspace of %zu bytes is below the %zu needed", ws_bytes, need);
+  if ((s = check_spans(in, 4, out, 4)) != DSV_OK) return s;
+  dsv::FfnParams p{};
+  p.M = M;
+  p.D = D;
+  p.F = F;
+  p.act = dims->act;
+  p.x = static_cast<const dsv::bf16*>(x);
+  p.w_gate = static_cast<const dsv::bf16*>(w_gate);
+  p.w_up = static_cast<const dsv::bf16*>(w_up);
+  p.dh = static_cast<const dsv::bf16*>(dh);
+  p.dg = static_cast<dsv::bf16*>(ws);
+  p.du = reinterpret_cast<dsv::bf16*>(static_cast<char*>(ws) + ffn_half_bytes(dims));
+  p.dx = static_cast<dsv::bf16*>(dx);
+  p.dw_gate = static_cast<dsv::bf16*>(dw_gate);
+  p.dw_up = static_cast<dsv::bf16*>(dw_up);
+  if ((s = status_word(&p.status)) != DSV_OK) return s;
+  cudaError_t e = dsv::launch_ffn_gated_bwd(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(DSV_ERR_CUDA, "ffn backward launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
 // ---------------------------------------------------------------- backward with library-held scratch
 // For callers that cannot allocate device memory (see include/dsv.h).  The scratch is a
 // fixed device array; host code only ever uses the address looked up per device below.

@@ -1,0 +1,493 @@
+// Gated feed-forward of a DiT block: h = act(x Wg^T) * (x Wu^T), forward and backward, on the tcgen05
+// tensor cores.
+//
+// One persistent GEMM kernel in four modes, all bf16 operands with fp32 accumulators in tensor memory:
+//   kGate      g, u = x Wg^T, x Wu^T;  h = act(g) u                      (K = D, both K-major)
+//   kGateGrad  the same products again; dg = dh u act'(g), du = dh act(g)   (nothing is kept of the forward)
+//   kDx        dx = dg Wg + du Wu                                         (K = F twice; W is MN-major)
+//   kDw        dWg = dg^T x, dWu = du^T x                                  (K = M; both MN-major)
+// An accumulator tile is 128 CG rows by 256 columns; in the gated modes its columns are 128 of g and the
+// 128 of u they meet in the epilogue, so g and u never leave the SM in kGate.  dg and du are rounded
+// to bf16 between the backward's kernels: the tensor cores take them as operands of that type (2^-8 of
+// each value, as every activation between layers).
+//
+// Roles (384 threads): thread 0 of warp 0 issues the TMA loads into a ring of stages; thread 0 of warp
+// 1 issues the MMAs, into one of two accumulators (2 x 256 of the 512 TMEM columns); warps 4-11 empty the
+// other one: two warpgroups, each on half of the columns, through 128-byte-swizzled staging tiles that
+// TMA stores write (rows and columns past the matrices are clipped there, and zero-filled by the
+// loads).  Every wait is bounded.
+#include <cuda.h>
+
+#include "dsv_common.cuh"
+#include "dsv_internal.h"
+#include "dsv_tc.cuh"
+
+namespace dsv {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kBK = 64;                    // K elements of a stage (128 bytes)
+constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr int kTile = 128 * 128;           // bytes of a [128 rows][64] or two [64 rows][64] bf16 tiles
+
+enum Mode { kGate = 0, kGateGrad = 1, kDx = 2, kDw = 3 };
+
+struct Maps {
+  CUtensorMap a0, a1, b0, b1, c0, c1, d;   // operands A and B, results C, dh
+};
+
+struct Shape {
+  int64_t m_tiles, n_tiles, tiles;
+  int kb_half;      // k blocks of one operand pair (kDx has two pairs)
+  int kb;           // k blocks of a tile
+  int64_t rows, cols;   // of the result (kDw: of one of the two results)
+  int64_t half_tiles;   // kDw: m tiles of the first result
+  int group;        // m tiles that share their n tiles' operands in L2
+  int act;
+};
+
+template <int MODE, int CG>
+struct Cfg {
+  static constexpr int kStageA = kTile;
+  static constexpr int kStageB = 2 * kTile / CG;
+  static constexpr int kStage = kStageA + kStageB;
+  static constexpr int kOut = (MODE == kGateGrad ? 2 : 1) * 2 * kTile;   // staging of two warpgroups
+  static constexpr int kStages = (227 * 1024 - 2048 - kOut) / kStage;
+  static constexpr int kSmem = kStages * kStage + kOut + 1024;
+};
+
+struct Bars {
+  uint64_t full[8], empty[8];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t dh_full[2];
+  uint64_t drain;
+  uint32_t tmem;
+  int fail;
+};
+
+DSV_DEVICE bool wait_bar(uint32_t bar, uint32_t parity, volatile int* fail) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if ((i & 255) == 255 && *fail) return false;
+  }
+  return false;
+}
+
+DSV_DEVICE uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+DSV_DEVICE void expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+DSV_DEVICE void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::
+          "r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+DSV_DEVICE void tma_store(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(map), "r"(x),
+               "r"(y), "r"(src)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+}
+DSV_DEVICE void store_read_done() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+DSV_DEVICE void store_done() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
+DSV_DEVICE void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
+// A barrier whose threads agree: true where all of them came with true.
+DSV_DEVICE bool bar_all(int id, int n, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %3, 0;\n bar.red.and.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return r != 0;
+}
+
+// Activation and its derivative.  Both activations are g times a logistic function:
+//   silu: s(g);  gelu (tanh form): s(2 c (g + 0.044715 g^3)), c = sqrt(2 / pi).
+DSV_DEVICE float logistic(float z) { return __fdividef(1.f, 1.f + fast_exp2(-kLog2e * z)); }
+constexpr float kGelu2C = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+DSV_DEVICE float act_value(float g, int act) {
+  const float z = act == 0 ? g : kGelu2C * fmaf(0.044715f * g * g, g, g);
+  return g * logistic(z);
+}
+DSV_DEVICE void act_both(float g, int act, float& a, float& slope) {
+  const float z = act == 0 ? g : kGelu2C * fmaf(0.044715f * g * g, g, g);
+  const float dz = act == 0 ? 1.f : kGelu2C * fmaf(3.f * 0.044715f * g, g, 1.f);
+  const float s = logistic(z);
+  a = g * s;
+  slope = fmaf(a * (1.f - s), dz, s);
+}
+
+DSV_DEVICE void tile_of(const Shape& sh, int64_t t, int64_t& m, int64_t& n) {
+  const int64_t per = static_cast<int64_t>(sh.group) * sh.n_tiles;
+  const int64_t g = t / per, r = t % per;
+  const int64_t left = sh.m_tiles - g * sh.group;
+  const int64_t gm = left < sh.group ? left : sh.group;
+  m = g * sh.group + r % gm;
+  n = r / gm;
+}
+
+template <int MODE, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* status) {
+  using C = Cfg<MODE, CG>;
+  constexpr bool kGated = MODE == kGate || MODE == kGateGrad;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) Bars bars;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t ring = (raw + 1023u) & ~1023u;          // swizzled tiles need 1024-byte alignment
+  const uint32_t out = ring + C::kStages * C::kStage;
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      tc::mbar_init(bar(bars.full[s]), 1);
+      tc::mbar_init(bar(bars.empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(bar(bars.acc_full[b]), 1);
+      tc::mbar_init(bar(bars.acc_empty[b]), 8);
+      tc::mbar_init(bar(bars.dh_full[b]), 1);
+    }
+    tc::mbar_init(bar(bars.drain), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    bars.fail = 0;
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(smem_u32(&bars.tmem), 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = bars.tmem;
+  volatile int* fail = &bars.fail;
+
+  if (warp == 0) {
+    // ================================================================ TMA loads (one thread)
+    if (lane == 0) {
+      int64_t it = 0;   // k blocks issued
+      bool ok = true;
+      for (int64_t t = blockIdx.x; t < sh.tiles && ok; t += gridDim.x) {
+        int64_t m, n;
+        tile_of(sh, t, m, n);
+        const CUtensorMap* a_map = MODE == kDw && m >= sh.half_tiles ? &maps.a1 : &maps.a0;
+        if (MODE == kDw && m >= sh.half_tiles) m -= sh.half_tiles;
+        const int m0 = static_cast<int>(m * 128);
+        const int n0 = static_cast<int>(n * (kGated ? 128 : 256));
+        for (int kb = 0; kb < sh.kb; ++kb, ++it) {
+          const int s = static_cast<int>(it % C::kStages);
+          if (it >= C::kStages && !wait_bar(bar(bars.empty[s]), static_cast<uint32_t>((it / C::kStages - 1) & 1), fail)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full = bar(bars.full[s]);
+          const uint32_t a = ring + s * C::kStage, b = a + C::kStageA;
+          expect_tx(full, C::kStage);
+          if constexpr (kGated) {
+            tma_load(a, &maps.a0, kb * kBK, m0, full);
+            tma_load(b, &maps.b0, kb * kBK, n0, full);
+            tma_load(b + kTile, &maps.b1, kb * kBK, n0, full);
+          } else if constexpr (MODE == kDx) {
+            const bool second = kb >= sh.kb_half;
+            const int k0 = (second ? kb - sh.kb_half : kb) * kBK;
+            tma_load(a, second ? &maps.a1 : &maps.a0, k0, m0, full);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tma_load(b + i * (kTile / 2), second ? &maps.b1 : &maps.b0, n0 + 64 * i, k0, full);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tma_load(a + i * (kTile / 2), a_map, m0 + 64 * i, kb * kBK, full);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tma_load(b + i * (kTile / 2), &maps.b0, n0 + 64 * i, kb * kBK, full);
+          }
+        }
+      }
+      if (!ok) {
+        *fail = 1;
+        // the copies in flight land before this CTA's shared memory can go away (again bounded)
+        for (int64_t c = it > C::kStages ? it - C::kStages : 0; c < it; ++c)
+          tc::mbar_wait(bar(bars.full[c % C::kStages]), static_cast<uint32_t>((c / C::kStages) & 1), kWaitLimit);
+      }
+    }
+  } else if (warp == 1) {
+    // ================================================================ MMA issue (one thread)
+    if (lane == 0) {
+      constexpr uint32_t id = tc::idesc_bf16(128 * CG, 256, MODE == kDw, !kGated);
+      int64_t it = 0;
+      int64_t tile = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; t < sh.tiles && ok; t += gridDim.x, ++tile) {
+        const int buf = static_cast<int>(tile & 1);
+        if (tile >= 2) ok = wait_bar(bar(bars.acc_empty[buf]), static_cast<uint32_t>(((tile >> 1) - 1) & 1), fail);
+        tc::tc_fence_after();
+        for (int kb = 0; kb < sh.kb && ok; ++kb, ++it) {
+          const int s = static_cast<int>(it % C::kStages);
+          ok = wait_bar(bar(bars.full[s]), static_cast<uint32_t>((it / C::kStages) & 1), fail);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint32_t a = ring + s * C::kStage, b = a + C::kStageA;
+#pragma unroll
+          for (int j = 0; j < kBK / 16; ++j) {
+            // K-major: 16 elements on are 32 bytes on; MN-major: two 8-row groups on (1024 bytes each),
+            // 64-element column blocks 8 KB apart
+            const uint64_t da = MODE == kDw ? tc::smem_desc(a + j * 2048, kTile / 2, 1024) : tc::smem_desc(a + j * 32, 16, 1024);
+            const uint64_t db = kGated ? tc::smem_desc(b + j * 32, 16, 1024) : tc::smem_desc(b + j * 2048, kTile / 2, 1024);
+            tc::mma_ss(tmem + buf * 256, da, db, id, kb > 0 || j > 0 ? 1u : 0u);
+          }
+          tc::mma_commit(bar(bars.empty[s]));
+        }
+        if (ok) tc::mma_commit(bar(bars.acc_full[buf]));
+      }
+      if (!ok) {   // what was issued ends before the accumulators are given back (again bounded)
+        *fail = 1;
+        tc::mma_commit(bar(bars.drain));
+        tc::mbar_wait(bar(bars.drain), 0, kWaitLimit);
+      }
+    }
+  } else if (warp >= 4) {
+    // ================================================================ epilogue
+    const int wg = (warp - 4) >> 2;                       // columns [64 wg, ..) of g and u, or [128 wg, ..)
+    const int row = (warp & 3) * 32 + lane;               // of the tile (TMEM lane)
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const bool elect = (tid & 127) == 0;
+    const uint32_t st0 = out + wg * (C::kOut / 2), st1 = st0 + kTile;
+    auto put = [&](uint32_t tile, int c, const uint32_t (&w)[8]) {   // 16 columns from c of this row
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(tile + tc::sw128(row, c)), "r"(w[0]), "r"(w[1]),
+                   "r"(w[2]), "r"(w[3]));
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(tile + tc::sw128(row, c + 8)), "r"(w[4]), "r"(w[5]),
+                   "r"(w[6]), "r"(w[7]));
+    };
+    int64_t tile = 0;
+    uint32_t loads = 0;                                   // of dh, this warpgroup's
+    bool ok = true;
+    for (int64_t t = blockIdx.x; t < sh.tiles && ok; t += gridDim.x, ++tile) {
+      int64_t m, n;
+      tile_of(sh, t, m, n);
+      const CUtensorMap* c_map = MODE == kDw && m >= sh.half_tiles ? &maps.c1 : &maps.c0;
+      if (MODE == kDw && m >= sh.half_tiles) m -= sh.half_tiles;
+      const int m0 = static_cast<int>(m * 128);
+      const int n0 = static_cast<int>(n * (kGated ? 128 : 256) + wg * (kGated ? 64 : 128));
+      const int buf = static_cast<int>(tile & 1);
+      const bool mine = n0 < sh.cols && m0 < sh.rows;     // some of this part is inside the result
+      if (elect) {
+        store_read_done();                                // the staging tiles are free again
+        if (MODE == kGateGrad && mine) {
+          expect_tx(bar(bars.dh_full[wg]), kTile);
+          tma_load(st0, &maps.d, n0, m0, bar(bars.dh_full[wg]));
+        }
+      }
+      ok = wait_bar(bar(bars.acc_full[buf]), static_cast<uint32_t>((tile >> 1) & 1), fail);
+      if (MODE == kGateGrad && mine) {
+        ok = wait_bar(bar(bars.dh_full[wg]), static_cast<uint32_t>(loads & 1), fail) && ok;
+        ++loads;
+      }
+      ok = bar_all(1 + wg, 128, ok);                      // the warpgroup goes on together, or not at all
+      if (!ok) break;
+      tc::tc_fence_after();
+      const uint32_t acc = tmem + lane_base + buf * 256;
+      if constexpr (kGated) {
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 16) {
+          uint32_t g[16], u[16], w0[8], w1[8];
+          tc::tmem_ld16(acc + wg * 64 + c, g);
+          tc::tmem_ld16(acc + 128 + wg * 64 + c, u);
+          tc::tmem_wait_ld();
+          if constexpr (MODE == kGate) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              w0[i] = pack_bf16x2(act_value(__uint_as_float(g[2 * i]), sh.act) * __uint_as_float(u[2 * i]),
+                                  act_value(__uint_as_float(g[2 * i + 1]), sh.act) * __uint_as_float(u[2 * i + 1]));
+            put(st0, c, w0);
+          } else {
+            uint32_t dh[8];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                           : "=r"(dh[4 * q]), "=r"(dh[4 * q + 1]), "=r"(dh[4 * q + 2]), "=r"(dh[4 * q + 3])
+                           : "r"(st0 + tc::sw128(row, c + 8 * q)));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float dg[2], du[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float a, slope;
+                act_both(__uint_as_float(g[2 * i + e]), sh.act, a, slope);
+                const float d = e ? bf16_hi(dh[i]) : bf16_lo(dh[i]);
+                dg[e] = d * __uint_as_float(u[2 * i + e]) * slope;
+                du[e] = d * a;
+              }
+              w0[i] = pack_bf16x2(dg[0], dg[1]);
+              w1[i] = pack_bf16x2(du[0], du[1]);
+            }
+            put(st0, c, w0);
+            put(st1, c, w1);
+          }
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(bars.acc_empty[buf]));
+        tc::fence_async_shared();
+        bar_sync(1 + wg, 128);
+        if (elect && mine) {
+          tma_store(c_map, n0, m0, st0);
+          if (MODE == kGateGrad) tma_store(&maps.c1, n0, m0, st1);
+        }
+      } else {
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (half == 1) {
+            if (elect) store_read_done();
+            bar_sync(1 + wg, 128);
+          }
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t a[16], b[16], w[8];
+            tc::tmem_ld16(acc + wg * 128 + half * 64 + c, a);
+            tc::tmem_ld16(acc + wg * 128 + half * 64 + c + 16, b);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+            put(st0, c, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
+            put(st0, c + 16, w);
+          }
+          if (half == 1) {
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar(bars.acc_empty[buf]));
+          }
+          tc::fence_async_shared();
+          bar_sync(1 + wg, 128);
+          if (elect && m0 < sh.rows && n0 + half * 64 < sh.cols) tma_store(c_map, n0 + half * 64, m0, st0);
+        }
+      }
+    }
+    if (!ok) {
+      *fail = 1;
+      if (MODE == kGateGrad && elect && loads > 0)        // a load of dh in flight lands first
+        tc::mbar_wait(bar(bars.dh_full[wg]), (loads - 1) & 1, kWaitLimit);
+    }
+    if (elect) store_done();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && bars.fail) flag_status(status, kStatusTimeout);
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- host
+// A [rows][cols] row-major bf16 matrix seen through boxes of box_rows x 64 columns (128 bytes, swizzled).
+bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t pitch, int box_rows) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<Encode>(f);
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t step[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <int MODE, int CG>
+cudaError_t launch_gemm(const char* name, const Maps& maps, Shape sh, unsigned int* status, cudaStream_t stream) {
+  using C = Cfg<MODE, CG>;
+  sh.tiles = sh.m_tiles * sh.n_tiles;
+  sh.group = 16;
+  auto kernel = ffn_gemm_kernel<MODE, CG>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = sh.tiles < 152 ? sh.tiles : 152;
+  ProfScope prof(name, stream);
+  kernel<<<static_cast<unsigned>(grid), kThreads, C::kSmem, stream>>>(maps, sh, status);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_ffn_gated_fwd(const FfnParams& p, cudaStream_t stream) {
+  Maps maps{};
+  if (!make_map(&maps.a0, p.x, p.M, p.D, p.D, 128) || !make_map(&maps.b0, p.w_gate, p.F, p.D, p.D, 128) ||
+      !make_map(&maps.b1, p.w_up, p.F, p.D, p.D, 128) || !make_map(&maps.c0, p.h, p.M, p.F, p.F, 128))
+    return cudaErrorInvalidValue;
+  Shape sh{};
+  sh.m_tiles = ceil_div(p.M, 128);
+  sh.n_tiles = ceil_div(p.F, 128);
+  sh.kb = static_cast<int>(ceil_div(p.D, kBK));
+  sh.rows = p.M;
+  sh.cols = p.F;
+  sh.act = p.act;
+  return launch_gemm<kGate, 1>("ffn_gate", maps, sh, p.status, stream);
+}
+
+cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream) {
+  cudaError_t e;
+  {
+    Maps maps{};
+    if (!make_map(&maps.a0, p.x, p.M, p.D, p.D, 128) || !make_map(&maps.b0, p.w_gate, p.F, p.D, p.D, 128) ||
+        !make_map(&maps.b1, p.w_up, p.F, p.D, p.D, 128) || !make_map(&maps.d, p.dh, p.M, p.F, p.F, 128) ||
+        !make_map(&maps.c0, p.dg, p.M, p.F, p.F, 128) || !make_map(&maps.c1, p.du, p.M, p.F, p.F, 128))
+      return cudaErrorInvalidValue;
+    Shape sh{};
+    sh.m_tiles = ceil_div(p.M, 128);
+    sh.n_tiles = ceil_div(p.F, 128);
+    sh.kb = static_cast<int>(ceil_div(p.D, kBK));
+    sh.rows = p.M;
+    sh.cols = p.F;
+    sh.act = p.act;
+    if ((e = launch_gemm<kGateGrad, 1>("ffn_gate_grad", maps, sh, p.status, stream)) != cudaSuccess) return e;
+  }
+  {
+    Maps maps{};
+    if (!make_map(&maps.a0, p.dg, p.M, p.F, p.F, 128) || !make_map(&maps.a1, p.du, p.M, p.F, p.F, 128) ||
+        !make_map(&maps.b0, p.w_gate, p.F, p.D, p.D, 64) || !make_map(&maps.b1, p.w_up, p.F, p.D, p.D, 64) ||
+        !make_map(&maps.c0, p.dx, p.M, p.D, p.D, 128))
+      return cudaErrorInvalidValue;
+    Shape sh{};
+    sh.m_tiles = ceil_div(p.M, 128);
+    sh.n_tiles = ceil_div(p.D, 256);
+    sh.kb_half = static_cast<int>(ceil_div(p.F, kBK));
+    sh.kb = 2 * sh.kb_half;
+    sh.rows = p.M;
+    sh.cols = p.D;
+    if ((e = launch_gemm<kDx, 1>("ffn_dx", maps, sh, p.status, stream)) != cudaSuccess) return e;
+  }
+  Maps maps{};
+  if (!make_map(&maps.a0, p.dg, p.M, p.F, p.F, 64) || !make_map(&maps.a1, p.du, p.M, p.F, p.F, 64) ||
+      !make_map(&maps.b0, p.x, p.M, p.D, p.D, 64) || !make_map(&maps.c0, p.dw_gate, p.F, p.D, p.D, 128) ||
+      !make_map(&maps.c1, p.dw_up, p.F, p.D, p.D, 128))
+    return cudaErrorInvalidValue;
+  Shape sh{};
+  sh.half_tiles = ceil_div(p.F, 128);
+  sh.m_tiles = 2 * sh.half_tiles;
+  sh.n_tiles = ceil_div(p.D, 256);
+  sh.kb = static_cast<int>(ceil_div(p.M, kBK));
+  sh.rows = p.F;
+  sh.cols = p.D;
+  return launch_gemm<kDw, 1>("ffn_dw", maps, sh, p.status, stream);
+}
+
+}  // namespace dsv

@@ -178,4 +178,18 @@ cudaError_t launch_rope3d(const RopeParams& p, cudaStream_t stream);
 cudaError_t launch_qk_norm_rope_fwd(const RopeParams& p, cudaStream_t stream);
 cudaError_t launch_qk_norm_rope_bwd(const RopeParams& p, cudaStream_t stream);
 
+// ---------------------------------------------------------------- gated feed-forward (dsv_ffn.cu)
+struct FfnParams {
+  int64_t M, D, F;
+  int act;                              // 0 silu, 1 gelu (tanh form)
+  const bf16 *x, *w_gate, *w_up;        // [M][D], [F][D], [F][D]
+  bf16* h;                              // [M][F] (forward)
+  const bf16* dh;                       // [M][F] (backward)
+  bf16 *dg, *du;                        // [M][F] each: the backward's workspace
+  bf16 *dx, *dw_gate, *dw_up;           // [M][D], [F][D], [F][D] (backward)
+  unsigned int* status;
+};
+cudaError_t launch_ffn_gated_fwd(const FfnParams& p, cudaStream_t stream);
+cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream);
+
 }  // namespace dsv

@@ -404,6 +404,40 @@ dsv_status dsv_qk_norm_rope_bwd(const dsv_rope_dims* dims, const void* d_q_out, 
                                 void* dk, void* dv, const dsv_view_strides d_strides[3], float* dwq, float* dwk,
                                 void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- gated feed-forward
+ * The feed-forward of a DiT block up to its down projection: both projections, the activation and
+ * the product in one kernel, and its backward.
+ *   g = x Wg^T,  u = x Wu^T,  h = act(g) * u
+ *   act: DSV_ACT_SILU      g / (1 + exp(-g))
+ *        DSV_ACT_GELU_TANH g / 2 (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))
+ * The backward recomputes g and u from x (the forward keeps nothing) and returns
+ *   dg = dh u act'(g), du = dh act(g);  dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x.
+ * Layouts (contiguous, 16-byte aligned device memory): x, dx bf16 [M][D]; w_gate, w_up, dw_gate,
+ * dw_up bf16 [F][D]; h, dh bf16 [M][F].  M is the token count (samples and tokens flattened).
+ * Products accumulate in fp32; h and the gradients are rounded to bf16 once, and dg, du once
+ * between the backward's kernels.  Bitwise reproducible.  Outputs must not overlap inputs.
+ * Validation before any launch: M, D, F >= 1; D and F multiples of 8; M < 2^31 - 256, D and F <=
+ * 2^20; act as above; no NULL, misaligned or overlapping pointer.
+ */
+typedef enum { DSV_ACT_SILU = 0, DSV_ACT_GELU_TANH = 1 } dsv_activation;
+
+typedef struct {
+  int64_t M;     /* tokens */
+  int64_t D;     /* features of x */
+  int64_t F;     /* features of h */
+  int32_t act;   /* dsv_activation */
+} dsv_ffn_dims;
+
+dsv_status dsv_ffn_gated_fwd(const dsv_ffn_dims* dims, const void* x, const void* w_gate, const void* w_up, void* h,
+                             void* stream);
+/* Bytes of workspace dsv_ffn_gated_bwd needs (dg and du). */
+size_t dsv_ffn_gated_bwd_workspace(const dsv_ffn_dims* dims);
+/* ws: at least dsv_ffn_gated_bwd_workspace(dims) bytes, 256-byte aligned; one workspace must not
+ * serve two calls that can run at the same time. */
+dsv_status dsv_ffn_gated_bwd(const dsv_ffn_dims* dims, const void* dh, const void* x, const void* w_gate,
+                             const void* w_up, void* dx, void* dw_gate, void* dw_up, void* ws, size_t ws_bytes,
+                             void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,7 +22,8 @@ Pins (what ties each function to something other than itself) live in ``tests/``
                      planted mistakes rejected;
   rotary, qk norm  : complex multiplication in torch fp64 and autograd through it, central
                      finite differences, closed forms (norms kept, relative positions,
-                     position 0 is the identity).
+                     position 0 is the identity);
+  gated feed-forward : torch fp64 activations and autograd, central finite differences.
 """
 from .dsv_oracle import (  # noqa: F401
     block_representatives,
@@ -48,3 +49,4 @@ from .rope_oracle import (  # noqa: F401,E402
     rope,
     rope_angles,
 )
+from .ffn_oracle import activation, ffn_gated_bwd, ffn_gated_fwd  # noqa: F401,E402
