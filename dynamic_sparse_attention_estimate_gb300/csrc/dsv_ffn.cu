@@ -88,6 +88,14 @@ DSV_DEVICE void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uin
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+// The same into this CTA's shared memory, counted on a barrier of either CTA of the pair.
+DSV_DEVICE void tma_load_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+      "[%4];\n" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(cluster_bar)
+      : "memory");
+}
 DSV_DEVICE void tma_store(const CUtensorMap* map, int x, int y, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(map), "r"(x),
                "r"(y), "r"(src)
@@ -106,6 +114,39 @@ DSV_DEVICE bool bar_all(int id, int n, bool ok) {
       : "r"(id), "r"(n), "r"(static_cast<uint32_t>(ok))
       : "memory");
   return r != 0;
+}
+
+// ---------------------------------------------------------------- pairs of CTAs (cta_group::2)
+DSV_DEVICE uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return r;
+}
+DSV_DEVICE void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;\n" ::: "memory");
+}
+DSV_DEVICE void arrive_cluster(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_bar) : "memory");
+}
+DSV_DEVICE void tmem_alloc_pair(uint32_t dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(dst), "r"(cols));
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::);
+}
+DSV_DEVICE void tmem_dealloc_pair(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(addr), "r"(cols));
+}
+DSV_DEVICE void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// Arrive on this barrier of both CTAs once every MMA issued so far has completed.
+DSV_DEVICE void commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
 }
 
 // Activation and its derivative.  Both activations are g times a logistic function:
@@ -141,6 +182,8 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) Bars bars;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
+  const int64_t first = blockIdx.x / CG, step = gridDim.x / CG;   // tiles first, first + step, ..
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;          // swizzled tiles need 1024-byte alignment
   const uint32_t out = ring + C::kStages * C::kStage;
@@ -153,7 +196,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(bar(bars.acc_full[b]), 1);
-      tc::mbar_init(bar(bars.acc_empty[b]), 8);
+      tc::mbar_init(bar(bars.acc_empty[b]), 8 * CG);
       tc::mbar_init(bar(bars.dh_full[b]), 1);
     }
     tc::mbar_init(bar(bars.drain), 1);
@@ -161,11 +204,16 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
     bars.fail = 0;
   }
   if (warp == 1) {
-    tc::tmem_alloc(smem_u32(&bars.tmem), 512);
-    tc::tmem_relinquish();
+    if constexpr (CG == 2) {
+      tmem_alloc_pair(smem_u32(&bars.tmem), 512);
+    } else {
+      tc::tmem_alloc(smem_u32(&bars.tmem), 512);
+      tc::tmem_relinquish();
+    }
   }
   tc::tc_fence_before();
   __syncthreads();
+  if constexpr (CG == 2) cluster_sync();   // the other CTA's barriers exist
   tc::tc_fence_after();
   const uint32_t tmem = bars.tmem;
   volatile int* fail = &bars.fail;
@@ -175,55 +223,65 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
     if (lane == 0) {
       int64_t it = 0;   // k blocks issued
       bool ok = true;
-      for (int64_t t = blockIdx.x; t < sh.tiles && ok; t += gridDim.x) {
+      for (int64_t t = first; t < sh.tiles && ok; t += step) {
         int64_t m, n;
         tile_of(sh, t, m, n);
         const CUtensorMap* a_map = MODE == kDw && m >= sh.half_tiles ? &maps.a1 : &maps.a0;
         if (MODE == kDw && m >= sh.half_tiles) m -= sh.half_tiles;
-        const int m0 = static_cast<int>(m * 128);
-        const int n0 = static_cast<int>(n * (kGated ? 128 : 256));
+        const int m0 = static_cast<int>(m * (128 * CG)) + rank * 128;
+        // B: the pair's second CTA holds the tile's second 128 columns (in the gated modes those of u)
+        const int n0 = static_cast<int>(n * (kGated ? 128 : 256)) + (kGated ? 0 : rank * 128);
         for (int kb = 0; kb < sh.kb; ++kb, ++it) {
           const int s = static_cast<int>(it % C::kStages);
           if (it >= C::kStages && !wait_bar(bar(bars.empty[s]), static_cast<uint32_t>((it / C::kStages - 1) & 1), fail)) {
             ok = false;
             break;
           }
-          const uint32_t full = bar(bars.full[s]);
+          // both CTAs' copies count on the first one's barrier, where the MMAs are issued
+          if (rank == 0) expect_tx(bar(bars.full[s]), CG * C::kStage);
+          const uint32_t full = CG == 2 ? map_rank(bar(bars.full[s]), 0) : bar(bars.full[s]);
           const uint32_t a = ring + s * C::kStage, b = a + C::kStageA;
-          expect_tx(full, C::kStage);
+          auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
+            if constexpr (CG == 2) tma_load_pair(dst, map, x, y, full);
+            else tma_load(dst, map, x, y, full);
+          };
           if constexpr (kGated) {
-            tma_load(a, &maps.a0, kb * kBK, m0, full);
-            tma_load(b, &maps.b0, kb * kBK, n0, full);
-            tma_load(b + kTile, &maps.b1, kb * kBK, n0, full);
+            load(a, &maps.a0, kb * kBK, m0);
+            load(b, rank == 0 ? &maps.b0 : &maps.b1, kb * kBK, n0);
+            if (CG == 1) load(b + kTile, &maps.b1, kb * kBK, n0);
           } else if constexpr (MODE == kDx) {
             const bool second = kb >= sh.kb_half;
             const int k0 = (second ? kb - sh.kb_half : kb) * kBK;
-            tma_load(a, second ? &maps.a1 : &maps.a0, k0, m0, full);
+            load(a, second ? &maps.a1 : &maps.a0, k0, m0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tma_load(b + i * (kTile / 2), second ? &maps.b1 : &maps.b0, n0 + 64 * i, k0, full);
+            for (int i = 0; i < 4 / CG; ++i) load(b + i * (kTile / 2), second ? &maps.b1 : &maps.b0, n0 + 64 * i, k0);
           } else {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) tma_load(a + i * (kTile / 2), a_map, m0 + 64 * i, kb * kBK, full);
+            for (int i = 0; i < 2; ++i) load(a + i * (kTile / 2), a_map, m0 + 64 * i, kb * kBK);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tma_load(b + i * (kTile / 2), &maps.b0, n0 + 64 * i, kb * kBK, full);
+            for (int i = 0; i < 4 / CG; ++i) load(b + i * (kTile / 2), &maps.b0, n0 + 64 * i, kb * kBK);
           }
         }
       }
       if (!ok) {
         *fail = 1;
         // the copies in flight land before this CTA's shared memory can go away (again bounded)
-        for (int64_t c = it > C::kStages ? it - C::kStages : 0; c < it; ++c)
+        for (int64_t c = it > C::kStages ? it - C::kStages : 0; c < it && rank == 0; ++c)
           tc::mbar_wait(bar(bars.full[c % C::kStages]), static_cast<uint32_t>((c / C::kStages) & 1), kWaitLimit);
       }
     }
   } else if (warp == 1) {
-    // ================================================================ MMA issue (one thread)
-    if (lane == 0) {
+    // ================================================================ MMA issue (one thread of the first CTA)
+    if (lane == 0 && rank == 0) {
+      auto commit = [&](uint64_t& b) {
+        if constexpr (CG == 2) commit_pair(bar(b));
+        else tc::mma_commit(bar(b));
+      };
       constexpr uint32_t id = tc::idesc_bf16(128 * CG, 256, MODE == kDw, !kGated);
       int64_t it = 0;
       int64_t tile = 0;
       bool ok = true;
-      for (int64_t t = blockIdx.x; t < sh.tiles && ok; t += gridDim.x, ++tile) {
+      for (int64_t t = first; t < sh.tiles && ok; t += step, ++tile) {
         const int buf = static_cast<int>(tile & 1);
         if (tile >= 2) ok = wait_bar(bar(bars.acc_empty[buf]), static_cast<uint32_t>(((tile >> 1) - 1) & 1), fail);
         tc::tc_fence_after();
@@ -239,15 +297,16 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
             // 64-element column blocks 8 KB apart
             const uint64_t da = MODE == kDw ? tc::smem_desc(a + j * 2048, kTile / 2, 1024) : tc::smem_desc(a + j * 32, 16, 1024);
             const uint64_t db = kGated ? tc::smem_desc(b + j * 32, 16, 1024) : tc::smem_desc(b + j * 2048, kTile / 2, 1024);
-            tc::mma_ss(tmem + buf * 256, da, db, id, kb > 0 || j > 0 ? 1u : 0u);
+            if constexpr (CG == 2) mma_pair(tmem + buf * 256, da, db, id, kb > 0 || j > 0 ? 1u : 0u);
+            else tc::mma_ss(tmem + buf * 256, da, db, id, kb > 0 || j > 0 ? 1u : 0u);
           }
-          tc::mma_commit(bar(bars.empty[s]));
+          commit(bars.empty[s]);
         }
-        if (ok) tc::mma_commit(bar(bars.acc_full[buf]));
+        if (ok) commit(bars.acc_full[buf]);
       }
       if (!ok) {   // what was issued ends before the accumulators are given back (again bounded)
         *fail = 1;
-        tc::mma_commit(bar(bars.drain));
+        commit(bars.drain);
         tc::mbar_wait(bar(bars.drain), 0, kWaitLimit);
       }
     }
@@ -264,15 +323,19 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
       asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(tile + tc::sw128(row, c + 8)), "r"(w[4]), "r"(w[5]),
                    "r"(w[6]), "r"(w[7]));
     };
+    auto release_acc = [&](int buf) {   // to the thread that issues the MMAs
+      if constexpr (CG == 2) arrive_cluster(map_rank(bar(bars.acc_empty[buf]), 0));
+      else tc::mbar_arrive(bar(bars.acc_empty[buf]));
+    };
     int64_t tile = 0;
     uint32_t loads = 0;                                   // of dh, this warpgroup's
     bool ok = true;
-    for (int64_t t = blockIdx.x; t < sh.tiles && ok; t += gridDim.x, ++tile) {
+    for (int64_t t = first; t < sh.tiles && ok; t += step, ++tile) {
       int64_t m, n;
       tile_of(sh, t, m, n);
       const CUtensorMap* c_map = MODE == kDw && m >= sh.half_tiles ? &maps.c1 : &maps.c0;
       if (MODE == kDw && m >= sh.half_tiles) m -= sh.half_tiles;
-      const int m0 = static_cast<int>(m * 128);
+      const int m0 = static_cast<int>(m * (128 * CG)) + rank * 128;
       const int n0 = static_cast<int>(n * (kGated ? 128 : 256) + wg * (kGated ? 64 : 128));
       const int buf = static_cast<int>(tile & 1);
       const bool mine = n0 < sh.cols && m0 < sh.rows;     // some of this part is inside the result
@@ -332,7 +395,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
         }
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(bars.acc_empty[buf]));
+        if (lane == 0) release_acc(buf);
         tc::fence_async_shared();
         bar_sync(1 + wg, 128);
         if (elect && mine) {
@@ -362,7 +425,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
           if (half == 1) {
             tc::tc_fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(bar(bars.acc_empty[buf]));
+            if (lane == 0) release_acc(buf);
           }
           tc::fence_async_shared();
           bar_sync(1 + wg, 128);
@@ -379,10 +442,12 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
   }
   tc::tc_fence_before();
   __syncthreads();
+  if constexpr (CG == 2) cluster_sync();   // nothing of the pair is in flight into this CTA any more
   if (tid == 0 && bars.fail) flag_status(status, kStatusTimeout);
   if (warp == 1) {
     tc::tc_fence_after();
-    tc::tmem_dealloc(tmem, 512);
+    if constexpr (CG == 2) tmem_dealloc_pair(tmem, 512);
+    else tc::tmem_dealloc(tmem, 512);
   }
 }
 
@@ -410,6 +475,7 @@ bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr int kCG = 2;
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <int MODE, int CG>
@@ -420,10 +486,20 @@ cudaError_t launch_gemm(const char* name, const Maps& maps, Shape sh, unsigned i
   auto kernel = ffn_gemm_kernel<MODE, CG>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t grid = sh.tiles < 152 ? sh.tiles : 152;
+  const int64_t most = 152 / CG;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(CG * (sh.tiles < most ? sh.tiles : most)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   ProfScope prof(name, stream);
-  kernel<<<static_cast<unsigned>(grid), kThreads, C::kSmem, stream>>>(maps, sh, status);
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, kernel, maps, sh, status);
 }
 
 }  // namespace
@@ -434,13 +510,13 @@ cudaError_t launch_ffn_gated_fwd(const FfnParams& p, cudaStream_t stream) {
       !make_map(&maps.b1, p.w_up, p.F, p.D, p.D, 128) || !make_map(&maps.c0, p.h, p.M, p.F, p.F, 128))
     return cudaErrorInvalidValue;
   Shape sh{};
-  sh.m_tiles = ceil_div(p.M, 128);
+  sh.m_tiles = ceil_div(p.M, 128 * kCG);
   sh.n_tiles = ceil_div(p.F, 128);
   sh.kb = static_cast<int>(ceil_div(p.D, kBK));
   sh.rows = p.M;
   sh.cols = p.F;
   sh.act = p.act;
-  return launch_gemm<kGate, 1>("ffn_gate", maps, sh, p.status, stream);
+  return launch_gemm<kGate, kCG>("ffn_gate", maps, sh, p.status, stream);
 }
 
 cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream) {
@@ -452,13 +528,13 @@ cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream) {
         !make_map(&maps.c0, p.dg, p.M, p.F, p.F, 128) || !make_map(&maps.c1, p.du, p.M, p.F, p.F, 128))
       return cudaErrorInvalidValue;
     Shape sh{};
-    sh.m_tiles = ceil_div(p.M, 128);
+    sh.m_tiles = ceil_div(p.M, 128 * kCG);
     sh.n_tiles = ceil_div(p.F, 128);
     sh.kb = static_cast<int>(ceil_div(p.D, kBK));
     sh.rows = p.M;
     sh.cols = p.F;
     sh.act = p.act;
-    if ((e = launch_gemm<kGateGrad, 1>("ffn_gate_grad", maps, sh, p.status, stream)) != cudaSuccess) return e;
+    if ((e = launch_gemm<kGateGrad, kCG>("ffn_gate_grad", maps, sh, p.status, stream)) != cudaSuccess) return e;
   }
   {
     Maps maps{};
@@ -467,13 +543,13 @@ cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream) {
         !make_map(&maps.c0, p.dx, p.M, p.D, p.D, 128))
       return cudaErrorInvalidValue;
     Shape sh{};
-    sh.m_tiles = ceil_div(p.M, 128);
+    sh.m_tiles = ceil_div(p.M, 128 * kCG);
     sh.n_tiles = ceil_div(p.D, 256);
     sh.kb_half = static_cast<int>(ceil_div(p.F, kBK));
     sh.kb = 2 * sh.kb_half;
     sh.rows = p.M;
     sh.cols = p.D;
-    if ((e = launch_gemm<kDx, 1>("ffn_dx", maps, sh, p.status, stream)) != cudaSuccess) return e;
+    if ((e = launch_gemm<kDx, kCG>("ffn_dx", maps, sh, p.status, stream)) != cudaSuccess) return e;
   }
   Maps maps{};
   if (!make_map(&maps.a0, p.dg, p.M, p.F, p.F, 64) || !make_map(&maps.a1, p.du, p.M, p.F, p.F, 64) ||
@@ -481,13 +557,13 @@ cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream) {
       !make_map(&maps.c1, p.dw_up, p.F, p.D, p.D, 128))
     return cudaErrorInvalidValue;
   Shape sh{};
-  sh.half_tiles = ceil_div(p.F, 128);
+  sh.half_tiles = ceil_div(p.F, 128 * kCG);
   sh.m_tiles = 2 * sh.half_tiles;
   sh.n_tiles = ceil_div(p.D, 256);
   sh.kb = static_cast<int>(ceil_div(p.M, kBK));
   sh.rows = p.F;
   sh.cols = p.D;
-  return launch_gemm<kDw, 1>("ffn_dw", maps, sh, p.status, stream);
+  return launch_gemm<kDw, kCG>("ffn_dw", maps, sh, p.status, stream);
 }
 
 }  // namespace dsv
