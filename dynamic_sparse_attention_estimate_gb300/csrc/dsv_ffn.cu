@@ -6,14 +6,14 @@
 //   kGateGrad  the same products again; dg = dh u act'(g), du = dh act(g)   (nothing is kept of the forward)
 //   kDx        dx = dg Wg + du Wu                                         (K = F twice; W is MN-major)
 //   kDw        dWg = dg^T x, dWu = du^T x                                  (K = M; both MN-major)
-// An accumulator tile is 128 CG rows by 256 columns; in the gated modes its columns are 128 of g and the
+// An accumulator tile is 256 rows by 256 columns, held by a pair of CTAs; in the gated modes its columns are 128 of g and the
 // 128 of u they meet in the epilogue, so g and u never leave the SM in kGate.  dg and du are rounded
 // to bf16 between the backward's kernels: the tensor cores take them as operands of that type (2^-8 of
 // each value, as every activation between layers).
 //
-// Roles (384 threads): thread 0 of warp 0 issues the TMA loads into a ring of stages; thread 0 of warp
-// 1 issues the MMAs, into one of two accumulators (2 x 256 of the 512 TMEM columns); warps 4-11 empty the
-// other one: two warpgroups, each on half of the columns, through 128-byte-swizzled staging tiles that
+// Roles (384 threads): one thread of warp 0 issues the TMA loads of A and one of warp 2 those of B into a
+// ring of stages; one thread of warp 1 issues the MMAs, into one of two accumulators (2 x 256 of the 512
+// TMEM columns); warps 4-11 empty the other one: two warpgroups, each on half of the columns, through 128-byte-swizzled staging tiles that
 // TMA stores write (rows and columns past the matrices are clipped there, and zero-filled by the
 // loads).  Every wait is bounded.
 #include <cuda.h>
@@ -27,7 +27,10 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kBK = 64;                    // K elements of a stage (128 bytes)
-constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr uint32_t kWaitLimit = 1u << 20;   // polls, each suspended in the hardware for up to kWaitNs
+// Without the hint the waiting warps poll, and pay for it in watts: at 16,384 x 2048 x 5632 a second of
+// forward calls at the card's power limit runs at 1.68 PFLOP/s without and 1.73 with it.
+constexpr uint32_t kWaitNs = 2000;
 constexpr int kTile = 128 * 128;           // bytes of a [128 rows][64] or two [64 rows][64] bf16 tiles
 
 enum Mode { kGate = 0, kGateGrad = 1, kDx = 2, kDw = 3 };
@@ -46,10 +49,10 @@ struct Shape {
   int act;
 };
 
-template <int MODE, int CG>
+template <int MODE>
 struct Cfg {
   static constexpr int kStageA = kTile;
-  static constexpr int kStageB = 2 * kTile / CG;
+  static constexpr int kStageB = kTile;
   static constexpr int kStage = kStageA + kStageB;
   static constexpr int kOut = (MODE == kGateGrad ? 2 : 1) * 2 * kTile;   // staging of two warpgroups
   static constexpr int kStages = (227 * 1024 - 2048 - kOut) / kStage;
@@ -67,11 +70,30 @@ struct Bars {
 
 DSV_DEVICE bool wait_bar(uint32_t bar, uint32_t parity, volatile int* fail) {
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
-    if ((i & 255) == 255 && *fail) return false;
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kWaitNs)
+        : "memory");
+    if (ok) return true;
+    if ((i & 255) == 255 && *fail) return false;   // (a look at it in every round costs the MMAs' rate)
   }
   return false;
 }
+
+// A place in a ring of N stages and the parity of its round (kept as two small numbers: a division of a
+// running count would sit between two stages' MMAs).
+template <int N>
+struct Ring {
+  uint32_t s = 0, round = 0;
+  DSV_DEVICE void next() {
+    if (++s == N) {
+      s = 0;
+      round ^= 1;
+    }
+  }
+};
 
 DSV_DEVICE uint32_t map_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -174,16 +196,16 @@ DSV_DEVICE void tile_of(const Shape& sh, int64_t t, int64_t& m, int64_t& n) {
   n = r / gm;
 }
 
-template <int MODE, int CG>
+template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* status) {
-  using C = Cfg<MODE, CG>;
+  using C = Cfg<MODE>;
   constexpr bool kGated = MODE == kGate || MODE == kGateGrad;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) Bars bars;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
-  const int64_t first = blockIdx.x / CG, step = gridDim.x / CG;   // tiles first, first + step, ..
+  const int rank = static_cast<int>(cluster_rank());              // of this CTA in its pair
+  const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;     // the pair's tiles: first, first + step, ..
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;          // swizzled tiles need 1024-byte alignment
   const uint32_t out = ring + C::kStages * C::kStage;
@@ -196,7 +218,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(bar(bars.acc_full[b]), 1);
-      tc::mbar_init(bar(bars.acc_empty[b]), 8 * CG);
+      tc::mbar_init(bar(bars.acc_empty[b]), 16);
       tc::mbar_init(bar(bars.dh_full[b]), 1);
     }
     tc::mbar_init(bar(bars.drain), 1);
@@ -204,109 +226,110 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
     bars.fail = 0;
   }
   if (warp == 1) {
-    if constexpr (CG == 2) {
-      tmem_alloc_pair(smem_u32(&bars.tmem), 512);
-    } else {
-      tc::tmem_alloc(smem_u32(&bars.tmem), 512);
-      tc::tmem_relinquish();
-    }
+    tmem_alloc_pair(smem_u32(&bars.tmem), 512);
   }
   tc::tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();   // the other CTA's barriers exist
+  cluster_sync();   // the other CTAs' barriers exist
   tc::tc_fence_after();
   const uint32_t tmem = bars.tmem;
   volatile int* fail = &bars.fail;
 
-  if (warp == 0) {
-    // ================================================================ TMA loads (one thread)
+  if (warp == 0 || warp == 2) {
+    // ================================================================ TMA loads: one thread for A (warp 0), one for B
     if (lane == 0) {
-      int64_t it = 0;   // k blocks issued
+      const bool for_a = warp == 0;
+      const uint32_t empty0 = bar(bars.empty[0]), full0 = bar(bars.full[0]);
+      const uint32_t lead0 = map_rank(full0, 0);   // the copies count on the first CTA's barriers, where the MMAs are issued
+      Ring<C::kStages> at;
+      int64_t issued = 0;   // stages
       bool ok = true;
       for (int64_t t = first; t < sh.tiles && ok; t += step) {
         int64_t m, n;
         tile_of(sh, t, m, n);
-        const CUtensorMap* a_map = MODE == kDw && m >= sh.half_tiles ? &maps.a1 : &maps.a0;
-        if (MODE == kDw && m >= sh.half_tiles) m -= sh.half_tiles;
-        const int m0 = static_cast<int>(m * (128 * CG)) + rank * 128;
+        const bool second = MODE == kDw && m >= sh.half_tiles;
+        const int m0 = static_cast<int>((second ? m - sh.half_tiles : m) * 256) + rank * 128;
         // B: the pair's second CTA holds the tile's second 128 columns (in the gated modes those of u)
         const int n0 = static_cast<int>(n * (kGated ? 128 : 256)) + (kGated ? 0 : rank * 128);
-        for (int kb = 0; kb < sh.kb; ++kb, ++it) {
-          const int s = static_cast<int>(it % C::kStages);
-          if (it >= C::kStages && !wait_bar(bar(bars.empty[s]), static_cast<uint32_t>((it / C::kStages - 1) & 1), fail)) {
+        for (int kb = 0; kb < sh.kb; ++kb, ++issued, at.next()) {
+          // (a fresh barrier passes for the parity before its first round)
+          if (!wait_bar(empty0 + 8 * at.s, at.round ^ 1, fail)) {
             ok = false;
             break;
           }
-          // both CTAs' copies count on the first one's barrier, where the MMAs are issued
-          if (rank == 0) expect_tx(bar(bars.full[s]), CG * C::kStage);
-          const uint32_t full = CG == 2 ? map_rank(bar(bars.full[s]), 0) : bar(bars.full[s]);
-          const uint32_t a = ring + s * C::kStage, b = a + C::kStageA;
-          auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
-            if constexpr (CG == 2) tma_load_pair(dst, map, x, y, full);
-            else tma_load(dst, map, x, y, full);
-          };
-          if constexpr (kGated) {
-            load(a, &maps.a0, kb * kBK, m0);
-            load(b, rank == 0 ? &maps.b0 : &maps.b1, kb * kBK, n0);
-            if (CG == 1) load(b + kTile, &maps.b1, kb * kBK, n0);
-          } else if constexpr (MODE == kDx) {
-            const bool second = kb >= sh.kb_half;
-            const int k0 = (second ? kb - sh.kb_half : kb) * kBK;
-            load(a, second ? &maps.a1 : &maps.a0, k0, m0);
-#pragma unroll
-            for (int i = 0; i < 4 / CG; ++i) load(b + i * (kTile / 2), second ? &maps.b1 : &maps.b0, n0 + 64 * i, k0);
+          const uint32_t full = lead0 + 8 * at.s;
+          const uint32_t a = ring + at.s * C::kStage, b = a + C::kStageA;
+          const bool late = MODE == kDx && kb >= sh.kb_half;   // the second of the two products
+          const int k0 = (late ? kb - sh.kb_half : kb) * kBK;
+          if (for_a) {
+            if (rank == 0) expect_tx(full0 + 8 * at.s, 2 * C::kStage);
+            const CUtensorMap* map = late || second ? &maps.a1 : &maps.a0;
+            if constexpr (MODE != kDw) {
+              tma_load_pair(a, map, k0, m0, full);
+            } else {
+              tma_load_pair(a, map, m0, k0, full);
+              tma_load_pair(a + kTile / 2, map, m0 + 64, k0, full);
+            }
           } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) load(a + i * (kTile / 2), a_map, m0 + 64 * i, kb * kBK);
-#pragma unroll
-            for (int i = 0; i < 4 / CG; ++i) load(b + i * (kTile / 2), &maps.b0, n0 + 64 * i, kb * kBK);
+            const CUtensorMap* map = late || (kGated && rank == 1) ? &maps.b1 : &maps.b0;
+            if constexpr (kGated) {
+              tma_load_pair(b, map, k0, n0, full);
+            } else {
+              tma_load_pair(b, map, n0, k0, full);
+              tma_load_pair(b + kTile / 2, map, n0 + 64, k0, full);
+            }
           }
         }
       }
+      // the stages still out come back before this CTA may leave: the MMAs arrive on them
+      const int64_t out_first = issued > C::kStages ? issued - C::kStages : 0;
+      Ring<C::kStages> last;
+      last.s = static_cast<uint32_t>(out_first % C::kStages);
+      last.round = static_cast<uint32_t>((out_first / C::kStages) & 1);
+      Ring<C::kStages> load = last;
+      for (int64_t c = out_first; c < issued && ok; ++c, last.next()) ok = wait_bar(empty0 + 8 * last.s, last.round, fail);
       if (!ok) {
         *fail = 1;
         // the copies in flight land before this CTA's shared memory can go away (again bounded)
-        for (int64_t c = it > C::kStages ? it - C::kStages : 0; c < it && rank == 0; ++c)
-          tc::mbar_wait(bar(bars.full[c % C::kStages]), static_cast<uint32_t>((c / C::kStages) & 1), kWaitLimit);
+        for (int64_t c = out_first; c < issued && rank == 0; ++c, load.next())
+          tc::mbar_wait(full0 + 8 * load.s, load.round, kWaitLimit);
       }
     }
   } else if (warp == 1) {
-    // ================================================================ MMA issue (one thread of the first CTA)
+    // ================================================================ MMA issue (one thread of the pair)
     if (lane == 0 && rank == 0) {
-      auto commit = [&](uint64_t& b) {
-        if constexpr (CG == 2) commit_pair(bar(b));
-        else tc::mma_commit(bar(b));
-      };
-      constexpr uint32_t id = tc::idesc_bf16(128 * CG, 256, MODE == kDw, !kGated);
-      int64_t it = 0;
+      constexpr uint32_t id = tc::idesc_bf16(256, 256, MODE == kDw, !kGated);
+      static_assert(id >> 29 == 0 && ((id >> 24) & 31) == 16 && ((id >> 17) & 63) == 32, "M and N in their fields");
+      // descriptors of the first stage; a stage, and 16 elements of K in it, are so many 16-byte units on
+      // (K-major: 16 elements are 32 bytes; MN-major: two 8-row groups of 1024 bytes, column blocks of 64
+      // elements 8 KB apart)
+      constexpr bool kMnA = MODE == kDw, kMnB = !kGated;
+      const uint64_t a0 = kMnA ? tc::smem_desc(ring, kTile / 2, 1024) : tc::smem_desc(ring, 16, 1024);
+      const uint64_t b0 = kMnB ? tc::smem_desc(ring + C::kStageA, kTile / 2, 1024) : tc::smem_desc(ring + C::kStageA, 16, 1024);
+      constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
+      Ring<C::kStages> at;
       int64_t tile = 0;
       bool ok = true;
       for (int64_t t = first; t < sh.tiles && ok; t += step, ++tile) {
         const int buf = static_cast<int>(tile & 1);
         if (tile >= 2) ok = wait_bar(bar(bars.acc_empty[buf]), static_cast<uint32_t>(((tile >> 1) - 1) & 1), fail);
         tc::tc_fence_after();
-        for (int kb = 0; kb < sh.kb && ok; ++kb, ++it) {
-          const int s = static_cast<int>(it % C::kStages);
-          ok = wait_bar(bar(bars.full[s]), static_cast<uint32_t>((it / C::kStages) & 1), fail);
+        const uint32_t acc = tmem + buf * 256;
+        for (int kb = 0; kb < sh.kb && ok; ++kb, at.next()) {
+          const uint32_t s = at.s;
+          ok = wait_bar(bar(bars.full[s]), at.round, fail);
           if (!ok) break;
           tc::tc_fence_after();
-          const uint32_t a = ring + s * C::kStage, b = a + C::kStageA;
+          const uint64_t da = a0 + s * (C::kStage >> 4), db = b0 + s * (C::kStage >> 4);
 #pragma unroll
-          for (int j = 0; j < kBK / 16; ++j) {
-            // K-major: 16 elements on are 32 bytes on; MN-major: two 8-row groups on (1024 bytes each),
-            // 64-element column blocks 8 KB apart
-            const uint64_t da = MODE == kDw ? tc::smem_desc(a + j * 2048, kTile / 2, 1024) : tc::smem_desc(a + j * 32, 16, 1024);
-            const uint64_t db = kGated ? tc::smem_desc(b + j * 32, 16, 1024) : tc::smem_desc(b + j * 2048, kTile / 2, 1024);
-            if constexpr (CG == 2) mma_pair(tmem + buf * 256, da, db, id, kb > 0 || j > 0 ? 1u : 0u);
-            else tc::mma_ss(tmem + buf * 256, da, db, id, kb > 0 || j > 0 ? 1u : 0u);
-          }
-          commit(bars.empty[s]);
+          for (int j = 0; j < kBK / 16; ++j) mma_pair(acc, da + j * kStepA, db + j * kStepB, id, kb > 0 || j > 0 ? 1u : 0u);
+          commit_pair(bar(bars.empty[s]));
         }
-        if (ok) commit(bars.acc_full[buf]);
+        if (ok) commit_pair(bar(bars.acc_full[buf]));
       }
       if (!ok) {   // what was issued ends before the accumulators are given back (again bounded)
         *fail = 1;
-        commit(bars.drain);
+        commit_pair(bar(bars.drain));
         tc::mbar_wait(bar(bars.drain), 0, kWaitLimit);
       }
     }
@@ -324,8 +347,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
                    "r"(w[6]), "r"(w[7]));
     };
     auto release_acc = [&](int buf) {   // to the thread that issues the MMAs
-      if constexpr (CG == 2) arrive_cluster(map_rank(bar(bars.acc_empty[buf]), 0));
-      else tc::mbar_arrive(bar(bars.acc_empty[buf]));
+      arrive_cluster(map_rank(bar(bars.acc_empty[buf]), 0));
     };
     int64_t tile = 0;
     uint32_t loads = 0;                                   // of dh, this warpgroup's
@@ -335,7 +357,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
       tile_of(sh, t, m, n);
       const CUtensorMap* c_map = MODE == kDw && m >= sh.half_tiles ? &maps.c1 : &maps.c0;
       if (MODE == kDw && m >= sh.half_tiles) m -= sh.half_tiles;
-      const int m0 = static_cast<int>(m * (128 * CG)) + rank * 128;
+      const int m0 = static_cast<int>(m * 256) + rank * 128;
       const int n0 = static_cast<int>(n * (kGated ? 128 : 256) + wg * (kGated ? 64 : 128));
       const int buf = static_cast<int>(tile & 1);
       const bool mine = n0 < sh.cols && m0 < sh.rows;     // some of this part is inside the result
@@ -442,12 +464,11 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
   }
   tc::tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();   // nothing of the pair is in flight into this CTA any more
+  cluster_sync();   // nothing of the cluster is in flight into this CTA any more
   if (tid == 0 && bars.fail) flag_status(status, kStatusTimeout);
   if (warp == 1) {
     tc::tc_fence_after();
-    if constexpr (CG == 2) tmem_dealloc_pair(tmem, 512);
-    else tc::tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -475,26 +496,25 @@ bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kCG = 2;
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-template <int MODE, int CG>
+template <int MODE>
 cudaError_t launch_gemm(const char* name, const Maps& maps, Shape sh, unsigned int* status, cudaStream_t stream) {
-  using C = Cfg<MODE, CG>;
+  using C = Cfg<MODE>;
   sh.tiles = sh.m_tiles * sh.n_tiles;
   sh.group = 16;
-  auto kernel = ffn_gemm_kernel<MODE, CG>;
+  auto kernel = ffn_gemm_kernel<MODE>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t most = 152 / CG;
+  constexpr int64_t most = 76;   // pairs on the card's 152 SMs
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(CG * (sh.tiles < most ? sh.tiles : most)));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (sh.tiles < most ? sh.tiles : most)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -510,13 +530,13 @@ cudaError_t launch_ffn_gated_fwd(const FfnParams& p, cudaStream_t stream) {
       !make_map(&maps.b1, p.w_up, p.F, p.D, p.D, 128) || !make_map(&maps.c0, p.h, p.M, p.F, p.F, 128))
     return cudaErrorInvalidValue;
   Shape sh{};
-  sh.m_tiles = ceil_div(p.M, 128 * kCG);
+  sh.m_tiles = ceil_div(p.M, 256);
   sh.n_tiles = ceil_div(p.F, 128);
   sh.kb = static_cast<int>(ceil_div(p.D, kBK));
   sh.rows = p.M;
   sh.cols = p.F;
   sh.act = p.act;
-  return launch_gemm<kGate, kCG>("ffn_gate", maps, sh, p.status, stream);
+  return launch_gemm<kGate>("ffn_gate", maps, sh, p.status, stream);
 }
 
 cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream) {
@@ -528,13 +548,13 @@ cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream) {
         !make_map(&maps.c0, p.dg, p.M, p.F, p.F, 128) || !make_map(&maps.c1, p.du, p.M, p.F, p.F, 128))
       return cudaErrorInvalidValue;
     Shape sh{};
-    sh.m_tiles = ceil_div(p.M, 128 * kCG);
+    sh.m_tiles = ceil_div(p.M, 256);
     sh.n_tiles = ceil_div(p.F, 128);
     sh.kb = static_cast<int>(ceil_div(p.D, kBK));
     sh.rows = p.M;
     sh.cols = p.F;
     sh.act = p.act;
-    if ((e = launch_gemm<kGateGrad, kCG>("ffn_gate_grad", maps, sh, p.status, stream)) != cudaSuccess) return e;
+    if ((e = launch_gemm<kGateGrad>("ffn_gate_grad", maps, sh, p.status, stream)) != cudaSuccess) return e;
   }
   {
     Maps maps{};
@@ -543,13 +563,13 @@ cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream) {
         !make_map(&maps.c0, p.dx, p.M, p.D, p.D, 128))
       return cudaErrorInvalidValue;
     Shape sh{};
-    sh.m_tiles = ceil_div(p.M, 128 * kCG);
+    sh.m_tiles = ceil_div(p.M, 256);
     sh.n_tiles = ceil_div(p.D, 256);
     sh.kb_half = static_cast<int>(ceil_div(p.F, kBK));
     sh.kb = 2 * sh.kb_half;
     sh.rows = p.M;
     sh.cols = p.D;
-    if ((e = launch_gemm<kDx, kCG>("ffn_dx", maps, sh, p.status, stream)) != cudaSuccess) return e;
+    if ((e = launch_gemm<kDx>("ffn_dx", maps, sh, p.status, stream)) != cudaSuccess) return e;
   }
   Maps maps{};
   if (!make_map(&maps.a0, p.dg, p.M, p.F, p.F, 64) || !make_map(&maps.a1, p.du, p.M, p.F, p.F, 64) ||
@@ -557,13 +577,13 @@ cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream) {
       !make_map(&maps.c1, p.dw_up, p.F, p.D, p.D, 128))
     return cudaErrorInvalidValue;
   Shape sh{};
-  sh.half_tiles = ceil_div(p.F, 128 * kCG);
+  sh.half_tiles = ceil_div(p.F, 256);
   sh.m_tiles = 2 * sh.half_tiles;
   sh.n_tiles = ceil_div(p.D, 256);
   sh.kb = static_cast<int>(ceil_div(p.M, kBK));
   sh.rows = p.F;
   sh.cols = p.D;
-  return launch_gemm<kDw, kCG>("ffn_dw", maps, sh, p.status, stream);
+  return launch_gemm<kDw>("ffn_dw", maps, sh, p.status, stream);
 }
 
 }  // namespace dsv
