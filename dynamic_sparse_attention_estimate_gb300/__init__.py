@@ -19,6 +19,7 @@ from .binding import (  # noqa: F401
     dsv_ffn_gated_bwd,
     dsv_ffn_gated_bwd_workspace,
     dsv_ffn_gated_fwd,
+    dsv_ffn_gated_fwd_workspace,
     dsv_qk_norm_rope_bwd,
     dsv_qk_norm_rope_bwd_workspace,
     dsv_qk_norm_rope_fwd,

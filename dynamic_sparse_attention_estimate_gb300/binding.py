@@ -33,7 +33,7 @@ EXPORTED = (
     "dsv_sparse_attn_bwd_prepare", "dsv_sparse_attn_bwd_prepared", "dsv_sparse_attn_fwd_workspace",
     "dsv_rope3d_table_bytes", "dsv_rope3d_table", "dsv_rope3d_fwd", "dsv_rope3d_bwd",
     "dsv_qk_norm_rope_fwd", "dsv_qk_norm_rope_bwd_workspace", "dsv_qk_norm_rope_bwd",
-    "dsv_ffn_gated_fwd", "dsv_ffn_gated_bwd_workspace", "dsv_ffn_gated_bwd",
+    "dsv_ffn_gated_fwd_workspace", "dsv_ffn_gated_fwd", "dsv_ffn_gated_bwd_workspace", "dsv_ffn_gated_bwd",
 )
 
 
@@ -149,10 +149,11 @@ def load_library(path: Optional[str] = None):
     lib.dsv_qk_norm_rope_bwd.argtypes = [rp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.dsv_qk_norm_rope_bwd.restype = st
     fp = ctypes.POINTER(FfnDims)
-    lib.dsv_ffn_gated_fwd.argtypes = [fp, vp, vp, vp, vp, vp]
+    lib.dsv_ffn_gated_fwd.argtypes = [fp, vp, vp, vp, vp, vp, sz, vp]
     lib.dsv_ffn_gated_fwd.restype = st
-    lib.dsv_ffn_gated_bwd_workspace.argtypes = [fp]
-    lib.dsv_ffn_gated_bwd_workspace.restype = sz
+    for f in (lib.dsv_ffn_gated_fwd_workspace, lib.dsv_ffn_gated_bwd_workspace):
+        f.argtypes = [fp]
+        f.restype = sz
     lib.dsv_ffn_gated_bwd.argtypes = [fp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.dsv_ffn_gated_bwd.restype = st
     lib.dsv_profile_enable.argtypes = [st]
@@ -548,6 +549,17 @@ def _need_on(t: torch.Tensor, name: str, dtype, shape, device: int):
                          f"{t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} device={t.device}")
 
 
+def _workspace(workspace: Optional[torch.Tensor], nbytes: int, like: torch.Tensor):
+    """(pointer, bytes, the tensor) of the caller's workspace, or of a new one of nbytes."""
+    if workspace is None:
+        if not nbytes:
+            return None, 0, None
+        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=like.device)
+    elif not workspace.is_contiguous() or workspace.get_device() != like.get_device():
+        raise ValueError(f"workspace: need a contiguous tensor on {like.device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
 def _rope_args(x: torch.Tensor, pos: Optional[torch.Tensor], rope: Optional[RopeTable], eps: float):
     """(dims struct, pos pointer, table pointer) for x [B, H, N, d]."""
     shape = x.shape
@@ -684,16 +696,10 @@ def dsv_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, dv_out: Opt
     dstrides += (0, 0, 0) if dv is None else _need_view(dv, "dv", shape, device)
     dwq, dwk = torch.empty((2, d), dtype=torch.float32, device=q.device).unbind(0)
     dwq, dwk = None if wq is None else dwq, None if wk is None else dwk
-    if workspace is None:
-        nbytes = 0 if wq is None and wk is None else _qk_norm_rope_ws(B, H, N, d)
-        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=q.device) if nbytes else None
-    else:
-        nbytes = workspace.numel() * workspace.element_size()
-        if not workspace.is_contiguous() or workspace.get_device() != device:
-            raise ValueError(f"workspace: need a contiguous tensor on cuda:{device}")
+    ws, nbytes, _keep = _workspace(workspace, 0 if wq is None and wk is None else _qk_norm_rope_ws(B, H, N, d), q)
     _call("dsv_qk_norm_rope_bwd", device, dims, dq_out.data_ptr(), dk_out.data_ptr(), _ptr(dv_out), q.data_ptr(),
           k.data_ptr(), _Strides6(*strides), _ptr(wq), _ptr(wk), pos_ptr, table_ptr, _ptr(dq), _ptr(dk), _ptr(dv),
-          _Strides9(*dstrides), _ptr(dwq), _ptr(dwk), _ptr(workspace), nbytes)
+          _Strides9(*dstrides), _ptr(dwq), _ptr(dwk), ws, nbytes)
     return dq, dk, dv, dwq, dwk
 
 
@@ -704,15 +710,16 @@ _ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
 
 @functools.lru_cache(maxsize=256)
 def _ffn_dims(M: int, D: int, F: int, act: str):
-    """(dims struct, workspace bytes of the backward)."""
+    """(dims struct, workspace bytes of the forward, of the backward)."""
     if act not in _ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(_ACTIVATIONS)}, got {act!r}")
     dims = FfnDims(M, D, F, _ACTIVATIONS[act])
-    return dims, int(load_library().dsv_ffn_gated_bwd_workspace(ctypes.byref(dims)))
+    lib = load_library()
+    return dims, int(lib.dsv_ffn_gated_fwd_workspace(dims)), int(lib.dsv_ffn_gated_bwd_workspace(dims))
 
 
 def _ffn_args(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: str):
-    """(dims struct, workspace bytes, h's shape) after the checks of the inputs."""
+    """((dims struct, workspace bytes of the forward, of the backward), h's shape) after the checks of the inputs."""
     for t, n in ((x, "x"), (w_gate, "w_gate")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{n} must be a torch.Tensor")
@@ -724,26 +731,30 @@ def _ffn_args(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: st
     D, F, device = x.shape[-1], w_gate.shape[0], x.get_device()
     _need_on(w_gate, "w_gate", torch.bfloat16, (F, D), device)
     _need_on(w_up, "w_up", torch.bfloat16, (F, D), device)
-    dims, ws = _ffn_dims(x.numel() // D if D else 0, D, F, act)
-    return dims, ws, (*x.shape[:-1], F)
+    return _ffn_dims(x.numel() // D if D else 0, D, F, act), (*x.shape[:-1], F)
 
 
 def dsv_ffn_gated_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: str = "silu",
-                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                      out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """h [..., F] = act(x w_gate^T) * (x w_up^T) for x bf16 [..., D] and weights bf16 [F, D]
     (act: "silu" or "gelu_tanh"; see include/dsv.h)."""
-    dims, _, shape = _ffn_args(x, w_gate, w_up, act)
+    (dims, nbytes, _), shape = _ffn_args(x, w_gate, w_up, act)
     device = x.get_device()
     if out is None:
         out = torch.empty(shape, dtype=x.dtype, device=x.device)
     else:
         _need_on(out, "out", torch.bfloat16, shape, device)
-    _call("dsv_ffn_gated_fwd", device, dims, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr())
+    ws, nbytes, _keep = _workspace(workspace, nbytes, x)
+    _call("dsv_ffn_gated_fwd", device, dims, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(), ws, nbytes)
     return out
 
 
-def dsv_ffn_gated_bwd_workspace(M: int, D: int, F: int) -> int:
+def dsv_ffn_gated_fwd_workspace(M: int, D: int, F: int) -> int:
     return _ffn_dims(int(M), int(D), int(F), "silu")[1]
+
+
+def dsv_ffn_gated_bwd_workspace(M: int, D: int, F: int) -> int:
+    return _ffn_dims(int(M), int(D), int(F), "silu")[2]
 
 
 def dsv_ffn_gated_bwd(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: str = "silu",
@@ -751,7 +762,7 @@ def dsv_ffn_gated_bwd(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w
                       workspace: Optional[torch.Tensor] = None):
     """(dx [..., D], dw_gate [F, D], dw_up [F, D]), all bf16, for the loss gradient dh [..., F]; g and u are
     recomputed from x (the forward keeps nothing)."""
-    dims, nbytes, shape = _ffn_args(x, w_gate, w_up, act)
+    (dims, _, nbytes), shape = _ffn_args(x, w_gate, w_up, act)
     device = x.get_device()
     _need_on(dh, "dh", torch.bfloat16, shape, device)
     if out is None:
@@ -760,14 +771,9 @@ def dsv_ffn_gated_bwd(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w
         dx, dwg, dwu = out
         for t, n, like in ((dx, "dx", x), (dwg, "dw_gate", w_gate), (dwu, "dw_up", w_up)):
             _need_on(t, n, torch.bfloat16, like.shape, device)
-    if workspace is None:
-        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=x.device)
-    else:
-        if not workspace.is_contiguous() or workspace.get_device() != device:
-            raise ValueError(f"workspace: need a contiguous tensor on cuda:{device}")
-        nbytes = workspace.numel() * workspace.element_size()
+    ws, nbytes, _keep = _workspace(workspace, nbytes, x)
     _call("dsv_ffn_gated_bwd", device, dims, dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
-          dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), workspace.data_ptr(), nbytes)
+          dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), ws, nbytes)
     return dx, dwg, dwu
 
 

@@ -994,14 +994,28 @@ static dsv_status check_spans(const NamedSpan* in, int n_in, const NamedSpan* ou
   return DSV_OK;
 }
 
+static dsv_status check_workspace(const void* ws, size_t ws_bytes, size_t need) {
+  if (!ws) return fail(DSV_ERR_WORKSPACE, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(ws) % kAlign) return fail(DSV_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (ws_bytes < need) return fail(DSV_ERR_WORKSPACE, "workspace of %zu bytes is below the %zu needed", ws_bytes, need);
+  return DSV_OK;
+}
+
+size_t dsv_ffn_gated_fwd_workspace(const dsv_ffn_dims* dims) {
+  if (check_ffn(dims) != DSV_OK) return 0;
+  return up(dsv::ffn_fwd_workspace(dims->M, dims->D, dims->F));
+}
+
 dsv_status dsv_ffn_gated_fwd(const dsv_ffn_dims* dims, const void* x, const void* w_gate, const void* w_up, void* h,
-                             void* stream) {
+                             void* ws, size_t ws_bytes, void* stream) {
   dsv_status s = check_ffn(dims);
   if (s != DSV_OK) return s;
   const int64_t M = dims->M, D = dims->D, F = dims->F;
+  const size_t need = up(dsv::ffn_fwd_workspace(M, D, F));
+  if (need && (s = check_workspace(ws, ws_bytes, need)) != DSV_OK) return s;
   const NamedSpan in[3] = {{"x", x, M * D}, {"w_gate", w_gate, F * D}, {"w_up", w_up, F * D}};
-  const NamedSpan out[1] = {{"h", h, M * F}};
-  if ((s = check_spans(in, 3, out, 1)) != DSV_OK) return s;
+  const NamedSpan out[2] = {{"h", h, M * F}, {"ws", ws, static_cast<int64_t>(need / 2)}};
+  if ((s = check_spans(in, 3, out, need ? 2 : 1)) != DSV_OK) return s;
   dsv::FfnParams p{};
   p.M = M;
   p.D = D;
@@ -1011,6 +1025,7 @@ dsv_status dsv_ffn_gated_fwd(const dsv_ffn_dims* dims, const void* x, const void
   p.w_gate = static_cast<const dsv::bf16*>(w_gate);
   p.w_up = static_cast<const dsv::bf16*>(w_up);
   p.h = static_cast<dsv::bf16*>(h);
+  p.partial = static_cast<float*>(ws);
   if ((s = status_word(&p.status)) != DSV_OK) return s;
   cudaError_t e = dsv::launch_ffn_gated_fwd(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(DSV_ERR_CUDA, "ffn forward launch: %s", cudaGetErrorString(e));
@@ -1021,7 +1036,7 @@ static size_t ffn_half_bytes(const dsv_ffn_dims* d) { return up(sizeof(uint16_t)
 
 size_t dsv_ffn_gated_bwd_workspace(const dsv_ffn_dims* dims) {
   if (check_ffn(dims) != DSV_OK) return 0;
-  return 2 * ffn_half_bytes(dims);
+  return 2 * ffn_half_bytes(dims) + up(dsv::ffn_bwd_partial(dims->M, dims->D, dims->F));
 }
 
 dsv_status dsv_ffn_gated_bwd(const dsv_ffn_dims* dims, const void* dh, const void* x, const void* w_gate,
@@ -1030,13 +1045,11 @@ dsv_status dsv_ffn_gated_bwd(const dsv_ffn_dims* dims, const void* dh, const voi
   dsv_status s = check_ffn(dims);
   if (s != DSV_OK) return s;
   const int64_t M = dims->M, D = dims->D, F = dims->F;
-  const size_t need = 2 * ffn_half_bytes(dims);
+  const size_t need = dsv_ffn_gated_bwd_workspace(dims);
   const NamedSpan in[4] = {{"dh", dh, M * F}, {"x", x, M * D}, {"w_gate", w_gate, F * D}, {"w_up", w_up, F * D}};
   const NamedSpan out[4] = {{"dx", dx, M * D}, {"dw_gate", dw_gate, F * D}, {"dw_up", dw_up, F * D},
                             {"ws", ws, static_cast<int64_t>(need / 2)}};
-  if (!ws) return fail(DSV_ERR_WORKSPACE, "workspace is NULL");
-  if (reinterpret_cast<uintptr_t>(ws) % kAlign) return fail(DSV_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-  if (ws_bytes < need) return fail(DSV_ERR_WORKSPACE, "workspace of %zu bytes is below the %zu needed", ws_bytes, need);
+  if ((s = check_workspace(ws, ws_bytes, need)) != DSV_OK) return s;
   if ((s = check_spans(in, 4, out, 4)) != DSV_OK) return s;
   dsv::FfnParams p{};
   p.M = M;
@@ -1049,6 +1062,7 @@ dsv_status dsv_ffn_gated_bwd(const dsv_ffn_dims* dims, const void* dh, const voi
   p.dh = static_cast<const dsv::bf16*>(dh);
   p.dg = static_cast<dsv::bf16*>(ws);
   p.du = reinterpret_cast<dsv::bf16*>(static_cast<char*>(ws) + ffn_half_bytes(dims));
+  p.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * ffn_half_bytes(dims));
   p.dx = static_cast<dsv::bf16*>(dx);
   p.dw_gate = static_cast<dsv::bf16*>(dw_gate);
   p.dw_up = static_cast<dsv::bf16*>(dw_up);

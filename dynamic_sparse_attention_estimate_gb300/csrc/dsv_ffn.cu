@@ -41,8 +41,11 @@ struct Maps {
 
 struct Shape {
   int64_t m_tiles, n_tiles, tiles;
+  int64_t units;    // tiles, or tiles times the parts of K they are split into (unit = part * tiles + tile)
   int kb_half;      // k blocks of one operand pair (kDx has two pairs)
   int kb;           // k blocks of a tile
+  int kb_part;      // of a unit
+  float* partial;   // split: [unit][256][256] sums
   int64_t rows, cols;   // of the result (kDw: of one of the two results)
   int64_t half_tiles;   // kDw: m tiles of the first result
   int group;        // m tiles that share their n tiles' operands in L2
@@ -196,7 +199,7 @@ DSV_DEVICE void tile_of(const Shape& sh, int64_t t, int64_t& m, int64_t& n) {
   n = r / gm;
 }
 
-template <int MODE>
+template <int MODE, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* status) {
   using C = Cfg<MODE>;
@@ -232,6 +235,8 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
   __syncthreads();
   cluster_sync();   // the other CTAs' barriers exist
   tc::tc_fence_after();
+  // what follows in this call may start setting itself up; this kernel goes on when what came before is done
+  asm volatile("griddepcontrol.launch_dependents;\n griddepcontrol.wait;\n" ::: "memory");
   const uint32_t tmem = bars.tmem;
   volatile int* fail = &bars.fail;
 
@@ -244,14 +249,16 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
       Ring<C::kStages> at;
       int64_t issued = 0;   // stages
       bool ok = true;
-      for (int64_t t = first; t < sh.tiles && ok; t += step) {
+      for (int64_t t = first; t < sh.units && ok; t += step) {
         int64_t m, n;
-        tile_of(sh, t, m, n);
+        tile_of(sh, SPLIT ? t % sh.tiles : t, m, n);
         const bool second = MODE == kDw && m >= sh.half_tiles;
         const int m0 = static_cast<int>((second ? m - sh.half_tiles : m) * 256) + rank * 128;
         // B: the pair's second CTA holds the tile's second 128 columns (in the gated modes those of u)
         const int n0 = static_cast<int>(n * (kGated ? 128 : 256)) + (kGated ? 0 : rank * 128);
-        for (int kb = 0; kb < sh.kb; ++kb, ++issued, at.next()) {
+        const int kb0 = SPLIT ? static_cast<int>(t / sh.tiles) * sh.kb_part : 0;
+        const int kb1 = SPLIT && kb0 + sh.kb_part < sh.kb ? kb0 + sh.kb_part : sh.kb;
+        for (int kb = kb0; kb < kb1; ++kb, ++issued, at.next()) {
           // (a fresh barrier passes for the parity before its first round)
           if (!wait_bar(empty0 + 8 * at.s, at.round ^ 1, fail)) {
             ok = false;
@@ -310,19 +317,21 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
       Ring<C::kStages> at;
       int64_t tile = 0;
       bool ok = true;
-      for (int64_t t = first; t < sh.tiles && ok; t += step, ++tile) {
+      for (int64_t t = first; t < sh.units && ok; t += step, ++tile) {
         const int buf = static_cast<int>(tile & 1);
         if (tile >= 2) ok = wait_bar(bar(bars.acc_empty[buf]), static_cast<uint32_t>(((tile >> 1) - 1) & 1), fail);
         tc::tc_fence_after();
         const uint32_t acc = tmem + buf * 256;
-        for (int kb = 0; kb < sh.kb && ok; ++kb, at.next()) {
+        const int kb0 = SPLIT ? static_cast<int>(t / sh.tiles) * sh.kb_part : 0;
+        const int kb1 = SPLIT && kb0 + sh.kb_part < sh.kb ? kb0 + sh.kb_part : sh.kb;
+        for (int kb = kb0; kb < kb1 && ok; ++kb, at.next()) {
           const uint32_t s = at.s;
           ok = wait_bar(bar(bars.full[s]), at.round, fail);
           if (!ok) break;
           tc::tc_fence_after();
           const uint64_t da = a0 + s * (C::kStage >> 4), db = b0 + s * (C::kStage >> 4);
 #pragma unroll
-          for (int j = 0; j < kBK / 16; ++j) mma_pair(acc, da + j * kStepA, db + j * kStepB, id, kb > 0 || j > 0 ? 1u : 0u);
+          for (int j = 0; j < kBK / 16; ++j) mma_pair(acc, da + j * kStepA, db + j * kStepB, id, kb > kb0 || j > 0 ? 1u : 0u);
           commit_pair(bar(bars.empty[s]));
         }
         if (ok) commit_pair(bar(bars.acc_full[buf]));
@@ -352,16 +361,16 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
     int64_t tile = 0;
     uint32_t loads = 0;                                   // of dh, this warpgroup's
     bool ok = true;
-    for (int64_t t = first; t < sh.tiles && ok; t += step, ++tile) {
+    for (int64_t t = first; t < sh.units && ok; t += step, ++tile) {
       int64_t m, n;
-      tile_of(sh, t, m, n);
+      tile_of(sh, SPLIT ? t % sh.tiles : t, m, n);
       const CUtensorMap* c_map = MODE == kDw && m >= sh.half_tiles ? &maps.c1 : &maps.c0;
       if (MODE == kDw && m >= sh.half_tiles) m -= sh.half_tiles;
       const int m0 = static_cast<int>(m * 256) + rank * 128;
       const int n0 = static_cast<int>(n * (kGated ? 128 : 256) + wg * (kGated ? 64 : 128));
       const int buf = static_cast<int>(tile & 1);
       const bool mine = n0 < sh.cols && m0 < sh.rows;     // some of this part is inside the result
-      if (elect) {
+      if (!SPLIT && elect) {
         store_read_done();                                // the staging tiles are free again
         if (MODE == kGateGrad && mine) {
           expect_tx(bar(bars.dh_full[wg]), kTile);
@@ -369,7 +378,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
         }
       }
       ok = wait_bar(bar(bars.acc_full[buf]), static_cast<uint32_t>((tile >> 1) & 1), fail);
-      if (MODE == kGateGrad && mine) {
+      if (MODE == kGateGrad && !SPLIT && mine) {
         ok = wait_bar(bar(bars.dh_full[wg]), static_cast<uint32_t>(loads & 1), fail) && ok;
         ++loads;
       }
@@ -377,7 +386,23 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
       if (!ok) break;
       tc::tc_fence_after();
       const uint32_t acc = tmem + lane_base + buf * 256;
-      if constexpr (kGated) {
+      if constexpr (SPLIT) {
+        // a part of K: its sums as they are, joined with the others' by ffn_join_kernel
+        float4* to = reinterpret_cast<float4*>(sh.partial + ((t * 256 + rank * 128 + row) * 256 + wg * 128));
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 16) {
+          uint32_t a[16];
+          tc::tmem_ld16(acc + wg * 128 + c, a);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            to[c / 4 + i] = make_float4(__uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1]),
+                                        __uint_as_float(a[4 * i + 2]), __uint_as_float(a[4 * i + 3]));
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) release_acc(buf);
+      } else if constexpr (kGated) {
 #pragma unroll 1
         for (int c = 0; c < 64; c += 16) {
           uint32_t g[16], u[16], w0[8], w1[8];
@@ -457,7 +482,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
     }
     if (!ok) {
       *fail = 1;
-      if (MODE == kGateGrad && elect && loads > 0)        // a load of dh in flight lands first
+      if (MODE == kGateGrad && !SPLIT && elect && loads > 0)        // a load of dh in flight lands first
         tc::mbar_wait(bar(bars.dh_full[wg]), (loads - 1) & 1, kWaitLimit);
     }
     if (elect) store_done();
@@ -469,6 +494,133 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
   if (warp == 1) {
     tc::tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- parts of K joined
+struct JoinOut {
+  bf16 *c0, *c1;    // kGate h; kGateGrad dg, du; kDx dx; kDw dWg, dWu
+  const bf16* dh;   // kGateGrad
+};
+
+// 8 columns of a unit's row, summed over the parts in their order.
+DSV_DEVICE void join8(const Shape& sh, int64_t tile, int row, int col, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+#pragma unroll 4
+  for (int64_t u = tile; u < sh.units; u += sh.tiles) {
+    const float4* p = reinterpret_cast<const float4*>(sh.partial + ((u * 256 + row) * 256 + col));
+    const float4 a = p[0], b = p[1];
+    v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+    v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+  }
+}
+DSV_DEVICE void store8(bf16* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                            pack_bf16x2(v[6], v[7]));
+}
+
+// One thread: 8 columns of a row of the result (blockIdx.y: kDw's second result).
+template <int MODE>
+__global__ void __launch_bounds__(256) ffn_join_kernel(Shape sh, JoinOut o) {
+  constexpr bool kGated = MODE == kGate || MODE == kGateGrad;
+  asm volatile("griddepcontrol.launch_dependents;\n griddepcontrol.wait;\n" ::: "memory");
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t per_row = sh.cols / 8;
+  if (i >= sh.rows * per_row) return;
+  const int64_t r = i / per_row, col = i % per_row * 8;
+  const int64_t m = r / 256 + (MODE == kDw ? blockIdx.y * sh.half_tiles : 0), n = col / (kGated ? 128 : 256);
+  const int64_t g = m / sh.group, left = sh.m_tiles - g * sh.group, gm = left < sh.group ? left : sh.group;
+  const int64_t tile = g * sh.group * sh.n_tiles + n * gm + (m - g * sh.group);   // tile_of's inverse
+  const int row = static_cast<int>(r % 256), c = static_cast<int>(col % (kGated ? 128 : 256));
+  const int64_t at = r * sh.cols + col;
+  float v[8];
+  join8(sh, tile, row, c, v);
+  if constexpr (kGated) {
+    float u[8];
+    join8(sh, tile, row, 128 + c, u);
+    if constexpr (MODE == kGate) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = act_value(v[e], sh.act) * u[e];
+      store8(o.c0 + at, v);
+    } else {
+      const uint4 d4 = *reinterpret_cast<const uint4*>(o.dh + at);
+      const uint32_t d[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float a, slope;
+        act_both(v[e], sh.act, a, slope);
+        const float dh = e & 1 ? bf16_hi(d[e >> 1]) : bf16_lo(d[e >> 1]);
+        v[e] = dh * u[e] * slope;
+        u[e] = dh * a;
+      }
+      store8(o.c0 + at, v);
+      store8(o.c1 + at, u);
+    }
+  } else {
+    store8((MODE == kDw && blockIdx.y ? o.c1 : o.c0) + at, v);
+  }
+}
+
+// ---------------------------------------------------------------- a few tokens, forward
+DSV_DEVICE uint64_t as_u64(float2 v) { return *reinterpret_cast<uint64_t*>(&v); }
+DSV_DEVICE float2 fma2(float2 a, float2 b, float2 c) {   // two fp32 FMAs in one instruction
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+DSV_DEVICE float2 pair_of(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+
+// For a few tokens the weights' bytes are the work: `warps` warps take a row of Wg and the same of Wu, read
+// them once, 16 bytes a lane, and meet all tokens with them in registers.
+template <int R>
+__global__ void __launch_bounds__(256)
+ffn_rows_kernel(const uint4* __restrict__ x, const uint4* __restrict__ w_gate, const uint4* __restrict__ w_up,
+                bf16* __restrict__ h, int M, int64_t D, int64_t F, int warps, int act) {
+  __shared__ float2 red[8][R];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % warps;
+  const int64_t f = static_cast<int64_t>(blockIdx.x) * (8 / warps) + warp / warps, nv = D / 8;
+  float2 g[R], u[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) g[r] = u[r] = make_float2(0.f, 0.f);
+  if (f < F) {
+    // (one vector of each row at a time: batches of 2 and 4 cost more in resident warps than they put in flight)
+    for (int64_t v = part * 32 + lane; v < nv; v += 32 * warps) {
+      const uint4 a4 = __ldcs(w_gate + f * nv + v), b4 = __ldcs(w_up + f * nv + v);
+      uint4 x4[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) x4[r] = r < M ? __ldg(x + r * nv + v) : make_uint4(0, 0, 0, 0);
+      const float2 a[4] = {pair_of(a4.x), pair_of(a4.y), pair_of(a4.z), pair_of(a4.w)};
+      const float2 b[4] = {pair_of(b4.x), pair_of(b4.y), pair_of(b4.z), pair_of(b4.w)};
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float2 xs[4] = {pair_of(x4[r].x), pair_of(x4[r].y), pair_of(x4[r].z), pair_of(x4[r].w)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          g[r] = fma2(a[j], xs[j], g[r]);
+          u[r] = fma2(b[j], xs[j], u[r]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float2 s = make_float2(g[r].x + g[r].y, u[r].x + u[r].y);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+      s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+    }
+    if (lane == 0) red[warp][r] = s;
+  }
+  __syncthreads();
+  if (part == 0 && lane < R && lane < M && f < F) {   // the row's warps in their order
+    float2 s = red[warp][lane];
+    for (int w = 1; w < warps; ++w) {
+      s.x += red[warp + w][lane].x;
+      s.y += red[warp + w][lane].y;
+    }
+    h[lane * F + f] = __float2bfloat16_rn(act_value(s.x, act) * s.y);
   }
 }
 
@@ -498,92 +650,148 @@ bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-template <int MODE>
-cudaError_t launch_gemm(const char* name, const Maps& maps, Shape sh, unsigned int* status, cudaStream_t stream) {
-  using C = Cfg<MODE>;
+// Where ffn_rows_kernel runs instead of a tile of 256 rows: for one and two tokens, and up to four on weights of at
+// most 2^22 entries (its unpacking of the tokens grows with them).  Measured rows / tiles, L2 cold: 1 token
+// 2048 -> 5632 15 / 23 us, 4096 -> 8192 35 / 41 us; 4 tokens 1024 -> 2816 12 / 15 us, 4096 -> 512 11 / 29 us,
+// 2048 -> 5632 28 / 23 us.
+bool few_rows(int64_t M, int64_t D, int64_t F) { return M <= 2 || (M <= 4 && D * F <= (1 << 22)); }
+constexpr int kSplitSaves = 24;     // k blocks that splitting K has to save
+
+constexpr int64_t kPairs = 76;      // of CTAs, on the card's 152 SMs
+constexpr int kGroup = 16;          // m tiles that take the same n tiles in turn (their operands meet in L2)
+
+// How one product is cut: tiles, and where they leave at least half of the pairs without work, parts of K.
+// A part costs its sums' way to memory and back and a second launch, about 6 us or 24 k blocks, so K is
+// split where that many are saved, into parts of 8 k blocks or more.
+Shape shape_of(Mode mode, int64_t M, int64_t D, int64_t F, int act) {
+  const bool gated = mode == kGate || mode == kGateGrad;
+  Shape sh{};
+  sh.half_tiles = mode == kDw ? ceil_div(F, 256) : 0;
+  sh.m_tiles = mode == kDw ? 2 * sh.half_tiles : ceil_div(M, 256);
+  sh.n_tiles = gated ? ceil_div(F, 128) : ceil_div(D, 256);
   sh.tiles = sh.m_tiles * sh.n_tiles;
-  sh.group = 16;
-  auto kernel = ffn_gemm_kernel<MODE>;
+  sh.kb_half = mode == kDx ? static_cast<int>(ceil_div(F, kBK)) : 0;
+  sh.kb = gated ? static_cast<int>(ceil_div(D, kBK)) : mode == kDx ? 2 * sh.kb_half : static_cast<int>(ceil_div(M, kBK));
+  sh.rows = mode == kDw ? F : M;
+  sh.cols = gated ? F : D;
+  sh.group = kGroup;
+  sh.act = act;
+  int64_t parts = kPairs / sh.tiles;
+  if (parts > sh.kb / 8) parts = sh.kb / 8;
+  if (parts < 2 || sh.kb - sh.kb / parts < kSplitSaves) parts = 1;
+  sh.kb_part = static_cast<int>(ceil_div(sh.kb, parts));
+  parts = ceil_div(sh.kb, sh.kb_part);
+  sh.units = sh.tiles * parts;
+  return sh;
+}
+size_t partial_bytes(const Shape& sh) {
+  return sh.units > sh.tiles ? static_cast<size_t>(sh.units) * 256 * 256 * sizeof(float) : 0;
+}
+
+template <int MODE, bool SPLIT>
+cudaError_t launch_part(const char* name, const Maps& maps, const Shape& sh, bool first, unsigned int* status,
+                        cudaStream_t stream) {
+  using C = Cfg<MODE>;
+  auto kernel = ffn_gemm_kernel<MODE, SPLIT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  constexpr int64_t most = 76;   // pairs on the card's 152 SMs
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * (sh.tiles < most ? sh.tiles : most)));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (sh.units < kPairs ? sh.units : kPairs)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = first ? 1 : 2;   // a call's first kernel waits for the stream, the others for the one before them
   ProfScope prof(name, stream);
   return cudaLaunchKernelEx(&cfg, kernel, maps, sh, status);
 }
 
+template <int MODE>
+cudaError_t launch_gemm(const char* name, const Maps& maps, Shape sh, bool first, float* partial, const JoinOut& out,
+                        unsigned int* status, cudaStream_t stream) {
+  if (sh.units == sh.tiles) return launch_part<MODE, false>(name, maps, sh, first, status, stream);
+  sh.partial = partial;
+  cudaError_t e = launch_part<MODE, true>(name, maps, sh, first, status, stream);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(sh.rows * (sh.cols / 8), 256)), MODE == kDw ? 2 : 1);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  ProfScope prof("ffn_join", stream);
+  return cudaLaunchKernelEx(&cfg, ffn_join_kernel<MODE>, sh, out);
+}
+
+template <int R>
+cudaError_t launch_rows(const FfnParams& p, cudaStream_t stream) {
+  // warps to a row: as many as bring four CTAs to each SM, while each has 512 features to read
+  int warps = 1;
+  while (warps < 8 && p.F * warps / 8 < 4 * 152 && p.D >= 1024 * warps) warps *= 2;
+  ProfScope prof("ffn_rows", stream);
+  ffn_rows_kernel<R><<<static_cast<unsigned>(ceil_div(p.F * warps, 8)), 256, 0, stream>>>(
+      reinterpret_cast<const uint4*>(p.x), reinterpret_cast<const uint4*>(p.w_gate),
+      reinterpret_cast<const uint4*>(p.w_up), p.h, static_cast<int>(p.M), p.D, p.F, warps, p.act);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
+size_t ffn_fwd_workspace(int64_t M, int64_t D, int64_t F) {
+  return few_rows(M, D, F) ? 0 : partial_bytes(shape_of(kGate, M, D, F, 0));
+}
+
+size_t ffn_bwd_partial(int64_t M, int64_t D, int64_t F) {
+  size_t most = 0;
+  for (Mode mode : {kGateGrad, kDx, kDw}) {
+    const size_t b = partial_bytes(shape_of(mode, M, D, F, 0));
+    if (b > most) most = b;
+  }
+  return most;
+}
+
 cudaError_t launch_ffn_gated_fwd(const FfnParams& p, cudaStream_t stream) {
+  if (few_rows(p.M, p.D, p.F))
+    return p.M == 1 ? launch_rows<1>(p, stream) : p.M == 2 ? launch_rows<2>(p, stream) : launch_rows<4>(p, stream);
   Maps maps{};
   if (!make_map(&maps.a0, p.x, p.M, p.D, p.D, 128) || !make_map(&maps.b0, p.w_gate, p.F, p.D, p.D, 128) ||
       !make_map(&maps.b1, p.w_up, p.F, p.D, p.D, 128) || !make_map(&maps.c0, p.h, p.M, p.F, p.F, 128))
     return cudaErrorInvalidValue;
-  Shape sh{};
-  sh.m_tiles = ceil_div(p.M, 256);
-  sh.n_tiles = ceil_div(p.F, 128);
-  sh.kb = static_cast<int>(ceil_div(p.D, kBK));
-  sh.rows = p.M;
-  sh.cols = p.F;
-  sh.act = p.act;
-  return launch_gemm<kGate>("ffn_gate", maps, sh, p.status, stream);
+  return launch_gemm<kGate>("ffn_gate", maps, shape_of(kGate, p.M, p.D, p.F, p.act), true, p.partial,
+                            JoinOut{p.h, nullptr, nullptr}, p.status, stream);
 }
 
 cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream) {
-  cudaError_t e;
-  {
-    Maps maps{};
-    if (!make_map(&maps.a0, p.x, p.M, p.D, p.D, 128) || !make_map(&maps.b0, p.w_gate, p.F, p.D, p.D, 128) ||
-        !make_map(&maps.b1, p.w_up, p.F, p.D, p.D, 128) || !make_map(&maps.d, p.dh, p.M, p.F, p.F, 128) ||
-        !make_map(&maps.c0, p.dg, p.M, p.F, p.F, 128) || !make_map(&maps.c1, p.du, p.M, p.F, p.F, 128))
-      return cudaErrorInvalidValue;
-    Shape sh{};
-    sh.m_tiles = ceil_div(p.M, 256);
-    sh.n_tiles = ceil_div(p.F, 128);
-    sh.kb = static_cast<int>(ceil_div(p.D, kBK));
-    sh.rows = p.M;
-    sh.cols = p.F;
-    sh.act = p.act;
-    if ((e = launch_gemm<kGateGrad>("ffn_gate_grad", maps, sh, p.status, stream)) != cudaSuccess) return e;
-  }
-  {
-    Maps maps{};
-    if (!make_map(&maps.a0, p.dg, p.M, p.F, p.F, 128) || !make_map(&maps.a1, p.du, p.M, p.F, p.F, 128) ||
-        !make_map(&maps.b0, p.w_gate, p.F, p.D, p.D, 64) || !make_map(&maps.b1, p.w_up, p.F, p.D, p.D, 64) ||
-        !make_map(&maps.c0, p.dx, p.M, p.D, p.D, 128))
-      return cudaErrorInvalidValue;
-    Shape sh{};
-    sh.m_tiles = ceil_div(p.M, 256);
-    sh.n_tiles = ceil_div(p.D, 256);
-    sh.kb_half = static_cast<int>(ceil_div(p.F, kBK));
-    sh.kb = 2 * sh.kb_half;
-    sh.rows = p.M;
-    sh.cols = p.D;
-    if ((e = launch_gemm<kDx>("ffn_dx", maps, sh, p.status, stream)) != cudaSuccess) return e;
-  }
-  Maps maps{};
-  if (!make_map(&maps.a0, p.dg, p.M, p.F, p.F, 64) || !make_map(&maps.a1, p.du, p.M, p.F, p.F, 64) ||
-      !make_map(&maps.b0, p.x, p.M, p.D, p.D, 64) || !make_map(&maps.c0, p.dw_gate, p.F, p.D, p.D, 128) ||
-      !make_map(&maps.c1, p.dw_up, p.F, p.D, p.D, 128))
+  Maps grad{}, dx{}, dw{};
+  if (!make_map(&grad.a0, p.x, p.M, p.D, p.D, 128) || !make_map(&grad.b0, p.w_gate, p.F, p.D, p.D, 128) ||
+      !make_map(&grad.b1, p.w_up, p.F, p.D, p.D, 128) || !make_map(&grad.d, p.dh, p.M, p.F, p.F, 128) ||
+      !make_map(&grad.c0, p.dg, p.M, p.F, p.F, 128) || !make_map(&grad.c1, p.du, p.M, p.F, p.F, 128) ||
+      !make_map(&dx.a0, p.dg, p.M, p.F, p.F, 128) || !make_map(&dx.a1, p.du, p.M, p.F, p.F, 128) ||
+      !make_map(&dx.b0, p.w_gate, p.F, p.D, p.D, 64) || !make_map(&dx.b1, p.w_up, p.F, p.D, p.D, 64) ||
+      !make_map(&dx.c0, p.dx, p.M, p.D, p.D, 128) ||
+      !make_map(&dw.a0, p.dg, p.M, p.F, p.F, 64) || !make_map(&dw.a1, p.du, p.M, p.F, p.F, 64) ||
+      !make_map(&dw.b0, p.x, p.M, p.D, p.D, 64) || !make_map(&dw.c0, p.dw_gate, p.F, p.D, p.D, 128) ||
+      !make_map(&dw.c1, p.dw_up, p.F, p.D, p.D, 128))
     return cudaErrorInvalidValue;
-  Shape sh{};
-  sh.half_tiles = ceil_div(p.F, 256);
-  sh.m_tiles = 2 * sh.half_tiles;
-  sh.n_tiles = ceil_div(p.D, 256);
-  sh.kb = static_cast<int>(ceil_div(p.M, kBK));
-  sh.rows = p.F;
-  sh.cols = p.D;
-  return launch_gemm<kDw>("ffn_dw", maps, sh, p.status, stream);
+  cudaError_t e = launch_gemm<kGateGrad>("ffn_gate_grad", grad, shape_of(kGateGrad, p.M, p.D, p.F, p.act), true, p.partial,
+                                         JoinOut{p.dg, p.du, p.dh}, p.status, stream);
+  if (e == cudaSuccess)
+    e = launch_gemm<kDx>("ffn_dx", dx, shape_of(kDx, p.M, p.D, p.F, p.act), false, p.partial,
+                         JoinOut{p.dx, nullptr, nullptr},
+                         p.status, stream);
+  if (e == cudaSuccess)
+    e = launch_gemm<kDw>("ffn_dw", dw, shape_of(kDw, p.M, p.D, p.F, p.act), false, p.partial,
+                         JoinOut{p.dw_gate, p.dw_up, nullptr}, p.status, stream);
+  return e;
 }
 
 }  // namespace dsv

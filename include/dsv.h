@@ -428,12 +428,16 @@ typedef struct {
   int32_t act;   /* dsv_activation */
 } dsv_ffn_dims;
 
+/* Bytes of workspace dsv_ffn_gated_fwd needs: 0 but for few tiles of output with a long D, whose
+ * products are split over D (at most 20 MB of fp32 sums). */
+size_t dsv_ffn_gated_fwd_workspace(const dsv_ffn_dims* dims);
+/* ws: at least dsv_ffn_gated_fwd_workspace(dims) bytes, 256-byte aligned (NULL where that is 0); one
+ * workspace must not serve two calls that can run at the same time (so too in the backward). */
 dsv_status dsv_ffn_gated_fwd(const dsv_ffn_dims* dims, const void* x, const void* w_gate, const void* w_up, void* h,
-                             void* stream);
-/* Bytes of workspace dsv_ffn_gated_bwd needs (dg and du). */
+                             void* ws, size_t ws_bytes, void* stream);
+/* Bytes of workspace dsv_ffn_gated_bwd needs: dg and du (4 M F), and the sums of split products. */
 size_t dsv_ffn_gated_bwd_workspace(const dsv_ffn_dims* dims);
-/* ws: at least dsv_ffn_gated_bwd_workspace(dims) bytes, 256-byte aligned; one workspace must not
- * serve two calls that can run at the same time. */
+/* ws: at least dsv_ffn_gated_bwd_workspace(dims) bytes, 256-byte aligned. */
 dsv_status dsv_ffn_gated_bwd(const dsv_ffn_dims* dims, const void* dh, const void* x, const void* w_gate,
                              const void* w_up, void* dx, void* dw_gate, void* dw_up, void* ws, size_t ws_bytes,
                              void* stream);

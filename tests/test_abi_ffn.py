@@ -25,8 +25,8 @@ def no_gpu():
 A = [0x1000000 * i for i in range(1, 10)]
 
 
-def fwd(lib, d, x=A[0], wg=A[1], wu=A[2], h=A[3]):
-    return lib.dsv_ffn_gated_fwd(d, x, wg, wu, h, None)
+def fwd(lib, d, x=A[0], wg=A[1], wu=A[2], h=A[3], ws=None, nbytes=0):
+    return lib.dsv_ffn_gated_fwd(d, x, wg, wu, h, ws, nbytes, None)
 
 
 def bwd(lib, d, dh=A[0], x=A[1], wg=A[2], wu=A[3], dx=A[4], dwg=A[5], dwu=A[6], ws=A[7], nbytes=1 << 30):
@@ -41,8 +41,8 @@ def test_bad_dims(lib, M, D, F, act, what):
     d = FfnDims(M, D, F, act)
     assert fwd(lib, d) == INVALID and what in lib.dsv_last_error_message()
     assert bwd(lib, d) == INVALID and what in lib.dsv_last_error_message()
-    assert lib.dsv_ffn_gated_bwd_workspace(d) == 0
-    assert lib.dsv_ffn_gated_fwd(None, *A[:4], None) == INVALID
+    assert lib.dsv_ffn_gated_bwd_workspace(d) == lib.dsv_ffn_gated_fwd_workspace(d) == 0
+    assert lib.dsv_ffn_gated_fwd(None, *A[:4], None, 0, None) == INVALID
 
 
 def test_pointers_overlaps_and_workspace(lib):
@@ -62,6 +62,19 @@ def test_pointers_overlaps_and_workspace(lib):
     assert bwd(lib, d, ws=None) == WORKSPACE
     assert bwd(lib, d, ws=A[7] + 16) == WORKSPACE
     assert bwd(lib, d, nbytes=need - 1) == WORKSPACE
+
+
+def test_forward_workspace(lib):
+    """Only products that are split over D need one: few tiles, a long D, more than a few tokens."""
+    for M, D, F in ((16, 64, 128), (65536, 2048, 5632), (1, 4096, 512), (4, 4096, 512), (16384, 768, 2048)):
+        assert lib.dsv_ffn_gated_fwd_workspace(FfnDims(M, D, F, 0)) == 0
+    d = FfnDims(128, 4096, 512, 0)
+    need = lib.dsv_ffn_gated_fwd_workspace(d)
+    assert 0 < need <= 76 * 256 * 256 * 4
+    assert fwd(lib, d) == WORKSPACE and b"NULL" in lib.dsv_last_error_message()
+    assert fwd(lib, d, ws=A[4] + 16, nbytes=need) == WORKSPACE
+    assert fwd(lib, d, ws=A[4], nbytes=need - 1) == WORKSPACE
+    assert fwd(lib, d, ws=A[1], nbytes=need) == INVALID and b"ws overlaps w_gate" in lib.dsv_last_error_message()
 
 
 def test_python_refuses_cpu_tensors(lib):

@@ -17,7 +17,7 @@ import torch
 
 import oracle
 from dynamic_sparse_attention_estimate_gb300 import (DSVError, dsv_ffn_gated_bwd, dsv_ffn_gated_bwd_workspace,
-                                                     dsv_ffn_gated_fwd)
+                                                     dsv_ffn_gated_fwd, dsv_ffn_gated_fwd_workspace)
 from dynamic_sparse_attention_estimate_gb300.binding import dsv_last_device_status
 from tests.gpu_helpers import need_gpu, np64
 
@@ -76,8 +76,9 @@ def check_bwd(c, dx, dwg, dwu, act):
     check("dw_up", dwu, ru, 2.0 ** -8 * np.abs(ru) + Eu.T @ ax + acc(M, du.T @ ax))
 
 
-# one token, one feature group, sides around 64, 128 and 256 and their multiples, several tiles to a CTA
-SHAPES = [(1, 8, 8), (1, 64, 128), (2, 72, 136), (127, 64, 64), (128, 128, 128), (129, 136, 264), (300, 200, 120),
+# one token and a few (2, 3, 4, 5, 8), one feature group, sides around 64, 128 and 256 and their multiples, several
+# tiles to a pair of CTAs, products split over a long D, F or M (with a last part that is shorter)
+SHAPES = [(3, 1000, 104), (4, 264, 1000), (5, 1000, 104), (8, 264, 1000), (1, 4096, 24), (40, 4096, 264), (260, 3080, 136), (9000, 72, 88), (16, 136, 6200), (1, 8, 8), (1, 64, 128), (2, 72, 136), (127, 64, 64), (128, 128, 128), (129, 136, 264), (300, 200, 120),
           (64, 8, 2056), (257, 520, 16), (777, 776, 520), (1000, 1032, 248), (4000, 136, 2600), (9, 2048, 1000),
           (3, 40, 4104)]
 
@@ -110,17 +111,18 @@ def guarded(t, pad=4096):
     return view, buf, pad
 
 
-@pytest.mark.parametrize("M,D,F", [(1, 8, 8), (129, 136, 264), (300, 200, 120)])
+@pytest.mark.parametrize("M,D,F", [(1, 8, 8), (129, 136, 264), (300, 200, 120), (40, 4096, 264), (16, 136, 6200)])
 def test_nothing_around_the_outputs_is_written(M, D, F):
     need_gpu()
     c = case(M, D, F)
     g = {n: t.cuda() for n, t in c.items()}
     outs = [guarded(t) for t in (torch.empty(M, F, dtype=BF16), c["x"], c["wg"], c["wu"])]
-    dsv_ffn_gated_fwd(g["x"], g["wg"], g["wu"], out=outs[0][0])
+    fws, fbuf, fpad = guarded(torch.empty(dsv_ffn_gated_fwd_workspace(M, D, F) // 2, dtype=BF16))
+    dsv_ffn_gated_fwd(g["x"], g["wg"], g["wu"], out=outs[0][0], workspace=fws)
     ws, wbuf, wpad = guarded(torch.empty(dsv_ffn_gated_bwd_workspace(M, D, F) // 2, dtype=BF16))
     dsv_ffn_gated_bwd(g["dh"], g["x"], g["wg"], g["wu"], out=tuple(o[0] for o in outs[1:]), workspace=ws)
     torch.cuda.synchronize()
-    for view, buf, pad in outs + [(ws, wbuf, wpad)]:
+    for view, buf, pad in outs + [(ws, wbuf, wpad), (fws, fbuf, fpad)]:
         assert (buf[:pad] == -77).all() and (buf[pad + view.numel():] == -77).all()
     check_fwd(c, outs[0][0], "silu")
     check_bwd(c, outs[1][0], outs[2][0], outs[3][0], "silu")
