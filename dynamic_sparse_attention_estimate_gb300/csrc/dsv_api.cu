@@ -1025,18 +1025,16 @@ dsv_status dsv_ffn_gated_fwd(const dsv_ffn_dims* dims, const void* x, const void
   p.w_gate = static_cast<const dsv::bf16*>(w_gate);
   p.w_up = static_cast<const dsv::bf16*>(w_up);
   p.h = static_cast<dsv::bf16*>(h);
-  p.partial = static_cast<float*>(ws);
+  p.ws = ws;
   if ((s = status_word(&p.status)) != DSV_OK) return s;
   cudaError_t e = dsv::launch_ffn_gated_fwd(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(DSV_ERR_CUDA, "ffn forward launch: %s", cudaGetErrorString(e));
   return ok();
 }
 
-static size_t ffn_half_bytes(const dsv_ffn_dims* d) { return up(sizeof(uint16_t) * static_cast<size_t>(d->M) * d->F); }
-
 size_t dsv_ffn_gated_bwd_workspace(const dsv_ffn_dims* dims) {
   if (check_ffn(dims) != DSV_OK) return 0;
-  return 2 * ffn_half_bytes(dims) + up(dsv::ffn_bwd_partial(dims->M, dims->D, dims->F));
+  return up(dsv::ffn_bwd_workspace(dims->M, dims->D, dims->F));
 }
 
 dsv_status dsv_ffn_gated_bwd(const dsv_ffn_dims* dims, const void* dh, const void* x, const void* w_gate,
@@ -1060,9 +1058,7 @@ dsv_status dsv_ffn_gated_bwd(const dsv_ffn_dims* dims, const void* dh, const voi
   p.w_gate = static_cast<const dsv::bf16*>(w_gate);
   p.w_up = static_cast<const dsv::bf16*>(w_up);
   p.dh = static_cast<const dsv::bf16*>(dh);
-  p.dg = static_cast<dsv::bf16*>(ws);
-  p.du = reinterpret_cast<dsv::bf16*>(static_cast<char*>(ws) + ffn_half_bytes(dims));
-  p.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * ffn_half_bytes(dims));
+  p.ws = ws;
   p.dx = static_cast<dsv::bf16*>(dx);
   p.dw_gate = static_cast<dsv::bf16*>(dw_gate);
   p.dw_up = static_cast<dsv::bf16*>(dw_up);

@@ -18,6 +18,8 @@
 // loads).  Every wait is bounded.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "dsv_common.cuh"
 #include "dsv_internal.h"
 #include "dsv_tc.cuh"
@@ -510,7 +512,7 @@ DSV_DEVICE void join8(const Shape& sh, int64_t tile, int row, int col, float (&v
 #pragma unroll 4
   for (int64_t u = tile; u < sh.units; u += sh.tiles) {
     const float4* p = reinterpret_cast<const float4*>(sh.partial + ((u * 256 + row) * 256 + col));
-    const float4 a = p[0], b = p[1];
+    const float4 a = __ldcg(p), b = __ldcg(p + 1);   // (of the kernel before: past L1)
     v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
     v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
   }
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(256) ffn_join_kernel(Shape sh, JoinOut o) {
   }
 }
 
-// ---------------------------------------------------------------- a few tokens, forward
+// ---------------------------------------------------------------- a few tokens
 DSV_DEVICE uint64_t as_u64(float2 v) { return *reinterpret_cast<uint64_t*>(&v); }
 DSV_DEVICE float2 fma2(float2 a, float2 b, float2 c) {   // two fp32 FMAs in one instruction
   uint64_t d;
@@ -573,10 +575,13 @@ DSV_DEVICE float2 pair_of(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w
 
 // For a few tokens the weights' bytes are the work: `warps` warps take a row of Wg and the same of Wu, read
 // them once, 16 bytes a lane, and meet all tokens with them in registers.
-template <int R>
+// GRAD: dg and du (fp32) from dh in place of h.
+template <int R, bool GRAD>
 __global__ void __launch_bounds__(256)
 ffn_rows_kernel(const uint4* __restrict__ x, const uint4* __restrict__ w_gate, const uint4* __restrict__ w_up,
-                bf16* __restrict__ h, int M, int64_t D, int64_t F, int warps, int act) {
+                bf16* __restrict__ h, const bf16* __restrict__ dh, float* __restrict__ dg, float* __restrict__ du,
+                int M, int64_t D, int64_t F, int warps, int act) {
+  if (GRAD) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   __shared__ float2 red[8][R];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % warps;
   const int64_t f = static_cast<int64_t>(blockIdx.x) * (8 / warps) + warp / warps, nv = D / 8;
@@ -620,7 +625,112 @@ ffn_rows_kernel(const uint4* __restrict__ x, const uint4* __restrict__ w_gate, c
       s.x += red[warp + w][lane].x;
       s.y += red[warp + w][lane].y;
     }
-    h[lane * F + f] = __float2bfloat16_rn(act_value(s.x, act) * s.y);
+    if constexpr (GRAD) {
+      float a, slope;
+      act_both(s.x, act, a, slope);
+      const float d = __bfloat162float(dh[lane * F + f]);
+      dg[lane * F + f] = d * s.y * slope;
+      du[lane * F + f] = d * a;
+    } else {
+      h[lane * F + f] = __float2bfloat16_rn(act_value(s.x, act) * s.y);
+    }
+  }
+}
+
+// The backward's two products for a few tokens, the weights read and their gradients written once: a lane owns 8
+// columns of D, a warp takes every eighth row f of the CTA's chunk of F and adds dg Wg + du Wu to its part of dx
+// while it writes dWg[f] = sum_r dg x and dWu[f].  dg and du stay fp32 here (of one or two tokens' rounding to
+// bf16 little averages out).  partial: [chunk][token][D].
+template <int R>
+__global__ void __launch_bounds__(256, R == 4 ? 2 : 0)
+ffn_rows_back_kernel(const uint4* __restrict__ x, const uint4* __restrict__ w_gate, const uint4* __restrict__ w_up,
+                     const float* dg, const float* du, uint4* __restrict__ dw_gate,
+                     uint4* __restrict__ dw_up, float* __restrict__ partial, int M, int64_t D, int64_t F,
+                     int64_t chunk) {
+  asm volatile("griddepcontrol.launch_dependents;\n griddepcontrol.wait;\n" ::: "memory");
+  __shared__ float2 red[8][R][4][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t nv = D / 8, v = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const int64_t f0 = blockIdx.y * chunk, f1 = f0 + chunk < F ? f0 + chunk : F;
+  const bool on = v < nv;
+  float2 xs[R][4], acc[R][4];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const uint4 t = on && r < M ? __ldg(x + r * nv + v) : make_uint4(0, 0, 0, 0);
+    xs[r][0] = pair_of(t.x), xs[r][1] = pair_of(t.y), xs[r][2] = pair_of(t.z), xs[r][3] = pair_of(t.w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[r][j] = make_float2(0.f, 0.f);
+  }
+#pragma unroll 2
+  for (int64_t f = f0 + warp; f < f1; f += 8) {
+    const uint4 a4 = on ? __ldcs(w_gate + f * nv + v) : make_uint4(0, 0, 0, 0);
+    const uint4 b4 = on ? __ldcs(w_up + f * nv + v) : make_uint4(0, 0, 0, 0);
+    const float2 a[4] = {pair_of(a4.x), pair_of(a4.y), pair_of(a4.z), pair_of(a4.w)};
+    const float2 b[4] = {pair_of(b4.x), pair_of(b4.y), pair_of(b4.z), pair_of(b4.w)};
+    float2 wa[4], wb[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) wa[j] = wb[j] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r >= M) continue;
+      const float g = __ldcg(dg + r * F + f), u = __ldcg(du + r * F + f);   // (of the kernel before: past L1)
+      const float2 g2 = make_float2(g, g), u2 = make_float2(u, u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[r][j] = fma2(u2, b[j], fma2(g2, a[j], acc[r][j]));
+        wa[j] = fma2(g2, xs[r][j], wa[j]);
+        wb[j] = fma2(u2, xs[r][j], wb[j]);
+      }
+    }
+    if (on) {
+      dw_gate[f * nv + v] = make_uint4(pack_bf16x2(wa[0].x, wa[0].y), pack_bf16x2(wa[1].x, wa[1].y),
+                                       pack_bf16x2(wa[2].x, wa[2].y), pack_bf16x2(wa[3].x, wa[3].y));
+      dw_up[f * nv + v] = make_uint4(pack_bf16x2(wb[0].x, wb[0].y), pack_bf16x2(wb[1].x, wb[1].y),
+                                     pack_bf16x2(wb[2].x, wb[2].y), pack_bf16x2(wb[3].x, wb[3].y));
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) red[warp][r][j][lane] = acc[r][j];
+  __syncthreads();
+  // warp w: pair j = w % 4 of tokens w / 4, w / 4 + 2, .. summed over the warps in their order
+  for (int r = warp >> 2; r < M; r += 2) {
+    const int j = warp & 3;
+    float2 s = red[0][r][j][lane];
+    for (int w = 1; w < 8; ++w) {
+      s.x += red[w][r][j][lane].x;
+      s.y += red[w][r][j][lane].y;
+    }
+    if (on)
+      *reinterpret_cast<float2*>(partial + (static_cast<int64_t>(blockIdx.y) * M + r) * D + v * 8 + 2 * j) = s;
+  }
+}
+
+// dx = the chunks' sums: 32 pairs of columns to a CTA, each warp takes every eighth chunk, then the warps in order.
+__global__ void __launch_bounds__(256)
+ffn_rows_join_kernel(const float2* partial, uint32_t* __restrict__ dx, int64_t pairs, int chunks) {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  __shared__ float2 red[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  float2 s = make_float2(0.f, 0.f);
+  if (i < pairs) {
+#pragma unroll 4
+    for (int c = warp; c < chunks; c += 8) {
+      const float2 p = __ldcg(partial + c * pairs + i);
+      s.x += p.x;
+      s.y += p.y;
+    }
+  }
+  red[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && i < pairs) {
+    for (int w = 1; w < 8; ++w) {
+      s.x += red[w][lane].x;
+      s.y += red[w][lane].y;
+    }
+    dx[i] = pack_bf16x2(s.x, s.y);
   }
 }
 
@@ -650,10 +760,10 @@ bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Where ffn_rows_kernel runs instead of a tile of 256 rows: for one and two tokens, and up to four on weights of at
+// Where the rows kernels run instead of tiles of 256 rows: for one and two tokens, and up to four on weights of at
 // most 2^22 entries (its unpacking of the tokens grows with them).  Measured rows / tiles, L2 cold: 1 token
 // 2048 -> 5632 15 / 23 us, 4096 -> 8192 35 / 41 us; 4 tokens 1024 -> 2816 12 / 15 us, 4096 -> 512 11 / 29 us,
-// 2048 -> 5632 28 / 23 us.
+// 2048 -> 5632 28 / 23 us; backward of 1 token 1024 -> 2816 32 / 56 us, of 4 54 / 55 us, of 4 4096 -> 8192 251 / 134 us.
 bool few_rows(int64_t M, int64_t D, int64_t F) { return M <= 2 || (M <= 4 && D * F <= (1 << 22)); }
 constexpr int kSplitSaves = 24;     // k blocks that splitting K has to save
 
@@ -688,6 +798,21 @@ size_t partial_bytes(const Shape& sh) {
   return sh.units > sh.tiles ? static_cast<size_t>(sh.units) * 256 * 256 * sizeof(float) : 0;
 }
 
+// A kernel that may set itself up while the one before it on the stream ends.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 template <int MODE, bool SPLIT>
 cudaError_t launch_part(const char* name, const Maps& maps, const Shape& sh, bool first, unsigned int* status,
                         cudaStream_t stream) {
@@ -719,30 +844,72 @@ cudaError_t launch_gemm(const char* name, const Maps& maps, Shape sh, bool first
   sh.partial = partial;
   cudaError_t e = launch_part<MODE, true>(name, maps, sh, first, status, stream);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(sh.rows * (sh.cols / 8), 256)), MODE == kDw ? 2 : 1);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   ProfScope prof("ffn_join", stream);
-  return cudaLaunchKernelEx(&cfg, ffn_join_kernel<MODE>, sh, out);
+  return launch_after(ffn_join_kernel<MODE>,
+                      dim3(static_cast<unsigned>(ceil_div(sh.rows * (sh.cols / 8), 256)), MODE == kDw ? 2 : 1), stream, sh,
+                      out);
 }
 
-template <int R>
-cudaError_t launch_rows(const FfnParams& p, cudaStream_t stream) {
+template <int R, bool GRAD>
+cudaError_t launch_rows(const FfnParams& p, float* dg, float* du, cudaStream_t stream) {
   // warps to a row: as many as bring four CTAs to each SM, while each has 512 features to read
   int warps = 1;
   while (warps < 8 && p.F * warps / 8 < 4 * 152 && p.D >= 1024 * warps) warps *= 2;
-  ProfScope prof("ffn_rows", stream);
-  ffn_rows_kernel<R><<<static_cast<unsigned>(ceil_div(p.F * warps, 8)), 256, 0, stream>>>(
+  ProfScope prof(GRAD ? "ffn_rows_grad" : "ffn_rows", stream);
+  ffn_rows_kernel<R, GRAD><<<static_cast<unsigned>(ceil_div(p.F * warps, 8)), 256, 0, stream>>>(
       reinterpret_cast<const uint4*>(p.x), reinterpret_cast<const uint4*>(p.w_gate),
-      reinterpret_cast<const uint4*>(p.w_up), p.h, static_cast<int>(p.M), p.D, p.F, warps, p.act);
+      reinterpret_cast<const uint4*>(p.w_up), p.h, p.dh, dg, du, static_cast<int>(p.M), p.D, p.F, warps, p.act);
   return cudaGetLastError();
 }
+
+// The few tokens' backward: workspace of dg, du (fp32 [M][F] each), then the chunks' parts of dx.
+struct RowsBack {
+  int64_t chunk, chunks;   // rows of F to a CTA; CTAs along F
+  size_t dg_bytes, total;
+};
+RowsBack rows_back(int64_t M, int64_t D, int64_t F) {
+  RowsBack b;
+  const int64_t d_tiles = ceil_div(D, 256);
+  b.chunk = 8 * ceil_div(F, 8 * ceil_div(4 * 152, d_tiles));   // about four CTAs to each SM, whole turns of 8 warps
+  if (b.chunk < 32) b.chunk = 32;
+  b.chunks = ceil_div(F, b.chunk);
+  b.dg_bytes = (sizeof(float) * static_cast<size_t>(M) * F + 255) / 256 * 256;
+  b.total = 2 * b.dg_bytes + sizeof(float) * static_cast<size_t>(b.chunks) * M * D;
+  return b;
+}
+
+template <int R>
+cudaError_t launch_rows_back(const FfnParams& p, cudaStream_t stream) {
+  const RowsBack b = rows_back(p.M, p.D, p.F);
+  char* ws = static_cast<char*>(p.ws);
+  float *dg = reinterpret_cast<float*>(ws), *du = reinterpret_cast<float*>(ws + b.dg_bytes);
+  float* partial = reinterpret_cast<float*>(ws + 2 * b.dg_bytes);
+  cudaError_t e = launch_rows<R, true>(p, dg, du, stream);
+  if (e != cudaSuccess) return e;
+  {
+    ProfScope prof("ffn_rows_back", stream);
+    e = launch_after(ffn_rows_back_kernel<R>,
+                     dim3(static_cast<unsigned>(ceil_div(p.D, 256)), static_cast<unsigned>(b.chunks)), stream,
+                     reinterpret_cast<const uint4*>(p.x), reinterpret_cast<const uint4*>(p.w_gate),
+                     reinterpret_cast<const uint4*>(p.w_up), dg, du, reinterpret_cast<uint4*>(p.dw_gate),
+                     reinterpret_cast<uint4*>(p.dw_up), partial, static_cast<int>(p.M), p.D, p.F, b.chunk);
+    if (e != cudaSuccess) return e;
+  }
+  ProfScope prof("ffn_rows_join", stream);
+  const int64_t pairs = p.M * p.D / 2;
+  return launch_after(ffn_rows_join_kernel, dim3(static_cast<unsigned>(ceil_div(pairs, 32))), stream,
+                      reinterpret_cast<const float2*>(partial), reinterpret_cast<uint32_t*>(p.dx), pairs,
+                      static_cast<int>(b.chunks));
+}
+
+template <class F>
+cudaError_t by_rows(int64_t M, F&& go) {
+  return M == 1 ? go(std::integral_constant<int, 1>()) : M == 2 ? go(std::integral_constant<int, 2>())
+                                                                : go(std::integral_constant<int, 4>());
+}
+
+// dg and du of the tiles' backward, bf16 [M][F] each at the front of its workspace.
+size_t half_bytes(int64_t M, int64_t F) { return (sizeof(bf16) * static_cast<size_t>(M) * F + 255) / 256 * 256; }
 
 }  // namespace
 
@@ -750,46 +917,52 @@ size_t ffn_fwd_workspace(int64_t M, int64_t D, int64_t F) {
   return few_rows(M, D, F) ? 0 : partial_bytes(shape_of(kGate, M, D, F, 0));
 }
 
-size_t ffn_bwd_partial(int64_t M, int64_t D, int64_t F) {
+size_t ffn_bwd_workspace(int64_t M, int64_t D, int64_t F) {
+  if (few_rows(M, D, F)) return rows_back(M, D, F).total;
   size_t most = 0;
   for (Mode mode : {kGateGrad, kDx, kDw}) {
     const size_t b = partial_bytes(shape_of(mode, M, D, F, 0));
     if (b > most) most = b;
   }
-  return most;
+  return 2 * half_bytes(M, F) + most;
 }
 
 cudaError_t launch_ffn_gated_fwd(const FfnParams& p, cudaStream_t stream) {
   if (few_rows(p.M, p.D, p.F))
-    return p.M == 1 ? launch_rows<1>(p, stream) : p.M == 2 ? launch_rows<2>(p, stream) : launch_rows<4>(p, stream);
+    return by_rows(p.M, [&](auto r) { return launch_rows<decltype(r)::value, false>(p, nullptr, nullptr, stream); });
   Maps maps{};
   if (!make_map(&maps.a0, p.x, p.M, p.D, p.D, 128) || !make_map(&maps.b0, p.w_gate, p.F, p.D, p.D, 128) ||
       !make_map(&maps.b1, p.w_up, p.F, p.D, p.D, 128) || !make_map(&maps.c0, p.h, p.M, p.F, p.F, 128))
     return cudaErrorInvalidValue;
-  return launch_gemm<kGate>("ffn_gate", maps, shape_of(kGate, p.M, p.D, p.F, p.act), true, p.partial,
-                            JoinOut{p.h, nullptr, nullptr}, p.status, stream);
+  return launch_gemm<kGate>("ffn_gate", maps, shape_of(kGate, p.M, p.D, p.F, p.act), true,
+                            static_cast<float*>(p.ws), JoinOut{p.h, nullptr, nullptr}, p.status, stream);
 }
 
 cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream) {
+  if (few_rows(p.M, p.D, p.F))
+    return by_rows(p.M, [&](auto r) { return launch_rows_back<decltype(r)::value>(p, stream); });
+  char* ws = static_cast<char*>(p.ws);
+  bf16 *dg = reinterpret_cast<bf16*>(ws), *du = reinterpret_cast<bf16*>(ws + half_bytes(p.M, p.F));
+  float* partial = reinterpret_cast<float*>(ws + 2 * half_bytes(p.M, p.F));
   Maps grad{}, dx{}, dw{};
   if (!make_map(&grad.a0, p.x, p.M, p.D, p.D, 128) || !make_map(&grad.b0, p.w_gate, p.F, p.D, p.D, 128) ||
       !make_map(&grad.b1, p.w_up, p.F, p.D, p.D, 128) || !make_map(&grad.d, p.dh, p.M, p.F, p.F, 128) ||
-      !make_map(&grad.c0, p.dg, p.M, p.F, p.F, 128) || !make_map(&grad.c1, p.du, p.M, p.F, p.F, 128) ||
-      !make_map(&dx.a0, p.dg, p.M, p.F, p.F, 128) || !make_map(&dx.a1, p.du, p.M, p.F, p.F, 128) ||
+      !make_map(&grad.c0, dg, p.M, p.F, p.F, 128) || !make_map(&grad.c1, du, p.M, p.F, p.F, 128) ||
+      !make_map(&dx.a0, dg, p.M, p.F, p.F, 128) || !make_map(&dx.a1, du, p.M, p.F, p.F, 128) ||
       !make_map(&dx.b0, p.w_gate, p.F, p.D, p.D, 64) || !make_map(&dx.b1, p.w_up, p.F, p.D, p.D, 64) ||
       !make_map(&dx.c0, p.dx, p.M, p.D, p.D, 128) ||
-      !make_map(&dw.a0, p.dg, p.M, p.F, p.F, 64) || !make_map(&dw.a1, p.du, p.M, p.F, p.F, 64) ||
+      !make_map(&dw.a0, dg, p.M, p.F, p.F, 64) || !make_map(&dw.a1, du, p.M, p.F, p.F, 64) ||
       !make_map(&dw.b0, p.x, p.M, p.D, p.D, 64) || !make_map(&dw.c0, p.dw_gate, p.F, p.D, p.D, 128) ||
       !make_map(&dw.c1, p.dw_up, p.F, p.D, p.D, 128))
     return cudaErrorInvalidValue;
-  cudaError_t e = launch_gemm<kGateGrad>("ffn_gate_grad", grad, shape_of(kGateGrad, p.M, p.D, p.F, p.act), true, p.partial,
-                                         JoinOut{p.dg, p.du, p.dh}, p.status, stream);
+  cudaError_t e = launch_gemm<kGateGrad>("ffn_gate_grad", grad, shape_of(kGateGrad, p.M, p.D, p.F, p.act), true, partial,
+                                         JoinOut{dg, du, p.dh}, p.status, stream);
   if (e == cudaSuccess)
-    e = launch_gemm<kDx>("ffn_dx", dx, shape_of(kDx, p.M, p.D, p.F, p.act), false, p.partial,
+    e = launch_gemm<kDx>("ffn_dx", dx, shape_of(kDx, p.M, p.D, p.F, p.act), false, partial,
                          JoinOut{p.dx, nullptr, nullptr},
                          p.status, stream);
   if (e == cudaSuccess)
-    e = launch_gemm<kDw>("ffn_dw", dw, shape_of(kDw, p.M, p.D, p.F, p.act), false, p.partial,
+    e = launch_gemm<kDw>("ffn_dw", dw, shape_of(kDw, p.M, p.D, p.F, p.act), false, partial,
                          JoinOut{p.dw_gate, p.dw_up, nullptr}, p.status, stream);
   return e;
 }

@@ -185,14 +185,12 @@ struct FfnParams {
   const bf16 *x, *w_gate, *w_up;        // [M][D], [F][D], [F][D]
   bf16* h;                              // [M][F] (forward)
   const bf16* dh;                       // [M][F] (backward)
-  bf16 *dg, *du;                        // [M][F] each: the backward's workspace
   bf16 *dx, *dw_gate, *dw_up;           // [M][D], [F][D], [F][D] (backward)
-  float* partial;                       // workspace of the sums of split products (ffn_*_workspace)
+  void* ws;                             // ffn_fwd_workspace / ffn_bwd_workspace bytes
   unsigned int* status;
 };
-// Bytes of partial sums: of the forward, and (the most that one of its products needs) of the backward.
 size_t ffn_fwd_workspace(int64_t M, int64_t D, int64_t F);
-size_t ffn_bwd_partial(int64_t M, int64_t D, int64_t F);
+size_t ffn_bwd_workspace(int64_t M, int64_t D, int64_t F);
 cudaError_t launch_ffn_gated_fwd(const FfnParams& p, cudaStream_t stream);
 cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream);
 

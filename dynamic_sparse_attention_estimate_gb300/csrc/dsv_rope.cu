@@ -405,7 +405,7 @@ qk_norm_rope_bwd_kernel(RopeGeom g, RopeView dqo, RopeView dko, RopeView dvo, Ro
 // every 32nd row each, then the 32 sums in warp order.
 constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(32 * kSumWarps)
-qk_norm_colsum_kernel(const float* __restrict__ partial, int rows, int D, float* __restrict__ dwq,
+qk_norm_colsum_kernel(const float* partial, int rows, int D, float* __restrict__ dwq,
                       float* __restrict__ dwk) {
   __shared__ float red[kSumWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -413,7 +413,7 @@ qk_norm_colsum_kernel(const float* __restrict__ partial, int rows, int D, float*
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   float s0 = 0.f;
 #pragma unroll 8
-  for (int r = warp; r < rows; r += kSumWarps) s0 += partial[static_cast<int64_t>(r) * 2 * D + col];
+  for (int r = warp; r < rows; r += kSumWarps) s0 += __ldcg(partial + static_cast<int64_t>(r) * 2 * D + col);
   red[warp][lane] = s0;
   __syncthreads();
   if (warp == 0) {

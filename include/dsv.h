@@ -415,7 +415,7 @@ dsv_status dsv_qk_norm_rope_bwd(const dsv_rope_dims* dims, const void* d_q_out, 
  * Layouts (contiguous, 16-byte aligned device memory): x, dx bf16 [M][D]; w_gate, w_up, dw_gate,
  * dw_up bf16 [F][D]; h, dh bf16 [M][F].  M is the token count (samples and tokens flattened).
  * Products accumulate in fp32; h and the gradients are rounded to bf16 once, and dg, du once
- * between the backward's kernels.  Bitwise reproducible.  Outputs must not overlap inputs.
+ * between the backward's kernels (for a few tokens they stay fp32).  Bitwise reproducible.  Outputs must not overlap inputs.
  * Validation before any launch: M, D, F >= 1; D and F multiples of 8; M < 2^31 - 256, D and F <=
  * 2^20; act as above; no NULL, misaligned or overlapping pointer.
  */
@@ -435,7 +435,8 @@ size_t dsv_ffn_gated_fwd_workspace(const dsv_ffn_dims* dims);
  * workspace must not serve two calls that can run at the same time (so too in the backward). */
 dsv_status dsv_ffn_gated_fwd(const dsv_ffn_dims* dims, const void* x, const void* w_gate, const void* w_up, void* h,
                              void* ws, size_t ws_bytes, void* stream);
-/* Bytes of workspace dsv_ffn_gated_bwd needs: dg and du (4 M F), and the sums of split products. */
+/* Bytes of workspace dsv_ffn_gated_bwd needs: dg and du (4 M F), and the sums of split products (a few
+ * tokens: dg and du in fp32, and parts of dx). */
 size_t dsv_ffn_gated_bwd_workspace(const dsv_ffn_dims* dims);
 /* ws: at least dsv_ffn_gated_bwd_workspace(dims) bytes, 256-byte aligned. */
 dsv_status dsv_ffn_gated_bwd(const dsv_ffn_dims* dims, const void* dh, const void* x, const void* w_gate,
