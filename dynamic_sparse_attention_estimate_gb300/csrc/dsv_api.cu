@@ -775,6 +775,32 @@ static dsv_status check_view(const dsv_rope_dims* d, const char* name, const voi
 }
 static bool apart(const ViewSpan& a, const ViewSpan& b) { return a.hi <= b.lo || b.hi <= a.lo; }
 
+// Whether delta = i st[0] + j st[1] + .. + t has a solution with every |i| < n of its stride and |t| < d, strides
+// falling and each past what the smaller ones span (so that only two i of each stride come into question).
+static bool reaches(int64_t delta, const int64_t* st, const int64_t* n, int dims, int64_t d) {
+  if (dims == 0) return delta > -d && delta < d;
+  if (n[0] == 1) return reaches(delta, st + 1, n + 1, dims - 1, d);
+  int64_t i = delta / st[0];
+  if (delta < 0 && delta % st[0]) --i;
+  for (int64_t c = i; c <= i + 1; ++c)
+    if (c > -n[0] && c < n[0] && reaches(delta - c * st[0], st + 1, n + 1, dims - 1, d)) return true;
+  return false;
+}
+// Two outputs that share no element: apart, or interleaved views of one layout.
+static bool distinct(const dsv_rope_dims* d, const dsv::RopeView& a, const ViewSpan& as, const dsv::RopeView& b,
+                     const ViewSpan& bs) {
+  if (apart(as, bs)) return true;
+  if (a.sb != b.sb || a.sh != b.sh || a.sn != b.sn) return false;
+  int64_t st[3] = {a.sb, a.sh, a.sn}, n[3] = {d->B, d->H, d->N};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (st[j] < st[j + 1]) {
+        std::swap(st[j], st[j + 1]);
+        std::swap(n[j], n[j + 1]);
+      }
+  return !reaches((bs.lo - as.lo) / 2, st, n, 3, d->d);
+}
+
 static dsv_status check_rope_tables(const dsv::RopeGeom& g, const int32_t* pos, const float* table) {
   if (!g.pairs) return DSV_OK;
   DSV_NEED_PTR(pos);
@@ -926,8 +952,9 @@ dsv_status dsv_qk_norm_rope_bwd(const dsv_rope_dims* dims, const void* d_q_out, 
   for (int j = 0; j < nt; ++j) {
     for (int i = 0; i < ni; ++i)
       if (!apart(is[i], os[j])) return fail(DSV_ERR_INVALID_ARG, "%s overlaps %s", out_name[j], in_name[i]);
-    for (int i = 0; i < j; ++i)   // packed outputs interleave; the same base cannot
-      if (out[i] == out[j]) return fail(DSV_ERR_INVALID_ARG, "%s and %s are the same tensor", out_name[i], out_name[j]);
+    for (int i = 0; i < j; ++i)   // the views of a packed gradient interleave
+      if (!distinct(dims, *ov[i], os[i], *ov[j], os[j]))
+        return fail(DSV_ERR_INVALID_ARG, "%s overlaps %s", out_name[j], out_name[i]);
   }
   if (wq) DSV_NEED_PTR(wq);
   if (wk) DSV_NEED_PTR(wk);

@@ -135,8 +135,50 @@ def test_backward_arguments(lib):
     assert bwd(lib, d, ws=None) == WORKSPACE
     assert bwd(lib, d, ws=0x5000010) == WORKSPACE
     assert bwd(lib, d, nbytes=need - 1) == WORKSPACE
-    assert bwd(lib, d, dk=Y) == INVALID and b"same tensor" in lib.dsv_last_error_message()
+    assert bwd(lib, d, dk=Y) == INVALID and b"dk overlaps dq" in lib.dsv_last_error_message()
     assert bwd(lib, d, dq=X) == INVALID and b"overlaps" in lib.dsv_last_error_message()
+
+
+def test_interleaved_outputs(lib):
+    """The three views of a packed [B][N][3][H][d] gradient share a range but no element; shifted ones do."""
+    d = dims()
+    B, H, N, f = d.B, d.H, d.N, d.d
+    packed = (ctypes.c_int64 * 9)(*(N * 3 * H * f, f, 3 * H * f) * 3)
+    at = lambda i: Y + 2 * i * H * f
+    # what follows the last check needs a device: the call gets there (no INVALID), or is refused for what is tested
+    assert bwd(lib, d, ds=packed, dq=at(0), dk=at(1), dv=at(2)) not in (INVALID, WORKSPACE)
+    assert bwd(lib, d, ds=packed, dq=at(2), dk=at(0), dv=at(1)) not in (INVALID, WORKSPACE)
+    for k in (at(1) - 2 * f, at(0) + 16, at(1) + 2 * f, at(0) + 2 * 3 * H * f, at(3)):
+        assert bwd(lib, d, ds=packed, dq=at(0), dk=k, dv=at(2)) == INVALID and b"overlaps" in lib.dsv_last_error_message()
+    other = (ctypes.c_int64 * 9)(*(N * 3 * H * f, f, 3 * H * f), *(N * H * f, f, H * f), *(N * 3 * H * f, f, 3 * H * f))
+    assert bwd(lib, d, ds=other, dq=at(0), dk=at(1), dv=at(2)) == INVALID
+
+
+def test_overlapping_outputs_against_their_elements(lib):
+    """Whether two outputs of one layout share an element, as the call sees it and by listing the elements."""
+    import itertools
+    import random
+    rng = random.Random(4)
+    seen = {True: 0, False: 0}
+    for _ in range(300):
+        B, H, N = (rng.randint(1, 3) for _ in range(3))
+        d = dims(B=B, H=H, N=N, rot=(0, 0, 0))
+        sizes, strides, extent = {"b": B, "h": H, "n": N}, {}, 64
+        for a in rng.sample("bhn", 3):
+            strides[a] = extent + 8 * rng.randint(0, 24)
+            extent = strides[a] * (sizes[a] - 1) + extent
+        shift = 8 * rng.randint(-40, 40)
+        rows = [b * strides["b"] + h * strides["h"] + n * strides["n"]
+                for b, h, n in itertools.product(range(B), range(H), range(N))]
+        shared = bool({r + 8 * c for r in rows for c in range(8)} & {r + shift + 8 * c for r in rows for c in range(8)})
+        view = (strides["b"], strides["h"], strides["n"])
+        ds = (ctypes.c_int64 * 9)(*view * 3)
+        far = 0x20000000
+        status = bwd(lib, d, pos=None, tab=None, ds=ds, dq=Y, dk=Y + 2 * shift, dv=far, dq_out=far + 0x1000000,
+                     dk_out=far + 0x2000000, dv_out=far + 0x3000000, q=far + 0x4000000, k=far + 0x5000000)
+        assert (status == INVALID) == shared, (B, H, N, view, shift)
+        seen[shared] += 1
+    assert min(seen.values()) > 30
 
 
 def test_python_refusals_without_a_gpu(lib):
