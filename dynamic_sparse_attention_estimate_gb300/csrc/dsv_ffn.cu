@@ -34,11 +34,12 @@ constexpr uint32_t kWaitLimit = 1u << 20;   // polls, each suspended in the hard
 // forward calls at the card's power limit runs at 1.68 PFLOP/s without and 1.73 with it.
 constexpr uint32_t kWaitNs = 2000;
 constexpr int kTile = 128 * 128;           // bytes of a [128 rows][64] or two [64 rows][64] bf16 tiles
+constexpr int kPart = 128 * 64;            // bytes of a [128 rows][32] bf16 tile: what one TMA store writes
 
 enum Mode { kGate = 0, kGateGrad = 1, kDx = 2, kDw = 3 };
 
 struct Maps {
-  CUtensorMap a0, a1, b0, b1, c0, c1, d;   // operands A and B, results C, dh
+  CUtensorMap a0, a1, b0, b1, c0, c1;   // operands A and B, results C
 };
 
 struct Shape {
@@ -48,6 +49,7 @@ struct Shape {
   int kb;           // k blocks of a tile
   int kb_part;      // of a unit
   float* partial;   // split: [unit][256][256] sums
+  const bf16* dh;   // kGateGrad
   int64_t rows, cols;   // of the result (kDw: of one of the two results)
   int64_t half_tiles;   // kDw: m tiles of the first result
   int group;        // m tiles that share their n tiles' operands in L2
@@ -59,7 +61,8 @@ struct Cfg {
   static constexpr int kStageA = kTile;
   static constexpr int kStageB = kTile;
   static constexpr int kStage = kStageA + kStageB;
-  static constexpr int kOut = (MODE == kGateGrad ? 2 : 1) * 2 * kTile;   // staging of two warpgroups
+  static constexpr int kResults = MODE == kGateGrad ? 2 : 1;
+  static constexpr int kOut = 2 * 2 * kResults * kPart;   // staging: two warpgroups, two parts of each result
   static constexpr int kStages = (227 * 1024 - 2048 - kOut) / kStage;
   static constexpr int kSmem = kStages * kStage + kOut + 1024;
 };
@@ -67,7 +70,6 @@ struct Cfg {
 struct Bars {
   uint64_t full[8], empty[8];
   uint64_t acc_full[2], acc_empty[2];
-  uint64_t dh_full[2];
   uint64_t drain;
   uint32_t tmem;
   int fail;
@@ -108,14 +110,7 @@ DSV_DEVICE uint32_t map_rank(uint32_t addr, uint32_t rank) {
 DSV_DEVICE void expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
 }
-DSV_DEVICE void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::
-          "r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-// The same into this CTA's shared memory, counted on a barrier of either CTA of the pair.
+// A box of a matrix into this CTA's shared memory, counted on a barrier of either CTA of the pair.
 DSV_DEVICE void tma_load_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t cluster_bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
@@ -127,9 +122,10 @@ DSV_DEVICE void tma_store(const CUtensorMap* map, int x, int y, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(map), "r"(x),
                "r"(y), "r"(src)
                : "memory");
-  asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
 }
-DSV_DEVICE void store_read_done() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+DSV_DEVICE void stores_commit() { asm volatile("cp.async.bulk.commit_group;\n" ::: "memory"); }
+// Waits until all groups of stores but the last one have read their tiles.
+DSV_DEVICE void stores_read_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;\n" ::: "memory"); }
 DSV_DEVICE void store_done() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
 DSV_DEVICE void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
 // A barrier whose threads agree: true where all of them came with true.
@@ -152,8 +148,10 @@ DSV_DEVICE uint32_t cluster_rank() {
 DSV_DEVICE void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;\n" ::: "memory");
 }
+// (What this arrival orders are reads of tensor memory, which the tcgen05 fences around it cover.  A release at
+// cluster scope would also wait for the thread's stores: 34,070 x 360 x 3312 forward 175 us with it, 155 without.)
 DSV_DEVICE void arrive_cluster(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_bar) : "memory");
 }
 DSV_DEVICE void tmem_alloc_pair(uint32_t dst, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(dst), "r"(cols));
@@ -224,7 +222,6 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(bar(bars.acc_full[b]), 1);
       tc::mbar_init(bar(bars.acc_empty[b]), 16);
-      tc::mbar_init(bar(bars.dh_full[b]), 1);
     }
     tc::mbar_init(bar(bars.drain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -350,18 +347,20 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
     const int row = (warp & 3) * 32 + lane;               // of the tile (TMEM lane)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const bool elect = (tid & 127) == 0;
-    const uint32_t st0 = out + wg * (C::kOut / 2), st1 = st0 + kTile;
-    auto put = [&](uint32_t tile, int c, const uint32_t (&w)[8]) {   // 16 columns from c of this row
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(tile + tc::sw128(row, c)), "r"(w[0]), "r"(w[1]),
-                   "r"(w[2]), "r"(w[3]));
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(tile + tc::sw128(row, c + 8)), "r"(w[4]), "r"(w[5]),
-                   "r"(w[6]), "r"(w[7]));
+    const uint32_t stage = out + wg * (C::kOut / 2);
+    // 16 columns from c (0 or 16) of this row into a [128 rows][32] tile, 64-byte rows, swizzled: 16-byte chunk k of
+    // row r sits at chunk k ^ (r / 2 % 4), so the 8 rows of a quarter warp fill all banks
+    auto put = [&](uint32_t tile, int c, const uint32_t (&w)[8]) {
+      const uint32_t base = tile + row * 64, turn = (row >> 1) & 3;
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(base + (((c / 8 + q) ^ turn) << 4)), "r"(w[4 * q]),
+                     "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3]));
     };
     auto release_acc = [&](int buf) {   // to the thread that issues the MMAs
       arrive_cluster(map_rank(bar(bars.acc_empty[buf]), 0));
     };
     int64_t tile = 0;
-    uint32_t loads = 0;                                   // of dh, this warpgroup's
     bool ok = true;
     for (int64_t t = first; t < sh.units && ok; t += step, ++tile) {
       int64_t m, n;
@@ -371,19 +370,17 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
       const int m0 = static_cast<int>(m * 256) + rank * 128;
       const int n0 = static_cast<int>(n * (kGated ? 128 : 256) + wg * (kGated ? 64 : 128));
       const int buf = static_cast<int>(tile & 1);
-      const bool mine = n0 < sh.cols && m0 < sh.rows;     // some of this part is inside the result
-      if (!SPLIT && elect) {
-        store_read_done();                                // the staging tiles are free again
-        if (MODE == kGateGrad && mine) {
-          expect_tx(bar(bars.dh_full[wg]), kTile);
-          tma_load(st0, &maps.d, n0, m0, bar(bars.dh_full[wg]));
-        }
+      // this row's 64 values of dh, on their way while the products end (through a TMA load into the staging tile, which
+      // has to be free first, 16,384 x 2048 x 5632 took 462 us instead of 445)
+      uint4 dh[MODE == kGateGrad && !SPLIT ? 8 : 1];
+      if constexpr (MODE == kGateGrad && !SPLIT) {
+        const bool in = m0 + row < sh.rows;
+        const bf16* p = sh.dh + (m0 + row) * sh.cols + n0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          dh[i] = in && n0 + 8 * i < sh.cols ? __ldg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
       }
       ok = wait_bar(bar(bars.acc_full[buf]), static_cast<uint32_t>((tile >> 1) & 1), fail);
-      if (MODE == kGateGrad && !SPLIT && mine) {
-        ok = wait_bar(bar(bars.dh_full[wg]), static_cast<uint32_t>(loads & 1), fail) && ok;
-        ++loads;
-      }
       ok = bar_all(1 + wg, 128, ok);                      // the warpgroup goes on together, or not at all
       if (!ok) break;
       tc::tc_fence_after();
@@ -404,89 +401,76 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) release_acc(buf);
-      } else if constexpr (kGated) {
-#pragma unroll 1
-        for (int c = 0; c < 64; c += 16) {
-          uint32_t g[16], u[16], w0[8], w1[8];
-          tc::tmem_ld16(acc + wg * 64 + c, g);
-          tc::tmem_ld16(acc + 128 + wg * 64 + c, u);
-          tc::tmem_wait_ld();
-          if constexpr (MODE == kGate) {
+      } else {
+        // 32 columns at a time through two staging tiles in turn: one is read by its store while the other fills (four
+        // warpgroups with one tile each win where D is short, 16,384 x 128 x 1024 20 us instead of 23, and lose
+        // elsewhere, 16,384 x 768 x 2048 67 instead of 64)
+        constexpr int kParts = kGated ? 2 : 4;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              w0[i] = pack_bf16x2(act_value(__uint_as_float(g[2 * i]), sh.act) * __uint_as_float(u[2 * i]),
-                                  act_value(__uint_as_float(g[2 * i + 1]), sh.act) * __uint_as_float(u[2 * i + 1]));
-            put(st0, c, w0);
-          } else {
-            uint32_t dh[8];
+        for (int part = 0; part < kParts; ++part) {
+          const uint32_t st0 = stage + (part & 1) * (C::kResults * kPart), st1 = st0 + kPart;
+          if (elect) stores_read_but_one();               // (a group to a part, empty ones too)
+          bar_sync(1 + wg, 128);
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
-                           : "=r"(dh[4 * q]), "=r"(dh[4 * q + 1]), "=r"(dh[4 * q + 2]), "=r"(dh[4 * q + 3])
-                           : "r"(st0 + tc::sw128(row, c + 8 * q)));
+          for (int c = 0; c < 32; c += 16) {
+            const int col = part * 32 + c;
+            uint32_t w0[8];
+            if constexpr (kGated) {
+              uint32_t g[16], u[16], w1[8];
+              tc::tmem_ld16(acc + wg * 64 + col, g);
+              tc::tmem_ld16(acc + 128 + wg * 64 + col, u);
+              tc::tmem_wait_ld();
+              if constexpr (MODE == kGate) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float dg[2], du[2];
+                for (int i = 0; i < 8; ++i)
+                  w0[i] = pack_bf16x2(act_value(__uint_as_float(g[2 * i]), sh.act) * __uint_as_float(u[2 * i]),
+                                      act_value(__uint_as_float(g[2 * i + 1]), sh.act) * __uint_as_float(u[2 * i + 1]));
+              } else {
+                const uint4 d0 = dh[col / 8], d1 = dh[col / 8 + 1];
+                const uint32_t d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float a, slope;
-                act_both(__uint_as_float(g[2 * i + e]), sh.act, a, slope);
-                const float d = e ? bf16_hi(dh[i]) : bf16_lo(dh[i]);
-                dg[e] = d * __uint_as_float(u[2 * i + e]) * slope;
-                du[e] = d * a;
+                for (int i = 0; i < 8; ++i) {
+                  float dg[2], du[2];
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    float a, slope;
+                    act_both(__uint_as_float(g[2 * i + e]), sh.act, a, slope);
+                    const float v = e ? bf16_hi(d[i]) : bf16_lo(d[i]);
+                    dg[e] = v * __uint_as_float(u[2 * i + e]) * slope;
+                    du[e] = v * a;
+                  }
+                  w0[i] = pack_bf16x2(dg[0], dg[1]);
+                  w1[i] = pack_bf16x2(du[0], du[1]);
+                }
+                put(st1, c, w1);
               }
-              w0[i] = pack_bf16x2(dg[0], dg[1]);
-              w1[i] = pack_bf16x2(du[0], du[1]);
+            } else {
+              uint32_t a[16];
+              tc::tmem_ld16(acc + wg * 128 + col, a);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w0[i] = pack_bf16x2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
             }
             put(st0, c, w0);
-            put(st1, c, w1);
           }
-        }
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) release_acc(buf);
-        tc::fence_async_shared();
-        bar_sync(1 + wg, 128);
-        if (elect && mine) {
-          tma_store(c_map, n0, m0, st0);
-          if (MODE == kGateGrad) tma_store(&maps.c1, n0, m0, st1);
-        }
-      } else {
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (half == 1) {
-            if (elect) store_read_done();
-            bar_sync(1 + wg, 128);
-          }
-#pragma unroll 1
-          for (int c = 0; c < 64; c += 32) {
-            uint32_t a[16], b[16], w[8];
-            tc::tmem_ld16(acc + wg * 128 + half * 64 + c, a);
-            tc::tmem_ld16(acc + wg * 128 + half * 64 + c + 16, b);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
-            put(st0, c, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
-            put(st0, c + 16, w);
-          }
-          if (half == 1) {
+          if (part == kParts - 1) {
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) release_acc(buf);
           }
           tc::fence_async_shared();
           bar_sync(1 + wg, 128);
-          if (elect && m0 < sh.rows && n0 + half * 64 < sh.cols) tma_store(c_map, n0 + half * 64, m0, st0);
+          if (elect) {
+            if (m0 < sh.rows && n0 + part * 32 < sh.cols) {
+              tma_store(c_map, n0 + part * 32, m0, st0);
+              if (MODE == kGateGrad) tma_store(&maps.c1, n0 + part * 32, m0, st1);
+            }
+            stores_commit();
+          }
         }
       }
     }
-    if (!ok) {
-      *fail = 1;
-      if (MODE == kGateGrad && !SPLIT && elect && loads > 0)        // a load of dh in flight lands first
-        tc::mbar_wait(bar(bars.dh_full[wg]), (loads - 1) & 1, kWaitLimit);
-    }
+    if (!ok) *fail = 1;
     if (elect) store_done();
   }
   tc::tc_fence_before();
@@ -502,7 +486,6 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
 // ---------------------------------------------------------------- parts of K joined
 struct JoinOut {
   bf16 *c0, *c1;    // kGate h; kGateGrad dg, du; kDx dx; kDw dWg, dWu
-  const bf16* dh;   // kGateGrad
 };
 
 // 8 columns of a unit's row, summed over the parts in their order.
@@ -546,7 +529,7 @@ __global__ void __launch_bounds__(256) ffn_join_kernel(Shape sh, JoinOut o) {
       for (int e = 0; e < 8; ++e) v[e] = act_value(v[e], sh.act) * u[e];
       store8(o.c0 + at, v);
     } else {
-      const uint4 d4 = *reinterpret_cast<const uint4*>(o.dh + at);
+      const uint4 d4 = *reinterpret_cast<const uint4*>(sh.dh + at);
       const uint32_t d[4] = {d4.x, d4.y, d4.z, d4.w};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -735,8 +718,9 @@ ffn_rows_join_kernel(const float2* partial, uint32_t* __restrict__ dx, int64_t p
 }
 
 // ---------------------------------------------------------------- host
-// A [rows][cols] row-major bf16 matrix seen through boxes of box_rows x 64 columns (128 bytes, swizzled).
-bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t pitch, int box_rows) {
+// A [rows][cols] row-major bf16 matrix seen through swizzled boxes of box_rows x box_cols (64: 128-byte rows,
+// operands; 32: 64-byte rows, results).
+bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int box_rows, int box_cols = 64) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -750,11 +734,11 @@ bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64
   }();
   if (!encode) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t step[2] = {1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, step,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -931,11 +915,11 @@ cudaError_t launch_ffn_gated_fwd(const FfnParams& p, cudaStream_t stream) {
   if (few_rows(p.M, p.D, p.F))
     return by_rows(p.M, [&](auto r) { return launch_rows<decltype(r)::value, false>(p, nullptr, nullptr, stream); });
   Maps maps{};
-  if (!make_map(&maps.a0, p.x, p.M, p.D, p.D, 128) || !make_map(&maps.b0, p.w_gate, p.F, p.D, p.D, 128) ||
-      !make_map(&maps.b1, p.w_up, p.F, p.D, p.D, 128) || !make_map(&maps.c0, p.h, p.M, p.F, p.F, 128))
+  if (!make_map(&maps.a0, p.x, p.M, p.D, 128) || !make_map(&maps.b0, p.w_gate, p.F, p.D, 128) ||
+      !make_map(&maps.b1, p.w_up, p.F, p.D, 128) || !make_map(&maps.c0, p.h, p.M, p.F, 128, 32))
     return cudaErrorInvalidValue;
   return launch_gemm<kGate>("ffn_gate", maps, shape_of(kGate, p.M, p.D, p.F, p.act), true,
-                            static_cast<float*>(p.ws), JoinOut{p.h, nullptr, nullptr}, p.status, stream);
+                            static_cast<float*>(p.ws), JoinOut{p.h, nullptr}, p.status, stream);
 }
 
 cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream) {
@@ -945,25 +929,27 @@ cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream) {
   bf16 *dg = reinterpret_cast<bf16*>(ws), *du = reinterpret_cast<bf16*>(ws + half_bytes(p.M, p.F));
   float* partial = reinterpret_cast<float*>(ws + 2 * half_bytes(p.M, p.F));
   Maps grad{}, dx{}, dw{};
-  if (!make_map(&grad.a0, p.x, p.M, p.D, p.D, 128) || !make_map(&grad.b0, p.w_gate, p.F, p.D, p.D, 128) ||
-      !make_map(&grad.b1, p.w_up, p.F, p.D, p.D, 128) || !make_map(&grad.d, p.dh, p.M, p.F, p.F, 128) ||
-      !make_map(&grad.c0, dg, p.M, p.F, p.F, 128) || !make_map(&grad.c1, du, p.M, p.F, p.F, 128) ||
-      !make_map(&dx.a0, dg, p.M, p.F, p.F, 128) || !make_map(&dx.a1, du, p.M, p.F, p.F, 128) ||
-      !make_map(&dx.b0, p.w_gate, p.F, p.D, p.D, 64) || !make_map(&dx.b1, p.w_up, p.F, p.D, p.D, 64) ||
-      !make_map(&dx.c0, p.dx, p.M, p.D, p.D, 128) ||
-      !make_map(&dw.a0, dg, p.M, p.F, p.F, 64) || !make_map(&dw.a1, du, p.M, p.F, p.F, 64) ||
-      !make_map(&dw.b0, p.x, p.M, p.D, p.D, 64) || !make_map(&dw.c0, p.dw_gate, p.F, p.D, p.D, 128) ||
-      !make_map(&dw.c1, p.dw_up, p.F, p.D, p.D, 128))
+  if (!make_map(&grad.a0, p.x, p.M, p.D, 128) || !make_map(&grad.b0, p.w_gate, p.F, p.D, 128) ||
+      !make_map(&grad.b1, p.w_up, p.F, p.D, 128) ||
+      !make_map(&grad.c0, dg, p.M, p.F, 128, 32) || !make_map(&grad.c1, du, p.M, p.F, 128, 32) ||
+      !make_map(&dx.a0, dg, p.M, p.F, 128) || !make_map(&dx.a1, du, p.M, p.F, 128) ||
+      !make_map(&dx.b0, p.w_gate, p.F, p.D, 64) || !make_map(&dx.b1, p.w_up, p.F, p.D, 64) ||
+      !make_map(&dx.c0, p.dx, p.M, p.D, 128, 32) ||
+      !make_map(&dw.a0, dg, p.M, p.F, 64) || !make_map(&dw.a1, du, p.M, p.F, 64) ||
+      !make_map(&dw.b0, p.x, p.M, p.D, 64) || !make_map(&dw.c0, p.dw_gate, p.F, p.D, 128, 32) ||
+      !make_map(&dw.c1, p.dw_up, p.F, p.D, 128, 32))
     return cudaErrorInvalidValue;
-  cudaError_t e = launch_gemm<kGateGrad>("ffn_gate_grad", grad, shape_of(kGateGrad, p.M, p.D, p.F, p.act), true, partial,
-                                         JoinOut{dg, du, p.dh}, p.status, stream);
+  Shape grad_shape = shape_of(kGateGrad, p.M, p.D, p.F, p.act);
+  grad_shape.dh = p.dh;
+  cudaError_t e = launch_gemm<kGateGrad>("ffn_gate_grad", grad, grad_shape, true, partial, JoinOut{dg, du}, p.status,
+                                         stream);
   if (e == cudaSuccess)
     e = launch_gemm<kDx>("ffn_dx", dx, shape_of(kDx, p.M, p.D, p.F, p.act), false, partial,
-                         JoinOut{p.dx, nullptr, nullptr},
+                         JoinOut{p.dx, nullptr},
                          p.status, stream);
   if (e == cudaSuccess)
     e = launch_gemm<kDw>("ffn_dw", dw, shape_of(kDw, p.M, p.D, p.F, p.act), false, partial,
-                         JoinOut{p.dw_gate, p.dw_up, nullptr}, p.status, stream);
+                         JoinOut{p.dw_gate, p.dw_up}, p.status, stream);
   return e;
 }
 
