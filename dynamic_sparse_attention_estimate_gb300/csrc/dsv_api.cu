@@ -700,7 +700,8 @@ static dsv_status check_rope(const dsv_rope_dims* d, dsv::RopeGeom* g) {
   if (!d) return fail(DSV_ERR_INVALID_ARG, "dims is NULL");
   constexpr int64_t kMax = 0x7fffffffLL;
   if (d->B < 1 || d->H < 1 || d->N < 1) return fail(DSV_ERR_INVALID_ARG, "B, H, N must be >= 1");
-  if (d->B > kMax || d->H > kMax || d->N > kMax || d->B * d->H > kMax || d->B * d->H * d->N > kMax)
+  // (64 short of 2^31: a tile's tokens are counted past the last one in 32 bits)
+  if (d->B > kMax || d->H > kMax || d->N > kMax || d->B * d->H > kMax || d->B * d->H * d->N > kMax - 64)
     return fail(DSV_ERR_INVALID_ARG, "B*H*N must fit int32 row coordinates (split the heads over calls)");
   if (d->d != 64 && d->d != 128)
     return fail(DSV_ERR_UNSUPPORTED, "head dim d must be 64 or 128 (got %lld)", (long long)d->d);
@@ -912,7 +913,7 @@ dsv_status dsv_qk_norm_rope_fwd(const dsv_rope_dims* dims, const void* q, const 
 }
 
 static size_t qk_norm_rope_ws(const dsv::RopeGeom& g, const dsv_rope_dims* d) {
-  const dsv::RopeGeom plan = dsv::rope_plan(g, static_cast<int>(d->d));
+  const dsv::RopeGeom plan = dsv::rope_plan(g, static_cast<int>(d->d), true);
   const int64_t rows = dsv::rope_bwd_ctas(plan);
   return up(static_cast<size_t>(rows) * 2 * d->d * sizeof(float));
 }

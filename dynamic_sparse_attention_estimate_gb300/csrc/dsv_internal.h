@@ -171,7 +171,7 @@ struct RopeParams {
   unsigned int* status;
 };
 constexpr int64_t kRopeWantCtas = 8 * 152;   // CTAs below which the heads of a token are split
-RopeGeom rope_plan(const RopeGeom& in, int d);
+RopeGeom rope_plan(const RopeGeom& in, int d, bool backward);
 int64_t rope_bwd_ctas(const RopeGeom& plan);
 cudaError_t launch_rope3d_table(const RopeGeom& g, const double (&theta)[3], float* table, cudaStream_t stream);
 cudaError_t launch_rope3d(const RopeParams& p, cudaStream_t stream);

@@ -25,6 +25,7 @@ namespace dsv {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr double kBackSetup = 1.5;
 constexpr int kBackCtas = 4;   // of the backward, on an SM (128 registers; 5 spill and take 389 us where 4 take 354)
 
 DSV_DEVICE uint32_t word(const uint4& u, int j) { return j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w; }
@@ -63,12 +64,23 @@ struct Turn {
   int turned;   // pairs of this vector that are rotated
 };
 
+struct Pos {
+  int v[3];
+};
+DSV_DEVICE Pos load_pos(const RopeGeom& g, const int32_t* __restrict__ pos, int64_t row, bool active) {
+  Pos p{{0, 0, 0}};
+  if (active && g.pairs) {
+#pragma unroll
+    for (int a = 0; a < 3; ++a) p.v[a] = __ldg(pos + row * 3 + a);
+  }
+  return p;
+}
+
 // sign: +1 forward, -1 backward.  An axis whose position is outside its table leaves its pairs
 // unrotated (angle 0) and sets the status bit.
 template <bool HALF>
-DSV_DEVICE void load_turn(Turn<HALF>& t, const RopeGeom& g, const float2* __restrict__ table,
-                          const int32_t* __restrict__ pos, int64_t row, bool active, int vec, float sign,
-                          unsigned int* status) {
+DSV_DEVICE void make_turn(Turn<HALF>& t, const RopeGeom& g, const float2* __restrict__ table, const Pos& pos,
+                          bool active, int vec, float sign, unsigned int* status) {
   const int half_vecs = g.pairs / 8;   // HALF: vectors of a half (pairs is a multiple of 8)
   int j0;
   if (HALF) {
@@ -90,7 +102,7 @@ DSV_DEVICE void load_turn(Turn<HALF>& t, const RopeGeom& g, const float2* __rest
   int p[3];
 #pragma unroll
   for (int a = 0; a < 3; ++a) {
-    p[a] = __ldg(pos + row * 3 + a);
+    p[a] = pos.v[a];
     if (g.axis_pairs[a] > 0 && static_cast<uint32_t>(p[a]) >= static_cast<uint32_t>(g.len[a])) {
       flag_status(status, kStatusBadPosition);
       p[a] = -1;
@@ -140,37 +152,34 @@ DSV_DEVICE int partner_lane(const RopeGeom& g, int lane, int vec) {
   return (lane & ~(LPR - 1)) | p;
 }
 
+// What a group of LPR lanes works on: a token and a chunk of its heads.  (Samples, heads and tokens fit 32 bits.)
 struct Lane {
-  int lane, vec;
-  int64_t b, n, row;   // sample, token, row of pos
-  int64_t h0, h1;
+  int b, n, h0, h1;
   bool active;
 };
 
-// blockIdx.x: token tile of a sample; blockIdx.y: head chunk
 template <int LPR>
 DSV_DEVICE Lane lane_of(const RopeGeom& g, int64_t unit) {
-  Lane l;
-  l.lane = threadIdx.x & 31;
-  l.vec = threadIdx.x & (LPR - 1);
   constexpr int kTok = kThreads / LPR;
-  const int64_t chunk = unit % g.chunks, tile = unit / g.chunks;
-  l.b = tile / g.tiles_per_b;
-  l.n = (tile % g.tiles_per_b) * kTok + threadIdx.x / LPR;
+  const int tile = static_cast<int>(unit / g.chunks), chunk = static_cast<int>(unit - tile * g.chunks);
+  const int tiles = static_cast<int>(g.tiles_per_b), per = static_cast<int>(g.heads_per_chunk);
+  Lane l;
+  l.b = tile / tiles;
+  l.n = (tile - l.b * tiles) * kTok + threadIdx.x / LPR;
   l.active = l.n < g.N;
-  l.row = l.b * g.pos_batch + l.n;
-  l.h0 = chunk * g.heads_per_chunk;
-  l.h1 = l.h0 + g.heads_per_chunk < g.H ? l.h0 + g.heads_per_chunk : g.H;
+  l.h0 = chunk * per;
+  l.h1 = l.h0 + per < g.H ? l.h0 + per : static_cast<int>(g.H);
   return l;
 }
+DSV_DEVICE int64_t pos_row(const RopeGeom& g, const Lane& l) { return l.b * g.pos_batch + l.n; }
 
+DSV_DEVICE uint4 load_row(const bf16* p) { return *reinterpret_cast<const uint4*>(p); }
 // U rows of a view, heads h .. h + U - 1 of this group's token (zeros past its heads).
 template <int U>
-DSV_DEVICE void load_rows(uint4 (&v)[U], const bf16* p, int64_t stride, int64_t h, const Lane& l) {
+DSV_DEVICE void load_rows(uint4 (&v)[U], const bf16* p, int64_t stride, int h, const Lane& l) {
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    v[u] = l.active && h + u < l.h1 ? *reinterpret_cast<const uint4*>(p + (h + u) * stride)
-                                    : make_uint4(0, 0, 0, 0);
+    v[u] = l.active && h + u < l.h1 ? load_row(p + (h + u) * stride) : make_uint4(0, 0, 0, 0);
 }
 DSV_DEVICE void store_row(bf16* p, const uint4& v) { *reinterpret_cast<uint4*>(p) = v; }
 
@@ -181,14 +190,15 @@ rope3d_kernel(RopeGeom g, RopeView x, RopeView y, const int32_t* __restrict__ po
               float sign, unsigned int* status) {
   constexpr int LPR = D / 8;
   const Lane l = lane_of<LPR>(g, blockIdx.x);
-  const bf16* xp = x.p + l.b * x.sb + l.n * x.sn + l.vec * 8;
-  bf16* yp = y.p + l.b * y.sb + l.n * y.sn + l.vec * 8;
+  const int vec = threadIdx.x & (LPR - 1);
+  const bf16* xp = x.p + l.b * x.sb + l.n * x.sn + vec * 8;
+  bf16* yp = y.p + l.b * y.sb + l.n * y.sn + vec * 8;
   uint4 next[U];
   load_rows<U>(next, xp, x.sh, l.h0, l);   // on their way while the table is read
   Turn<HALF> t;
-  load_turn<HALF>(t, g, table, pos, l.row, l.active, l.vec, sign, status);
-  const int partner = HALF ? partner_lane<LPR>(g, l.lane, l.vec) : 0;
-  for (int64_t h = l.h0; h < l.h1; h += U) {
+  make_turn<HALF>(t, g, table, load_pos(g, pos, pos_row(g, l), l.active), l.active, vec, sign, status);
+  const int partner = HALF ? partner_lane<LPR>(g, threadIdx.x & 31, vec) : 0;
+  for (int h = l.h0; h < l.h1; h += U) {
     uint4 v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) v[u] = next[u];
@@ -243,30 +253,31 @@ qk_norm_rope_fwd_kernel(RopeGeom g, RopeView q, RopeView k, RopeView v, RopeView
                         const float2* __restrict__ table, float eps, unsigned int* status) {
   constexpr int LPR = D / 8;
   const Lane l = lane_of<LPR>(g, blockIdx.x);
+  const int vec = threadIdx.x & (LPR - 1);
   const bool has_v = v.p != nullptr;
-  const bf16* qp = q.p + l.b * q.sb + l.n * q.sn + l.vec * 8;
-  const bf16* kp = k.p + l.b * k.sb + l.n * k.sn + l.vec * 8;
-  const bf16* vp = has_v ? v.p + l.b * v.sb + l.n * v.sn + l.vec * 8 : nullptr;
-  bf16* qop = qo.p + l.b * qo.sb + l.n * qo.sn + l.vec * 8;
-  bf16* kop = ko.p + l.b * ko.sb + l.n * ko.sn + l.vec * 8;
-  bf16* vop = has_v ? vo.p + l.b * vo.sb + l.n * vo.sn + l.vec * 8 : nullptr;
+  const bf16* qp = q.p + l.b * q.sb + l.n * q.sn + vec * 8;
+  const bf16* kp = k.p + l.b * k.sb + l.n * k.sn + vec * 8;
+  const bf16* vp = has_v ? v.p + l.b * v.sb + l.n * v.sn + vec * 8 : nullptr;
+  bf16* qop = qo.p + l.b * qo.sb + l.n * qo.sn + vec * 8;
+  bf16* kop = ko.p + l.b * ko.sb + l.n * ko.sn + vec * 8;
+  bf16* vop = has_v ? vo.p + l.b * vo.sb + l.n * vo.sn + vec * 8 : nullptr;
   uint4 na[U], nb[U], nc[U];
-  auto fetch = [&](int64_t h) {
+  auto fetch = [&](int h) {
     load_rows<U>(na, qp, q.sh, h, l);
     load_rows<U>(nb, kp, k.sh, h, l);
     if (has_v) load_rows<U>(nc, vp, v.sh, h, l);
   };
   fetch(l.h0);   // on their way while the table and the weights are read
   Turn<HALF> t;
-  load_turn<HALF>(t, g, table, pos, l.row, l.active, l.vec, 1.f, status);
-  const int partner = HALF ? partner_lane<LPR>(g, l.lane, l.vec) : 0;
-  const uint4 fq = load_weight(wq, l.vec), fk = load_weight(wk, l.vec);
+  make_turn<HALF>(t, g, table, load_pos(g, pos, pos_row(g, l), l.active), l.active, vec, 1.f, status);
+  const int partner = HALF ? partner_lane<LPR>(g, threadIdx.x & 31, vec) : 0;
+  const uint4 fq = load_weight(wq, vec), fk = load_weight(wk, vec);
   uint4 fqp = fq, fkp = fk;
   if constexpr (HALF) {
     fqp = shfl(fq, partner);
     fkp = shfl(fk, partner);
   }
-  for (int64_t h = l.h0; h < l.h1; h += U) {
+  for (int h = l.h0; h < l.h1; h += U) {
     uint4 a[U], b[U], c[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -320,7 +331,7 @@ DSV_DEVICE uint4 norm_turn_back(const uint4& dy, const uint4& x, const uint4& w,
   return pack(f);
 }
 
-template <int D, bool HALF, int U>
+template <int D, bool HALF>
 __global__ void __launch_bounds__(kThreads, kBackCtas)
 qk_norm_rope_bwd_kernel(RopeGeom g, RopeView dqo, RopeView dko, RopeView dvo, RopeView q, RopeView k, RopeView dq,
                         RopeView dk, RopeView dv, const bf16* __restrict__ wq, const bf16* __restrict__ wk,
@@ -329,70 +340,70 @@ qk_norm_rope_bwd_kernel(RopeGeom g, RopeView dqo, RopeView dko, RopeView dvo, Ro
   constexpr int LPR = D / 8, kTok = kThreads / LPR;
   // the column sums may be scheduled once every CTA of this grid has started; they wait for its end
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  __shared__ float red[kTok][2 * D];
+  __shared__ __align__(16) float red[kTok][2 * D];
   const int vec = threadIdx.x & (LPR - 1), grp = threadIdx.x / LPR;
   const uint4 fq = load_weight(wq, vec), fk = load_weight(wk, vec);
-  float aq[8], ak[8];
+  const int partner = HALF ? partner_lane<LPR>(g, threadIdx.x & 31, vec) : 0;
+  const bool has_v = dvo.p != nullptr;
+  // the thread's own sums so far, in its own places (16 registers more would cost spills)
+  float4 *sum_q = reinterpret_cast<float4*>(&red[grp][vec * 8]), *sum_k = reinterpret_cast<float4*>(&red[grp][D + vec * 8]);
+  sum_q[0] = sum_q[1] = sum_k[0] = sum_k[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [](float4* to, const float (&v)[8]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) aq[e] = ak[e] = 0.f;
+    for (int i = 0; i < 2; ++i) {
+      float4 s = to[i];
+      s.x += v[4 * i], s.y += v[4 * i + 1], s.z += v[4 * i + 2], s.w += v[4 * i + 3];
+      to[i] = s;
+    }
+  };
+  auto at = [&](const RopeView& r, const Lane& l) { return r.p + l.b * r.sb + l.n * r.sn + vec * 8; };
+  // A step is a head of all three tensors, its loads one step ahead through everything the CTA does (n..: the rows on
+  // their way).  Two heads of one tensor to a step had as many rows in flight and took 2 % less at 16 heads, 8 %
+  // more at 4 and 50 % more at one.
+  uint4 nqy, nqx, nky, nkx, nv;
+  auto fetch = [&](const Lane& l, int h) {
+    const bool on = l.active;
+    auto row = [&](const RopeView& r) { return on ? load_row(at(r, l) + h * r.sh) : make_uint4(0, 0, 0, 0); };
+    nqy = row(dqo);
+    nqx = row(q);
+    nky = row(dko);
+    nkx = row(k);
+    if (has_v) nv = row(dvo);
+  };
+  Lane l = lane_of<LPR>(g, blockIdx.x);
+  fetch(l, l.h0);
+  Pos ahead = load_pos(g, pos, pos_row(g, l), l.active);
   for (int64_t unit = blockIdx.x; unit < g.units; unit += gridDim.x) {
-    const Lane l = lane_of<LPR>(g, unit);
-    auto at = [&](const RopeView& r) { return r.p + l.b * r.sb + l.n * r.sn + vec * 8; };
     Turn<HALF> t;
-    const int partner = HALF ? partner_lane<LPR>(g, l.lane, l.vec) : 0;
-    // one tensor's heads of this token, then the next tensor's (half the registers of both at once);
-    // values ride along: c = copied rows, if any
-    auto walk = [&](const RopeView& ry, const RopeView& rx, const RopeView& rd, const RopeView& rc,
-                    const RopeView& rcd, const uint4& w, float (&acc)[8], bool first) {
-      const bf16 *py = at(ry), *px = at(rx);
-      bf16* pd = at(rd);
-      const bool copy = rc.p != nullptr;
-      const bf16* pc = copy ? at(rc) : nullptr;
-      bf16* pcd = copy ? at(rcd) : nullptr;
-      uint4 ny[U], nx[U], nc[U];
-      auto fetch = [&](int64_t h) {
-        load_rows<U>(ny, py, ry.sh, h, l);
-        load_rows<U>(nx, px, rx.sh, h, l);
-        if (copy) load_rows<U>(nc, pc, rc.sh, h, l);
-      };
-      fetch(l.h0);
-      if (first) load_turn<HALF>(t, g, table, pos, l.row, l.active, l.vec, -1.f, status);
-      // a token's heads are summed first and its sum then added: two short chains of fp32
-      // additions instead of one as long as the clip
-      float tok[8];
+    make_turn<HALF>(t, g, table, ahead, l.active, vec, -1.f, status);
+    Lane nl = l;
+    nl.active = false;
+    if (unit + gridDim.x < g.units) {
+      nl = lane_of<LPR>(g, unit + gridDim.x);
+      ahead = load_pos(g, pos, pos_row(g, nl), nl.active);
+    }
+    // a token's heads are summed first and its sum then added: two short chains of fp32 additions instead of one as
+    // long as the clip
+    float tq[8], tk[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) tok[e] = 0.f;
-      for (int64_t h = l.h0; h < l.h1; h += U) {
-        uint4 y[U], x[U], c[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          y[u] = ny[u];
-          x[u] = nx[u];
-          c[u] = nc[u];
-        }
-        fetch(h + U);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const bool on = l.active && h + u < l.h1;
-          const uint4 r = norm_turn_back<D, HALF>(y[u], x[u], w, t, partner, eps, on, tok);
-          if (on) {
-            store_row(pd + (h + u) * rd.sh, r);
-            if (copy) store_row(pcd + (h + u) * rcd.sh, c[u]);
-          }
-        }
+    for (int e = 0; e < 8; ++e) tq[e] = tk[e] = 0.f;
+    for (int h = l.h0; h < l.h1; ++h) {
+      const uint4 qy = nqy, qx = nqx, ky = nky, kx = nkx, v = nv;
+      if (h + 1 < l.h1) fetch(l, h + 1);
+      else fetch(nl, nl.h0);
+      const uint4 rq = norm_turn_back<D, HALF>(qy, qx, fq, t, partner, eps, l.active, tq);
+      if (l.active) {
+        store_row(at(dq, l) + h * dq.sh, rq);
+        if (has_v) store_row(at(dv, l) + h * dv.sh, v);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += tok[e];
-    };
-    walk(dqo, q, dq, dvo, dv, fq, aq, true);
-    walk(dko, k, dk, RopeView(), RopeView(), fk, ak, false);
+      const uint4 rk = norm_turn_back<D, HALF>(ky, kx, fk, t, partner, eps, l.active, tk);
+      if (l.active) store_row(at(dk, l) + h * dk.sh, rk);
+    }
+    add(sum_q, tq);
+    add(sum_k, tk);
+    l = nl;
   }
   if (!partial) return;   // no weights: nothing to sum
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    red[grp][vec * 8 + e] = aq[e];
-    red[grp][D + vec * 8 + e] = ak[e];
-  }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
     float s = 0.f;
@@ -443,13 +454,9 @@ rope3d_table_kernel(RopeGeom g, double th0, double th1, double th2, int64_t tota
   table[e] = make_float2(static_cast<float>(c), static_cast<float>(s));
 }
 
-// Head chunks: a CTA walks all heads of its tokens unless that leaves the card's 152 SMs short of
-// CTAs; then the heads are split.
-void split_heads(RopeGeom& g, int tok) {
-  g.tiles_per_b = (g.N + tok - 1) / tok;
-  const int64_t tiles = g.B * g.tiles_per_b;
-  int64_t chunks = (kRopeWantCtas + tiles - 1) / tiles;
-  if (chunks > g.H) chunks = g.H;
+constexpr int64_t kBackAtOnce = 152 * kBackCtas;   // persistent CTAs of the backward
+
+void cut_heads(RopeGeom& g, int64_t tiles, int64_t chunks) {
   g.heads_per_chunk = (g.H + chunks - 1) / chunks;
   g.chunks = (g.H + g.heads_per_chunk - 1) / g.heads_per_chunk;
   g.units = tiles * g.chunks;
@@ -457,14 +464,37 @@ void split_heads(RopeGeom& g, int tok) {
 
 }  // namespace
 
-RopeGeom rope_plan(const RopeGeom& in, int d) {
+// How the work is cut into units of a CTA: a tile of tokens and a chunk of their heads.
+// Forward: a CTA walks all heads of its tokens unless that leaves the card's 152 SMs short of CTAs.
+// Backward: its CTAs take units in turns, so the cut with the least turns times the length of one (a step for each
+// head, and kBackSetup steps' worth of positions and table) is taken.
+RopeGeom rope_plan(const RopeGeom& in, int d, bool backward) {
   RopeGeom g = in;
-  split_heads(g, kThreads / (d / 8));
+  const int64_t tok = kThreads / (d / 8);
+  g.tiles_per_b = (g.N + tok - 1) / tok;
+  const int64_t tiles = g.B * g.tiles_per_b;
+  if (!backward) {
+    const int64_t chunks = (kRopeWantCtas + tiles - 1) / tiles;
+    cut_heads(g, tiles, chunks < g.H ? chunks : g.H);
+    return g;
+  }
+  int64_t best = 1;
+  double least = 0;
+  for (int64_t chunks = 1; chunks <= g.H && chunks <= 64; ++chunks) {
+    cut_heads(g, tiles, chunks);
+    const double turns = static_cast<double>((g.units + kBackAtOnce - 1) / kBackAtOnce);
+    const double cost = turns * (static_cast<double>(g.heads_per_chunk) + kBackSetup);
+    if (chunks == 1 || cost < least) {
+      least = cost;
+      best = chunks;
+    }
+  }
+  cut_heads(g, tiles, best);
   return g;
 }
 
-// Persistent CTAs of the backward (rows of its partial sums): as many as are resident at once.
-int64_t rope_bwd_ctas(const RopeGeom& g) { return g.units < 152 * kBackCtas ? g.units : 152 * kBackCtas; }
+// Persistent CTAs of the backward (rows of its partial sums).
+int64_t rope_bwd_ctas(const RopeGeom& g) { return g.units < kBackAtOnce ? g.units : kBackAtOnce; }
 
 cudaError_t launch_rope3d_table(const RopeGeom& g, const double (&theta)[3], float* table, cudaStream_t stream) {
   int64_t total = 0;
@@ -476,10 +506,10 @@ cudaError_t launch_rope3d_table(const RopeGeom& g, const double (&theta)[3], flo
   return cudaGetLastError();
 }
 
-// A group loads U = 2 heads of each tensor ahead.  Where it has only one or two heads to walk, half
-// of that would be loads of nothing or registers that keep other CTAs out: U = 1.  Measured with
-// U = 2 / U = 1: forward of 1 head 167 / 117 us (524,288 tokens, d = 64), 2 heads 99 / 82 us, 8 heads
-// 71 / 74 us; backward of 1 head 231 / 191 us, 2 heads 136 / 148 us; rope3d alone 66 / 60, 40 / 39, 29 / 33.
+// The forward and rope3d load U = 2 heads of each tensor ahead.  Where a group has only one or two heads to walk, half
+// of that would be loads of nothing or registers that keep other CTAs out: U = 1.  Measured with U = 2 / U = 1
+// (524,288 tokens, d = 64): norm and rotation of 1 head 167 / 117 us, 2 heads 99 / 82 us, 8 heads (65,536 tokens) 71 / 74 us; rope3d
+// alone 66 / 60, 40 / 39, 29 / 33.
 template <class F>
 void pick(const RopeParams& p, bool one, F&& go) {
   auto rows = [&](auto d, auto half) {
@@ -492,7 +522,7 @@ void pick(const RopeParams& p, bool one, F&& go) {
 }
 
 cudaError_t launch_rope3d(const RopeParams& p, cudaStream_t stream) {
-  const RopeGeom g = rope_plan(p.g, p.d);
+  const RopeGeom g = rope_plan(p.g, p.d, false);
   const float2* table = reinterpret_cast<const float2*>(p.table);
   ProfScope prof(p.backward ? "rope3d_bwd" : "rope3d_fwd", stream);
   pick(p, g.heads_per_chunk <= 2, [&](auto d, auto half, auto u) {
@@ -504,7 +534,7 @@ cudaError_t launch_rope3d(const RopeParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_qk_norm_rope_fwd(const RopeParams& p, cudaStream_t stream) {
-  const RopeGeom g = rope_plan(p.g, p.d);
+  const RopeGeom g = rope_plan(p.g, p.d, false);
   const float2* table = reinterpret_cast<const float2*>(p.table);
   ProfScope prof("qk_norm_rope_fwd", stream);
   pick(p, g.heads_per_chunk <= 2, [&](auto d, auto half, auto u) {
@@ -516,14 +546,14 @@ cudaError_t launch_qk_norm_rope_fwd(const RopeParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_qk_norm_rope_bwd(const RopeParams& p, cudaStream_t stream) {
-  const RopeGeom g = rope_plan(p.g, p.d);
+  const RopeGeom g = rope_plan(p.g, p.d, true);
   const float2* table = reinterpret_cast<const float2*>(p.table);
   const int64_t ctas = rope_bwd_ctas(g);
   float* partial = p.dwq || p.dwk ? p.partial : nullptr;
   {
     ProfScope prof("qk_norm_rope_bwd", stream);
-    pick(p, g.heads_per_chunk == 1, [&](auto d, auto half, auto u) {
-      qk_norm_rope_bwd_kernel<decltype(d)::value, decltype(half)::value, decltype(u)::value>
+    pick(p, true, [&](auto d, auto half, auto) {
+      qk_norm_rope_bwd_kernel<decltype(d)::value, decltype(half)::value>
           <<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(g, p.qo, p.ko, p.vo, p.q, p.k, p.dq, p.dk, p.dv, p.wq,
                                                                  p.wk, p.pos, table, p.eps, partial, p.status);
     });

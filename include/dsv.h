@@ -340,7 +340,7 @@ dsv_status dsv_adaln_bwd(const dsv_adaln_dims* dims, const void* x, const void* 
  * strides).  A memory range that overlaps an input's in any other way is refused; outputs of one
  * call may interleave in one range with the same strides (a packed gradient).
  *
- * Validation before any launch: B, H, N >= 1; B*H*N < 2^31; d in {64, 128}; rot even, >= 0, sum
+ * Validation before any launch: B, H, N >= 1; B*H*N < 2^31 - 64; d in {64, 128}; rot even, >= 0, sum
  * <= d (a multiple of 16 for DSV_PAIRS_HALVES); len >= 1 for every axis in use, and at most 2^31
  * (cos, sin) pairs in all; eps >= 0 and finite.  Any N: it need not be a multiple of the
  * attention's block.

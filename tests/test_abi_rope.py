@@ -47,6 +47,7 @@ def rope(lib, d, x=X, xs=None, y=Y, ys=None, pos=POS, tab=TAB, fn="dsv_rope3d_fw
 @pytest.mark.parametrize("over,status,what", [
     (dict(B=0), INVALID, b"B, H, N"), (dict(H=0), INVALID, b"B, H, N"), (dict(N=0), INVALID, b"B, H, N"),
     (dict(N=-1), INVALID, b"B, H, N"), (dict(N=1 << 33), INVALID, b"int32"), (dict(N=1 << 30, H=4), INVALID, b"int32"),
+    (dict(B=1, H=1, N=2 ** 31 - 64), INVALID, b"int32"),
     (dict(d=96), UNSUPPORTED, b"64 or 128"), (dict(pairing=2), INVALID, b"pairing"),
     (dict(rot=(3, 0, 0)), INVALID, b"even"), (dict(rot=(-2, 0, 0)), INVALID, b"even"),
     (dict(rot=(32, 32, 2)), INVALID, b"at most d"), (dict(rot=(66, 0, 0)), INVALID, b"rot"),
