@@ -6,16 +6,26 @@
 //   kGateGrad  the same products again; dg = dh u act'(g), du = dh act(g)   (nothing is kept of the forward)
 //   kDx        dx = dg Wg + du Wu                                         (K = F twice; W is MN-major)
 //   kDw        dWg = dg^T x, dWu = du^T x                                  (K = M; both MN-major)
-// An accumulator tile is 256 rows by 256 columns, held by a pair of CTAs; in the gated modes its columns are 128 of g and the
-// 128 of u they meet in the epilogue, so g and u never leave the SM in kGate.  dg and du are rounded
-// to bf16 between the backward's kernels: the tensor cores take them as operands of that type (2^-8 of
-// each value, as every activation between layers).
+// An accumulator tile is 256 rows by 256 columns, held by a pair of CTAs (cta_group::2: each holds 128 rows
+// of A and of the result, and half of B); in the gated modes its columns are 128 of g and the 128 of u
+// they meet in the epilogue, so g and u never leave the SM in kGate.  dg and du are rounded to bf16
+// between the backward's kernels: the tensor cores take them as operands of that type (at most 2^-8 of
+// each value, as every activation between layers; a few tokens keep them in fp32, below).
 //
-// Roles (384 threads): one thread of warp 0 issues the TMA loads of A and one of warp 2 those of B into a
-// ring of stages; one thread of warp 1 issues the MMAs, into one of two accumulators (2 x 256 of the 512
-// TMEM columns); warps 4-11 empty the other one: two warpgroups, each on half of the columns, through 128-byte-swizzled staging tiles that
-// TMA stores write (rows and columns past the matrices are clipped there, and zero-filled by the
-// loads).  Every wait is bounded.
+// Roles (384 threads a CTA): one thread of warp 0 issues the TMA loads of A and one of warp 2 those of B into a
+// ring of 64-wide stages; one thread of warp 1 of the pair's first CTA issues the MMAs, into one of two
+// accumulators (2 x 256 of the 512 TMEM columns); warps 4-11 empty the other one: two warpgroups, each on half
+// of the columns, through swizzled staging tiles that TMA stores write (rows and columns past the matrices
+// are clipped there, and zero-filled by the loads).  Every wait is bounded.
+//
+// What bounds it (GB300, M x D x F): the tensor cores.  65,536 x 2048 x 5632 forward 1.51 ms = 2.0 PFLOP/s from a cool start,
+// the rate of the library's plain product of that size (1.51 ms), 527 to 540 of the ideal 512 cycles to a
+// stage; run for a second the card's 1.4 kW limit holds both back (1.72 ms here, 1.69 ms there).
+// 16,384-token backward 1.30 ms = 1.75 PFLOP/s: its three products pass 0.6 GB of dh, dg and du and end in
+// partial rounds of tiles.  Short D is bound by the epilogue and, where rows do not start on 128 bytes,
+// by the loads: 34,070 x 360 x 3312 forward 155 us against 85.  A pair beats single CTAs of 128 x 256 tiles (1.74 ms)
+// for its half B to a CTA and six stages instead of four; pairs of pairs that shared B by multicast ran at
+// the same cycles to a stage on 144 of the 152 SMs (1.69 ms).
 #include <cuda.h>
 
 #include <type_traits>
@@ -752,7 +762,10 @@ bool few_rows(int64_t M, int64_t D, int64_t F) { return M <= 2 || (M <= 4 && D *
 constexpr int kSplitSaves = 24;     // k blocks that splitting K has to save
 
 constexpr int64_t kPairs = 76;      // of CTAs, on the card's 152 SMs
-constexpr int kGroup = 16;          // m tiles that take the same n tiles in turn (their operands meet in L2)
+// m tiles that take the same n tiles in turn, so that their operands meet in L2: 19, so that the 76 pairs work on 19
+// by 4 tiles at a time (a second of 2048 x 5632 calls at the power limit: 65,536-token forward 1713 us with 19, 1735 with 16,
+// 1760 with 8 or 10; 16,384-token backward 1410, 1432, 1430).
+constexpr int kGroup = 19;
 
 // How one product is cut: tiles, and where they leave at least half of the pairs without work, parts of K.
 // A part costs its sums' way to memory and back and a second launch, about 6 us or 24 k blocks, so K is

@@ -358,8 +358,8 @@ qk_norm_rope_bwd_kernel(RopeGeom g, RopeView dqo, RopeView dko, RopeView dvo, Ro
   };
   auto at = [&](const RopeView& r, const Lane& l) { return r.p + l.b * r.sb + l.n * r.sn + vec * 8; };
   // A step is a head of all three tensors, its loads one step ahead through everything the CTA does (n..: the rows on
-  // their way).  Two heads of one tensor to a step had as many rows in flight and took 2 % less at 16 heads, 8 %
-  // more at 4 and 50 % more at one.
+  // their way).  Two heads of one tensor to a step keep as many rows in flight and took 349 us where this takes
+  // 341 (mid clip, 16 heads), 766 where it takes 729 (long clip, 4 heads).
   uint4 nqy, nqx, nky, nkx, nv;
   auto fetch = [&](const Lane& l, int h) {
     const bool on = l.active;
@@ -506,26 +506,31 @@ cudaError_t launch_rope3d_table(const RopeGeom& g, const double (&theta)[3], flo
   return cudaGetLastError();
 }
 
-// The forward and rope3d load U = 2 heads of each tensor ahead.  Where a group has only one or two heads to walk, half
-// of that would be loads of nothing or registers that keep other CTAs out: U = 1.  Measured with U = 2 / U = 1
-// (524,288 tokens, d = 64): norm and rotation of 1 head 167 / 117 us, 2 heads 99 / 82 us, 8 heads (65,536 tokens) 71 / 74 us; rope3d
-// alone 66 / 60, 40 / 39, 29 / 33.
 template <class F>
-void pick(const RopeParams& p, bool one, F&& go) {
-  auto rows = [&](auto d, auto half) {
-    one ? go(d, half, std::integral_constant<int, 1>()) : go(d, half, std::integral_constant<int, 2>());
-  };
+void pick(const RopeParams& p, F&& go) {
   auto dim = [&](auto half) {
-    p.d == 128 ? rows(std::integral_constant<int, 128>(), half) : rows(std::integral_constant<int, 64>(), half);
+    p.d == 128 ? go(std::integral_constant<int, 128>(), half) : go(std::integral_constant<int, 64>(), half);
   };
   p.half ? dim(std::true_type()) : dim(std::false_type());
+}
+
+// The forward and rope3d load U = 2 heads of each tensor ahead.  Where a group has only one or two heads to walk, half
+// of that would be loads of nothing or registers that keep other CTAs out: U = 1.  Measured with U = 2 / U = 1
+// (d = 64, 524,288 tokens): norm and rotation of 1 head 167 / 117 us, 2 heads (262,144 tokens) 99 / 82 us,
+// 8 heads (65,536 tokens) 71 / 74 us; rope3d alone 66 / 60, 40 / 39, 29 / 33.  Persistent CTAs as in the backward cost the
+// forward 8 to 10 % (mid clip 241 -> 266 us): it has registers for more CTAs than they take.
+template <class F>
+void pick_rows(const RopeParams& p, const RopeGeom& g, F&& go) {
+  pick(p, [&](auto d, auto half) {
+    g.heads_per_chunk <= 2 ? go(d, half, std::integral_constant<int, 1>()) : go(d, half, std::integral_constant<int, 2>());
+  });
 }
 
 cudaError_t launch_rope3d(const RopeParams& p, cudaStream_t stream) {
   const RopeGeom g = rope_plan(p.g, p.d, false);
   const float2* table = reinterpret_cast<const float2*>(p.table);
   ProfScope prof(p.backward ? "rope3d_bwd" : "rope3d_fwd", stream);
-  pick(p, g.heads_per_chunk <= 2, [&](auto d, auto half, auto u) {
+  pick_rows(p, g, [&](auto d, auto half, auto u) {
     rope3d_kernel<decltype(d)::value, decltype(half)::value, decltype(u)::value>
         <<<static_cast<unsigned>(g.units), kThreads, 0, stream>>>(g, p.q, p.qo, p.pos, table, p.backward ? -1.f : 1.f,
                                                                   p.status);
@@ -537,7 +542,7 @@ cudaError_t launch_qk_norm_rope_fwd(const RopeParams& p, cudaStream_t stream) {
   const RopeGeom g = rope_plan(p.g, p.d, false);
   const float2* table = reinterpret_cast<const float2*>(p.table);
   ProfScope prof("qk_norm_rope_fwd", stream);
-  pick(p, g.heads_per_chunk <= 2, [&](auto d, auto half, auto u) {
+  pick_rows(p, g, [&](auto d, auto half, auto u) {
     qk_norm_rope_fwd_kernel<decltype(d)::value, decltype(half)::value, decltype(u)::value>
         <<<static_cast<unsigned>(g.units), kThreads, 0, stream>>>(g, p.q, p.k, p.v, p.qo, p.ko, p.vo, p.wq, p.wk,
                                                                   p.pos, table, p.eps, p.status);
@@ -552,7 +557,7 @@ cudaError_t launch_qk_norm_rope_bwd(const RopeParams& p, cudaStream_t stream) {
   float* partial = p.dwq || p.dwk ? p.partial : nullptr;
   {
     ProfScope prof("qk_norm_rope_bwd", stream);
-    pick(p, true, [&](auto d, auto half, auto) {
+    pick(p, [&](auto d, auto half) {
       qk_norm_rope_bwd_kernel<decltype(d)::value, decltype(half)::value>
           <<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(g, p.qo, p.ko, p.vo, p.q, p.k, p.dq, p.dk, p.dv, p.wq,
                                                                  p.wk, p.pos, table, p.eps, partial, p.status);
