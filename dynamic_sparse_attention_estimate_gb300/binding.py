@@ -540,13 +540,17 @@ def _need_view(t: torch.Tensor, name: str, shape=None, device: Optional[int] = N
                      + f", got {t.dtype} {tuple(t.shape)} strides={strides} device={t.device}")
 
 
-def _need_on(t: torch.Tensor, name: str, dtype, shape, device: int):
-    """A contiguous CUDA tensor of this type and shape on this device."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
-        raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{device}, got "
-                         f"{t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} device={t.device}")
+def _need_on(dtype, shape, device: int, *named):
+    """Contiguous CUDA tensors of this type and shape on this device: (tensor, name) pairs.  None is passed over: the
+    library refuses it where the tensor is needed."""
+    for t, name in named:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+            raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{device}, got "
+                             f"{t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} device={t.device}")
 
 
 def _workspace(workspace: Optional[torch.Tensor], nbytes: int, like: torch.Tensor):
@@ -572,7 +576,7 @@ def _rope_args(x: torch.Tensor, pos: Optional[torch.Tensor], rope: Optional[Rope
         raise ValueError("a RopeTable needs pos")
     batched = pos.dim() == 3
     dims, numbers = _rope_dims(shape, tuple(rope.axes), tuple(rope.lengths), rope.pairing, batched, float(eps))
-    _need_on(pos, "pos", torch.int32, (shape[0], shape[2], 3) if batched else (shape[2], 3), device)
+    _need_on(torch.int32, (shape[0], shape[2], 3) if batched else (shape[2], 3), device, (pos, "pos"))
     table = rope.data
     if table.dtype != torch.float32 or table.numel() < numbers or not table.is_contiguous() or \
             table.get_device() != device:
@@ -647,18 +651,14 @@ def dsv_qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Ten
     strides += _need_view(k, "k", shape, device)
     strides += (0, 0, 0) if v is None else _need_view(v, "v", shape, device)
     dims, pos_ptr, table_ptr = _rope_args(q, pos, rope, eps)
-    for w, n in ((wq, "wq"), (wk, "wk")):
-        if w is not None:
-            _need_on(w, n, torch.bfloat16, shape[3:], device)
+    _need_on(torch.bfloat16, shape[3:], device, (wq, "wq"), (wk, "wk"))
     if out is None:
         # one allocation: the three live and die together
         outs = torch.empty((2 if v is None else 3, *shape), dtype=q.dtype, device=q.device)
         qo, ko, vo = (*outs.unbind(0), None)[:3]
     else:
         qo, ko, vo = out
-        for t, n in ((qo, "q_out"), (ko, "k_out"), (vo, "v_out")):
-            if t is not None:
-                _need_on(t, n, torch.bfloat16, shape, device)
+        _need_on(torch.bfloat16, shape, device, (qo, "q_out"), (ko, "k_out"), (vo, "v_out"))
     _call("dsv_qk_norm_rope_fwd", device, dims, q.data_ptr(), k.data_ptr(), _ptr(v), _Strides9(*strides), _ptr(wq),
           _ptr(wk), pos_ptr, table_ptr, _ptr(qo), _ptr(ko), _ptr(vo))
     return qo, ko, vo
@@ -679,13 +679,9 @@ def dsv_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, dv_out: Opt
     strides = _need_view(q, "q")
     shape, device = q.shape, q.get_device()
     strides += _need_view(k, "k", shape, device)
-    for t, n in ((dq_out, "dq_out"), (dk_out, "dk_out"), (dv_out, "dv_out")):
-        if t is not None or n != "dv_out":
-            _need_on(t, n, torch.bfloat16, shape, device)
+    _need_on(torch.bfloat16, shape, device, (dq_out, "dq_out"), (dk_out, "dk_out"), (dv_out, "dv_out"))
     dims, pos_ptr, table_ptr = _rope_args(q, pos, rope, eps)
-    for w, n in ((wq, "wq"), (wk, "wk")):
-        if w is not None:
-            _need_on(w, n, torch.bfloat16, shape[3:], device)
+    _need_on(torch.bfloat16, shape[3:], device, (wq, "wq"), (wk, "wk"))
     B, H, N, d = shape
     if out is None:
         packed = torch.empty((B, N, 2 if dv_out is None else 3, H, d), dtype=q.dtype, device=q.device)
@@ -697,7 +693,7 @@ def dsv_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, dv_out: Opt
     dwq, dwk = torch.empty((2, d), dtype=torch.float32, device=q.device).unbind(0)
     dwq, dwk = None if wq is None else dwq, None if wk is None else dwk
     ws, nbytes, _keep = _workspace(workspace, 0 if wq is None and wk is None else _qk_norm_rope_ws(B, H, N, d), q)
-    _call("dsv_qk_norm_rope_bwd", device, dims, dq_out.data_ptr(), dk_out.data_ptr(), _ptr(dv_out), q.data_ptr(),
+    _call("dsv_qk_norm_rope_bwd", device, dims, _ptr(dq_out), _ptr(dk_out), _ptr(dv_out), q.data_ptr(),
           k.data_ptr(), _Strides6(*strides), _ptr(wq), _ptr(wk), pos_ptr, table_ptr, _ptr(dq), _ptr(dk), _ptr(dv),
           _Strides9(*dstrides), _ptr(dwq), _ptr(dwk), ws, nbytes)
     return dq, dk, dv, dwq, dwk
@@ -729,8 +725,7 @@ def _ffn_args(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: st
     if w_gate.dim() != 2:
         raise ValueError(f"w_gate must be [F, D], got {tuple(w_gate.shape)}")
     D, F, device = x.shape[-1], w_gate.shape[0], x.get_device()
-    _need_on(w_gate, "w_gate", torch.bfloat16, (F, D), device)
-    _need_on(w_up, "w_up", torch.bfloat16, (F, D), device)
+    _need_on(torch.bfloat16, (F, D), device, (w_gate, "w_gate"), (w_up, "w_up"))
     return _ffn_dims(x.numel() // D if D else 0, D, F, act), (*x.shape[:-1], F)
 
 
@@ -743,9 +738,9 @@ def dsv_ffn_gated_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
     if out is None:
         out = torch.empty(shape, dtype=x.dtype, device=x.device)
     else:
-        _need_on(out, "out", torch.bfloat16, shape, device)
+        _need_on(torch.bfloat16, shape, device, (out, "out"))
     ws, nbytes, _keep = _workspace(workspace, nbytes, x)
-    _call("dsv_ffn_gated_fwd", device, dims, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(), ws, nbytes)
+    _call("dsv_ffn_gated_fwd", device, dims, x.data_ptr(), w_gate.data_ptr(), _ptr(w_up), out.data_ptr(), ws, nbytes)
     return out
 
 
@@ -764,16 +759,16 @@ def dsv_ffn_gated_bwd(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w
     recomputed from x (the forward keeps nothing)."""
     (dims, _, nbytes), shape = _ffn_args(x, w_gate, w_up, act)
     device = x.get_device()
-    _need_on(dh, "dh", torch.bfloat16, shape, device)
+    _need_on(torch.bfloat16, shape, device, (dh, "dh"))
     if out is None:
-        dx, dwg, dwu = torch.empty_like(x), torch.empty_like(w_gate), torch.empty_like(w_up)
+        dx, dwg, dwu = torch.empty_like(x), torch.empty_like(w_gate), torch.empty_like(w_gate)
     else:
         dx, dwg, dwu = out
-        for t, n, like in ((dx, "dx", x), (dwg, "dw_gate", w_gate), (dwu, "dw_up", w_up)):
-            _need_on(t, n, torch.bfloat16, like.shape, device)
+        _need_on(torch.bfloat16, x.shape, device, (dx, "dx"))
+        _need_on(torch.bfloat16, w_gate.shape, device, (dwg, "dw_gate"), (dwu, "dw_up"))
     ws, nbytes, _keep = _workspace(workspace, nbytes, x)
-    _call("dsv_ffn_gated_bwd", device, dims, dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
-          dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), ws, nbytes)
+    _call("dsv_ffn_gated_bwd", device, dims, _ptr(dh), x.data_ptr(), w_gate.data_ptr(), _ptr(w_up), _ptr(dx), _ptr(dwg),
+          _ptr(dwu), ws, nbytes)
     return dx, dwg, dwu
 
 

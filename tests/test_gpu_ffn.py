@@ -240,3 +240,9 @@ def test_python_refusals():
         dsv_ffn_gated_bwd(dh, x, wg, wu, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError, match="dh"):
         dsv_ffn_gated_bwd(dh[:, :64], x, wg, wu)
+    for bad in ((None, x, wg, wu), (dh, x, wg, None)):
+        with pytest.raises(DSVError, match="NULL"):
+            dsv_ffn_gated_bwd(*bad)
+    for bad in ((None, wg, wu), (x, None, wu)):
+        with pytest.raises(TypeError):
+            dsv_ffn_gated_fwd(*bad)

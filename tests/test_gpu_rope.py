@@ -467,3 +467,9 @@ def test_python_refusals():
         dsv_qk_norm_rope_fwd(x[:, :, :0], x[:, :, :0], None, None, None, pos[:0], rope)
     with pytest.raises(ValueError, match="RopeTable"):
         dsv_qk_norm_rope_fwd(x, x, None, None, None, pos, None)
+    with pytest.raises(DSVError, match="NULL"):
+        dsv_qk_norm_rope_bwd(None, x, None, x, x, None, None, pos, rope)
+    with pytest.raises(DSVError, match="both"):
+        dsv_qk_norm_rope_bwd(x, x, x, x, x, None, None, pos, rope, out=(torch.empty_like(x), torch.empty_like(x), None))
+    with pytest.raises(ValueError, match="dk_out"):
+        dsv_qk_norm_rope_bwd(x, x.transpose(1, 2), None, x, x, None, None, pos, rope)
