@@ -194,7 +194,8 @@ DSV_DEVICE float act_value(float g, int act) {
 }
 DSV_DEVICE void act_both(float g, int act, float& a, float& slope) {
   const float z = act == 0 ? g : kGelu2C * fmaf(0.044715f * g * g, g, g);
-  const float dz = act == 0 ? 1.f : kGelu2C * fmaf(3.f * 0.044715f * g, g, 1.f);
+  // (held finite: beyond |g| = 1.8e19 g^2 is not, and the factor it meets below is then 0, not small)
+  const float dz = act == 0 ? 1.f : fminf(kGelu2C * fmaf(3.f * 0.044715f * g, g, 1.f), 1e30f);
   const float s = logistic(z);
   a = g * s;
   slope = fmaf(a * (1.f - s), dz, s);

@@ -160,6 +160,26 @@ def test_large_activations_do_not_overflow(act):
     assert all(torch.isfinite(t).all() for t in out)
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M", [1, 3, 5, 300])
+def test_the_slope_where_g_squared_overflows(M, act):
+    """|g| = 2^67: act(g) is g or 0 and its slope 1 or 0, all in powers of two, so every result is exact."""
+    D, F = 16, 32
+    x, wg, wu = torch.zeros(M, D, dtype=BF16), torch.zeros(F, D, dtype=BF16), torch.zeros(F, D, dtype=BF16)
+    x[:, 0], wg[:, 0], wu[:, 0] = 2.0 ** 34, 2.0 ** 33, 2.0 ** -34
+    wg[F // 2:, 0] *= -1
+    dh = torch.ones(M, F, dtype=BF16)
+    dx, dwg, dwu = dsv_ffn_gated_bwd(dh.cuda(), x.cuda(), wg.cuda(), wu.cuda(), act)
+    h = dsv_ffn_gated_fwd(x.cuda(), wg.cuda(), wu.cuda(), act)
+    rx, rg, ru, rh = (torch.zeros(*s, dtype=torch.float64) for s in ((M, D), (F, D), (F, D), (M, F)))
+    rx[:, 0] = F // 2 * (2.0 ** 33 + 2.0 ** 67 * 2.0 ** -34)
+    rg[:F // 2, 0] = M * 2.0 ** 34
+    ru[:F // 2, 0] = M * 2.0 ** 67 * 2.0 ** 34
+    rh[:, :F // 2] = 2.0 ** 67
+    for got, ref in ((dx, rx), (dwg, rg), (dwu, ru), (h, rh)):
+        assert torch.equal(got.double().cpu(), ref.to(BF16).double())
+
+
 def test_leading_dims_repeatability_streams_and_graphs():
     need_gpu()
     B, N, D, F = 3, 70, 264, 520
