@@ -749,9 +749,9 @@ static dsv_status check_view(const dsv_rope_dims* d, const char* name, const voi
     if (st[i] < 0 || st[i] % 8 || st[i] > (1LL << 40))
       return fail(DSV_ERR_INVALID_ARG, "%s: strides must be multiples of 8 elements in [0, 2^40] (got %lld)", name,
                   (long long)st[i]);
-    last += (n[i] - 1) * (st[i] / 8) * 8;
-    if (n[i] > (1LL << 48) / (st[i] + 1) || last > (1LL << 48))
+    if (n[i] > (1LL << 48) / (st[i] + 1) || last + (n[i] - 1) * st[i] > (1LL << 48))
       return fail(DSV_ERR_INVALID_ARG, "%s: the view spans too much memory", name);
+    last += (n[i] - 1) * st[i];
   }
   if (output) {   // innermost to outermost: each stride must pass what the inner ones span
     int order[3] = {0, 1, 2};
@@ -969,6 +969,18 @@ dsv_status dsv_qk_norm_rope_bwd(const dsv_rope_dims* dims, const void* d_q_out, 
       return fail(DSV_ERR_WORKSPACE, "workspace must be 256-byte aligned");
     if (ws_bytes < need)
       return fail(DSV_ERR_WORKSPACE, "workspace of %zu bytes is below the %zu needed", ws_bytes, need);
+    const char* sum_name[3] = {"dwq", "dwk", "ws"};
+    const void* sum[3] = {dwq, dwk, ws};
+    ViewSpan ss[3];
+    for (int j = 0; j < 3; ++j) {
+      ss[j].lo = static_cast<const char*>(sum[j]);
+      ss[j].hi = ss[j].lo + (!sum[j] ? 0 : j < 2 ? dims->d * 4 : static_cast<int64_t>(need));
+      for (int i = 0; i < ni + nt + j && sum[j]; ++i) {
+        const ViewSpan& t = i < ni ? is[i] : i < ni + nt ? os[i - ni] : ss[i - ni - nt];
+        const char* name = i < ni ? in_name[i] : i < ni + nt ? out_name[i - ni] : sum_name[i - ni - nt];
+        if (!apart(t, ss[j])) return fail(DSV_ERR_INVALID_ARG, "%s overlaps %s", sum_name[j], name);
+      }
+    }
   }
   p.d = static_cast<int>(dims->d);
   p.half = dims->pairing == DSV_PAIRS_HALVES;

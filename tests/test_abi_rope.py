@@ -99,6 +99,12 @@ def test_strides(lib):
         assert rope(lib, d, ys=ViewStrides(*s)) == INVALID and b"overlap" in lib.dsv_last_error_message()
 
 
+def test_strides_that_span_too_much(lib):
+    d = dims(B=1, H=1, N=2 ** 31 - 66)
+    for s in (1 << 40, 1 << 39, 1 << 20):
+        assert rope(lib, d, xs=ViewStrides(0, 0, s)) == INVALID and b"spans too much" in lib.dsv_last_error_message()
+
+
 def test_outputs_over_inputs(lib):
     d = dims()
     size = 2 * 3 * 40 * 64 * 2
@@ -138,6 +144,19 @@ def test_backward_arguments(lib):
     assert bwd(lib, d, nbytes=need - 1) == WORKSPACE
     assert bwd(lib, d, dk=Y) == INVALID and b"dk overlaps dq" in lib.dsv_last_error_message()
     assert bwd(lib, d, dq=X) == INVALID and b"overlaps" in lib.dsv_last_error_message()
+
+
+def test_sums_and_workspace_over_other_tensors(lib):
+    d = dims()
+    size = 2 * 3 * 40 * 64 * 2
+    ws = lib.dsv_qk_norm_rope_bwd_workspace(d)
+    for over, what in ((dict(dwq=Y), b"dwq overlaps dq"), (dict(dwk=X + 5 * size - 16), b"dwk overlaps k"),
+                       (dict(dwk=0x4000000), b"dwk overlaps dwq"), (dict(ws=Y + 2 * size & ~255), b"ws overlaps"),
+                       (dict(ws=0x4001000, nbytes=ws), b"ws overlaps dwk"), (dict(dwq=0x5000000 + ws - 16), b"ws overlaps dwq")):
+        assert bwd(lib, d, **over) == INVALID and what in lib.dsv_last_error_message(), over
+    # without sums the workspace is not read; side by side is fine
+    assert bwd(lib, d, dwq=None, dwk=None, ws=Y) not in (INVALID, WORKSPACE)
+    assert bwd(lib, d, dwq=0x5000000 + ws, nbytes=ws) not in (INVALID, WORKSPACE)
 
 
 def test_interleaved_outputs(lib):
