@@ -1,11 +1,12 @@
 // Gated feed-forward of a DiT block: h = act(x Wg^T) * (x Wu^T), forward and backward, on the tcgen05
 // tensor cores.
 //
-// One persistent GEMM kernel in four modes, all bf16 operands with fp32 accumulators in tensor memory:
+// One persistent GEMM kernel in five modes, all bf16 operands with fp32 accumulators in tensor memory:
 //   kGate      g, u = x Wg^T, x Wu^T;  h = act(g) u                      (K = D, both K-major)
 //   kGateGrad  the same products again; dg = dh u act'(g), du = dh act(g)   (nothing is kept of the forward)
 //   kDx        dx = dg Wg + du Wu                                         (K = F twice; W is MN-major)
 //   kDw        dWg = dg^T x, dWu = du^T x                                  (K = M; both MN-major)
+//   kBack      kDx and kDw in one launch, where each alone leaves many pairs idle
 // An accumulator tile is 256 rows by 256 columns, held by a pair of CTAs (cta_group::2: each holds 128 rows
 // of A and of the result, and half of B); in the gated modes its columns are 128 of g and the 128 of u
 // they meet in the epilogue, so g and u never leave the SM in kGate.  dg and du are rounded to bf16
@@ -46,24 +47,88 @@ constexpr uint32_t kWaitNs = 2000;
 constexpr int kTile = 128 * 128;           // bytes of a [128 rows][64] or two [64 rows][64] bf16 tiles
 constexpr int kPart = 128 * 64;            // bytes of a [128 rows][32] bf16 tile: what one TMA store writes
 
-enum Mode { kGate = 0, kGateGrad = 1, kDx = 2, kDw = 3 };
+enum Mode { kGate = 0, kGateGrad = 1, kDx = 2, kDw = 3, kBack = 4 };
 
 struct Maps {
-  CUtensorMap a0, a1, b0, b1, c0, c1;   // operands A and B, results C
+  CUtensorMap a0, a1;      // A: x; dg, du for dx
+  CUtensorMap t0, t1;      // dg, du for the weights' gradients
+  CUtensorMap b0, b1, b2;  // B: Wg, Wu; x for the weights' gradients
+  CUtensorMap c0, c1, c2;  // results: h; dg, du; dx, dWg, dWu
 };
 
-struct Shape {
+// One product and how it is cut.
+struct Product {
+  bool dw;          // the weights' gradients
   int64_t m_tiles, n_tiles, tiles;
   int64_t units;    // tiles, or tiles times the parts of K they are split into (unit = part * tiles + tile)
-  int kb_half;      // k blocks of one operand pair (kDx has two pairs)
+  int kb_half;      // dx: k blocks of one of its two pairs of operands
   int kb;           // k blocks of a tile
   int kb_part;      // of a unit
   float* partial;   // split: [unit][256][256] sums
+  int64_t rows, cols;   // of the result (the weights': of one of the two)
+  int64_t half_tiles;   // the weights': m tiles of the first result
+};
+struct Shape {
+  Product p[2];     // kBack: dx and the weights' gradients, the one with longer units first; else p[0]
+  int64_t skip;     // see Walk
   const bf16* dh;   // kGateGrad
-  int64_t rows, cols;   // of the result (kDw: of one of the two results)
-  int64_t half_tiles;   // kDw: m tiles of the first result
   int group;        // m tiles that share their n tiles' operands in L2
   int act;
+};
+
+// The units of one pair of CTAs of P: they go round the pairs.
+template <bool TWO>
+struct Walk {
+  static constexpr int cls = 0;
+  int64_t n, pairs, t;
+  DSV_DEVICE Walk(const Shape& sh) {
+    n = sh.p[0].units;
+    pairs = gridDim.x / 2;
+    t = blockIdx.x / 2;
+  }
+  DSV_DEVICE bool more() const { return t < n; }
+  DSV_DEVICE void next() { t += pairs; }
+};
+// Of two products (cls: which): those of p[0] go round the pairs; after its last round, L pairs have had
+// one less, and take `skip` units of p[1] each (unit i of these: pair P - L + i % L) before the rest of p[1] goes round all of
+// them, the L first.
+template <>
+struct Walk<true> {
+  int64_t n0, n1, pairs, pair, skip, t;
+  int64_t short_from;   // P - L (0: every pair had the same number)
+  int64_t extra;        // units of `skip` still to come
+  int cls;
+  DSV_DEVICE Walk(const Shape& sh) {
+    n0 = sh.p[0].units;
+    n1 = sh.p[1].units;
+    pairs = gridDim.x / 2;
+    t = pair = blockIdx.x / 2;
+    skip = sh.skip;
+    short_from = n0 % pairs;
+    cls = 0;
+    extra = 0;
+    if (t >= n0) second();
+  }
+  DSV_DEVICE void second() {
+    cls = 1;
+    extra = short_from && pair >= short_from ? skip : 0;
+    t = extra ? pair - short_from : rest();
+  }
+  DSV_DEVICE int64_t rest() const {
+    const int64_t i = pair - short_from;
+    return (short_from ? skip * (pairs - short_from) : 0) + (i < 0 ? i + pairs : i);
+  }
+  DSV_DEVICE bool more() const { return t < (cls ? n1 : n0); }
+  DSV_DEVICE void next() {
+    if (cls == 0) {
+      t += pairs;
+      if (t >= n0) second();
+    } else if (extra) {
+      t = --extra ? t + pairs - short_from : rest();
+    } else {
+      t += pairs;
+    }
+  }
 };
 
 template <int MODE>
@@ -201,12 +266,12 @@ DSV_DEVICE void act_both(float g, int act, float& a, float& slope) {
   slope = fmaf(a * (1.f - s), dz, s);
 }
 
-DSV_DEVICE void tile_of(const Shape& sh, int64_t t, int64_t& m, int64_t& n) {
-  const int64_t per = static_cast<int64_t>(sh.group) * sh.n_tiles;
+DSV_DEVICE void tile_of(const Product& pr, int64_t group, int64_t t, int64_t& m, int64_t& n) {
+  const int64_t per = group * pr.n_tiles;
   const int64_t g = t / per, r = t % per;
-  const int64_t left = sh.m_tiles - g * sh.group;
-  const int64_t gm = left < sh.group ? left : sh.group;
-  m = g * sh.group + r % gm;
+  const int64_t left = pr.m_tiles - g * group;
+  const int64_t gm = left < group ? left : group;
+  m = g * group + r % gm;
   n = r / gm;
 }
 
@@ -214,12 +279,11 @@ template <int MODE, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* status) {
   using C = Cfg<MODE>;
-  constexpr bool kGated = MODE == kGate || MODE == kGateGrad;
+  constexpr bool kGated = MODE == kGate || MODE == kGateGrad, kTwo = MODE == kBack;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) Bars bars;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cluster_rank());              // of this CTA in its pair
-  const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;     // the pair's tiles: first, first + step, ..
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;          // swizzled tiles need 1024-byte alignment
   const uint32_t out = ring + C::kStages * C::kStage;
@@ -259,15 +323,18 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
       Ring<C::kStages> at;
       int64_t issued = 0;   // stages
       bool ok = true;
-      for (int64_t t = first; t < sh.units && ok; t += step) {
+      for (Walk<kTwo> w(sh); w.more() && ok; w.next()) {
+        const Product& pr = sh.p[w.cls];
+        const bool dw = MODE == kDw || (kTwo && pr.dw);
         int64_t m, n;
-        tile_of(sh, SPLIT ? t % sh.tiles : t, m, n);
-        const bool second = MODE == kDw && m >= sh.half_tiles;
-        const int m0 = static_cast<int>((second ? m - sh.half_tiles : m) * 256) + rank * 128;
+        tile_of(pr, sh.group, SPLIT ? w.t % pr.tiles : w.t, m, n);
+        const bool second = dw && m >= pr.half_tiles;
+        const int m0 = static_cast<int>((second ? m - pr.half_tiles : m) * 256) + rank * 128;
         // B: the pair's second CTA holds the tile's second 128 columns (in the gated modes those of u)
         const int n0 = static_cast<int>(n * (kGated ? 128 : 256)) + (kGated ? 0 : rank * 128);
-        const int kb0 = SPLIT ? static_cast<int>(t / sh.tiles) * sh.kb_part : 0;
-        const int kb1 = SPLIT && kb0 + sh.kb_part < sh.kb ? kb0 + sh.kb_part : sh.kb;
+        const int kb0 = SPLIT ? static_cast<int>(w.t / pr.tiles) * pr.kb_part : 0;
+        const int kb1 = SPLIT && kb0 + pr.kb_part < pr.kb ? kb0 + pr.kb_part : pr.kb;
+        const int kb_half = !kGated && !dw ? pr.kb_half : kb1;   // dx: from here on the second of its two products
         for (int kb = kb0; kb < kb1; ++kb, ++issued, at.next()) {
           // (a fresh barrier passes for the parity before its first round)
           if (!wait_bar(empty0 + 8 * at.s, at.round ^ 1, fail)) {
@@ -276,22 +343,22 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
           }
           const uint32_t full = lead0 + 8 * at.s;
           const uint32_t a = ring + at.s * C::kStage, b = a + C::kStageA;
-          const bool late = MODE == kDx && kb >= sh.kb_half;   // the second of the two products
-          const int k0 = (late ? kb - sh.kb_half : kb) * kBK;
+          const bool late = kb >= kb_half;
+          const int k0 = (late ? kb - kb_half : kb) * kBK;
           if (for_a) {
             if (rank == 0) expect_tx(full0 + 8 * at.s, 2 * C::kStage);
-            const CUtensorMap* map = late || second ? &maps.a1 : &maps.a0;
-            if constexpr (MODE != kDw) {
-              tma_load_pair(a, map, k0, m0, full);
-            } else {
+            if (dw) {
+              const CUtensorMap* map = second ? &maps.t1 : &maps.t0;
               tma_load_pair(a, map, m0, k0, full);
               tma_load_pair(a + kTile / 2, map, m0 + 64, k0, full);
+            } else {
+              tma_load_pair(a, late ? &maps.a1 : &maps.a0, k0, m0, full);
             }
           } else {
-            const CUtensorMap* map = late || (kGated && rank == 1) ? &maps.b1 : &maps.b0;
             if constexpr (kGated) {
-              tma_load_pair(b, map, k0, n0, full);
+              tma_load_pair(b, rank == 1 ? &maps.b1 : &maps.b0, k0, n0, full);
             } else {
+              const CUtensorMap* map = dw ? &maps.b2 : late ? &maps.b1 : &maps.b0;
               tma_load_pair(b, map, n0, k0, full);
               tma_load_pair(b + kTile / 2, map, n0 + 64, k0, full);
             }
@@ -315,25 +382,29 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
   } else if (warp == 1) {
     // ================================================================ MMA issue (one thread of the pair)
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t id = tc::idesc_bf16(256, 256, MODE == kDw, !kGated);
-      static_assert(id >> 29 == 0 && ((id >> 24) & 31) == 16 && ((id >> 17) & 63) == 32, "M and N in their fields");
+      constexpr uint32_t id_k = tc::idesc_bf16(256, 256, 0, !kGated), id_mn = tc::idesc_bf16(256, 256, 1, 1);
+      static_assert((id_k | id_mn) >> 29 == 0 && ((id_k >> 24) & 31) == 16 && ((id_mn >> 24) & 31) == 16 &&
+                        ((id_k >> 17) & 63) == 32 && ((id_mn >> 17) & 63) == 32, "M and N in their fields");
       // descriptors of the first stage; a stage, and 16 elements of K in it, are so many 16-byte units on
       // (K-major: 16 elements are 32 bytes; MN-major: two 8-row groups of 1024 bytes, column blocks of 64
       // elements 8 KB apart)
-      constexpr bool kMnA = MODE == kDw, kMnB = !kGated;
-      const uint64_t a0 = kMnA ? tc::smem_desc(ring, kTile / 2, 1024) : tc::smem_desc(ring, 16, 1024);
-      const uint64_t b0 = kMnB ? tc::smem_desc(ring + C::kStageA, kTile / 2, 1024) : tc::smem_desc(ring + C::kStageA, 16, 1024);
-      constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
+      const uint64_t a_k = tc::smem_desc(ring, 16, 1024), a_mn = tc::smem_desc(ring, kTile / 2, 1024);
+      const uint64_t b0 = kGated ? tc::smem_desc(ring + C::kStageA, 16, 1024) : tc::smem_desc(ring + C::kStageA, kTile / 2, 1024);
+      constexpr uint32_t kStepK = 32 >> 4, kStepMn = 2048 >> 4, kStepB = kGated ? kStepK : kStepMn;
       Ring<C::kStages> at;
       int64_t tile = 0;
       bool ok = true;
-      for (int64_t t = first; t < sh.units && ok; t += step, ++tile) {
+      for (Walk<kTwo> w(sh); w.more() && ok; w.next(), ++tile) {
+        const Product& pr = sh.p[w.cls];
+        const bool dw = MODE == kDw || (kTwo && pr.dw);
+        const uint32_t id = dw ? id_mn : id_k, step_a = dw ? kStepMn : kStepK;
+        const uint64_t a0 = dw ? a_mn : a_k;
         const int buf = static_cast<int>(tile & 1);
         if (tile >= 2) ok = wait_bar(bar(bars.acc_empty[buf]), static_cast<uint32_t>(((tile >> 1) - 1) & 1), fail);
         tc::tc_fence_after();
         const uint32_t acc = tmem + buf * 256;
-        const int kb0 = SPLIT ? static_cast<int>(t / sh.tiles) * sh.kb_part : 0;
-        const int kb1 = SPLIT && kb0 + sh.kb_part < sh.kb ? kb0 + sh.kb_part : sh.kb;
+        const int kb0 = SPLIT ? static_cast<int>(w.t / pr.tiles) * pr.kb_part : 0;
+        const int kb1 = SPLIT && kb0 + pr.kb_part < pr.kb ? kb0 + pr.kb_part : pr.kb;
         for (int kb = kb0; kb < kb1 && ok; ++kb, at.next()) {
           const uint32_t s = at.s;
           ok = wait_bar(bar(bars.full[s]), at.round, fail);
@@ -341,7 +412,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
           tc::tc_fence_after();
           const uint64_t da = a0 + s * (C::kStage >> 4), db = b0 + s * (C::kStage >> 4);
 #pragma unroll
-          for (int j = 0; j < kBK / 16; ++j) mma_pair(acc, da + j * kStepA, db + j * kStepB, id, kb > kb0 || j > 0 ? 1u : 0u);
+          for (int j = 0; j < kBK / 16; ++j) mma_pair(acc, da + j * step_a, db + j * kStepB, id, kb > kb0 || j > 0 ? 1u : 0u);
           commit_pair(bar(bars.empty[s]));
         }
         if (ok) commit_pair(bar(bars.acc_full[buf]));
@@ -373,11 +444,15 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
     };
     int64_t tile = 0;
     bool ok = true;
-    for (int64_t t = first; t < sh.units && ok; t += step, ++tile) {
+    for (Walk<kTwo> w(sh); w.more() && ok; w.next(), ++tile) {
+      const Product& pr = sh.p[w.cls];
       int64_t m, n;
-      tile_of(sh, SPLIT ? t % sh.tiles : t, m, n);
-      const CUtensorMap* c_map = MODE == kDw && m >= sh.half_tiles ? &maps.c1 : &maps.c0;
-      if (MODE == kDw && m >= sh.half_tiles) m -= sh.half_tiles;
+      tile_of(pr, sh.group, SPLIT ? w.t % pr.tiles : w.t, m, n);
+      const CUtensorMap* c_map = &maps.c0;
+      if (MODE == kDw || (kTwo && pr.dw)) {
+        c_map = m >= pr.half_tiles ? &maps.c2 : &maps.c1;
+        if (m >= pr.half_tiles) m -= pr.half_tiles;
+      }
       const int m0 = static_cast<int>(m * 256) + rank * 128;
       const int n0 = static_cast<int>(n * (kGated ? 128 : 256) + wg * (kGated ? 64 : 128));
       const int buf = static_cast<int>(tile & 1);
@@ -385,20 +460,20 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
       // has to be free first, 16,384 x 2048 x 5632 took 462 us instead of 445)
       uint4 dh[MODE == kGateGrad && !SPLIT ? 8 : 1];
       if constexpr (MODE == kGateGrad && !SPLIT) {
-        const bool in = m0 + row < sh.rows;
-        const bf16* p = sh.dh + (m0 + row) * sh.cols + n0;
+        const bool in = m0 + row < pr.rows;
+        const bf16* p = sh.dh + (m0 + row) * pr.cols + n0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          dh[i] = in && n0 + 8 * i < sh.cols ? __ldg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
+          dh[i] = in && n0 + 8 * i < pr.cols ? __ldg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
       }
       ok = wait_bar(bar(bars.acc_full[buf]), static_cast<uint32_t>((tile >> 1) & 1), fail);
       ok = bar_all(1 + wg, 128, ok);                      // the warpgroup goes on together, or not at all
       if (!ok) break;
       tc::tc_fence_after();
       const uint32_t acc = tmem + lane_base + buf * 256;
-      if constexpr (SPLIT) {
+      if (SPLIT && (!kTwo || pr.partial)) {
         // a part of K: its sums as they are, joined with the others' by ffn_join_kernel
-        float4* to = reinterpret_cast<float4*>(sh.partial + ((t * 256 + rank * 128 + row) * 256 + wg * 128));
+        float4* to = reinterpret_cast<float4*>(pr.partial + ((w.t * 256 + rank * 128 + row) * 256 + wg * 128));
 #pragma unroll 1
         for (int c = 0; c < 128; c += 16) {
           uint32_t a[16];
@@ -412,7 +487,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) release_acc(buf);
-      } else {
+      } else if constexpr (!SPLIT || kTwo) {
         // 32 columns at a time through two staging tiles in turn: one is read by its store while the other fills (four
         // warpgroups with one tile each win where D is short, 16,384 x 128 x 1024 20 us instead of 23, and lose
         // elsewhere, 16,384 x 768 x 2048 67 instead of 64)
@@ -472,7 +547,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
           tc::fence_async_shared();
           bar_sync(1 + wg, 128);
           if (elect) {
-            if (m0 < sh.rows && n0 + part * 32 < sh.cols) {
+            if (m0 < pr.rows && n0 + part * 32 < pr.cols) {
               tma_store(c_map, n0 + part * 32, m0, st0);
               if (MODE == kGateGrad) tma_store(&maps.c1, n0 + part * 32, m0, st1);
             }
@@ -496,16 +571,16 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
 
 // ---------------------------------------------------------------- parts of K joined
 struct JoinOut {
-  bf16 *c0, *c1;    // kGate h; kGateGrad dg, du; kDx dx; kDw dWg, dWu
+  bf16 *c0, *c1, *c2;    // kGate h; kGateGrad dg, du; else dx, dWg, dWu
 };
 
 // 8 columns of a unit's row, summed over the parts in their order.
-DSV_DEVICE void join8(const Shape& sh, int64_t tile, int row, int col, float (&v)[8]) {
+DSV_DEVICE void join8(const Product& pr, int64_t tile, int row, int col, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.f;
 #pragma unroll 4
-  for (int64_t u = tile; u < sh.units; u += sh.tiles) {
-    const float4* p = reinterpret_cast<const float4*>(sh.partial + ((u * 256 + row) * 256 + col));
+  for (int64_t u = tile; u < pr.units; u += pr.tiles) {
+    const float4* p = reinterpret_cast<const float4*>(pr.partial + ((u * 256 + row) * 256 + col));
     const float4 a = __ldcg(p), b = __ldcg(p + 1);   // (of the kernel before: past L1)
     v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
     v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
@@ -516,25 +591,28 @@ DSV_DEVICE void store8(bf16* p, const float (&v)[8]) {
                                             pack_bf16x2(v[6], v[7]));
 }
 
-// One thread: 8 columns of a row of the result (blockIdx.y: kDw's second result).
+// One thread: 8 columns of a row of a result (blockIdx.y: of dx, dWg, dWu those the launch is for).
 template <int MODE>
 __global__ void __launch_bounds__(256) ffn_join_kernel(Shape sh, JoinOut o) {
   constexpr bool kGated = MODE == kGate || MODE == kGateGrad;
   asm volatile("griddepcontrol.launch_dependents;\n griddepcontrol.wait;\n" ::: "memory");
+  const int result = blockIdx.y + (MODE == kDw);   // 0, or 1 and 2: the weights' gradients
+  const Product& pr = sh.p[MODE == kBack && sh.p[0].dw != (result > 0)];
+  if (!pr.partial) return;   // whole tiles: stored by the products' kernel
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t per_row = sh.cols / 8;
-  if (i >= sh.rows * per_row) return;
+  const int64_t per_row = pr.cols / 8;
+  if (i >= pr.rows * per_row) return;
   const int64_t r = i / per_row, col = i % per_row * 8;
-  const int64_t m = r / 256 + (MODE == kDw ? blockIdx.y * sh.half_tiles : 0), n = col / (kGated ? 128 : 256);
-  const int64_t g = m / sh.group, left = sh.m_tiles - g * sh.group, gm = left < sh.group ? left : sh.group;
-  const int64_t tile = g * sh.group * sh.n_tiles + n * gm + (m - g * sh.group);   // tile_of's inverse
+  const int64_t m = r / 256 + (result > 1 ? pr.half_tiles : 0), n = col / (kGated ? 128 : 256);
+  const int64_t g = m / sh.group, left = pr.m_tiles - g * sh.group, gm = left < sh.group ? left : sh.group;
+  const int64_t tile = g * sh.group * pr.n_tiles + n * gm + (m - g * sh.group);   // tile_of's inverse
   const int row = static_cast<int>(r % 256), c = static_cast<int>(col % (kGated ? 128 : 256));
-  const int64_t at = r * sh.cols + col;
+  const int64_t at = r * pr.cols + col;
   float v[8];
-  join8(sh, tile, row, c, v);
+  join8(pr, tile, row, c, v);
   if constexpr (kGated) {
     float u[8];
-    join8(sh, tile, row, 128 + c, u);
+    join8(pr, tile, row, 128 + c, u);
     if constexpr (MODE == kGate) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = act_value(v[e], sh.act) * u[e];
@@ -554,7 +632,7 @@ __global__ void __launch_bounds__(256) ffn_join_kernel(Shape sh, JoinOut o) {
       store8(o.c1 + at, u);
     }
   } else {
-    store8((MODE == kDw && blockIdx.y ? o.c1 : o.c0) + at, v);
+    store8((result == 0 ? o.c0 : result == 1 ? o.c1 : o.c2) + at, v);
   }
 }
 
@@ -760,7 +838,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // 2048 -> 5632 15 / 23 us, 4096 -> 8192 35 / 41 us; 4 tokens 1024 -> 2816 12 / 15 us, 4096 -> 512 11 / 29 us,
 // 2048 -> 5632 28 / 23 us; backward of 1 token 1024 -> 2816 32 / 56 us, of 4 54 / 55 us, of 4 4096 -> 8192 251 / 134 us.
 bool few_rows(int64_t M, int64_t D, int64_t F) { return M <= 2 || (M <= 4 && D * F <= (1 << 22)); }
-constexpr int kSplitSaves = 24;     // k blocks that splitting K has to save
+// A part costs its sums' way to memory and back and a second launch, about 6 us or 24 k blocks: K is split where more
+// than that is saved.
+constexpr int kSplitSaves = 24;
 
 constexpr int64_t kPairs = 76;      // of CTAs, on the card's 152 SMs
 // m tiles that take the same n tiles in turn, so that their operands meet in L2: 19, so that the 76 pairs work on 19
@@ -768,32 +848,114 @@ constexpr int64_t kPairs = 76;      // of CTAs, on the card's 152 SMs
 // 1760 with 8 or 10; 16,384-token backward 1410, 1432, 1430).
 constexpr int kGroup = 19;
 
-// How one product is cut: tiles, and where they leave at least half of the pairs without work, parts of K.
-// A part costs its sums' way to memory and back and a second launch, about 6 us or 24 k blocks, so K is
-// split where that many are saved, into parts of 8 k blocks or more.
-Shape shape_of(Mode mode, int64_t M, int64_t D, int64_t F, int act) {
-  const bool gated = mode == kGate || mode == kGateGrad;
+Product product(Mode mode, int64_t M, int64_t D, int64_t F) {
+  const bool gated = mode == kGate || mode == kGateGrad, dw = mode == kDw;
+  Product p{};
+  p.dw = dw;
+  p.half_tiles = dw ? ceil_div(F, 256) : 0;
+  p.m_tiles = dw ? 2 * p.half_tiles : ceil_div(M, 256);
+  p.n_tiles = gated ? ceil_div(F, 128) : ceil_div(D, 256);
+  p.tiles = p.m_tiles * p.n_tiles;
+  p.kb_half = gated || dw ? 0 : static_cast<int>(ceil_div(F, kBK));
+  p.kb = gated ? static_cast<int>(ceil_div(D, kBK)) : dw ? static_cast<int>(ceil_div(M, kBK)) : 2 * p.kb_half;
+  p.rows = dw ? F : M;
+  p.cols = gated ? F : D;
+  return p;
+}
+void cut(Product& p, int64_t parts) {
+  p.kb_part = static_cast<int>(ceil_div(p.kb, parts));
+  p.units = p.tiles * ceil_div(p.kb, p.kb_part);
+}
+// Parts of K that a product may be cut into: of 8 k blocks or more, and where at least half of the pairs would have
+// no tile.
+int64_t most_parts(const Product& p) {
+  const int64_t parts = kPairs / p.tiles, long_enough = p.kb / 8;
+  const int64_t most = parts < long_enough ? parts : long_enough;
+  return most < 1 ? 1 : most;
+}
+
+// K blocks that the busiest pair works through, with the best `skip` for it (Walk's rounds, counted).
+int64_t busiest(const Shape& sh, int64_t* skip) {
+  const Product &a = sh.p[0], &b = sh.p[1];
+  const int64_t pairs = a.units + b.units < kPairs ? a.units + b.units : kPairs;
+  const int64_t rounds = a.units / pairs, h = a.units % pairs, l = h ? pairs - h : 0;
+  int64_t best = 0;
+  for (int64_t s = 0; s <= 8 && s * l <= b.units; ++s) {
+    const int64_t left = b.units - s * l, full = left / pairs, rest = left % pairs;
+    const int64_t few = rounds * a.kb_part + (s + full + (rest > 0)) * b.kb_part;
+    const int64_t many = h ? (rounds + 1) * a.kb_part + (full + (rest > l)) * b.kb_part : 0;
+    const int64_t most = few > many ? few : many;
+    if (s == 0 || most < best) {
+      best = most;
+      *skip = s;
+    }
+    if (!l) break;
+  }
+  return best;
+}
+
+// One product: whole tiles, or parts of K where that saves more than a part costs.
+Shape one_shape(Mode mode, int64_t M, int64_t D, int64_t F, int act) {
   Shape sh{};
-  sh.half_tiles = mode == kDw ? ceil_div(F, 256) : 0;
-  sh.m_tiles = mode == kDw ? 2 * sh.half_tiles : ceil_div(M, 256);
-  sh.n_tiles = gated ? ceil_div(F, 128) : ceil_div(D, 256);
-  sh.tiles = sh.m_tiles * sh.n_tiles;
-  sh.kb_half = mode == kDx ? static_cast<int>(ceil_div(F, kBK)) : 0;
-  sh.kb = gated ? static_cast<int>(ceil_div(D, kBK)) : mode == kDx ? 2 * sh.kb_half : static_cast<int>(ceil_div(M, kBK));
-  sh.rows = mode == kDw ? F : M;
-  sh.cols = gated ? F : D;
+  sh.p[0] = product(mode, M, D, F);
   sh.group = kGroup;
   sh.act = act;
-  int64_t parts = kPairs / sh.tiles;
-  if (parts > sh.kb / 8) parts = sh.kb / 8;
-  if (parts < 2 || sh.kb - sh.kb / parts < kSplitSaves) parts = 1;
-  sh.kb_part = static_cast<int>(ceil_div(sh.kb, parts));
-  parts = ceil_div(sh.kb, sh.kb_part);
-  sh.units = sh.tiles * parts;
+  int64_t parts = most_parts(sh.p[0]);
+  if (sh.p[0].kb - sh.p[0].kb / parts < kSplitSaves) parts = 1;
+  cut(sh.p[0], parts);
   return sh;
 }
-size_t partial_bytes(const Shape& sh) {
-  return sh.units > sh.tiles ? static_cast<size_t>(sh.units) * 256 * 256 * sizeof(float) : 0;
+
+// The backward's last two products in one launch: the longer units first, and either cut into parts of K where the
+// busiest pair is saved more than the parts cost.
+int64_t split_cost(const Product& p) { return p.units > p.tiles ? kSplitSaves : 0; }
+Shape back_shape(int64_t M, int64_t D, int64_t F, int64_t* cost) {
+  Product dx = product(kDx, M, D, F), dw = product(kDw, M, D, F);
+  const int64_t most_dx = most_parts(dx), most_dw = most_parts(dw);
+  Shape best{};
+  *cost = -1;
+  for (int64_t i = 1; i <= most_dx; i += 1 + i / 2)      // (1, 2, 4, 7, 11, ..)
+    for (int64_t j = 1; j <= most_dw; j += 1 + j / 2) {
+      cut(dx, i);
+      cut(dw, j);
+      Shape sh{};
+      sh.p[0] = dx.kb_part > dw.kb_part ? dx : dw;
+      sh.p[1] = dx.kb_part > dw.kb_part ? dw : dx;
+      const int64_t c = busiest(sh, &sh.skip) + (split_cost(dx) > split_cost(dw) ? split_cost(dx) : split_cost(dw));
+      if (*cost < 0 || c < *cost) {
+        *cost = c;
+        best = sh;
+      }
+    }
+  best.group = kGroup;
+  return best;
+}
+struct BackPlan {
+  bool merged;
+  Shape both, dx, dw;
+};
+// Whether they share a launch.  It saves the rounds in which one product leaves pairs idle, and a launch (kLaunch k
+// blocks); but its pairs fall out of step, and tiles that were read together no longer meet in L2, which costs a
+// long run about 6 % (16,384 x 2048 x 5632: 810 us merged, 792 in two launches, for 2432 against 2512 k blocks; 2048 x
+// 1024 x 2816 backward 54 us merged, 73 in two, for 152 against 216).
+constexpr int64_t kLaunch = 16;
+BackPlan back_plan(int64_t M, int64_t D, int64_t F) {
+  BackPlan b{};
+  int64_t merged = 0, skip = 0;
+  b.both = back_shape(M, D, F, &merged);
+  b.dx = one_shape(kDx, M, D, F, 0);
+  b.dw = one_shape(kDw, M, D, F, 0);
+  const int64_t apart = busiest(b.dx, &skip) + split_cost(b.dx.p[0]) + busiest(b.dw, &skip) + split_cost(b.dw.p[0]);
+  b.merged = merged + merged / 16 < apart + kLaunch;
+  return b;
+}
+size_t partial_bytes(const Product& p) {
+  return p.units > p.tiles ? static_cast<size_t>(p.units) * 256 * 256 * sizeof(float) : 0;
+}
+size_t partial_bytes(const Shape& sh) { return partial_bytes(sh.p[0]) + partial_bytes(sh.p[1]); }
+size_t partial_bytes(const BackPlan& b) {
+  const size_t dx = partial_bytes(b.dx), dw = partial_bytes(b.dw);
+  return b.merged ? partial_bytes(b.both) : dx > dw ? dx : dw;
 }
 
 // A kernel that may set itself up while the one before it on the stream ends.
@@ -819,7 +981,8 @@ cudaError_t launch_part(const char* name, const Maps& maps, const Shape& sh, boo
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * (sh.units < kPairs ? sh.units : kPairs)));
+  const int64_t units = sh.p[0].units + sh.p[1].units;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (units < kPairs ? units : kPairs)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
@@ -838,14 +1001,19 @@ cudaError_t launch_part(const char* name, const Maps& maps, const Shape& sh, boo
 template <int MODE>
 cudaError_t launch_gemm(const char* name, const Maps& maps, Shape sh, bool first, float* partial, const JoinOut& out,
                         unsigned int* status, cudaStream_t stream) {
-  if (sh.units == sh.tiles) return launch_part<MODE, false>(name, maps, sh, first, status, stream);
-  sh.partial = partial;
+  if (!partial_bytes(sh)) return launch_part<MODE, false>(name, maps, sh, first, status, stream);
+  int64_t vectors = 0;
+  for (Product& p : sh.p) {
+    if (!partial_bytes(p)) continue;
+    p.partial = partial;
+    partial += partial_bytes(p) / sizeof(float);
+    if (p.rows * (p.cols / 8) > vectors) vectors = p.rows * (p.cols / 8);
+  }
   cudaError_t e = launch_part<MODE, true>(name, maps, sh, first, status, stream);
   if (e != cudaSuccess) return e;
   ProfScope prof("ffn_join", stream);
-  return launch_after(ffn_join_kernel<MODE>,
-                      dim3(static_cast<unsigned>(ceil_div(sh.rows * (sh.cols / 8), 256)), MODE == kDw ? 2 : 1), stream, sh,
-                      out);
+  return launch_after(ffn_join_kernel<MODE>, dim3(static_cast<unsigned>(ceil_div(vectors, 256)), MODE == kBack ? 3 : MODE == kDw ? 2 : 1),
+                      stream, sh, out);
 }
 
 template <int R, bool GRAD>
@@ -912,17 +1080,13 @@ size_t half_bytes(int64_t M, int64_t F) { return (sizeof(bf16) * static_cast<siz
 }  // namespace
 
 size_t ffn_fwd_workspace(int64_t M, int64_t D, int64_t F) {
-  return few_rows(M, D, F) ? 0 : partial_bytes(shape_of(kGate, M, D, F, 0));
+  return few_rows(M, D, F) ? 0 : partial_bytes(one_shape(kGate, M, D, F, 0));
 }
 
 size_t ffn_bwd_workspace(int64_t M, int64_t D, int64_t F) {
   if (few_rows(M, D, F)) return rows_back(M, D, F).total;
-  size_t most = 0;
-  for (Mode mode : {kGateGrad, kDx, kDw}) {
-    const size_t b = partial_bytes(shape_of(mode, M, D, F, 0));
-    if (b > most) most = b;
-  }
-  return 2 * half_bytes(M, F) + most;
+  const size_t grad = partial_bytes(one_shape(kGateGrad, M, D, F, 0)), back = partial_bytes(back_plan(M, D, F));
+  return 2 * half_bytes(M, F) + (grad > back ? grad : back);
 }
 
 cudaError_t launch_ffn_gated_fwd(const FfnParams& p, cudaStream_t stream) {
@@ -932,8 +1096,8 @@ cudaError_t launch_ffn_gated_fwd(const FfnParams& p, cudaStream_t stream) {
   if (!make_map(&maps.a0, p.x, p.M, p.D, 128) || !make_map(&maps.b0, p.w_gate, p.F, p.D, 128) ||
       !make_map(&maps.b1, p.w_up, p.F, p.D, 128) || !make_map(&maps.c0, p.h, p.M, p.F, 128, 32))
     return cudaErrorInvalidValue;
-  return launch_gemm<kGate>("ffn_gate", maps, shape_of(kGate, p.M, p.D, p.F, p.act), true,
-                            static_cast<float*>(p.ws), JoinOut{p.h, nullptr}, p.status, stream);
+  return launch_gemm<kGate>("ffn_gate", maps, one_shape(kGate, p.M, p.D, p.F, p.act), true,
+                            static_cast<float*>(p.ws), JoinOut{p.h, nullptr, nullptr}, p.status, stream);
 }
 
 cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream) {
@@ -942,29 +1106,26 @@ cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream) {
   char* ws = static_cast<char*>(p.ws);
   bf16 *dg = reinterpret_cast<bf16*>(ws), *du = reinterpret_cast<bf16*>(ws + half_bytes(p.M, p.F));
   float* partial = reinterpret_cast<float*>(ws + 2 * half_bytes(p.M, p.F));
-  Maps grad{}, dx{}, dw{};
+  Maps grad{}, back{};
   if (!make_map(&grad.a0, p.x, p.M, p.D, 128) || !make_map(&grad.b0, p.w_gate, p.F, p.D, 128) ||
       !make_map(&grad.b1, p.w_up, p.F, p.D, 128) ||
       !make_map(&grad.c0, dg, p.M, p.F, 128, 32) || !make_map(&grad.c1, du, p.M, p.F, 128, 32) ||
-      !make_map(&dx.a0, dg, p.M, p.F, 128) || !make_map(&dx.a1, du, p.M, p.F, 128) ||
-      !make_map(&dx.b0, p.w_gate, p.F, p.D, 64) || !make_map(&dx.b1, p.w_up, p.F, p.D, 64) ||
-      !make_map(&dx.c0, p.dx, p.M, p.D, 128, 32) ||
-      !make_map(&dw.a0, dg, p.M, p.F, 64) || !make_map(&dw.a1, du, p.M, p.F, 64) ||
-      !make_map(&dw.b0, p.x, p.M, p.D, 64) || !make_map(&dw.c0, p.dw_gate, p.F, p.D, 128, 32) ||
-      !make_map(&dw.c1, p.dw_up, p.F, p.D, 128, 32))
+      !make_map(&back.a0, dg, p.M, p.F, 128) || !make_map(&back.a1, du, p.M, p.F, 128) ||
+      !make_map(&back.t0, dg, p.M, p.F, 64) || !make_map(&back.t1, du, p.M, p.F, 64) ||
+      !make_map(&back.b0, p.w_gate, p.F, p.D, 64) || !make_map(&back.b1, p.w_up, p.F, p.D, 64) ||
+      !make_map(&back.b2, p.x, p.M, p.D, 64) || !make_map(&back.c0, p.dx, p.M, p.D, 128, 32) ||
+      !make_map(&back.c1, p.dw_gate, p.F, p.D, 128, 32) || !make_map(&back.c2, p.dw_up, p.F, p.D, 128, 32))
     return cudaErrorInvalidValue;
-  Shape grad_shape = shape_of(kGateGrad, p.M, p.D, p.F, p.act);
+  Shape grad_shape = one_shape(kGateGrad, p.M, p.D, p.F, p.act);
   grad_shape.dh = p.dh;
-  cudaError_t e = launch_gemm<kGateGrad>("ffn_gate_grad", grad, grad_shape, true, partial, JoinOut{dg, du}, p.status,
-                                         stream);
-  if (e == cudaSuccess)
-    e = launch_gemm<kDx>("ffn_dx", dx, shape_of(kDx, p.M, p.D, p.F, p.act), false, partial,
-                         JoinOut{p.dx, nullptr},
-                         p.status, stream);
-  if (e == cudaSuccess)
-    e = launch_gemm<kDw>("ffn_dw", dw, shape_of(kDw, p.M, p.D, p.F, p.act), false, partial,
-                         JoinOut{p.dw_gate, p.dw_up}, p.status, stream);
-  return e;
+  cudaError_t e = launch_gemm<kGateGrad>("ffn_gate_grad", grad, grad_shape, true, partial, JoinOut{dg, du, nullptr},
+                                         p.status, stream);
+  if (e != cudaSuccess) return e;
+  const BackPlan plan = back_plan(p.M, p.D, p.F);
+  const JoinOut out{p.dx, p.dw_gate, p.dw_up};
+  if (plan.merged) return launch_gemm<kBack>("ffn_back", back, plan.both, false, partial, out, p.status, stream);
+  e = launch_gemm<kDx>("ffn_dx", back, plan.dx, false, partial, out, p.status, stream);
+  return e != cudaSuccess ? e : launch_gemm<kDw>("ffn_dw", back, plan.dw, false, partial, out, p.status, stream);
 }
 
 }  // namespace dsv
