@@ -17,8 +17,8 @@
 // rows are issued before the first is used, which is what keeps HBM busy (no staging is needed:
 // nothing is read twice).  Measured (GB300, 16 heads of 128, 65,536 tokens; a plain copy runs at 6.67 TB/s): rope3d
 // 6.3 TB/s, norm and rotation forward 241 us = 6.7 TB/s (520,192 tokens 1.82 ms = 7.0), backward 341 us = 6.3 TB/s,
-// in halves 364.  One head of 524,288 tokens: forward 215 us, backward 311 us, half of that rate, for each token's
-// positions and table.
+// halves 2 to 4 % below.  One head of 524,288 tokens: forward 216 us, backward 311 us, about half of that rate, for
+// each token's positions and table; two heads are at 0.82 and 0.74 of the copy, eight at the rates above.
 #include <type_traits>
 
 #include "dsv_common.cuh"
@@ -80,15 +80,18 @@ DSV_DEVICE Pos load_pos(const RopeGeom& g, const int32_t* __restrict__ pos, int6
 }
 
 // sign: +1 forward, -1 backward.  An axis whose position is outside its table leaves its pairs
-// unrotated (angle 0) and sets the status bit.
+// unrotated (angle 0) and sets the status bit.  All lanes of the warp call it.
+// A lane reads four pairs.  In halves two vectors turn by the same eight: each lane gets the other four from its partner
+// (pairs are read 64 bytes apart there, many L1 accesses to a load: with all eight read by both, 524,288 tokens of one
+// head took 330 us forward and 396 backward where they take 285 and 336; 131,072 of 16 heads 483 and 710, now 477 and 690).
 template <bool HALF>
 DSV_DEVICE void make_turn(Turn<HALF>& t, const RopeGeom& g, const float2* __restrict__ table, const Pos& pos,
-                          bool active, int vec, float sign, unsigned int* status) {
+                          bool active, int vec, int partner, float sign, unsigned int* status) {
   const int half_vecs = g.pairs / 8;   // HALF: vectors of a half (pairs is a multiple of 8)
+  const bool second = HALF && vec >= half_vecs;
   int j0;
   if (HALF) {
-    const bool second = vec >= half_vecs;
-    j0 = (second ? vec - half_vecs : vec) * 8;
+    j0 = second ? (vec - half_vecs) * 8 + 4 : vec * 8;
     t.turned = vec < 2 * half_vecs ? 8 : 0;
     if (!second) sign = -sign;   // y0 = x0 c - x1 s; y1 = x1 c + x0 s
   } else {
@@ -101,30 +104,42 @@ DSV_DEVICE void make_turn(Turn<HALF>& t, const RopeGeom& g, const float2* __rest
     t.c[i] = 1.f;
     t.s[i] = 0.f;
   }
-  if (!active || t.turned == 0) return;
-  int p[3];
+  if (active && t.turned != 0) {
+    int p[3];
 #pragma unroll
-  for (int a = 0; a < 3; ++a) {
-    p[a] = pos.v[a];
-    if (g.axis_pairs[a] > 0 && static_cast<uint32_t>(p[a]) >= static_cast<uint32_t>(g.len[a])) {
-      flag_status(status, kStatusBadPosition);
-      p[a] = -1;
+    for (int a = 0; a < 3; ++a) {
+      p[a] = pos.v[a];
+      if (g.axis_pairs[a] > 0 && static_cast<uint32_t>(p[a]) >= static_cast<uint32_t>(g.len[a])) {
+        flag_status(status, kStatusBadPosition);
+        p[a] = -1;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = j0 + i;
+      if (i >= t.turned) continue;
+      int a = 0, first = 0;
+      if (j >= g.axis_pairs[0]) { a = 1; first = g.axis_pairs[0]; }
+      if (j >= g.axis_pairs[0] + g.axis_pairs[1]) { a = 2; first = g.axis_pairs[0] + g.axis_pairs[1]; }
+      const int pa = a == 0 ? p[0] : a == 1 ? p[1] : p[2];
+      const int np = a == 0 ? g.axis_pairs[0] : a == 1 ? g.axis_pairs[1] : g.axis_pairs[2];
+      const int64_t off = a == 0 ? 0 : a == 1 ? g.table_off[1] : g.table_off[2];
+      if (pa < 0) continue;
+      const float2 cs = __ldg(table + off + static_cast<int64_t>(pa) * np + (j - first));
+      t.c[i] = cs.x;
+      t.s[i] = HALF ? cs.y : sign * cs.y;
     }
   }
+  if constexpr (HALF) {
 #pragma unroll
-  for (int i = 0; i < Turn<HALF>::P; ++i) {
-    const int j = j0 + i;
-    if (i >= t.turned) continue;
-    int a = 0, first = 0;
-    if (j >= g.axis_pairs[0]) { a = 1; first = g.axis_pairs[0]; }
-    if (j >= g.axis_pairs[0] + g.axis_pairs[1]) { a = 2; first = g.axis_pairs[0] + g.axis_pairs[1]; }
-    const int pa = a == 0 ? p[0] : a == 1 ? p[1] : p[2];
-    const int np = a == 0 ? g.axis_pairs[0] : a == 1 ? g.axis_pairs[1] : g.axis_pairs[2];
-    const int64_t off = a == 0 ? 0 : a == 1 ? g.table_off[1] : g.table_off[2];
-    if (pa < 0) continue;
-    const float2 cs = __ldg(table + off + static_cast<int64_t>(pa) * np + (j - first));
-    t.c[i] = cs.x;
-    t.s[i] = sign * cs.y;
+    for (int i = 0; i < 4; ++i) {
+      const float c = t.c[i], s = t.s[i];
+      const float oc = __shfl_sync(0xffffffffu, c, partner), os = __shfl_sync(0xffffffffu, s, partner);
+      t.c[i] = second ? oc : c;
+      t.s[i] = sign * (second ? os : s);
+      t.c[i + 4] = second ? c : oc;
+      t.s[i + 4] = sign * (second ? s : os);
+    }
   }
 }
 
@@ -198,9 +213,9 @@ rope3d_kernel(RopeGeom g, RopeView x, RopeView y, const int32_t* __restrict__ po
   bf16* yp = y.p + l.b * y.sb + l.n * y.sn + vec * 8;
   uint4 next[U];
   load_rows<U>(next, xp, x.sh, l.h0, l);   // on their way while the table is read
-  Turn<HALF> t;
-  make_turn<HALF>(t, g, table, load_pos(g, pos, pos_row(g, l), l.active), l.active, vec, sign, status);
   const int partner = HALF ? partner_lane<LPR>(g, threadIdx.x & 31, vec) : 0;
+  Turn<HALF> t;
+  make_turn<HALF>(t, g, table, load_pos(g, pos, pos_row(g, l), l.active), l.active, vec, partner, sign, status);
   for (int h = l.h0; h < l.h1; h += U) {
     uint4 v[U];
 #pragma unroll
@@ -248,7 +263,7 @@ DSV_DEVICE uint4 load_weight(const bf16* w, int vec) {
 }
 
 // Pairs in halves need 143 registers: held to 128 a fourth CTA fits on the SM (mid clip 285 -> 252 us; the
-// interleaved form has 112, and any bound there costs it: 247 -> 268 us).
+// interleaved form has 96, and any bound there costs it: 247 -> 268 us).
 template <int D, bool HALF, int U>
 __global__ void __launch_bounds__(kThreads, HALF ? 4 : 0)
 qk_norm_rope_fwd_kernel(RopeGeom g, RopeView q, RopeView k, RopeView v, RopeView qo, RopeView ko, RopeView vo,
@@ -271,9 +286,9 @@ qk_norm_rope_fwd_kernel(RopeGeom g, RopeView q, RopeView k, RopeView v, RopeView
     if (has_v) load_rows<U>(nc, vp, v.sh, h, l);
   };
   fetch(l.h0);   // on their way while the table and the weights are read
-  Turn<HALF> t;
-  make_turn<HALF>(t, g, table, load_pos(g, pos, pos_row(g, l), l.active), l.active, vec, 1.f, status);
   const int partner = HALF ? partner_lane<LPR>(g, threadIdx.x & 31, vec) : 0;
+  Turn<HALF> t;
+  make_turn<HALF>(t, g, table, load_pos(g, pos, pos_row(g, l), l.active), l.active, vec, partner, 1.f, status);
   const uint4 fq = load_weight(wq, vec), fk = load_weight(wk, vec);
   uint4 fqp = fq, fkp = fk;
   if constexpr (HALF) {
@@ -378,7 +393,7 @@ qk_norm_rope_bwd_kernel(RopeGeom g, RopeView dqo, RopeView dko, RopeView dvo, Ro
   Pos ahead = load_pos(g, pos, pos_row(g, l), l.active);
   for (int64_t unit = blockIdx.x; unit < g.units; unit += gridDim.x) {
     Turn<HALF> t;
-    make_turn<HALF>(t, g, table, ahead, l.active, vec, -1.f, status);
+    make_turn<HALF>(t, g, table, ahead, l.active, vec, partner, -1.f, status);
     Lane nl = l;
     nl.active = false;
     if (unit + gridDim.x < g.units) {
