@@ -19,11 +19,11 @@
 // of the columns, through swizzled staging tiles that TMA stores write (rows and columns past the matrices
 // are clipped there, and zero-filled by the loads).  Every wait is bounded.
 //
-// What bounds it (GB300, M x D x F): the tensor cores.  65,536 x 2048 x 5632 forward 1.51 ms = 2.0 PFLOP/s from a cool start,
-// the rate of the library's plain product of that size (1.51 ms), 527 to 540 of the ideal 512 cycles to a
-// stage; run for a second the card's 1.4 kW limit holds both back (1.72 ms here, 1.69 ms there).
-// 16,384-token backward 1.30 ms = 1.75 PFLOP/s: its three products pass 0.6 GB of dh, dg and du and end in
-// partial rounds of tiles.  Short D is bound by the epilogue and, where rows do not start on 128 bytes,
+// What bounds it (GB300, M x D x F): the tensor cores.  65,536 x 2048 x 5632 forward 1.48 ms = 2.05 PFLOP/s from a cool start
+// (a library's plain product of that size 1.51 ms), 520 to 540 of the ideal 512 cycles to a
+// stage; run for a second the card's 1.4 kW limit holds both back (1.71 ms here, 1.69 ms there).
+// 16,384-token backward 1.21 to 1.29 ms = 1.76 to 1.88 PFLOP/s, 1.39 at the limit: its three products pass 0.6 GB of dh, dg
+// and du and end in partial rounds of tiles.  Few tiles: 5.5 us a launch and 0.28 us a stage.  Short D is bound by the epilogue and, where rows do not start on 128 bytes,
 // by the loads: 34,070 x 360 x 3312 forward 155 us against 85.  A pair beats single CTAs of 128 x 256 tiles (1.74 ms)
 // for its half B to a CTA and six stages instead of four; pairs of pairs that shared B by multicast ran at
 // the same cycles to a stage on 144 of the 152 SMs (1.69 ms).
