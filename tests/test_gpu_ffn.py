@@ -113,6 +113,25 @@ def guarded(t, pad=4096):
     return view, buf, pad
 
 
+# dx and the weights' gradients in one launch or two, either cut along K, either first, with and without units that
+# a pair takes ahead of the others
+CUTS = [(10127, 8, 1320), (4, 2600, 6232), (10155, 8, 5112), (10796, 8, 8), (2216, 8, 264), (8846, 8, 320), (513, 8, 1056),
+        (806, 8, 4696), (5, 8, 6704), (2205, 8, 456), (1187, 8, 2880), (4948, 8, 1048), (792, 3088, 8)]
+
+
+@pytest.mark.parametrize("M,D,F", CUTS)
+def test_backward_however_it_is_cut(M, D, F):
+    need_gpu()
+    c = case(M, D, F, seed=5)
+    g = {n: t.cuda() for n, t in c.items()}
+    ws = torch.full((dsv_ffn_gated_bwd_workspace(M, D, F),), 0xff, dtype=torch.uint8, device="cuda")   # NaN sums
+    first = dsv_ffn_gated_bwd(g["dh"], g["x"], g["wg"], g["wu"], workspace=ws)
+    assert dsv_last_device_status() == 0
+    check_bwd(c, *first, "silu")
+    again = dsv_ffn_gated_bwd(g["dh"], g["x"], g["wg"], g["wu"], workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
 @pytest.mark.parametrize("M,D,F", [(1, 8, 8), (129, 136, 264), (300, 200, 120), (40, 4096, 264), (16, 136, 6200)])
 def test_nothing_around_the_outputs_is_written(M, D, F):
     need_gpu()
