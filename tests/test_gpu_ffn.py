@@ -230,6 +230,27 @@ def test_leading_dims_repeatability_streams_and_graphs():
     assert dsv_last_device_status() == 0
 
 
+def test_offsets_past_32_bits():
+    """h, dh, dg and du of more than 2^31 elements: the last rows as a call of their own (dh is zero before them, so
+    the weights' gradients are theirs too)."""
+    need_gpu()
+    last, D, F = 300, 8, 1032
+    M = 2 ** 21 + 5
+    assert (M - last) * F > 2 ** 31
+    c = case(last, D, F, seed=9)
+    x, dh = torch.ones(M, D, dtype=BF16, device="cuda"), torch.zeros(M, F, dtype=BF16, device="cuda")
+    x[-last:], dh[-last:] = c["x"].cuda(), c["dh"].cuda()
+    wg, wu = c["wg"].cuda(), c["wu"].cuda()
+    h = dsv_ffn_gated_fwd(x, wg, wu)
+    check_fwd(c, h[-last:], "silu")
+    assert torch.equal(h[0], h[M - last - 1])   # rows of ones, first and last of them
+    del h
+    dx, dwg, dwu = dsv_ffn_gated_bwd(dh, x, wg, wu)
+    assert dsv_last_device_status() == 0
+    check_bwd(c, dx[-last:], dwg, dwu, "silu")
+    assert not dx[:M - last].any()
+
+
 def test_gradients_against_differences():
     """Central differences of the fp64 loss sum(dh * forward) along random directions: what separates them is the
     roundings of the gradient's entries (norm NORM), of random sign against a random direction."""
