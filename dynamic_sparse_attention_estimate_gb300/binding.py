@@ -523,6 +523,22 @@ def _rope_dims(shape: Tuple[int, ...], axes: Tuple, lengths: Tuple, pairing: str
     return dims, 2 * sum((r // 2) * n for r, n in zip(axes, lengths))
 
 
+# strides as the calls take them (read only, and the same for every call on one layout)
+@functools.lru_cache(maxsize=256)
+def _view_strides(strides: Tuple[int, ...]) -> ViewStrides:
+    return ViewStrides(*strides)
+
+
+@functools.lru_cache(maxsize=256)
+def _strides6(strides: Tuple[int, ...]):
+    return _Strides6(*strides)
+
+
+@functools.lru_cache(maxsize=256)
+def _strides9(strides: Tuple[int, ...]):
+    return _Strides9(*strides)
+
+
 @functools.lru_cache(maxsize=256)
 def _qk_norm_rope_ws(B: int, H: int, N: int, d: int) -> int:
     return int(load_library().dsv_qk_norm_rope_bwd_workspace(ctypes.byref(RopeDims(B, H, N, d))))
@@ -589,7 +605,7 @@ def _rope_args(x: torch.Tensor, pos: Optional[torch.Tensor], rope: Optional[Rope
 def _call(name: str, device: int, *args):
     """One library call on this device's current stream, with the device made current for it."""
     f = getattr(load_library(), name)
-    if torch.cuda.current_device() == device:
+    if torch._C._cuda_getDevice() == device:
         status = f(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
@@ -615,15 +631,16 @@ def dsv_rope3d_table(axes: Sequence[int], lengths: Sequence[int], theta: Union[f
 
 
 def _rope3d(fn: str, name: str, x: torch.Tensor, pos: torch.Tensor, rope: RopeTable, out: Optional[torch.Tensor]):
-    xs = _need_view(x, name)
+    xs = _view_strides(_need_view(x, name))
     if rope is None:
         raise ValueError("need a RopeTable")
     dims, pos_ptr, table_ptr = _rope_args(x, pos, rope, 0.0)
-    device = x.get_device()
+    device, os_ = x.get_device(), None
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    os_ = _need_view(out, "out", x.shape, device)
-    _call(fn, device, dims, x.data_ptr(), ViewStrides(*xs), pos_ptr, table_ptr, out.data_ptr(), ViewStrides(*os_))
+    else:
+        os_ = _view_strides(_need_view(out, "out", x.shape, device))
+    _call(fn, device, dims, x.data_ptr(), xs, pos_ptr, table_ptr, out.data_ptr(), os_)
     return out
 
 
@@ -659,7 +676,7 @@ def dsv_qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Ten
     else:
         qo, ko, vo = out
         _need_on(torch.bfloat16, shape, device, (qo, "q_out"), (ko, "k_out"), (vo, "v_out"))
-    _call("dsv_qk_norm_rope_fwd", device, dims, q.data_ptr(), k.data_ptr(), _ptr(v), _Strides9(*strides), _ptr(wq),
+    _call("dsv_qk_norm_rope_fwd", device, dims, q.data_ptr(), k.data_ptr(), _ptr(v), _strides9(strides), _ptr(wq),
           _ptr(wk), pos_ptr, table_ptr, _ptr(qo), _ptr(ko), _ptr(vo))
     return qo, ko, vo
 
@@ -698,8 +715,8 @@ def dsv_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, dv_out: Opt
     dwk = None if wk is None else torch.empty((d,), dtype=torch.float32, device=q.device)
     ws, nbytes, _keep = _workspace(workspace, 0 if wq is None and wk is None else _qk_norm_rope_ws(B, H, N, d), q)
     _call("dsv_qk_norm_rope_bwd", device, dims, _ptr(dq_out), _ptr(dk_out), _ptr(dv_out), q.data_ptr(),
-          k.data_ptr(), _Strides6(*strides), _ptr(wq), _ptr(wk), pos_ptr, table_ptr, _ptr(dq), _ptr(dk), _ptr(dv),
-          _Strides9(*dstrides), _ptr(dwq), _ptr(dwk), ws, nbytes)
+          k.data_ptr(), _strides6(strides), _ptr(wq), _ptr(wk), pos_ptr, table_ptr, _ptr(dq), _ptr(dk), _ptr(dv),
+          _strides9(dstrides), _ptr(dwq), _ptr(dwk), ws, nbytes)
     return dq, dk, dv, dwq, dwk
 
 
