@@ -591,6 +591,8 @@ def _rope_args(x: torch.Tensor, pos: Optional[torch.Tensor], rope: Optional[Rope
     device = x.get_device()
     if pos is None:
         raise ValueError("a RopeTable needs pos")
+    if not isinstance(pos, torch.Tensor):
+        raise TypeError("pos must be a torch.Tensor")
     batched = pos.dim() == 3
     dims, numbers = _rope_dims(shape, tuple(rope.axes), tuple(rope.lengths), rope.pairing, batched, float(eps))
     _need_on(torch.int32, (shape[0], shape[2], 3) if batched else (shape[2], 3), device, (pos, "pos"))

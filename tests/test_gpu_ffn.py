@@ -230,6 +230,32 @@ def test_leading_dims_repeatability_streams_and_graphs():
     assert dsv_last_device_status() == 0
 
 
+def test_host_threads_side_by_side():
+    """Calls of three host threads on streams of their own, in turn on sizes that take different kernels."""
+    import threading
+    need_gpu()
+    cases = [{n: t.cuda() for n, t in case(*s).items()} for s in ((300, 512, 1232), (777, 776, 520), (5, 1000, 104), (2, 72, 136))]
+    step = lambda g: (dsv_ffn_gated_fwd(g["x"], g["wg"], g["wu"]), *dsv_ffn_gated_bwd(g["dh"], g["x"], g["wg"], g["wu"]))
+    want = [step(g) for g in cases]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for i in range(40):
+                got = step(cases[i % 4])
+                stream.synchronize()
+                wrong.extend(i for a, w in zip(got, want[i % 4]) if not torch.equal(a, w))
+
+    threads = [threading.Thread(target=work) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and dsv_last_device_status() == 0
+
+
 def test_offsets_past_32_bits():
     """h, dh, dg and du of more than 2^31 elements: the last rows as a call of their own (dh is zero before them, so
     the weights' gradients are theirs too)."""

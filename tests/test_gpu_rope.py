@@ -407,6 +407,21 @@ def test_graph_capture_and_other_streams():
 
 
 @pytest.mark.slow
+def test_positions_from_any_row_of_a_list():
+    need_gpu()
+    latent = (2, 5, 7)
+    pos, rope = token_positions(latent, None).cuda(), dsv_rope3d_table((24, 20, 20), latent)
+    x = torch.randn(2, 3, 70, 64, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    want = dsv_rope3d_fwd(x, pos, rope)
+    for first in (1, 2, 3):   # 12 bytes a row: a list's slice is copied where it does not start on 16
+        with pytest.raises(DSVError, match="pos is not 16-byte aligned"):
+            dsv_rope3d_fwd(x[:, :, first:], pos[first:], rope)
+        assert torch.equal(dsv_rope3d_fwd(x[:, :, first:], pos[first:].clone(), rope), want[:, :, first:])
+    assert torch.equal(dsv_rope3d_fwd(x[:, :, 4:], pos[4:], rope), want[:, :, 4:])
+    with pytest.raises(TypeError, match="pos"):
+        dsv_rope3d_fwd(x, [0], rope)
+
+
 def test_offsets_past_32_bits():
     """The long clip, 16 heads: 3.2 G elements in the packed tensor; its last tokens against the oracle."""
     need_gpu()
