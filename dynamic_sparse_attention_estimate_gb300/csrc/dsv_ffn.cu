@@ -472,7 +472,8 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
       tc::tc_fence_after();
       const uint32_t acc = tmem + lane_base + buf * 256;
       if (SPLIT && (!kTwo || pr.partial)) {
-        // a part of K: its sums as they are, joined with the others' by ffn_join_kernel
+        // a part of K: its sums as they are, joined with the others' by ffn_join_kernel (rows past the result's stay out)
+        const bool in = m0 + row < pr.rows;
         float4* to = reinterpret_cast<float4*>(pr.partial + ((w.t * 256 + rank * 128 + row) * 256 + wg * 128));
 #pragma unroll 1
         for (int c = 0; c < 128; c += 16) {
@@ -481,7 +482,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
           tc::tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            to[c / 4 + i] = make_float4(__uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1]),
+            if (in) to[c / 4 + i] = make_float4(__uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1]),
                                         __uint_as_float(a[4 * i + 2]), __uint_as_float(a[4 * i + 3]));
         }
         tc::tc_fence_before();
