@@ -802,19 +802,52 @@ static bool distinct(const dsv_rope_dims* d, const dsv::RopeView& a, const ViewS
   return !reaches((bs.lo - as.lo) / 2, st, n, 3, d->d);
 }
 
-static dsv_status check_rope_tables(const dsv::RopeGeom& g, const int32_t* pos, const float* table) {
+static size_t rope_table_bytes(const dsv::RopeGeom& g) {
+  size_t n = 0;
+  for (int a = 0; a < 3; ++a) n += static_cast<size_t>(g.len[a]) * g.axis_pairs[a];
+  return n * 2 * sizeof(float);
+}
+
+// What a call reads besides its views: the weights, and with anything to rotate the positions and the table.
+struct RopeSmall {
+  const char* name[4];
+  ViewSpan span[4];
+  int n = 0;
+  void add(const char* what, const void* p, size_t bytes) {
+    name[n] = what;
+    span[n].lo = static_cast<const char*>(p);
+    span[n++].hi = static_cast<const char*>(p) + bytes;
+  }
+};
+static dsv_status check_rope_small(const dsv_rope_dims* d, const dsv::RopeGeom& g, const void* wq, const void* wk,
+                                   const int32_t* pos, const float* table, RopeSmall* small) {
+  const size_t w_bytes = static_cast<size_t>(d->d) * sizeof(dsv::bf16);
+  if (wq) {
+    DSV_NEED_PTR(wq);
+    small->add("wq", wq, w_bytes);
+  }
+  if (wk) {
+    DSV_NEED_PTR(wk);
+    small->add("wk", wk, w_bytes);
+  }
   if (!g.pairs) return DSV_OK;
   DSV_NEED_PTR(pos);
   DSV_NEED_PTR(table);
+  small->add("pos", pos, static_cast<size_t>(d->pos_batched ? d->B : 1) * d->N * 3 * sizeof(int32_t));
+  small->add("table", table, rope_table_bytes(g));
+  return DSV_OK;
+}
+// An output lies over none of them.
+static dsv_status apart_from_small(const RopeSmall& small, const char* name, const ViewSpan& out) {
+  for (int i = 0; i < small.n; ++i)
+    if (!apart(small.span[i], out)) return fail(DSV_ERR_INVALID_ARG, "%s overlaps %s", name, small.name[i]);
   return DSV_OK;
 }
 
 size_t dsv_rope3d_table_bytes(const dsv_rope_dims* dims) {
   dsv::RopeGeom g{};
   if (check_rope(dims, &g) != DSV_OK) return 0;
-  size_t n = 0;
-  for (int a = 0; a < 3; ++a) n += static_cast<size_t>(g.len[a]) * g.axis_pairs[a];
-  return n * 2 * sizeof(float);
+  return rope_table_bytes(g);
 }
 
 dsv_status dsv_rope3d_table(const dsv_rope_dims* dims, const double theta[3], float* table, void* stream) {
@@ -846,7 +879,9 @@ static dsv_status rope3d_impl(const dsv_rope_dims* dims, const void* x, const ds
   const bool in_place = p.q.p == p.qo.p && p.q.sb == p.qo.sb && p.q.sh == p.qo.sh && p.q.sn == p.qo.sn;
   if (!in_place && !apart(a, b))
     return fail(DSV_ERR_INVALID_ARG, "the output overlaps the input (in place needs the same pointer and strides)");
-  if ((s = check_rope_tables(p.g, pos, table)) != DSV_OK) return s;
+  RopeSmall small;
+  if ((s = check_rope_small(dims, p.g, nullptr, nullptr, pos, table, &small)) != DSV_OK) return s;
+  if ((s = apart_from_small(small, backward ? "dx" : "y", b)) != DSV_OK) return s;
   p.d = static_cast<int>(dims->d);
   p.half = dims->pairing == DSV_PAIRS_HALVES;
   p.backward = backward;
@@ -896,9 +931,10 @@ dsv_status dsv_qk_norm_rope_fwd(const dsv_rope_dims* dims, const void* q, const 
       if (!apart(is[i], os[j])) return fail(DSV_ERR_INVALID_ARG, "%s overlaps %s", out_name[j], in_name[i]);
       if (i < j && !apart(os[i], os[j])) return fail(DSV_ERR_INVALID_ARG, "%s overlaps %s", out_name[j], out_name[i]);
     }
-  if (wq) DSV_NEED_PTR(wq);
-  if (wk) DSV_NEED_PTR(wk);
-  if ((s = check_rope_tables(p.g, pos, table)) != DSV_OK) return s;
+  RopeSmall small;
+  if ((s = check_rope_small(dims, p.g, wq, wk, pos, table, &small)) != DSV_OK) return s;
+  for (int i = 0; i < nt; ++i)
+    if ((s = apart_from_small(small, out_name[i], os[i])) != DSV_OK) return s;
   p.d = static_cast<int>(dims->d);
   p.half = dims->pairing == DSV_PAIRS_HALVES;
   p.eps = dims->eps;
@@ -957,11 +993,12 @@ dsv_status dsv_qk_norm_rope_bwd(const dsv_rope_dims* dims, const void* d_q_out, 
       if (!distinct(dims, *ov[i], os[i], *ov[j], os[j]))
         return fail(DSV_ERR_INVALID_ARG, "%s overlaps %s", out_name[j], out_name[i]);
   }
-  if (wq) DSV_NEED_PTR(wq);
-  if (wk) DSV_NEED_PTR(wk);
   if (dwq) DSV_NEED_PTR(dwq);
   if (dwk) DSV_NEED_PTR(dwk);
-  if ((s = check_rope_tables(p.g, pos, table)) != DSV_OK) return s;
+  RopeSmall small;
+  if ((s = check_rope_small(dims, p.g, wq, wk, pos, table, &small)) != DSV_OK) return s;
+  for (int i = 0; i < nt; ++i)
+    if ((s = apart_from_small(small, out_name[i], os[i])) != DSV_OK) return s;
   if (dwq || dwk) {
     const size_t need = qk_norm_rope_ws(p.g, dims);
     if (!ws) return fail(DSV_ERR_WORKSPACE, "workspace is NULL");
@@ -980,6 +1017,7 @@ dsv_status dsv_qk_norm_rope_bwd(const dsv_rope_dims* dims, const void* d_q_out, 
         const char* name = i < ni ? in_name[i] : i < ni + nt ? out_name[i - ni] : sum_name[i - ni - nt];
         if (!apart(t, ss[j])) return fail(DSV_ERR_INVALID_ARG, "%s overlaps %s", sum_name[j], name);
       }
+      if (sum[j] && (s = apart_from_small(small, sum_name[j], ss[j])) != DSV_OK) return s;
     }
   }
   p.d = static_cast<int>(dims->d);

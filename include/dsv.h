@@ -337,8 +337,9 @@ dsv_status dsv_adaln_bwd(const dsv_adaln_dims* dims, const void* x, const void* 
  * [B][H][N][d]).  A packed projection [B][N][3][H][d] is three such views.  Inputs may be broadcast
  * (stride 0).  An output's elements must be distinct (its strides are checked), and outputs must
  * not overlap inputs or each other, except that rope3d may run in place (the same pointer and
- * strides).  A memory range that overlaps an input's in any other way is refused; outputs of one
- * call may interleave in one range with the same strides (a packed gradient).
+ * strides).  A memory range that overlaps an input's in any other way is refused, the weights', pos
+ * and the table (where the call reads them) among the inputs; outputs of one call may interleave in
+ * one range with the same strides (a packed gradient).
  *
  * Validation before any launch: B, H, N >= 1; B*H*N < 2^31 - 64; d in {64, 128}; rot even, >= 0, sum
  * <= d (a multiple of 16 for DSV_PAIRS_HALVES); len >= 1 for every axis in use, and at most 2^31

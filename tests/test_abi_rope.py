@@ -159,6 +159,56 @@ def test_sums_and_workspace_over_other_tensors(lib):
     assert bwd(lib, d, dwq=0x5000000 + ws, nbytes=ws) not in (INVALID, WORKSPACE)
 
 
+def test_outputs_over_weights_positions_and_table(lib):
+    """No output, sum or workspace may lie over a tensor that the same call reads: pos, table, wq, wk."""
+    d = dims()
+    N, f = d.N, d.d
+    table, pos = lib.dsv_rope3d_table_bytes(d), 12 * N
+    error = lib.dsv_last_error_message
+    size = 2 * 3 * N * f * 2
+    for fn in ("dsv_rope3d_fwd", "dsv_rope3d_bwd"):
+        for kw, what in ((dict(pos=Y), b"pos"), (dict(pos=Y + size - 16), b"pos"), (dict(pos=Y - pos + 16 & ~15), b"pos"),
+                         (dict(tab=Y), b"table"), (dict(tab=Y - table + 16), b"table"), (dict(tab=Y + size - 16), b"table")):
+            assert rope(lib, d, fn=fn, **kw) == INVALID and b"overlaps " + what in error(), kw
+        # in place too
+        assert rope(lib, d, fn=fn, y=X, pos=X + 128) == INVALID and b"overlaps pos" in error()
+        # side by side is fine
+        assert rope(lib, d, fn=fn, pos=Y + size, tab=Y - table) not in (INVALID, WORKSPACE)
+    # positions of every sample reach further
+    b = dims(pos_batched=1)
+    assert rope(lib, b, pos=Y - 2 * pos + 16) == INVALID and b"overlaps pos" in error()
+    assert rope(lib, b, pos=Y - 2 * pos) not in (INVALID, WORKSPACE)
+
+    def fwd(d=d, q_out=Y, k_out=Y + size, v_out=Y + 2 * size, wq=TAB, wk=TAB + 256, pos=POS, tab=TAB + 4096):
+        return lib.dsv_qk_norm_rope_fwd(d, X, X + size, X + 2 * size, None, wq, wk, pos, tab, q_out, k_out, v_out, None)
+
+    assert fwd() not in (INVALID, WORKSPACE)
+    for i, name in enumerate((b"q_out", b"k_out", b"v_out")):
+        at = Y + i * size
+        for kw, what in ((dict(wq=at), b"wq"), (dict(wk=at + size - 16), b"wk"), (dict(pos=at + 256), b"pos"),
+                         (dict(tab=at + 256), b"table")):
+            assert fwd(**kw) == INVALID and name + b" overlaps " + what in error(), kw
+    assert fwd(wq=Y - 2 * f) not in (INVALID, WORKSPACE)
+    assert fwd(wq=Y - 2 * f + 16) == INVALID
+
+    far, ws = 0x6000000, lib.dsv_qk_norm_rope_bwd_workspace(d)
+    for out, start, end in (("dq", Y, Y + size), ("dk", Y + size, Y + 2 * size), ("dv", Y + 2 * size, Y + 3 * size),
+                            ("dwq", 0x4000000, 0x4000000 + 4 * f), ("dwk", 0x4001000, 0x4001000 + 4 * f),
+                            ("ws", 0x5000000, 0x5000000 + ws)):
+        for name, key, span in (("wq", "wq", 2 * f), ("wk", "wk", 2 * f), ("pos", "pos", pos), ("table", "tab", table)):
+            others = dict(wq=far, wk=far + 0x1000, pos=far + 0x2000, tab=far + 0x10000)
+            for at in (start, end - 16) + ((start - span + 16,) if out not in ("dk", "dv") else ()):
+                assert bwd(lib, d, **{**others, key: at}) == INVALID, (out, name, at)
+                assert f"{out} overlaps {name}".encode() in error(), (out, name, at)
+            if out not in ("dq", "dk"):   # (what follows those is the next output)
+                assert bwd(lib, d, **{**others, key: end}) not in (INVALID, WORKSPACE), (out, name, error())
+    # what a call does not read may lie anywhere: pos and table with nothing rotated, the workspace without sums
+    still = dims(rot=(0, 0, 0))
+    assert rope(lib, still, pos=Y, tab=Y) not in (INVALID, WORKSPACE)
+    assert fwd(d=still, pos=Y, tab=Y) not in (INVALID, WORKSPACE)
+    assert bwd(lib, d, dwq=None, dwk=None, ws=TAB) not in (INVALID, WORKSPACE)
+
+
 def test_interleaved_outputs(lib):
     """The three views of a packed [B][N][3][H][d] gradient share a range but no element; shifted ones do."""
     d = dims()
