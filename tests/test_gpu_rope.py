@@ -352,6 +352,73 @@ def test_gradients_against_differences():
         assert abs(float((np64(dwq) * ew).sum()) - want) <= 2.0 ** -14 * float(np.abs(np64(dwq) * ew).sum()) + 1e-6 * abs(want)
 
 
+def check_weight_sum(name, dw, dy, x, w, ang, pairing, eps, L):
+    excess = np.abs(np64(dw) - oracle.qk_norm_rope_bwd(dy, x, w, ang, pairing, eps)[1])
+    xhat = np.abs(oracle.qk_norm(x, None, eps))
+    excess -= (L * 2.0 ** -24 + 2.0 ** -20) * (rope_mag(dy, ang, pairing) * xhat).sum((0, 1, 2))
+    assert float(excess.max()) <= 0, f"{name}: bound exceeded by {excess.max():.3e}"
+
+
+# Clips whose backward's 608 persistent CTAs take several units (a tile of tokens, all heads or a chunk of them) each, with
+# a last turn that not all of them have: both head dims and pairings, one chunk of heads and several.
+MANY = [(2, 3, (59, 113, 3), 64), (2, 3, (59, 113, 3), 128), (1, 9, (5, 23, 43), 64), (2, 4, (1, 47, 53), 128)]
+
+
+@pytest.mark.parametrize("pairing", ["interleaved", "halves"])
+@pytest.mark.parametrize("B,H,latent,d", MANY)
+def test_backward_of_several_units_to_a_cta(B, H, latent, d, pairing):
+    """dq, dk, dwq and dwk in full.  A weight's gradient is a chain of L fp32 additions on terms within 2^-20: the heads
+    and turns of a thread, a CTA's groups of lanes, the CTAs a warp sums, the 32 warps; off by at most
+    (L 2^-24 + 2^-20) sum |term|."""
+    need_gpu()
+    c = norm_case(B, H, latent, d, 21 + H)
+    axes, eps = (24, 20, 20) if d == 64 else (44, 42, 42), 1e-5
+    rope, pos = dsv_rope3d_table(axes, latent, pairing=pairing), positions(latent)
+    ang, N = oracle.rope_angles(pos, axes), int(np.prod(latent))
+    tokens = 1024 // d                                           # of a tile
+    ctas = dsv_qk_norm_rope_bwd_workspace(B, H, N, d) // (8 * d)   # a row of two sums of d for each
+    units = B * -(-N // tokens) * H
+    assert units > ctas                                          # (at most: with a chunk for each head)
+    L = H + -(-units // ctas) + tokens + -(-ctas // 32) + 32
+    q, k = (laid_out(c[n], "packed") for n in "qk")
+    dq, dk, dv, dwq, dwk = dsv_qk_norm_rope_bwd(*(c[n].cuda() for n in ("dq", "dk", "dv")), q, k, c["wq"].cuda(),
+                                                c["wk"].cuda(), pos.cuda(), rope, eps)
+    assert dsv_last_device_status() == 0 and torch.equal(dv.cpu(), c["dv"])
+    for x, dx, dw in (("q", dq, dwq), ("k", dk, dwk)):
+        check_bwd(x, dx, None, c["d" + x], c[x], c["w" + x], ang, pairing, eps)
+        check_weight_sum("d" + x, dw, c["d" + x], c[x], c["w" + x], ang, pairing, eps, L)
+
+
+def direction_check(got, grad_name, c, ang, eps, rng):
+    """Central differences of the fp64 loss sum(dy * forward) along a random direction against `got`.  dq: its entries'
+    roundings are uniform within half a step, at most 2^-8 / sqrt 3 of a value each and of random sign: six standard
+    deviations of their sum.  dwq: the fp32 sums' worst case, L = 120 additions on terms within 2^-20."""
+    x, w, dy, h = np64(c["q"]), np64(c["wq"]), np64(c["dq"]), 1e-5
+    loss = lambda a, b: float((oracle.qk_norm_rope_fwd(a, b, ang, "interleaved", eps) * dy).sum())
+    e = rng.standard_normal(got.shape)
+    if grad_name == "dq":
+        want = (loss(x + h * e, w) - loss(x - h * e, w)) / (2 * h)
+        bound = 6 * 2.0 ** -8 / 3 ** 0.5 * float(np.linalg.norm(got))
+    else:
+        want = (loss(x, w + h * e) - loss(x, w - h * e)) / (2 * h)
+        S = (rope_mag(c["dq"], ang, "interleaved") * np.abs(oracle.qk_norm(c["q"], None, eps))).sum((0, 1, 2))
+        bound = (120 * 2.0 ** -24 + 2.0 ** -20) * float((S * np.abs(e)).sum())
+    return abs(float((got * e).sum()) - want) <= bound + 1e-6 * abs(want)
+
+
+def test_gradients_against_differences_within_their_roundings():
+    need_gpu()
+    c = norm_case(2, 3, (2, 3, 4), 64, 5)
+    axes, latent, eps = (24, 20, 20), (2, 3, 4), 1e-5
+    rope, pos = dsv_rope3d_table(axes, latent), positions(latent)
+    ang = oracle.rope_angles(pos, axes)
+    g = {n: t.cuda() for n, t in c.items()}
+    dq, _, _, dwq, _ = dsv_qk_norm_rope_bwd(g["dq"], g["dk"], g["dv"], g["q"], g["k"], g["wq"], g["wk"], pos.cuda(), rope, eps)
+    rng = np.random.default_rng(6)
+    for _ in range(4):
+        assert direction_check(np64(dq), "dq", c, ang, eps, rng) and direction_check(np64(dwq), "dwq", c, ang, eps, rng)
+
+
 def test_bitwise_repeatable_and_workspace_contents_do_not_matter():
     need_gpu()
     B, H, latent, d = 1, 9, (4, 32, 33), 128
