@@ -265,6 +265,8 @@ DSV_DEVICE void act_both(float g, int act, float& a, float& slope) {
   a = g * s;
   slope = fmaf(a * (1.f - s), dz, s);
 }
+// dg = dh act'(g) u, the slope (at most 1.13) first: dh u alone can pass fp32 where a slope of 0 makes dg 0.
+DSV_DEVICE float grad_gate(float dh, float slope, float u) { return dh * slope * u; }
 
 DSV_DEVICE void tile_of(const Product& pr, int64_t group, int64_t t, int64_t& m, int64_t& n) {
   const int64_t per = group * pr.n_tiles;
@@ -523,7 +525,7 @@ ffn_gemm_kernel(const __grid_constant__ Maps maps, Shape sh, unsigned int* statu
                     float a, slope;
                     act_both(__uint_as_float(g[2 * i + e]), sh.act, a, slope);
                     const float v = e ? bf16_hi(d[i]) : bf16_lo(d[i]);
-                    dg[e] = v * __uint_as_float(u[2 * i + e]) * slope;
+                    dg[e] = grad_gate(v, slope, __uint_as_float(u[2 * i + e]));
                     du[e] = v * a;
                   }
                   w0[i] = pack_bf16x2(dg[0], dg[1]);
@@ -626,7 +628,7 @@ __global__ void __launch_bounds__(256) ffn_join_kernel(Shape sh, JoinOut o) {
         float a, slope;
         act_both(v[e], sh.act, a, slope);
         const float dh = e & 1 ? bf16_hi(d[e >> 1]) : bf16_lo(d[e >> 1]);
-        v[e] = dh * u[e] * slope;
+        v[e] = grad_gate(dh, slope, u[e]);
         u[e] = dh * a;
       }
       store8(o.c0 + at, v);
@@ -702,7 +704,7 @@ ffn_rows_kernel(const uint4* __restrict__ x, const uint4* __restrict__ w_gate, c
       float a, slope;
       act_both(s.x, act, a, slope);
       const float d = __bfloat162float(dh[lane * F + f]);
-      dg[lane * F + f] = d * s.y * slope;
+      dg[lane * F + f] = grad_gate(d, slope, s.y);
       du[lane * F + f] = d * a;
     } else {
       h[lane * F + f] = __float2bfloat16_rn(act_value(s.x, act) * s.y);

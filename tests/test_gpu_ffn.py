@@ -199,6 +199,24 @@ def test_the_slope_where_g_squared_overflows(M, act):
         assert torch.equal(got.double().cpu(), ref.to(BF16).double())
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M,D", [(1, 16), (3, 16), (5, 16), (40, 4096), (300, 16)])
+def test_a_zero_slope_where_dh_times_u_overflows(M, D, act):
+    """g = -2^67: act(g) and its slope are 0, dh u = 2^160 is past fp32; every result is 0 all the same (the second
+    half of the features has u = 0 and nothing large: act'(0) = 1/2)."""
+    need_gpu()
+    F = 32
+    x, wg, wu = torch.zeros(M, D, dtype=BF16), torch.zeros(F, D, dtype=BF16), torch.zeros(F, D, dtype=BF16)
+    x[:, 0] = 2.0 ** 34
+    wg[:F // 2, 0], wu[:F // 2, 0] = -2.0 ** 33, 2.0 ** 26
+    dh = torch.ones(M, F, dtype=BF16)
+    dh[:, :F // 2] = 2.0 ** 100
+    assert dsv_ffn_gated_fwd_workspace(M, D, F) == 0 or M == 40
+    for t in dsv_ffn_gated_bwd(dh.cuda(), x.cuda(), wg.cuda(), wu.cuda(), act):
+        assert not t.any() and not torch.isnan(t).any()
+    assert not dsv_ffn_gated_fwd(x.cuda(), wg.cuda(), wu.cuda(), act).any()
+
+
 def test_leading_dims_repeatability_streams_and_graphs():
     need_gpu()
     B, N, D, F = 3, 70, 264, 520
