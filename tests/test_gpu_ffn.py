@@ -217,6 +217,31 @@ def test_a_zero_slope_where_dh_times_u_overflows(M, D, act):
     assert not dsv_ffn_gated_fwd(x.cuda(), wg.cuda(), wu.cuda(), act).any()
 
 
+# dx and the weights' gradients in one launch whose first product goes round the 76 pairs once or twice and on: either
+# first, its last round whole or with pairs that take a unit of the other ahead, more than one group of 19 m tiles
+ROUNDS = [(1140, 3176, 520), (1171, 3368, 552), (1029, 4024, 520), (2230, 3864, 1040), (4858, 776, 2352), (5055, 1816, 2520),
+          (8192, 1024, 2816)]
+
+
+@pytest.mark.parametrize("M,D,F", ROUNDS)
+def test_backward_of_several_rounds_in_one_launch(M, D, F):
+    need_gpu()
+    c = case(M, D, F, seed=6)
+    g = {n: t.cuda() for n, t in c.items()}
+    ws = torch.full((dsv_ffn_gated_bwd_workspace(M, D, F),), 0xff, dtype=torch.uint8, device="cuda")   # dg, du of NaN
+    outs = [guarded(t) for t in (c["x"], c["wg"], c["wu"])]
+    for o, _, _ in outs:
+        o.fill_(float("nan"))
+    dsv_ffn_gated_bwd(g["dh"], g["x"], g["wg"], g["wu"], out=tuple(o[0] for o in outs), workspace=ws)
+    assert dsv_last_device_status() == 0
+    for view, buf, pad in outs:
+        assert (buf[:pad] == -77).all() and (buf[pad + view.numel():] == -77).all()
+    first = [o[0] for o in outs]
+    check_bwd(c, *first, "silu")
+    again = dsv_ffn_gated_bwd(g["dh"], g["x"], g["wg"], g["wu"])
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
 def test_leading_dims_repeatability_streams_and_graphs():
     need_gpu()
     B, N, D, F = 3, 70, 264, 520
