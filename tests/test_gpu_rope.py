@@ -283,6 +283,37 @@ def test_qk_norm_rope_matches_oracle(B, H, latent, d, axes, pairing, layout):
         assert torch.equal(base.view(torch.int16), was.view(torch.int16))
 
 
+@pytest.mark.parametrize("pairing", ["interleaved", "halves"])
+def test_qk_norm_rope_positions_of_each_sample_and_keys_shared_by_the_heads(pairing):
+    """pos [B, N, 3]; keys and values of one head read by all (stride 0): their gradients come out for each head."""
+    need_gpu()
+    gen = torch.Generator().manual_seed(13)
+    B, H, N, d, axes, eps = 3, 5, 37, 64, (24, 20, 20), 1e-5
+    c = norm_case(B, H, (1, 1, N), d, 14)
+    pos = torch.stack([torch.randint(0, 9, (N, 3), generator=gen) for _ in range(B)]).to(torch.int32)
+    rope = dsv_rope3d_table(axes, (9, 9, 9), pairing=pairing)
+    ang = oracle.rope_angles(pos, axes)
+    one = ang[:, None]   # for the magnitudes
+    for n in "kv":
+        c[n] = c[n][:, :1].expand(B, H, N, d)
+    k1, v1 = (c[n][:, :1].contiguous().cuda().expand(B, H, N, d) for n in "kv")
+    assert k1.stride(1) == 0
+    q, wq, wk = laid_out(c["q"], "packed"), c["wq"].cuda(), c["wk"].cuda()
+    qo, ko, vo = dsv_qk_norm_rope_fwd(q, k1, v1, wq, wk, pos.cuda(), rope, eps)
+    assert torch.equal(vo.cpu(), c["v"])
+    dq, dk, dv, dwq, dwk = dsv_qk_norm_rope_bwd(*(c[n].cuda() for n in ("dq", "dk", "dv")), q, k1, wq, wk, pos.cuda(), rope, eps)
+    assert torch.equal(dv.cpu(), c["dv"]) and dsv_last_device_status() == 0
+    for n, y, dx, dw in (("q", qo, dq, dwq), ("k", ko, dk, dwk)):
+        x, w, dy = c[n], c["w" + n], c["d" + n]
+        close(n, y, oracle.qk_norm_rope_fwd(x, w, ang, pairing, eps), rope_mag(oracle.qk_norm(x, w, eps), one, pairing))
+        for b in range(B):   # (a sample at a time: the checks take one list of angles)
+            s = slice(b, b + 1)
+            check_bwd("d" + n, dx[s], None, dy[s], x[s], w, ang[b], pairing, eps)
+        rw = sum(oracle.qk_norm_rope_bwd(dy[b:b + 1], x[b:b + 1], w, ang[b], pairing, eps)[1] for b in range(B))
+        bound = 2.0 ** -16 * (rope_mag(dy, one, pairing) * np.abs(oracle.qk_norm(x, None, eps))).sum((0, 1, 2))
+        assert (np.abs(np64(dw) - rw) <= bound).all()
+
+
 def test_qk_norm_alone_without_weights_and_without_values():
     need_gpu()
     c = norm_case(2, 3, (1, 5, 5), 64, 3)
