@@ -649,7 +649,8 @@ DSV_DEVICE float2 fma2(float2 a, float2 b, float2 c) {   // two fp32 FMAs in one
 DSV_DEVICE float2 pair_of(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 
 // For a few tokens the weights' bytes are the work: `warps` warps take a row of Wg and the same of Wu, read
-// them once, 16 bytes a lane, and meet all tokens with them in registers.
+// them once, 16 bytes a lane, and meet all tokens with them in registers.  One vector of each weight row is in flight to a
+// lane: 4096 -> 8192 runs at 3.8 TB/s, 0.57 of the copy rate.
 // GRAD: dg and du (fp32) from dh in place of h.
 template <int R, bool GRAD>
 __global__ void __launch_bounds__(256)
@@ -712,8 +713,8 @@ ffn_rows_kernel(const uint4* __restrict__ x, const uint4* __restrict__ w_gate, c
   }
 }
 
-// The backward's two products for a few tokens, the weights read and their gradients written once: a lane owns 8
-// columns of D, a warp takes every eighth row f of the CTA's chunk of F and adds dg Wg + du Wu to its part of dx
+// The backward's two products for a few tokens, in one pass over the weights (the call's second: dg and du needed all of
+// a row first) that also writes their gradients: a lane owns 8 columns of D, a warp takes every eighth row f of the CTA's chunk of F and adds dg Wg + du Wu to its part of dx
 // while it writes dWg[f] = sum_r dg x and dWu[f].  dg and du stay fp32 here (of one or two tokens' rounding to
 // bf16 little averages out).  partial: [chunk][token][D].
 template <int R>
@@ -837,9 +838,11 @@ bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int b
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Where the rows kernels run instead of tiles of 256 rows: for one and two tokens, and up to four on weights of at
-// most 2^22 entries (its unpacking of the tokens grows with them).  Measured rows / tiles, L2 cold: 1 token
-// 2048 -> 5632 15 / 23 us, 4096 -> 8192 35 / 41 us; 4 tokens 1024 -> 2816 12 / 15 us, 4096 -> 512 11 / 29 us,
-// 2048 -> 5632 28 / 23 us; backward of 1 token 1024 -> 2816 32 / 56 us, of 4 54 / 55 us, of 4 4096 -> 8192 251 / 134 us.
+// most 2^22 entries (its unpacking of the tokens grows with them).  Measured rows / tiles, us, L2 cold:
+//   forward   1 token 1024 -> 2816 9 / 16, 2048 -> 5632 15 / 23, 4096 -> 8192 35 / 43; 2 tokens 2048 -> 5632 16 / 23;
+//             4 tokens 1024 -> 2816 12.5 / 15, 4096 -> 512 10.5 / 20.5, 2048 -> 5632 27 / 24, 4096 -> 8192 49 / 46
+//   backward  1 token 17 / 32, 40 / 53, 95 / 105; 2 tokens 48 / 53; 4 tokens 34 / 30, 21.5 / 30, 75 / 53, 161 / 104
+// (the same sizes in the same order; 4 tokens 1024 -> 2816 stay with the rows, which keep dg and du in fp32).
 bool few_rows(int64_t M, int64_t D, int64_t F) { return M <= 2 || (M <= 4 && D * F <= (1 << 22)); }
 // A part costs its sums' way to memory and back and a second launch, about 6 us or 24 k blocks: K is split where more
 // than that is saved.
@@ -847,7 +850,9 @@ constexpr int kSplitSaves = 24;
 
 constexpr int64_t kPairs = 76;      // of CTAs, on the card's 152 SMs
 // m tiles that take the same n tiles in turn, so that their operands meet in L2: 19, so that the 76 pairs work on 19
-// by 4 tiles at a time (a second of 2048 x 5632 calls at the power limit: 65,536-token forward 1713 us with 19, 1735 with 16,
+// by 4 tiles at a time.  One number for all products, measured at one width: the gated ones have 44 n tiles there, dx and
+// dW 8, so a group of theirs takes two rounds and its dg and du are read from memory twice (dx of 8,192 tokens 569 MB, its
+// operands are 231; neither is bound by HBM) (a second of 2048 x 5632 calls at the power limit: 65,536-token forward 1713 us with 19, 1735 with 16,
 // 1760 with 8 or 10; 16,384-token backward 1410, 1432, 1430).
 constexpr int kGroup = 19;
 

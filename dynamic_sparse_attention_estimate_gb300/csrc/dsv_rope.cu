@@ -17,8 +17,9 @@
 // rows are issued before the first is used, which is what keeps HBM busy (no staging is needed:
 // nothing is read twice).  Measured (GB300, 16 heads of 128, 65,536 tokens; a plain copy runs at 6.67 TB/s): rope3d
 // 6.3 TB/s, norm and rotation forward 241 us = 6.7 TB/s (520,192 tokens 1.82 ms = 7.0), backward 341 us = 6.3 TB/s,
-// halves 2 to 4 % below.  One head of 524,288 tokens: forward 216 us, backward 311 us, about half of that rate, for
-// each token's positions and table; two heads are at 0.82 and 0.74 of the copy, eight at the rates above.
+// halves 2 to 4 % below.  One head of 524,288 tokens: forward 216 us, backward 311 us, about half of that rate: each
+// token has its positions, its table entries and, worked out for it anew though they are the lane's, the axis, row
+// length and offset of each pair, shared by its heads; two heads are at 0.82 and 0.74 of the copy, eight at the rates above.
 #include <type_traits>
 
 #include "dsv_common.cuh"
@@ -79,8 +80,8 @@ DSV_DEVICE Pos load_pos(const RopeGeom& g, const int32_t* __restrict__ pos, int6
   return p;
 }
 
-// sign: +1 forward, -1 backward.  An axis whose position is outside its table leaves its pairs
-// unrotated (angle 0) and sets the status bit.  All lanes of the warp call it.
+// sign: +1 forward, -1 backward.  An axis whose position is outside its table turns its pairs by the
+// angle 0 and sets the status bit.  All lanes of the warp call it.
 // A lane reads four pairs.  In halves two vectors turn by the same eight: each lane gets the other four from its partner
 // (pairs are read 64 bytes apart there, many L1 accesses to a load: with all eight read by both, 524,288 tokens of one
 // head took 330 us forward and 396 backward where they take 285 and 336; 131,072 of 16 heads 483 and 710, now 477 and 690).

@@ -328,8 +328,9 @@ dsv_status dsv_adaln_bwd(const dsv_adaln_dims* dims, const void* x, const void* 
  *     positions or frequencies fills its own);
  *   pos: int32 [N][3] (pos_batched = 0, shared by the samples) or [B][N][3]: each token's
  *     (t, h, w), 0 <= pos < len of that axis.  Tokens may be in any order (e.g. block-major).  An
- *     axis whose position is outside its table is not rotated for that token, and the device status
- *     word is set (dsv_last_device_status).
+ *     axis whose position is outside its table turns by the angle 0 for that token (finite features
+ *     stay as they are), and the device status word is set (dsv_last_device_status).  A list that
+ *     starts at another list's row i is 16-byte aligned where 4 divides i.
  *   With R = 0 nothing is rotated (norm alone); pos and table may then be NULL.
  *
  * Views.  Tensors are bf16 [B][H][N][d] with contiguous features; dsv_view_strides gives the
@@ -381,7 +382,9 @@ dsv_status dsv_rope3d_bwd(const dsv_rope_dims* dims, const void* dy, const dsv_v
  *   v_out = v  (v and v_out both NULL: no values in this call).
  * wq, wk: bf16 [d] (NULL: ones).  strides: of q, k, v in this order (NULL: all contiguous).
  * q_out, k_out, v_out: contiguous [B][H][N][d], as the attention calls take them.
- * fp32 arithmetic, one rounding to bf16 at the end.
+ * fp32 arithmetic, one rounding to bf16 at the end.  The mean square is an fp32 number too: a row whose
+ * squares pass its range (features beyond about 1e18) comes out as 0, and with eps = 0 a row whose squares
+ * vanish in it (all features below about 1e-23, zero rows among them) as NaN or infinite, in that row alone.
  */
 dsv_status dsv_qk_norm_rope_fwd(const dsv_rope_dims* dims, const void* q, const void* k, const void* v,
                                 const dsv_view_strides strides[3], const void* wq, const void* wk,
@@ -415,8 +418,10 @@ dsv_status dsv_qk_norm_rope_bwd(const dsv_rope_dims* dims, const void* d_q_out, 
  *   dg = dh u act'(g), du = dh act(g);  dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x.
  * Layouts (contiguous, 16-byte aligned device memory): x, dx bf16 [M][D]; w_gate, w_up, dw_gate,
  * dw_up bf16 [F][D]; h, dh bf16 [M][F].  M is the token count (samples and tokens flattened).
- * Products accumulate in fp32; h and the gradients are rounded to bf16 once, and dg, du once
- * between the backward's kernels (for a few tokens they stay fp32).  Bitwise reproducible.  Outputs must not overlap inputs.
+ * Products accumulate in fp32; h and the gradients are rounded to bf16 once, and dg, du once between the
+ * backward's kernels, where the tensor cores take them as operands: the gradients are then off by about 2.3e-3
+ * of their norm (1.7e-3 with their own rounding alone).  For one and two tokens, and up to four with D * F <= 2^22, dg
+ * and du stay fp32.  Bitwise reproducible.  Outputs must not overlap inputs.
  * Validation before any launch: M, D, F >= 1; D and F multiples of 8; M < 2^31 - 256, D and F <=
  * 2^20; act as above; no NULL, misaligned or overlapping pointer.
  */
