@@ -714,9 +714,9 @@ ffn_rows_kernel(const uint4* __restrict__ x, const uint4* __restrict__ w_gate, c
 }
 
 // The backward's two products for a few tokens, in one pass over the weights (the call's second: dg and du needed all of
-// a row first) that also writes their gradients: a lane owns 8 columns of D, a warp takes every eighth row f of the CTA's chunk of F and adds dg Wg + du Wu to its part of dx
-// while it writes dWg[f] = sum_r dg x and dWu[f].  dg and du stay fp32 here (of one or two tokens' rounding to
-// bf16 little averages out).  partial: [chunk][token][D].
+// a row first) that also writes their gradients: a lane owns 8 columns of D, a warp takes every eighth row f of the CTA's
+// chunk of F and adds dg Wg + du Wu to its part of dx while it writes dWg[f] = sum_r dg x and dWu[f].  dg and du stay
+// fp32 here (of one or two tokens' rounding to bf16 little averages out).  partial: [chunk][token][D].
 template <int R>
 __global__ void __launch_bounds__(256, R == 4 ? 2 : 0)
 ffn_rows_back_kernel(const uint4* __restrict__ x, const uint4* __restrict__ w_gate, const uint4* __restrict__ w_up,
@@ -850,10 +850,10 @@ constexpr int kSplitSaves = 24;
 
 constexpr int64_t kPairs = 76;      // of CTAs, on the card's 152 SMs
 // m tiles that take the same n tiles in turn, so that their operands meet in L2: 19, so that the 76 pairs work on 19
-// by 4 tiles at a time.  One number for all products, measured at one width: the gated ones have 44 n tiles there, dx and
-// dW 8, so a group of theirs takes two rounds and its dg and du are read from memory twice (dx of 8,192 tokens 569 MB, its
-// operands are 231; neither is bound by HBM) (a second of 2048 x 5632 calls at the power limit: 65,536-token forward 1713 us with 19, 1735 with 16,
-// 1760 with 8 or 10; 16,384-token backward 1410, 1432, 1430).
+// by 4 tiles at a time (a second of 2048 x 5632 calls at the power limit: 65,536-token forward 1713 us with 19, 1735 with 16,
+// 1760 with 8 or 10; 16,384-token backward 1410, 1432, 1430).  One number for all products: the gated ones have 44 n tiles
+// there, dx and dW 8, so a group of theirs takes two rounds, and its dg and du are read from memory twice (dx of 8,192
+// tokens reads 569 MB, its operands are 231; it is not bound by HBM).
 constexpr int kGroup = 19;
 
 Product product(Mode mode, int64_t M, int64_t D, int64_t F) {

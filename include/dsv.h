@@ -419,9 +419,9 @@ dsv_status dsv_qk_norm_rope_bwd(const dsv_rope_dims* dims, const void* d_q_out, 
  * Layouts (contiguous, 16-byte aligned device memory): x, dx bf16 [M][D]; w_gate, w_up, dw_gate,
  * dw_up bf16 [F][D]; h, dh bf16 [M][F].  M is the token count (samples and tokens flattened).
  * Products accumulate in fp32; h and the gradients are rounded to bf16 once, and dg, du once between the
- * backward's kernels, where the tensor cores take them as operands: the gradients are then off by about 2.3e-3
- * of their norm (1.7e-3 with their own rounding alone).  For one and two tokens, and up to four with D * F <= 2^22, dg
- * and du stay fp32.  Bitwise reproducible.  Outputs must not overlap inputs.
+ * backward's kernels, where the tensor cores take them as operands: the gradients are then off by about
+ * 2.3e-3 of their norm (1.7e-3 with their own rounding alone).  For one and two tokens, and up to four with
+ * D * F <= 2^22, dg and du stay fp32.  Bitwise reproducible.  Outputs must not overlap inputs.
  * Validation before any launch: M, D, F >= 1; D and F multiples of 8; M < 2^31 - 256, D and F <=
  * 2^20; act as above; no NULL, misaligned or overlapping pointer.
  */
