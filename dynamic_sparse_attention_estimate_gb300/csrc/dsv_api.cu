@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "../../include/dsv.h"
+#include "dsv_block.h"
 #include "dsv_internal.h"
 
 // Device status word: kernels OR in kStatusBadIndex when they meet a key index outside

@@ -13,8 +13,6 @@ namespace dsv {
 constexpr unsigned int kStatusBadIndex = 1u;
 // Bit set when a kernel gave up waiting on one of its own mbarriers (bounded waits).
 constexpr unsigned int kStatusTimeout = 2u;
-// Bit set when a kernel meets a token position outside its axis' table.
-constexpr unsigned int kStatusBadPosition = 4u;
 
 // log2(e): softmax runs in base 2 with the scale folded in.
 constexpr float kLog2e = 1.4426950408889634f;

@@ -31,6 +31,7 @@
 
 #include <type_traits>
 
+#include "dsv_block.h"
 #include "dsv_common.cuh"
 #include "dsv_internal.h"
 #include "dsv_tc.cuh"

@@ -22,6 +22,7 @@
 // length and offset of each pair, shared by its heads; two heads are at 0.82 and 0.74 of the copy, eight at the rates above.
 #include <type_traits>
 
+#include "dsv_block.h"
 #include "dsv_common.cuh"
 #include "dsv_internal.h"
 
