@@ -9,6 +9,7 @@ load the library; the first call does, and fails loudly if it has not been built
 from .binding import (  # noqa: F401
     DSVError,
     RopeTable,
+    W4Weight,
     dsv_adaln_bwd,
     dsv_adaln_bwd_workspace,
     dsv_adaln_fwd,
@@ -23,6 +24,9 @@ from .binding import (  # noqa: F401
     dsv_qk_norm_rope_bwd,
     dsv_qk_norm_rope_bwd_workspace,
     dsv_qk_norm_rope_fwd,
+    dsv_residual_norm_bwd,
+    dsv_residual_norm_bwd_workspace,
+    dsv_residual_norm_fwd,
     dsv_rope3d_bwd,
     dsv_rope3d_fwd,
     dsv_rope3d_table,
@@ -33,6 +37,10 @@ from .binding import (  # noqa: F401
     dsv_sparse_attn_bwd_workspace,
     dsv_sparse_attn_fwd,
     dsv_sparse_attn_fwd_csr,
+    dsv_w4_linear_bwd,
+    dsv_w4_linear_bwd_workspace,
+    dsv_w4_linear_fwd,
+    dsv_w4_quantize,
     library_path,
     load_library,
 )

@@ -34,6 +34,8 @@ EXPORTED = (
     "dsv_rope3d_table_bytes", "dsv_rope3d_table", "dsv_rope3d_fwd", "dsv_rope3d_bwd",
     "dsv_qk_norm_rope_fwd", "dsv_qk_norm_rope_bwd_workspace", "dsv_qk_norm_rope_bwd",
     "dsv_ffn_gated_fwd_workspace", "dsv_ffn_gated_fwd", "dsv_ffn_gated_bwd_workspace", "dsv_ffn_gated_bwd",
+    "dsv_residual_norm_fwd", "dsv_residual_norm_bwd_workspace", "dsv_residual_norm_bwd",
+    "dsv_w4_quantize", "dsv_w4_linear_fwd", "dsv_w4_linear_bwd_workspace", "dsv_w4_linear_bwd",
 )
 
 
@@ -61,6 +63,18 @@ class RopeDims(ctypes.Structure):
 
 class FfnDims(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int64), ("D", ctypes.c_int64), ("F", ctypes.c_int64), ("act", ctypes.c_int32)]
+
+
+class ResidualDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("N", ctypes.c_int64), ("D", ctypes.c_int64), ("post", ctypes.c_int32),
+                ("pre", ctypes.c_int32), ("stream_f32", ctypes.c_int32), ("alpha", ctypes.c_float), ("eps", ctypes.c_float),
+                ("gate_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64), ("shift_stride", ctypes.c_int64),
+                ("d_stride", ctypes.c_int64)]
+
+
+class W4Dims(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("D", ctypes.c_int64), ("F", ctypes.c_int64), ("group", ctypes.c_int32),
+                ("dy_f32", ctypes.c_int32)]
 
 
 class ViewStrides(ctypes.Structure):
@@ -156,6 +170,22 @@ def load_library(path: Optional[str] = None):
         f.restype = sz
     lib.dsv_ffn_gated_bwd.argtypes = [fp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.dsv_ffn_gated_bwd.restype = st
+    rd = ctypes.POINTER(ResidualDims)
+    lib.dsv_residual_norm_fwd.argtypes = [rd, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.dsv_residual_norm_fwd.restype = st
+    lib.dsv_residual_norm_bwd_workspace.argtypes = [rd]
+    lib.dsv_residual_norm_bwd_workspace.restype = sz
+    lib.dsv_residual_norm_bwd.argtypes = [rd, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.dsv_residual_norm_bwd.restype = st
+    wp = ctypes.POINTER(W4Dims)
+    lib.dsv_w4_quantize.argtypes = [wp, vp, vp, vp, vp, vp]
+    lib.dsv_w4_quantize.restype = st
+    lib.dsv_w4_linear_fwd.argtypes = [wp, vp, vp, vp, vp, vp, vp, vp]
+    lib.dsv_w4_linear_fwd.restype = st
+    lib.dsv_w4_linear_bwd_workspace.argtypes = [wp]
+    lib.dsv_w4_linear_bwd_workspace.restype = sz
+    lib.dsv_w4_linear_bwd.argtypes = [wp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.dsv_w4_linear_bwd.restype = st
     lib.dsv_profile_enable.argtypes = [st]
     lib.dsv_profile_enable.restype = st
     lib.dsv_profile_read.argtypes = [ctypes.c_char_p, sz]
@@ -793,6 +823,225 @@ def dsv_ffn_gated_bwd(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w
     _call("dsv_ffn_gated_bwd", device, dims, _ptr(dh), x.data_ptr(), w_gate.data_ptr(), _ptr(w_up), _ptr(dx), _ptr(dwg),
           _ptr(dwu), ws, nbytes)
     return dx, dwg, dwu
+
+
+# ---------------------------------------------------------------- gated residual with the norms around a branch
+
+_NORMS = {"none": 0, "rms": 1, "layer": 2}
+
+
+@functools.lru_cache(maxsize=256)
+def _residual_dims(B: int, N: int, D: int, f32: bool, post: str, pre: str, alpha: float, eps: float, strides: Tuple):
+    """(dims struct, workspace bytes of the backward)."""
+    if post not in ("none", "rms") or pre not in _NORMS:
+        raise ValueError(f"post must be 'none' or 'rms' and pre 'none', 'rms' or 'layer', got {post!r} and {pre!r}")
+    dims = ResidualDims(B, N, D, _NORMS[post], _NORMS[pre], int(f32), alpha, eps, *strides)
+    return dims, int(load_library().dsv_residual_norm_bwd_workspace(dims))
+
+
+def _need_stream(t: torch.Tensor, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (torch.bfloat16, torch.float32) or t.dim() != 3 or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: need a contiguous CUDA bfloat16 or float32 [B, N, D] tensor, got {t.dtype} "
+                         f"{tuple(t.shape)} contiguous={t.is_contiguous()} device={t.device}")
+
+
+def _row_stride(t: Optional[torch.Tensor], name: str, dtype, B: int, D: int, device: int) -> int:
+    """The stride between samples of a [B, D] tensor with contiguous features (a part of a projection, say)."""
+    if t is None:
+        return D
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype or t.shape != (B, D) or t.get_device() != device or (D > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: need a {dtype} [{B}, {D}] tensor with contiguous features on cuda:{device}, got {t.dtype} "
+                         f"{tuple(t.shape)} strides={t.stride()} device={t.device}")
+    return t.stride(0)
+
+
+def dsv_residual_norm_fwd(x: torch.Tensor, z: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                          w_post: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                          shift: Optional[torch.Tensor] = None, w_pre: Optional[torch.Tensor] = None, post: str = "none",
+                          pre: str = "layer", alpha: float = 1.0, eps: float = 1e-6,
+                          out: Optional[Tuple[torch.Tensor, Optional[torch.Tensor]]] = None):
+    """(r, y): the residual stream r = x + alpha * gate * t after a branch's result z (t = z, or with post="rms" its RMS
+    norm times w_post) and y = norm(r) * w_pre * (1 + scale) + shift in front of the next branch (pre: "layer", "rms", or
+    "none": y is None).  x, r [B, N, D] bf16 or fp32; z, y bf16; gate, scale, shift bf16 [B, D] (any stride between samples,
+    e.g. parts of one projection [B, 6, D]); w_post, w_pre bf16 [D]; None: 1, 0, 0, 1, 1.  out: (r, y); r may be x itself."""
+    _need_stream(x, "x")
+    B, N, D = x.shape
+    device = x.get_device()
+    _need_on(torch.bfloat16, x.shape, device, (z, "z"))
+    _need_on(torch.bfloat16, x.shape[2:], device, (w_post, "w_post"), (w_pre, "w_pre"))
+    bf = torch.bfloat16
+    strides = (_row_stride(gate, "gate", bf, B, D, device), _row_stride(scale, "scale", bf, B, D, device),
+               _row_stride(shift, "shift", bf, B, D, device), D)
+    dims, _ = _residual_dims(B, N, D, x.dtype is torch.float32, post, pre, float(alpha), float(eps), strides)
+    if out is None:
+        r = torch.empty_like(x)
+        y = None if pre == "none" else torch.empty(x.shape, dtype=bf, device=x.device)
+    else:
+        r, y = out
+        _need_on(x.dtype, x.shape, device, (r, "r"))
+        _need_on(bf, x.shape, device, (y, "y"))
+    _call("dsv_residual_norm_fwd", device, dims, x.data_ptr(), _ptr(z), _ptr(gate), _ptr(w_post), _ptr(scale), _ptr(shift),
+          _ptr(w_pre), _ptr(r), _ptr(y))
+    return r, y
+
+
+def dsv_residual_norm_bwd_workspace(B: int, N: int, D: int, pre: str = "layer") -> int:
+    return _residual_dims(int(B), int(N), int(D), False, "none", pre, 1.0, 0.0, (int(D),) * 4)[1]
+
+
+def dsv_residual_norm_bwd(dr: Optional[torch.Tensor], dy: Optional[torch.Tensor], r: Optional[torch.Tensor], z: torch.Tensor,
+                          gate: Optional[torch.Tensor] = None, w_post: Optional[torch.Tensor] = None,
+                          scale: Optional[torch.Tensor] = None, w_pre: Optional[torch.Tensor] = None, post: str = "none",
+                          pre: str = "layer", alpha: float = 1.0, eps: float = 1e-6,
+                          out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None, d_mod: Optional[Tuple] = None,
+                          workspace: Optional[torch.Tensor] = None):
+    """(dx, dz, d_gate, dw_post, d_scale, d_shift, dw_pre) of dsv_residual_norm_fwd for the gradients dr of r (None: none) and
+    dy of y (None with pre="none", as r).  r is the forward's output, z its input.  dx has the stream's type, dz is bf16; the
+    vectors' gradients are fp32: d_gate, d_scale, d_shift [B, D] (None for a gate or scale that is None; d_shift with any
+    norm behind r) and dw_post, dw_pre [D] (None where the weight is None).  out: (dx, dz), dx may be dr itself;
+    d_mod: (d_gate, d_scale, d_shift) to write, e.g. parts of one [B, 6, D] gradient (None: not wanted)."""
+    stream = dr if dr is not None else r
+    _need_stream(stream, "r" if dr is None else "dr")
+    shape, device, f32 = stream.shape, stream.get_device(), torch.float32
+    B, N, D = shape
+    bf, vec = torch.bfloat16, (shape[0], shape[2])
+    _need_on(stream.dtype, shape, device, (r, "r"))
+    _need_on(bf, shape, device, (z, "z"), (dy, "dy"))
+    _need_on(bf, shape[2:], device, (w_post, "w_post"), (w_pre, "w_pre"))
+    if out is None:
+        dx, dz = torch.empty_like(stream), torch.empty(shape, dtype=bf, device=stream.device)
+    else:
+        dx, dz = out
+        _need_on(stream.dtype, shape, device, (dx, "dx"))
+        _need_on(bf, shape, device, (dz, "dz"))
+    d_stride = D
+    if d_mod is None:
+        d_gate = None if gate is None else torch.empty(vec, dtype=f32, device=stream.device)
+        d_scale = None if scale is None else torch.empty(vec, dtype=f32, device=stream.device)
+        d_shift = None if pre == "none" else torch.empty(vec, dtype=f32, device=stream.device)
+    else:
+        d_gate, d_scale, d_shift = d_mod
+        found = {_row_stride(t, n, f32, B, D, device) for t, n in ((d_gate, "d_gate"), (d_scale, "d_scale"), (d_shift, "d_shift"))
+                 if t is not None}
+        if len(found) > 1 and B > 1:
+            raise ValueError(f"d_mod: d_gate, d_scale and d_shift need one stride between samples, got {sorted(found)}")
+        if found:
+            d_stride = found.pop()
+    dw_post = None if w_post is None else torch.empty((D,), dtype=f32, device=stream.device)
+    dw_pre = None if w_pre is None else torch.empty((D,), dtype=f32, device=stream.device)
+    strides = (_row_stride(gate, "gate", bf, B, D, device), _row_stride(scale, "scale", bf, B, D, device), D, d_stride)
+    dims, nbytes = _residual_dims(B, N, D, stream.dtype is f32, post, pre, float(alpha), float(eps), strides)
+    ws, nbytes, _keep = _workspace(workspace, nbytes, stream)
+    _call("dsv_residual_norm_bwd", device, dims, _ptr(dr), _ptr(dy), _ptr(r), _ptr(z), _ptr(gate), _ptr(w_post), _ptr(scale),
+          _ptr(w_pre), _ptr(dx), _ptr(dz), _ptr(d_gate), _ptr(dw_post), _ptr(d_scale), _ptr(d_shift), _ptr(dw_pre), ws, nbytes)
+    return dx, dz, d_gate, dw_post, d_scale, d_shift, dw_pre
+
+
+# ---------------------------------------------------------------- products of a few vectors with 4-bit weights
+
+class W4Weight(NamedTuple):
+    """Weights [F, D] of 4 bits: w = scale * (q - zero), a scale (and zero point) to each group of D / scale.shape[1]
+    columns (32, 64 or 128).
+
+    data: uint8 [F, D / 2], the even column in the low four bits; scale: bf16 [F, D / group]; zero: uint8 [F, D / group] in
+    0 .. 15, or None (8)."""
+    data: torch.Tensor
+    scale: torch.Tensor
+    zero: Optional[torch.Tensor] = None
+
+
+@functools.lru_cache(maxsize=256)
+def _w4_dims(M: int, D: int, F: int, group: int, dy_f32: bool):
+    """(dims struct, workspace bytes of the backward)."""
+    dims = W4Dims(M, D, F, group, int(dy_f32))
+    return dims, int(load_library().dsv_w4_linear_bwd_workspace(dims))
+
+
+def _w4_args(w: W4Weight, device: int):
+    """(D, F, group) after the checks of the weights."""
+    for t, n in ((w.data, "w.data"), (w.scale, "w.scale")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{n} must be a torch.Tensor")
+        if t.dim() != 2:
+            raise ValueError(f"{n} needs 2 dims, got {tuple(t.shape)}")
+    F, half = w.data.shape
+    groups = w.scale.shape[1]
+    _need_on(torch.uint8, (F, half), device, (w.data, "w.data"))
+    _need_on(torch.bfloat16, (F, groups), device, (w.scale, "w.scale"))
+    _need_on(torch.uint8, (F, groups), device, (w.zero, "w.zero"))
+    if not groups or (2 * half) % groups:
+        raise ValueError(f"w: {2 * half} columns do not divide into {groups} groups")
+    return 2 * half, F, 2 * half // groups
+
+
+def dsv_w4_quantize(w: torch.Tensor, group: int = 64, symmetric: bool = True) -> W4Weight:
+    """The 4-bit form of w bf16 [F, D], once per model (see include/dsv.h): symmetric around 0 or with zero points."""
+    _need(w, "w", torch.bfloat16, 2)
+    F, D = w.shape
+    if group not in (32, 64, 128) or D % group:
+        raise ValueError(f"group must be 32, 64 or 128 and divide D, got {group} and {D}")
+    data = torch.empty((F, D // 2), dtype=torch.uint8, device=w.device)
+    scale = torch.empty((F, D // group), dtype=torch.bfloat16, device=w.device)
+    zero = None if symmetric else torch.empty((F, D // group), dtype=torch.uint8, device=w.device)
+    _call("dsv_w4_quantize", w.get_device(), W4Dims(1, D, F, group, 0), w.data_ptr(), data.data_ptr(), scale.data_ptr(),
+          _ptr(zero))
+    return W4Weight(data, scale, zero)
+
+
+def _need_vectors(t: torch.Tensor, name: str, dtypes):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes or t.dim() < 1 or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: need a contiguous CUDA tensor of {' or '.join(map(str, dtypes))}, got {t.dtype} "
+                         f"{tuple(t.shape)} contiguous={t.is_contiguous()} device={t.device}")
+
+
+def dsv_w4_linear_fwd(x: torch.Tensor, w: W4Weight, bias: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [..., F] = x W^T + bias for x bf16 [..., D] of at most 64 vectors and 4-bit weights; bias bf16 [F] or None."""
+    _need_vectors(x, "x", (torch.bfloat16,))
+    device = x.get_device()
+    D, F, group = _w4_args(w, device)
+    if x.shape[-1] != D:
+        raise ValueError(f"x: need {D} features, got {tuple(x.shape)}")
+    _need_on(torch.bfloat16, (F,), device, (bias, "bias"))
+    shape = (*x.shape[:-1], F)
+    dims, _ = _w4_dims(x.numel() // D if D else 0, D, F, group, False)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    else:
+        _need_on(torch.bfloat16, shape, device, (out, "out"))
+    _call("dsv_w4_linear_fwd", device, dims, x.data_ptr(), w.data.data_ptr(), w.scale.data_ptr(), _ptr(w.zero), _ptr(bias),
+          out.data_ptr())
+    return out
+
+
+def dsv_w4_linear_bwd_workspace(M: int, D: int, F: int, group: int = 64) -> int:
+    return _w4_dims(int(M), int(D), int(F), int(group), False)[1]
+
+
+def dsv_w4_linear_bwd(dy: torch.Tensor, w: W4Weight, out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dx bf16 [..., D] = dy W for dy bf16 or fp32 [..., F] (the weights are frozen; a bias has the gradient dy itself)."""
+    _need_vectors(dy, "dy", (torch.bfloat16, torch.float32))
+    device = dy.get_device()
+    D, F, group = _w4_args(w, device)
+    if dy.shape[-1] != F:
+        raise ValueError(f"dy: need {F} features, got {tuple(dy.shape)}")
+    shape = (*dy.shape[:-1], D)
+    dims, nbytes = _w4_dims(dy.numel() // F if F else 0, D, F, group, dy.dtype is torch.float32)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dy.device)
+    else:
+        _need_on(torch.bfloat16, shape, device, (out, "out"))
+    ws, nbytes, _keep = _workspace(workspace, nbytes, dy)
+    _call("dsv_w4_linear_bwd", device, dims, dy.data_ptr(), w.data.data_ptr(), w.scale.data_ptr(), _ptr(w.zero),
+          out.data_ptr(), ws, nbytes)
+    return out
 
 
 def dsv_last_device_status(device: Optional[torch.device] = None) -> int:

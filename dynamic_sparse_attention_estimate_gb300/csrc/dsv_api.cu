@@ -1147,6 +1147,258 @@ dsv_status dsv_ffn_gated_bwd(const dsv_ffn_dims* dims, const void* dh, const voi
   return ok();
 }
 
+// ---------------------------------------------------------------- gated residual with its norms, 4-bit weights
+// Checks a call's tensors by their bytes: aligned, not NULL unless optional, no output over an input or another output.
+struct ByteSpan {
+  const char* name;
+  const void* p;
+  int64_t bytes;
+  bool optional;
+};
+static dsv_status check_byte_spans(const ByteSpan* in, int n_in, const ByteSpan* out, int n_out) {
+  for (int i = 0; i < n_in + n_out; ++i) {
+    const ByteSpan& t = i < n_in ? in[i] : out[i - n_in];
+    if (!t.p && !t.optional) return fail(DSV_ERR_INVALID_ARG, "%s is NULL", t.name);
+    if (!aligned16(t.p)) return fail(DSV_ERR_INVALID_ARG, "%s is not 16-byte aligned", t.name);
+  }
+  auto span = [](const ByteSpan& t) {
+    const char* lo = static_cast<const char*>(t.p);
+    return ViewSpan{lo, lo + t.bytes};
+  };
+  for (int j = 0; j < n_out; ++j)
+    for (int i = 0; i < n_in + j; ++i) {
+      const ByteSpan& t = i < n_in ? in[i] : out[i - n_in];
+      if (t.p && out[j].p && !apart(span(t), span(out[j])))
+        return fail(DSV_ERR_INVALID_ARG, "%s overlaps %s", out[j].name, t.name);
+    }
+  return DSV_OK;
+}
+
+static dsv_status check_residual(const dsv_residual_dims* d) {
+  if (!d) return fail(DSV_ERR_INVALID_ARG, "dims is NULL");
+  if (d->B < 1 || d->N < 1 || d->B > 65535) return fail(DSV_ERR_INVALID_ARG, "B must be in [1, 65535], N >= 1");
+  if (d->N > 0x7fffffffLL / d->B) return fail(DSV_ERR_INVALID_ARG, "B*N must be below 2^31");
+  if (d->D < 8 || d->D > 8192 || d->D % 8)
+    return fail(DSV_ERR_INVALID_ARG, "D must be a multiple of 8 in [8, 8192] (got %lld)", (long long)d->D);
+  if (d->post != DSV_NORM_NONE && d->post != DSV_NORM_RMS)
+    return fail(DSV_ERR_INVALID_ARG, "post must be DSV_NORM_NONE or DSV_NORM_RMS (got %d)", d->post);
+  if (d->pre != DSV_NORM_NONE && d->pre != DSV_NORM_RMS && d->pre != DSV_NORM_LAYER)
+    return fail(DSV_ERR_INVALID_ARG, "pre must be DSV_NORM_NONE, DSV_NORM_RMS or DSV_NORM_LAYER (got %d)", d->pre);
+  if (!(d->eps >= 0.f) || d->eps > 3.0e38f) return fail(DSV_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!isfinite(d->alpha)) return fail(DSV_ERR_INVALID_ARG, "alpha must be finite");
+  return DSV_OK;
+}
+
+// Bytes from a vector's first row to the end of its last; its stride must be one that the kernels take.
+static dsv_status vector_span(const dsv_residual_dims* d, const char* name, const void* p, int64_t stride, ByteSpan* span) {
+  *span = {name, p, 2 * d->D, true};
+  if (!p || d->B == 1) return DSV_OK;
+  if (stride < 0 || stride % 8 || stride > (1LL << 40))
+    return fail(DSV_ERR_INVALID_ARG, "%s: the stride must be a multiple of 8 elements in [0, 2^40] (got %lld)", name, (long long)stride);
+  span->bytes += 2 * (d->B - 1) * stride;
+  return DSV_OK;
+}
+
+static dsv_status residual_params(const dsv_residual_dims* d, const void* z, const void* gate, const void* w_post,
+                                  const void* scale, const void* shift, const void* w_pre, dsv::ResidualParams* p) {
+  if (d->post == DSV_NORM_NONE && w_post) return fail(DSV_ERR_INVALID_ARG, "w_post without a post norm");
+  if (d->pre == DSV_NORM_NONE && (scale || shift || w_pre))
+    return fail(DSV_ERR_INVALID_ARG, "scale, shift or w_pre without a pre norm");
+  p->B = d->B;
+  p->N = d->N;
+  p->D = d->D;
+  p->post = d->post;
+  p->pre = d->pre;
+  p->f32 = d->stream_f32 != 0;
+  p->alpha = d->alpha;
+  p->eps = d->eps;
+  p->z = static_cast<const dsv::bf16*>(z);
+  p->gate = static_cast<const dsv::bf16*>(gate);
+  p->scale = static_cast<const dsv::bf16*>(scale);
+  p->shift = static_cast<const dsv::bf16*>(shift);
+  p->gate_stride = d->B > 1 ? d->gate_stride : 0;
+  p->scale_stride = d->B > 1 ? d->scale_stride : 0;
+  p->shift_stride = d->B > 1 ? d->shift_stride : 0;
+  p->w_post = static_cast<const dsv::bf16*>(w_post);
+  p->w_pre = static_cast<const dsv::bf16*>(w_pre);
+  return DSV_OK;
+}
+
+dsv_status dsv_residual_norm_fwd(const dsv_residual_dims* dims, const void* x, const void* z, const void* gate,
+                                 const void* w_post, const void* scale, const void* shift, const void* w_pre, void* r,
+                                 void* y, void* stream) {
+  dsv_status s = check_residual(dims);
+  if (s != DSV_OK) return s;
+  dsv::ResidualParams p{};
+  if ((s = residual_params(dims, z, gate, w_post, scale, shift, w_pre, &p)) != DSV_OK) return s;
+  const bool pre = dims->pre != DSV_NORM_NONE;
+  if (!pre && y) return fail(DSV_ERR_INVALID_ARG, "y without a pre norm");
+  const int64_t e = dims->B * dims->N * dims->D, stream_bytes = e * (p.f32 ? 4 : 2);
+  // r may be x: then it is not one of the inputs that r must lie apart from
+  ByteSpan in[7] = {{"x", x, r == x ? 0 : stream_bytes, false}, {"z", z, 2 * e, false}, {}, {}, {},
+                    {"w_post", w_post, 2 * dims->D, true}, {"w_pre", w_pre, 2 * dims->D, true}};
+  if ((s = vector_span(dims, "gate", gate, dims->gate_stride, &in[2])) != DSV_OK) return s;
+  if ((s = vector_span(dims, "scale", scale, dims->scale_stride, &in[3])) != DSV_OK) return s;
+  if ((s = vector_span(dims, "shift", shift, dims->shift_stride, &in[4])) != DSV_OK) return s;
+  const ByteSpan out[2] = {{"r", r, stream_bytes, false}, {"y", y, 2 * e, !pre}};
+  if ((s = check_byte_spans(in, 7, out, 2)) != DSV_OK) return s;
+  p.x = x;
+  p.r = r;
+  p.y = static_cast<dsv::bf16*>(y);
+  cudaError_t err = dsv::launch_residual_norm_fwd(p, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return fail(DSV_ERR_CUDA, "residual_norm forward launch: %s", cudaGetErrorString(err));
+  return ok();
+}
+
+size_t dsv_residual_norm_bwd_workspace(const dsv_residual_dims* dims) {
+  if (check_residual(dims) != DSV_OK) return 0;
+  return up(dsv::residual_bwd_workspace(dims->B, dims->N, dims->D, dims->pre));
+}
+
+// Two outputs of B rows of D floats, `stride` apart: apart, or interleaved.
+static bool rows_apart(const dsv_residual_dims* d, const float* a, const float* b) {
+  const int64_t delta = b - a, span = (d->B - 1) * d->d_stride + d->D;
+  if (delta >= span || -delta >= span) return true;
+  if (d->B == 1) return false;
+  const int64_t at = ((delta % d->d_stride) + d->d_stride) % d->d_stride;
+  return at >= d->D && at <= d->d_stride - d->D;
+}
+
+dsv_status dsv_residual_norm_bwd(const dsv_residual_dims* dims, const void* dr, const void* dy, const void* r, const void* z,
+                                 const void* gate, const void* w_post, const void* scale, const void* w_pre, void* dx,
+                                 void* dz, float* d_gate, float* dw_post, float* d_scale, float* d_shift, float* dw_pre,
+                                 void* ws, size_t ws_bytes, void* stream) {
+  dsv_status s = check_residual(dims);
+  if (s != DSV_OK) return s;
+  dsv::ResidualParams p{};
+  if ((s = residual_params(dims, z, gate, w_post, scale, nullptr, w_pre, &p)) != DSV_OK) return s;
+  const bool pre = dims->pre != DSV_NORM_NONE;
+  if (!pre && (dy || r)) return fail(DSV_ERR_INVALID_ARG, "dy or r without a pre norm");
+  if (!pre && (d_scale || d_shift || dw_pre)) return fail(DSV_ERR_INVALID_ARG, "d_scale, d_shift or dw_pre without a pre norm");
+  if (dims->post == DSV_NORM_NONE && dw_post) return fail(DSV_ERR_INVALID_ARG, "dw_post without a post norm");
+  if ((d_gate || d_scale || d_shift) && dims->B > 1 &&
+      (dims->d_stride < dims->D || dims->d_stride % 4 || dims->d_stride > (1LL << 40)))
+    return fail(DSV_ERR_INVALID_ARG, "d_stride must be a multiple of 4 in [D, 2^40] (got %lld)", (long long)dims->d_stride);
+  const size_t need = dsv_residual_norm_bwd_workspace(dims);
+  if ((s = check_workspace(ws, ws_bytes, need)) != DSV_OK) return s;
+  const int64_t D = dims->D, e = dims->B * dims->N * D, stream_bytes = e * (p.f32 ? 4 : 2);
+  const int64_t rows = 4 * (D + (dims->B > 1 ? (dims->B - 1) * dims->d_stride : 0));
+  ByteSpan in[8] = {{"dr", dr, dx == dr ? 0 : stream_bytes, true}, {"dy", dy, 2 * e, !pre}, {"r", r, stream_bytes, !pre},
+                    {"z", z, 2 * e, false}, {}, {}, {"w_post", w_post, 2 * D, true}, {"w_pre", w_pre, 2 * D, true}};
+  if ((s = vector_span(dims, "gate", gate, dims->gate_stride, &in[4])) != DSV_OK) return s;
+  if ((s = vector_span(dims, "scale", scale, dims->scale_stride, &in[5])) != DSV_OK) return s;
+  const ByteSpan out[5] = {{"dx", dx, stream_bytes, false}, {"dz", dz, 2 * e, false}, {"dw_post", dw_post, 4 * D, true},
+                           {"dw_pre", dw_pre, 4 * D, true}, {"ws", ws, static_cast<int64_t>(need), false}};
+  if ((s = check_byte_spans(in, 8, out, 5)) != DSV_OK) return s;
+  // the vectors' gradients: over no input or other output, and apart from or interleaved with each other
+  const ByteSpan vec[3] = {{"d_gate", d_gate, rows, true}, {"d_scale", d_scale, rows, true}, {"d_shift", d_shift, rows, true}};
+  ByteSpan all[13];
+  for (int i = 0; i < 8; ++i) all[i] = in[i];
+  for (int i = 0; i < 5; ++i) all[8 + i] = out[i];
+  float* const vp[3] = {d_gate, d_scale, d_shift};
+  for (int i = 0; i < 3; ++i) {
+    if ((s = check_byte_spans(all, 13, &vec[i], 1)) != DSV_OK) return s;
+    for (int j = 0; j < i; ++j)
+      if (vp[i] && vp[j] && !rows_apart(dims, vp[j], vp[i]))
+        return fail(DSV_ERR_INVALID_ARG, "%s overlaps %s", vec[i].name, vec[j].name);
+  }
+  p.r = const_cast<void*>(r);
+  p.dr = dr;
+  p.dy = static_cast<const dsv::bf16*>(dy);
+  p.dx = dx;
+  p.dz = static_cast<dsv::bf16*>(dz);
+  p.d_gate = d_gate;
+  p.d_scale = d_scale;
+  p.d_shift = d_shift;
+  p.d_stride = dims->B > 1 ? dims->d_stride : 0;
+  p.dw_post = dw_post;
+  p.dw_pre = dw_pre;
+  p.partial = static_cast<float*>(ws);
+  cudaError_t err = dsv::launch_residual_norm_bwd(p, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return fail(DSV_ERR_CUDA, "residual_norm backward launch: %s", cudaGetErrorString(err));
+  return ok();
+}
+
+static dsv_status check_w4(const dsv_w4_dims* d, bool vectors) {
+  if (!d) return fail(DSV_ERR_INVALID_ARG, "dims is NULL");
+  if (vectors && (d->M < 1 || d->M > 64)) return fail(DSV_ERR_INVALID_ARG, "M must be in [1, 64] (got %lld)", (long long)d->M);
+  if (d->group != 32 && d->group != 64 && d->group != 128)
+    return fail(DSV_ERR_UNSUPPORTED, "group must be 32, 64 or 128 (got %d)", d->group);
+  if (d->D < d->group || d->D % d->group || d->D > (1 << 20))
+    return fail(DSV_ERR_INVALID_ARG, "D must be a multiple of group, at most 2^20 (got %lld)", (long long)d->D);
+  if (d->F < 1 || d->F > (1LL << 40) / d->D) return fail(DSV_ERR_INVALID_ARG, "need F >= 1 and F*D <= 2^40 (got %lld)", (long long)d->F);
+  return DSV_OK;
+}
+static dsv::W4Params w4_params(const dsv_w4_dims* d, const uint8_t* data, const void* scale, const uint8_t* zero) {
+  dsv::W4Params p{};
+  p.M = d->M;
+  p.D = d->D;
+  p.F = d->F;
+  p.group = d->group;
+  p.data = const_cast<uint8_t*>(data);
+  p.scale = static_cast<dsv::bf16*>(const_cast<void*>(scale));
+  p.zero = const_cast<uint8_t*>(zero);
+  return p;
+}
+
+dsv_status dsv_w4_quantize(const dsv_w4_dims* dims, const void* w, uint8_t* data, void* scale, uint8_t* zero, void* stream) {
+  dsv_status s = check_w4(dims, false);
+  if (s != DSV_OK) return s;
+  const int64_t e = dims->F * dims->D, groups = e / dims->group;
+  const ByteSpan in[1] = {{"w", w, 2 * e, false}};
+  const ByteSpan out[3] = {{"data", data, e / 2, false}, {"scale", scale, 2 * groups, false}, {"zero", zero, groups, true}};
+  if ((s = check_byte_spans(in, 1, out, 3)) != DSV_OK) return s;
+  dsv::W4Params p = w4_params(dims, data, scale, zero);
+  p.w = static_cast<const dsv::bf16*>(w);
+  cudaError_t err = dsv::launch_w4_quantize(p, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return fail(DSV_ERR_CUDA, "w4_quantize launch: %s", cudaGetErrorString(err));
+  return ok();
+}
+
+dsv_status dsv_w4_linear_fwd(const dsv_w4_dims* dims, const void* x, const uint8_t* data, const void* scale,
+                             const uint8_t* zero, const void* bias, void* y, void* stream) {
+  dsv_status s = check_w4(dims, true);
+  if (s != DSV_OK) return s;
+  const int64_t M = dims->M, e = dims->F * dims->D, groups = e / dims->group;
+  const ByteSpan in[5] = {{"x", x, 2 * M * dims->D, false}, {"data", data, e / 2, false}, {"scale", scale, 2 * groups, false},
+                          {"zero", zero, groups, true}, {"bias", bias, 2 * dims->F, true}};
+  const ByteSpan out[1] = {{"y", y, 2 * M * dims->F, false}};
+  if ((s = check_byte_spans(in, 5, out, 1)) != DSV_OK) return s;
+  dsv::W4Params p = w4_params(dims, data, scale, zero);
+  p.x = static_cast<const dsv::bf16*>(x);
+  p.bias = static_cast<const dsv::bf16*>(bias);
+  p.y = static_cast<dsv::bf16*>(y);
+  cudaError_t err = dsv::launch_w4_fwd(p, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return fail(DSV_ERR_CUDA, "w4_linear forward launch: %s", cudaGetErrorString(err));
+  return ok();
+}
+
+size_t dsv_w4_linear_bwd_workspace(const dsv_w4_dims* dims) {
+  if (check_w4(dims, true) != DSV_OK) return 0;
+  return up(dsv::w4_bwd_workspace(dims->M, dims->D, dims->F));
+}
+
+dsv_status dsv_w4_linear_bwd(const dsv_w4_dims* dims, const void* dy, const uint8_t* data, const void* scale,
+                             const uint8_t* zero, void* dx, void* ws, size_t ws_bytes, void* stream) {
+  dsv_status s = check_w4(dims, true);
+  if (s != DSV_OK) return s;
+  const int64_t M = dims->M, e = dims->F * dims->D, groups = e / dims->group;
+  const size_t need = dsv_w4_linear_bwd_workspace(dims);
+  if ((s = check_workspace(ws, ws_bytes, need)) != DSV_OK) return s;
+  const ByteSpan in[4] = {{"dy", dy, (dims->dy_f32 ? 4 : 2) * M * dims->F, false}, {"data", data, e / 2, false},
+                          {"scale", scale, 2 * groups, false}, {"zero", zero, groups, true}};
+  const ByteSpan out[2] = {{"dx", dx, 2 * M * dims->D, false}, {"ws", ws, static_cast<int64_t>(need), false}};
+  if ((s = check_byte_spans(in, 4, out, 2)) != DSV_OK) return s;
+  dsv::W4Params p = w4_params(dims, data, scale, zero);
+  p.dy = dy;
+  p.dy_f32 = dims->dy_f32 != 0;
+  p.dx = static_cast<dsv::bf16*>(dx);
+  p.partial = static_cast<float*>(ws);
+  cudaError_t err = dsv::launch_w4_bwd(p, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return fail(DSV_ERR_CUDA, "w4_linear backward launch: %s", cudaGetErrorString(err));
+  return ok();
+}
+
 // ---------------------------------------------------------------- backward with library-held scratch
 // For callers that cannot allocate device memory (see include/dsv.h).  The scratch is a
 // fixed device array; host code only ever uses the address looked up per device below.

@@ -1,5 +1,5 @@
-// The launch interface of what a DiT block does around the attention: rotary positions, the qk norm and the gated
-// feed-forward.  Apart from dsv_internal.h, so that a change here leaves the attention's own sources as they were
+// The launch interface of what a DiT block does around the attention: rotary positions, the qk norm, the gated
+// feed-forward, the branches' way back into the residual stream and the modulation's projection.  Apart from dsv_internal.h, so that a change here leaves the attention's own sources as they were
 // measured (the bench counts a kernel's captured DRAM traffic only for the sources it was captured on).
 #pragma once
 
@@ -64,5 +64,52 @@ size_t ffn_fwd_workspace(int64_t M, int64_t D, int64_t F);
 size_t ffn_bwd_workspace(int64_t M, int64_t D, int64_t F);
 cudaError_t launch_ffn_gated_fwd(const FfnParams& p, cudaStream_t stream);
 cudaError_t launch_ffn_gated_bwd(const FfnParams& p, cudaStream_t stream);
+
+// ---------------------------------------------------------------- gated residual with its norms (dsv_residual.cu)
+enum { kNormNone = 0, kNormRms = 1, kNormLayer = 2 };
+struct ResidualParams {
+  int64_t B, N, D;
+  int post, pre;                        // norm of the branch (none, rms), of the new stream (none, rms, layer)
+  bool f32;                             // x, r, dr, dx are fp32 instead of bf16
+  float alpha, eps;
+  const bf16 *z;                        // [B][N][D]
+  const bf16 *gate, *scale, *shift;     // [B] rows of D, the strides apart; null: gate 1, scale and shift 0
+  int64_t gate_stride, scale_stride, shift_stride;
+  const bf16 *w_post, *w_pre;           // [D] or null (ones)
+  const void* x;                        // [B][N][D] (forward)
+  void* r;                              // [B][N][D]: the forward's output, the backward's input
+  bf16* y;                              // [B][N][D] (forward)
+  const void* dr;                       // [B][N][D] or null (backward)
+  const bf16* dy;                       // [B][N][D] (backward)
+  void* dx;                             // [B][N][D] (backward)
+  bf16* dz;                             // [B][N][D] (backward)
+  float *d_gate, *d_scale, *d_shift;    // [B] rows of D, d_stride apart, or null (backward)
+  int64_t d_stride;
+  float *dw_post, *dw_pre;              // [D] or null (backward)
+  float* partial;                       // residual_bwd_workspace bytes (backward)
+};
+size_t residual_bwd_workspace(int64_t B, int64_t N, int64_t D, int pre);
+cudaError_t launch_residual_norm_fwd(const ResidualParams& p, cudaStream_t stream);
+cudaError_t launch_residual_norm_bwd(const ResidualParams& p, cudaStream_t stream);
+
+// ---------------------------------------------------------------- 4-bit weights (dsv_w4.cu)
+struct W4Params {
+  int64_t M, D, F;
+  int group;                            // columns to a scale: 32, 64 or 128
+  uint8_t* data;                        // [F][D / 2]: column 2 i in the low bits of byte i
+  bf16* scale;                          // [F][D / group]
+  uint8_t* zero;                        // [F][D / group] or null (8)
+  const bf16* w;                        // [F][D] (quantize)
+  const bf16 *x, *bias;                 // [M][D], [F] or null (forward)
+  bf16* y;                              // [M][F] (forward)
+  const void* dy;                       // [M][F], bf16 or fp32 (backward)
+  bool dy_f32;
+  bf16* dx;                             // [M][D] (backward)
+  float* partial;                       // w4_bwd_workspace bytes (backward)
+};
+size_t w4_bwd_workspace(int64_t M, int64_t D, int64_t F);
+cudaError_t launch_w4_quantize(const W4Params& p, cudaStream_t stream);
+cudaError_t launch_w4_fwd(const W4Params& p, cudaStream_t stream);
+cudaError_t launch_w4_bwd(const W4Params& p, cudaStream_t stream);
 
 }  // namespace dsv

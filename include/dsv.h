@@ -449,6 +449,90 @@ dsv_status dsv_ffn_gated_bwd(const dsv_ffn_dims* dims, const void* dh, const voi
                              const void* w_up, void* dx, void* dw_gate, void* dw_up, void* ws, size_t ws_bytes,
                              void* stream);
 
+/* ------------------------------------------- gated residual with the norms around a block's branches
+ * What happens where a branch of a DiT block (attention, feed-forward) returns to the residual stream,
+ * with the norm and modulation in front of the next branch, in one pass over HBM, and its backward.
+ * Per token n of sample b, over its D features:
+ *   t = z (post DSV_NORM_NONE)  or  z / sqrt(mean z^2 + eps) * w_post (DSV_NORM_RMS);
+ *   r = x + alpha * gate[b] * t;
+ *   y = xhat * w_pre * (1 + scale[b]) + shift[b]  with  xhat = (r - mean r) / sqrt(var r + eps)
+ *       (pre DSV_NORM_LAYER, var the biased one) or r / sqrt(mean r^2 + eps) (DSV_NORM_RMS);
+ *       DSV_NORM_NONE: no y (the last branch of a model), and scale, shift, w_pre, y are NULL.
+ * The backward takes the gradients dr (of r along the stream; NULL: none) and dy (of y) and returns, with
+ * f = w_pre (1 + scale[b]), g = dr + rstd (dy f - mean(dy f) - xhat mean(dy f xhat)) (RMS: without mean(dy f)):
+ *   dx = g,   dz = alpha gate[b] g  or, through the branch's norm, rz (u - zhat mean(u zhat)), u = alpha gate[b] w_post g;
+ *   d_gate[b] = alpha sum_n g t,  dw_post = alpha sum_{b,n} gate[b] g zhat,
+ *   d_scale[b] = sum_n dy xhat w_pre,  d_shift[b] = sum_n dy,  dw_pre = sum_{b,n} dy xhat (1 + scale[b]).
+ * It reads r as the forward stored it (NULL without a norm behind it), recomputes the norms' sums, and keeps nothing.
+ * Types: z, y, dy, dz bf16; x, r, dr, dx bf16 or, with stream_f32, fp32; gate, scale, shift, w_post, w_pre bf16, each NULL
+ * where it is not there (1, 0, 0, 1, 1); the vectors' gradients fp32, each NULL where not wanted.  fp32 arithmetic and
+ * sums, one rounding at each output (the forward's y comes from r before its rounding).  The mean squares are fp32
+ * numbers too: features beyond about 1e18 leave their row 0 or NaN, and with eps = 0 a row of zeros becomes NaN.
+ * Layouts: x, z, r, y, dr, dy, dx, dz contiguous [B][N][D]; gate, scale, shift: rows of D, gate_stride, scale_stride,
+ * shift_stride elements apart (multiples of 8; 0: one row for all samples), so that parts of one modulation projection
+ * [B][6][D] are passed as they are; d_gate, d_scale, d_shift: rows of D, d_stride elements apart (a multiple of 4, >= D), which may
+ * interleave in one [B][6][D] gradient.  With B = 1 no stride is read.
+ * Outputs must not overlap inputs or each other, except that r may be x and dx may be dr (the same pointer).
+ * Bitwise reproducible.  Validation before any launch: 1 <= B <= 65535, N >= 1, B * N < 2^31; D a multiple of 8 in
+ * [8, 8192]; eps >= 0 and finite, alpha finite; pointers 16-byte aligned, NULL only as above.
+ */
+typedef enum { DSV_NORM_NONE = 0, DSV_NORM_RMS = 1, DSV_NORM_LAYER = 2 } dsv_norm;
+
+typedef struct {
+  int64_t B, N, D;
+  int32_t post;          /* dsv_norm of the branch's result: none or RMS */
+  int32_t pre;           /* dsv_norm in front of the next branch */
+  int32_t stream_f32;    /* x, r, dr, dx are fp32 */
+  float alpha, eps;
+  int64_t gate_stride, scale_stride, shift_stride;   /* elements between samples */
+  int64_t d_stride;      /* of d_gate, d_scale, d_shift (backward) */
+} dsv_residual_dims;
+
+dsv_status dsv_residual_norm_fwd(const dsv_residual_dims* dims, const void* x, const void* z, const void* gate,
+                                 const void* w_post, const void* scale, const void* shift, const void* w_pre, void* r,
+                                 void* y, void* stream);
+/* Bytes of workspace dsv_residual_norm_bwd needs (partial sums of the vectors' gradients). */
+size_t dsv_residual_norm_bwd_workspace(const dsv_residual_dims* dims);
+/* ws: at least dsv_residual_norm_bwd_workspace(dims) bytes, 256-byte aligned; one workspace must not serve two calls that
+ * can run at the same time. */
+dsv_status dsv_residual_norm_bwd(const dsv_residual_dims* dims, const void* dr, const void* dy, const void* r, const void* z,
+                                 const void* gate, const void* w_post, const void* scale, const void* w_pre, void* dx,
+                                 void* dz, float* d_gate, float* dw_post, float* d_scale, float* d_shift, float* dw_pre,
+                                 void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------- products of a few vectors with 4-bit weights
+ * The projection that makes a block's modulation vectors from its condition (one vector a sample), and any other
+ * product of a few vectors, with weights held in 4 bits:
+ *   w[f, c] = scale[f, c / group] * (q[f, c] - zero[f, c / group]),   q in 0 .. 15,
+ *   y = x W^T + bias   and, the weights being frozen,   dx = dy W.
+ * data: uint8 [F][D / 2], q of column 2 i in the low four bits of byte i and of column 2 i + 1 in the high four;
+ * scale: bf16 [F][D / group], finite; zero: uint8 [F][D / group], 0 .. 15 (its low four bits are read), or NULL: 8.
+ * x, dx bf16 [M][D]; y bf16 [M][F]; bias bf16 [F] or NULL; dy [M][F], bf16 or, with dy_f32, fp32.  Contiguous.
+ * Sums are fp32, with one rounding at the output.  Forward: products are exact.  Backward: dy * scale enters its products as
+ * two bf16 numbers, which is exact for dy in bf16 and within 2^-16 of the value in fp32.
+ * Bitwise reproducible.  Outputs must not overlap inputs.
+ * Validation before any launch: 1 <= M <= 64; F >= 1; group 32, 64 or 128; D a multiple of group, D <= 2^20, F * D <= 2^40.
+ */
+typedef struct {
+  int64_t M;             /* vectors (dsv_w4_quantize does not read it) */
+  int64_t D, F;          /* columns and rows of W */
+  int32_t group;         /* columns to a scale */
+  int32_t dy_f32;        /* dy is fp32 (backward) */
+} dsv_w4_dims;
+
+/* Weights of 4 bits from w bf16 [F][D] (finite), once per model: each group's scale is max |w| / 7 (zero NULL) or (max(w, 0) -
+ * min(w, 0)) / 15 with the zero point -min(w, 0) / scale, rounded to bf16 and to a whole number; q is w / scale rounded to the
+ * nearest whole number (ties to even) plus the zero point, held to 0 .. 15.  A group of zeros has the scale 0. */
+dsv_status dsv_w4_quantize(const dsv_w4_dims* dims, const void* w, uint8_t* data, void* scale, uint8_t* zero, void* stream);
+dsv_status dsv_w4_linear_fwd(const dsv_w4_dims* dims, const void* x, const uint8_t* data, const void* scale,
+                             const uint8_t* zero, const void* bias, void* y, void* stream);
+/* Bytes of workspace dsv_w4_linear_bwd needs (partial sums of dx). */
+size_t dsv_w4_linear_bwd_workspace(const dsv_w4_dims* dims);
+/* ws: at least dsv_w4_linear_bwd_workspace(dims) bytes, 256-byte aligned; one workspace must not serve two calls that can
+ * run at the same time. */
+dsv_status dsv_w4_linear_bwd(const dsv_w4_dims* dims, const void* dy, const uint8_t* data, const void* scale,
+                             const uint8_t* zero, void* dx, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

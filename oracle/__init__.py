@@ -23,7 +23,10 @@ Pins (what ties each function to something other than itself) live in ``tests/``
   rotary, qk norm  : complex multiplication in torch fp64 and autograd through it, central
                      finite differences, closed forms (norms kept, relative positions,
                      position 0 is the identity);
-  gated feed-forward : torch fp64 activations and autograd, central finite differences.
+  gated feed-forward : torch fp64 activations and autograd, central finite differences;
+  gated residual   : torch fp64 layer_norm / rms_norm and autograd, central finite differences,
+                     the AdaLN oracle where the branch adds nothing;
+  4-bit weights    : a byte worked by hand, torch fp64 autograd, the nearest value by search.
 """
 from .dsv_oracle import (  # noqa: F401
     block_representatives,
@@ -50,3 +53,5 @@ from .rope_oracle import (  # noqa: F401,E402
     rope_angles,
 )
 from .ffn_oracle import activation, ffn_gated_bwd, ffn_gated_fwd  # noqa: F401,E402
+from .residual_oracle import residual_norm_bwd, residual_norm_fwd  # noqa: F401,E402
+from .w4_oracle import w4_linear_bwd, w4_linear_fwd, w4_quantize, w4_values  # noqa: F401,E402
