@@ -16,29 +16,41 @@ namespace dsv {
 namespace {
 
 // ---------------------------------------------------------------- eight features of a row
-struct Vec8 {
-  float v[8];
-};
-DSV_DEVICE Vec8 unpack8(const uint4& a) {
-  Vec8 o;
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    o.v[2 * j] = bf16_lo(w[j]);
-    o.v[2 * j + 1] = bf16_hi(w[j]);
-  }
-  return o;
+// Elementwise work runs on pairs (fma.rn.f32x2 and its like: two IEEE operations to an instruction).
+DSV_DEVICE uint64_t as_u64(float2 v) { return *reinterpret_cast<uint64_t*>(&v); }
+DSV_DEVICE float2 as_f2(uint64_t v) { return *reinterpret_cast<float2*>(&v); }
+DSV_DEVICE float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+  return as_f2(d);
 }
-DSV_DEVICE uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+DSV_DEVICE float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+  return as_f2(d);
+}
+DSV_DEVICE float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+  return as_f2(d);
+}
+DSV_DEVICE float2 both(float v) { return make_float2(v, v); }
+
+struct Vec8 {
+  float2 v[4];
+};
+DSV_DEVICE Vec8 all8(float v) { return Vec8{{both(v), both(v), both(v), both(v)}}; }
+DSV_DEVICE Vec8 unpack8(const uint4& a) {
+  return Vec8{{make_float2(bf16_lo(a.x), bf16_hi(a.x)), make_float2(bf16_lo(a.y), bf16_hi(a.y)),
+               make_float2(bf16_lo(a.z), bf16_hi(a.z)), make_float2(bf16_lo(a.w), bf16_hi(a.w))}};
+}
+DSV_DEVICE uint4 pack8(const Vec8& a) {
+  return make_uint4(pack_bf16x2(a.v[0].x, a.v[0].y), pack_bf16x2(a.v[1].x, a.v[1].y), pack_bf16x2(a.v[2].x, a.v[2].y),
+                    pack_bf16x2(a.v[3].x, a.v[3].y));
 }
 // Eight entries of a bf16 vector, or of one that is not there.
 DSV_DEVICE Vec8 vector8(const bf16* p, int vec, float absent) {
-  if (p) return unpack8(__ldg(reinterpret_cast<const uint4*>(p) + vec));
-  Vec8 o;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) o.v[j] = absent;
-  return o;
+  return p ? unpack8(__ldg(reinterpret_cast<const uint4*>(p) + vec)) : all8(absent);
 }
 
 // Eight features of the residual stream, bf16 or fp32, in 16-byte parts.
@@ -47,18 +59,25 @@ struct Stream {
   static constexpr int kParts = F32 ? 2 : 1;
   static DSV_DEVICE Vec8 get(const uint4 (&a)[kParts]) {
     if constexpr (F32) {
-      return Vec8{{__uint_as_float(a[0].x), __uint_as_float(a[0].y), __uint_as_float(a[0].z), __uint_as_float(a[0].w),
-                   __uint_as_float(a[1].x), __uint_as_float(a[1].y), __uint_as_float(a[1].z), __uint_as_float(a[1].w)}};
+      return Vec8{{make_float2(__uint_as_float(a[0].x), __uint_as_float(a[0].y)), make_float2(__uint_as_float(a[0].z), __uint_as_float(a[0].w)),
+                   make_float2(__uint_as_float(a[1].x), __uint_as_float(a[1].y)), make_float2(__uint_as_float(a[1].z), __uint_as_float(a[1].w))}};
     } else {
       return unpack8(a[0]);
     }
   }
-  static DSV_DEVICE void store(void* p, int64_t vec, const float (&v)[8]) {
-    if constexpr (F32) {
-      static_cast<float4*>(p)[2 * vec] = make_float4(v[0], v[1], v[2], v[3]);
-      static_cast<float4*>(p)[2 * vec + 1] = make_float4(v[4], v[5], v[6], v[7]);
+  // At a byte offset; `wide`: fp32 features at a 32-byte boundary, stored whole (in two parts they cost the L2 twice the
+  // sectors).
+  static DSV_DEVICE void store(void* p, int64_t bytes, const Vec8& a, bool wide) {
+    char* to = static_cast<char*>(p) + bytes;
+    if constexpr (!F32) {
+      *reinterpret_cast<uint4*>(to) = pack8(a);
+    } else if (wide) {
+      asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(to), "f"(a.v[0].x), "f"(a.v[0].y), "f"(a.v[1].x),
+                   "f"(a.v[1].y), "f"(a.v[2].x), "f"(a.v[2].y), "f"(a.v[3].x), "f"(a.v[3].y)
+                   : "memory");
     } else {
-      static_cast<uint4*>(p)[vec] = pack8(v);
+      reinterpret_cast<float4*>(to)[0] = make_float4(a.v[0].x, a.v[0].y, a.v[1].x, a.v[1].y);
+      reinterpret_cast<float4*>(to)[1] = make_float4(a.v[2].x, a.v[2].y, a.v[3].x, a.v[3].y);
     }
   }
 };
@@ -67,16 +86,19 @@ struct Stream {
 constexpr int kMaxWarps = 16;           // of a row and of a CTA
 struct RowPlan {
   int nvec, V, W, G;                    // vectors of eight features, V to a lane, W warps to a row, G rows at a time
+  int warps;                            // that a CTA may have: its kernel's registers allow no more
   int64_t slabs, rows;                  // slabs of a sample (one CTA each), rows of a slab
 };
-// One vector a lane where 512 threads hold the row, else two (D <= 8192).  About `ctas` slabs over all samples, but no more
-// than give each group of a CTA a row.
-RowPlan row_plan(int64_t B, int64_t N, int64_t D, int64_t ctas) {
+// Two vectors a lane where a row has more than 32: a row's sums, its scalars and its addresses cost a lane about as much as
+// eight features do, so one vector a lane was half the rate (32,768 x 2048 backward, both norms: 268 us).  About `ctas` slabs
+// over all samples, but no more than give each group of a CTA a row.
+RowPlan row_plan(int64_t B, int64_t N, int64_t D, int64_t ctas, int warps) {
   RowPlan q;
   q.nvec = static_cast<int>(D / 8);
-  q.V = q.nvec > 32 * kMaxWarps ? 2 : 1;
+  q.V = q.nvec > 32 ? 2 : 1;
   q.W = (q.nvec + 32 * q.V - 1) / (32 * q.V);
-  q.G = kMaxWarps / q.W;
+  q.warps = q.W > warps ? kMaxWarps : warps;
+  q.G = q.warps / q.W;
   if (q.G > 15) q.G = 15;               // named barriers 1 .. 15
   q.slabs = (ctas + B - 1) / B;
   const int64_t most = (N + q.G - 1) / q.G;
@@ -114,171 +136,210 @@ constexpr int kRedFloats = 2 * kSums * kMaxWarps;   // of a row group
 struct RowSums {
   int W, group, warp, lane, turn;
   float* red;                           // [2][kSums][kMaxWarps] of the group, zero from W on
-  // K sums over the row, the same bits in every thread.  Two buffers in turn: a thread writes one only after the
-  // barrier of the sum in between, which every reader of its last use has passed.
+  // K sums over the row, the same bits in every thread.  Two and three sums share their shuffles: the lanes' halves
+  // (quarters) each go on with one of them.  Two buffers in turn: a thread writes one only after the barrier of the sum in
+  // between, which every reader of its last use has passed.
   template <int K>
   DSV_DEVICE void operator()(float (&s)[K]) {
+    constexpr unsigned kAll = 0xffffffffu;
+    float v = s[0];
+    if constexpr (K > 1) {
+      const bool high = lane & 16;
+      const float give = high ? s[0] : s[1];
+      v = (high ? s[1] : s[0]) + __shfl_xor_sync(kAll, give, 16);
+    }
+    if constexpr (K > 2) {
+      const bool third = lane & 8;
+      const float w = s[2] + __shfl_xor_sync(kAll, s[2], 16), give = third ? v : w;
+      v = (third ? w : v) + __shfl_xor_sync(kAll, give, 8);
+    }
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-#pragma unroll
-      for (int i = 0; i < K; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
-    if (W == 1) return;
+    for (int o = K == 1 ? 16 : K == 2 ? 8 : 4; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    // sum k is in lane 0, 16, 8
+    if (W == 1) {
+      s[0] = K == 1 ? v : __shfl_sync(kAll, v, 0);
+      if constexpr (K > 1) s[1] = __shfl_sync(kAll, v, 16);
+      if constexpr (K > 2) s[2] = __shfl_sync(kAll, v, 8);
+      return;
+    }
     float* buf = red + turn * (kSums * kMaxWarps);
     turn ^= 1;
-    if (lane == 0)
-#pragma unroll
-      for (int i = 0; i < K; ++i) buf[i * kMaxWarps + warp] = s[i];
+    if (lane == 0 || (K > 1 && lane == 16) || (K > 2 && lane == 8)) buf[(lane == 16 ? 1 : lane == 8 ? 2 : 0) * kMaxWarps + warp] = v;
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * W) : "memory");
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const float4* p = reinterpret_cast<const float4*>(buf + i * kMaxWarps);
       float4 t = p[0];
-      s[i] = (t.x + t.y) + (t.z + t.w);
+      float2 a = add2(make_float2(t.x, t.y), make_float2(t.z, t.w));
       for (int w = 4; w < W; w += 4) {
         t = p[w / 4];
-        s[i] += (t.x + t.y) + (t.z + t.w);
+        a = add2(a, add2(make_float2(t.x, t.y), make_float2(t.z, t.w)));
       }
+      s[i] = a.x + a.y;
     }
   }
 };
+// s / D to the last bit wherever that is a number of fp32 (so that a constant row's deviations are 0), without a division.
+DSV_DEVICE float mean_of(float s, float D, float inv_d) {
+  const float m = s * inv_d;
+  return fmaf(fmaf(-m, D, s), inv_d, m);
+}
 DSV_DEVICE RowSums row_sums(const RowPlan& plan, float* red, int group, int warp, int lane) {
   for (int i = threadIdx.x; i < 15 * kRedFloats; i += blockDim.x) red[i] = 0.f;
   __syncthreads();
   return RowSums{plan.W, group, warp, lane, 0, red + group * kRedFloats};
 }
 
-// A thread's rows on their way: `S` stages of P 16-byte parts for each of its vectors in shared memory.
+// A row's features on their way: S stages of P 16-byte parts for each vector of a thread in shared memory.  A part of a bf16
+// tensor is a lane's own; of an fp32 one the warp copies 512 bytes at a time, so that lane l brings half l % 2 of
+// vector 16 k + l / 2 (a lane's own two halves in two copies cost the L2 each sector twice): those are read after a
+// __syncwarp.
 template <int P, int V, int S>
 struct Ring {
   uint32_t base, stride;                // this thread's part 0 of stage 0; bytes between parts
   DSV_DEVICE Ring(void* smem) : base(smem_u32(smem) + 16 * threadIdx.x), stride(16 * blockDim.x) {}
   DSV_DEVICE uint32_t at(int stage, int i, int part) const { return base + ((stage * V + i) * P + part) * stride; }
-  DSV_DEVICE void copy(int stage, int i, int part, const void* p, int64_t part16) const {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(at(stage, i, part)),
-                 "l"(static_cast<const uint4*>(p) + part16)
-                 : "memory");
+  static DSV_DEVICE void copy16(uint32_t to, const void* p, int64_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(static_cast<const char*>(p) + bytes) : "memory");
+  }
+  // the lane's part of a bf16 tensor, at byte `bytes`
+  DSV_DEVICE void copy(int stage, int i, int part, const void* p, int64_t bytes, bool valid) const {
+    if (valid) copy16(at(stage, i, part), p, bytes);
+  }
+  // the lane's eight features of the stream, bf16 offset `bytes`; left: vectors from this lane's to the row's end
+  template <bool F32>
+  DSV_DEVICE void copy_stream(int stage, int i, int part, const void* p, int64_t bytes, int left, int lane) const {
+    if constexpr (!F32) {
+      copy(stage, i, part, p, bytes, left > 0);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int ahead = 16 * k + lane / 2 - lane;   // from this lane to the vector that it brings a half of
+        if (ahead < left) copy16(at(stage, i, part + lane % 2) + 16 * ahead, p, 2 * bytes + 32 * ahead + 16 * (lane % 2));
+      }
+    }
   }
   DSV_DEVICE uint4 read(int stage, int i, int part) const {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at(stage, i, part)) : "memory");
     return v;
   }
-  static size_t bytes(int threads) { return static_cast<size_t>(S) * V * P * 16 * threads; }
+  static __host__ __device__ size_t bytes(int threads) { return static_cast<size_t>(S) * V * P * 16 * threads; }
 };
 
 // ---------------------------------------------------------------- forward
 constexpr int kFwdStages = 4;
-constexpr int64_t kFwdCtas = 2 * 152;
+constexpr int64_t kFwdCtas = 152;
 
 template <bool F32, int V, bool POST, int PRE>
-__global__ void __launch_bounds__(32 * kMaxWarps, V == 1 ? 2 : 1)
-residual_norm_fwd_kernel(ResidualParams p, RowPlan plan) {
+__global__ void __launch_bounds__(32 * kMaxWarps, 1)
+residual_norm_fwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
   extern __shared__ __align__(16) uint4 ring_mem[];
   __shared__ __align__(16) float red[15 * kRedFloats];
   using St = Stream<F32>;
-  constexpr int P = St::kParts + 1, S = kFwdStages;
+  constexpr int SP = St::kParts, P = SP + 1, S = kFwdStages;
   const Place<V> at(plan, p.N);
   RowSums sum = row_sums(plan, red, at.group, at.warp, at.lane);
   const Ring<P, V, S> ring(ring_mem);
   const float D = static_cast<float>(p.D), inv_d = 1.f / D;
 
-  auto issue = [&](int64_t n, int stage) {
+  // byte offset of this thread's first vector in a bf16 tensor; a vector further is 512 bytes on
+  const int64_t first = at.n0 + at.group, step = 16LL * plan.G * plan.nvec;
+  int64_t off = ((at.b * p.N + first) * plan.nvec + at.vec[0]) * 16;
+  auto issue = [&](int64_t n, int64_t o, int stage) {
     if (n < at.n1) {
-      const int64_t base = (at.b * p.N + n) * plan.nvec;
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (at.valid[i]) {
-#pragma unroll
-          for (int k = 0; k < St::kParts; ++k) ring.copy(stage, i, k, p.x, (base + at.vec[i]) * St::kParts + k);
-          ring.copy(stage, i, St::kParts, p.z, base + at.vec[i]);
-        }
+      for (int i = 0; i < V; ++i) {
+        ring.template copy_stream<F32>(stage, i, 0, p.x, o + 512 * i, plan.nvec - at.vec[i], at.lane);
+        ring.copy(stage, i, SP, p.z, o + 512 * i, at.valid[i]);
+      }
     }
     cp_async_commit();                  // one group a row, so that the wait below counts rows
   };
-  const int64_t first = at.n0 + at.group;
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) issue(first + s * plan.G, s);
+  for (int s = 0; s < S - 1; ++s) issue(first + s * plan.G, off + s * step, s);
 
   Vec8 c[V], f[V], sh[V];               // alpha gate w_post, w_pre (1 + scale), shift
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int vec = at.valid[i] ? at.vec[i] : 0;
+    c[i] = f[i] = sh[i] = all8(0.f);
+    if (!at.valid[i]) continue;
+    const int vec = at.vec[i];
     const Vec8 g = vector8(p.gate ? p.gate + at.b * p.gate_stride : nullptr, vec, 1.f);
     const Vec8 wz = vector8(POST ? p.w_post : nullptr, vec, 1.f), wr = vector8(p.w_pre, vec, 1.f);
     const Vec8 sc = vector8(p.scale ? p.scale + at.b * p.scale_stride : nullptr, vec, 0.f);
     sh[i] = vector8(p.shift ? p.shift + at.b * p.shift_stride : nullptr, vec, 0.f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      c[i].v[j] = p.alpha * g.v[j] * wz.v[j];
-      f[i].v[j] = wr.v[j] * (1.f + sc.v[j]);
+    for (int j = 0; j < 4; ++j) {
+      c[i].v[j] = mul2(mul2(both(p.alpha), g.v[j]), wz.v[j]);
+      f[i].v[j] = mul2(wr.v[j], add2(both(1.f), sc.v[j]));
     }
   }
 
   int stage = 0;
-  for (int64_t n = first; n < at.n1; n += plan.G) {
+  for (int64_t n = first; n < at.n1; n += plan.G, off += step) {
     cp_async_wait<S - 2>();
+    if (F32) __syncwarp();
     Vec8 r[V], z[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (at.valid[i]) {
-        uint4 x[St::kParts];
+      r[i] = z[i] = all8(0.f);
+      if (!at.valid[i]) continue;
+      uint4 x[SP];
 #pragma unroll
-        for (int k = 0; k < St::kParts; ++k) x[k] = ring.read(stage, i, k);
-        r[i] = St::get(x);
-        z[i] = unpack8(ring.read(stage, i, St::kParts));
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[i].v[j] = z[i].v[j] = 0.f;
-      }
+      for (int k = 0; k < SP; ++k) x[k] = ring.read(stage, i, k);
+      r[i] = St::get(x);
+      z[i] = unpack8(ring.read(stage, i, SP));
     }
-    issue(n + (S - 1) * plan.G, stage ? stage - 1 : S - 1);   // the stage that the last row was read from
+    if (F32) __syncwarp();
+    issue(n + (S - 1) * plan.G, off + (S - 1) * step, stage ? stage - 1 : S - 1);   // where the last row was read from
     stage = stage + 1 < S ? stage + 1 : 0;
-    const int64_t base = (at.b * p.N + n) * plan.nvec;
 
     float rz = 1.f;
     if constexpr (POST) {
-      float s[1] = {0.f};
+      float2 a = both(0.f);
 #pragma unroll
       for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[0] += z[i].v[j] * z[i].v[j];
+        for (int j = 0; j < 4; ++j) a = fma2(z[i].v[j], z[i].v[j], a);
+      float s[1] = {a.x + a.y};
       sum(s);
-      rz = __frsqrt_rn(s[0] * inv_d + p.eps);
+      rz = rsqrtf(s[0] * inv_d + p.eps);
     }
-    float s[1] = {0.f};                 // of r (layer) or r^2 (rms)
+    float2 a = both(0.f);               // sum of r (layer) or r^2 (rms)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (!at.valid[i]) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        r[i].v[j] += c[i].v[j] * (POST ? z[i].v[j] * rz : z[i].v[j]);
-        s[0] += PRE == kNormLayer ? r[i].v[j] : r[i].v[j] * r[i].v[j];
+      for (int j = 0; j < 4; ++j) {
+        r[i].v[j] = fma2(c[i].v[j], POST ? mul2(z[i].v[j], both(rz)) : z[i].v[j], r[i].v[j]);
+        a = PRE == kNormLayer ? add2(a, r[i].v[j]) : fma2(r[i].v[j], r[i].v[j], a);
       }
-      St::store(p.r, base + at.vec[i], r[i].v);
+      if (at.valid[i]) St::store(p.r, (off + 512 * i) * SP, r[i], wide);
     }
     if constexpr (PRE != kNormNone) {
+      float s[1] = {a.x + a.y};
       sum(s);
       if constexpr (PRE == kNormLayer) {
-        const float mean = s[0] / D;    // divided, so that a constant row's deviations are 0
-        s[0] = 0.f;
+        const float mean = mean_of(s[0], D, inv_d);
+        a = both(0.f);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (at.valid[i])
+        for (int i = 0; i < V; ++i) {
+          const float2 m = both(at.valid[i] ? -mean : 0.f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              r[i].v[j] -= mean;
-              s[0] += r[i].v[j] * r[i].v[j];
-            }
+          for (int j = 0; j < 4; ++j) {
+            r[i].v[j] = add2(r[i].v[j], m);
+            a = fma2(r[i].v[j], r[i].v[j], a);
+          }
+        }
+        s[0] = a.x + a.y;
         sum(s);
       }
-      const float rstd = __frsqrt_rn(s[0] * inv_d + p.eps);
+      const float2 rstd = both(rsqrtf(s[0] * inv_d + p.eps));
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if (!at.valid[i]) continue;
-        float y[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = r[i].v[j] * rstd * f[i].v[j] + sh[i].v[j];
-        reinterpret_cast<uint4*>(p.y)[base + at.vec[i]] = pack8(y);
+        for (int j = 0; j < 4; ++j) r[i].v[j] = fma2(mul2(r[i].v[j], rstd), f[i].v[j], sh[i].v[j]);
+        if (at.valid[i]) *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.y) + off + 512 * i) = pack8(r[i]);
       }
     }
   }
@@ -291,20 +352,32 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan) {
 // S = sum g zhat,  T = sum dy xhat,  U = sum dy  of its features, from which every vector's gradient follows.  The CTA's
 // sums, its row groups added in order, are one partial row.
 constexpr int64_t kBwdCtas = 152;
+constexpr int kBwdWarps = 12;           // 168 registers a thread; rows of more warps take the kernel of 16 with 128
 int sums_of(int pre) { return pre == kNormNone ? 1 : 3; }
-// Stages that fit beside each other: parts of 16 bytes a thread and vector, 512 threads.
-template <int P, int V>
+// The factors alpha gate w_post and w_pre (1 + scale) would take 32 registers of a thread's 168: they stay in shared memory
+// (64 bytes a thread and vector), or, where 512 threads leave no room for that, are made again from the bf16 vectors.
+template <int WARPS>
+constexpr bool kept_factors() {
+  return WARPS <= kBwdWarps;
+}
+template <int V, int WARPS>
+constexpr int factor_bytes() {
+  return kept_factors<WARPS>() ? V * 64 * 32 * WARPS : 0;
+}
+// Stages that fit beside each other and the factors in 216 KB: parts of 16 bytes a thread and vector.
+template <int P, int V, int WARPS>
 constexpr int bwd_stages() {
-  return P * V <= 4 ? 4 : P * V <= 8 ? 3 : 2;
+  constexpr int fit = (216 * 1024 - factor_bytes<V, WARPS>()) / (P * V * 16 * 32 * WARPS);
+  return fit > 4 ? 4 : fit;
 }
 
-template <bool F32, int V, bool POST, int PRE>
-__global__ void __launch_bounds__(32 * kMaxWarps, 1)
-residual_norm_bwd_kernel(ResidualParams p, RowPlan plan) {
+template <bool F32, int V, bool POST, int PRE, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 1)
+residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
   extern __shared__ __align__(16) uint4 ring_mem[];
   __shared__ __align__(16) float red[15 * kRedFloats];
   using St = Stream<F32>;
-  constexpr int SP = St::kParts, P = PRE == kNormNone ? SP + 1 : 2 * SP + 2, S = bwd_stages<P, V>();
+  constexpr int SP = St::kParts, P = PRE == kNormNone ? SP + 1 : 2 * SP + 2, S = bwd_stages<P, V, WARPS>();
   constexpr int K = PRE == kNormNone ? 1 : 3;
   constexpr int kDr = 0, kZ = SP, kDy = SP + 1, kR = SP + 2;    // parts of a vector
   const Place<V> at(plan, p.N);
@@ -312,155 +385,198 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan) {
   const Ring<P, V, S> ring(ring_mem);
   const float D = static_cast<float>(p.D), inv_d = 1.f / D;
 
-  auto issue = [&](int64_t n, int stage) {
+  const int64_t first = at.n0 + at.group, step = 16LL * plan.G * plan.nvec;
+  int64_t off = ((at.b * p.N + first) * plan.nvec + at.vec[0]) * 16;
+  auto issue = [&](int64_t n, int64_t o, int stage) {
     if (n < at.n1) {
-      const int64_t base = (at.b * p.N + n) * plan.nvec;
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (at.valid[i]) {
-          const int64_t v = base + at.vec[i];
-          if constexpr (PRE != kNormNone) {
-#pragma unroll
-            for (int k = 0; k < SP; ++k) ring.copy(stage, i, kR + k, p.r, v * SP + k);
-            ring.copy(stage, i, kDy, p.dy, v);
-          }
-          ring.copy(stage, i, kZ, p.z, v);
-          if (p.dr)
-#pragma unroll
-            for (int k = 0; k < SP; ++k) ring.copy(stage, i, kDr + k, p.dr, v * SP + k);
+      for (int i = 0; i < V; ++i) {
+        const int left = plan.nvec - at.vec[i];
+        if constexpr (PRE != kNormNone) {
+          ring.template copy_stream<F32>(stage, i, kR, p.r, o + 512 * i, left, at.lane);
+          ring.copy(stage, i, kDy, p.dy, o + 512 * i, left > 0);
         }
+        ring.copy(stage, i, kZ, p.z, o + 512 * i, left > 0);
+        if (p.dr) ring.template copy_stream<F32>(stage, i, kDr, p.dr, o + 512 * i, left, at.lane);
+      }
     }
     cp_async_commit();
   };
-  const int64_t first = at.n0 + at.group;
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) issue(first + s * plan.G, s);
+  for (int s = 0; s < S - 1; ++s) issue(first + s * plan.G, off + s * step, s);
 
-  Vec8 c[V], f[V];                      // alpha gate w_post, w_pre (1 + scale)
-  float acc[K][V][8];
+  // the two factors of vector i
+  auto make_c = [&](int i) {
+    Vec8 c = all8(0.f);
+    if (!at.valid[i]) return c;
+    const Vec8 g = vector8(p.gate ? p.gate + at.b * p.gate_stride : nullptr, at.vec[i], 1.f);
+    const Vec8 w = vector8(POST ? p.w_post : nullptr, at.vec[i], 1.f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c.v[j] = mul2(mul2(both(p.alpha), g.v[j]), w.v[j]);
+    return c;
+  };
+  auto make_f = [&](int i) {
+    Vec8 f = all8(0.f);
+    if (!at.valid[i]) return f;
+    const Vec8 w = vector8(p.w_pre, at.vec[i], 1.f), sc = vector8(p.scale ? p.scale + at.b * p.scale_stride : nullptr, at.vec[i], 0.f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f.v[j] = mul2(w.v[j], add2(both(1.f), sc.v[j]));
+    return f;
+  };
+  constexpr bool kKept = kept_factors<WARPS>();
+  float4* const kept = reinterpret_cast<float4*>(reinterpret_cast<char*>(ring_mem) + Ring<P, V, S>::bytes(blockDim.x)) + threadIdx.x;
+  auto keep = [&](int slot, const Vec8& a) {
+    kept[2 * slot * blockDim.x] = make_float4(a.v[0].x, a.v[0].y, a.v[1].x, a.v[1].y);
+    kept[(2 * slot + 1) * blockDim.x] = make_float4(a.v[2].x, a.v[2].y, a.v[3].x, a.v[3].y);
+  };
+  auto kept8 = [&](int slot) {
+    const float4 lo = kept[2 * slot * blockDim.x], hi = kept[(2 * slot + 1) * blockDim.x];
+    return Vec8{{make_float2(lo.x, lo.y), make_float2(lo.z, lo.w), make_float2(hi.x, hi.y), make_float2(hi.z, hi.w)}};
+  };
+  Vec8 acc[K][V];                       // S, T, U
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int vec = at.valid[i] ? at.vec[i] : 0;
-    const Vec8 g = vector8(p.gate ? p.gate + at.b * p.gate_stride : nullptr, vec, 1.f);
-    const Vec8 wz = vector8(POST ? p.w_post : nullptr, vec, 1.f), wr = vector8(p.w_pre, vec, 1.f);
-    const Vec8 sc = vector8(p.scale ? p.scale + at.b * p.scale_stride : nullptr, vec, 0.f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      c[i].v[j] = p.alpha * g.v[j] * wz.v[j];
-      f[i].v[j] = wr.v[j] * (1.f + sc.v[j]);
-#pragma unroll
-      for (int k = 0; k < K; ++k) acc[k][i][j] = 0.f;
+    if (kKept) {
+      keep(2 * i, make_c(i));
+      keep(2 * i + 1, make_f(i));
     }
+#pragma unroll
+    for (int k = 0; k < K; ++k) acc[k][i] = all8(0.f);
   }
 
   int stage = 0;
-  for (int64_t n = first; n < at.n1; n += plan.G) {
+  // Lanes past the row's end hold zeros: they add nothing to a sum, and are not stored.
+  for (int64_t n = first; n < at.n1; n += plan.G, off += step) {
     cp_async_wait<S - 2>();
-    const uint4 none = make_uint4(0, 0, 0, 0);
-    uint4 rr[V][SP], gr[V][SP], zr[V], yr[V];
+    if (F32) __syncwarp();
+    Vec8 r[V], g[V], z[V], h[V];
+    uint4 dy[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const bool in = at.valid[i];
-      zr[i] = in ? ring.read(stage, i, kZ) : none;
-      yr[i] = PRE != kNormNone && in ? ring.read(stage, i, kDy) : none;
+      r[i] = g[i] = z[i] = h[i] = all8(0.f);
+      dy[i] = make_uint4(0, 0, 0, 0);
+      if (!at.valid[i]) continue;
+      uint4 part[SP];
+      if constexpr (PRE != kNormNone) {
 #pragma unroll
-      for (int k = 0; k < SP; ++k) {
-        rr[i][k] = PRE != kNormNone && in ? ring.read(stage, i, kR + k) : none;
-        gr[i][k] = p.dr && in ? ring.read(stage, i, kDr + k) : none;
+        for (int k = 0; k < SP; ++k) part[k] = ring.read(stage, i, kR + k);
+        r[i] = St::get(part);
+        dy[i] = ring.read(stage, i, kDy);
+        const Vec8 f = kKept ? kept8(2 * i + 1) : make_f(i), d = unpack8(dy[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[i].v[j] = mul2(d.v[j], f.v[j]);
+      }
+      z[i] = unpack8(ring.read(stage, i, kZ));
+      if (p.dr) {
+#pragma unroll
+        for (int k = 0; k < SP; ++k) part[k] = ring.read(stage, i, kDr + k);
+        g[i] = St::get(part);
       }
     }
-    issue(n + (S - 1) * plan.G, stage ? stage - 1 : S - 1);
+    if (F32) __syncwarp();
+    issue(n + (S - 1) * plan.G, off + (S - 1) * step, stage ? stage - 1 : S - 1);   // where the last row was read from
     stage = stage + 1 < S ? stage + 1 : 0;
-    const int64_t base = (at.b * p.N + n) * plan.nvec;
 
-    float rz = 1.f, mean = 0.f, mh = 0.f, rstd = 0.f, mhx = 0.f;
-    {
-      float s[3] = {0.f, 0.f, 0.f};     // sum z^2; layer: sum r, sum h; rms: sum r^2, sum h r
+    float rz = 1.f;
+    if constexpr (POST || PRE != kNormNone) {
+      float2 a0 = both(0.f), a1 = both(0.f), a2 = both(0.f);   // sum z^2; layer: sum r, sum h; rms: sum r^2, sum h r
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const Vec8 z = unpack8(zr[i]), r = St::get(rr[i]), dy = unpack8(yr[i]);
+      for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (POST) s[0] += z.v[j] * z.v[j];
-          const float h = dy.v[j] * f[i].v[j];
-          s[1] += PRE == kNormLayer ? r.v[j] : r.v[j] * r.v[j];
-          s[2] += PRE == kNormLayer ? h : h * r.v[j];
+        for (int j = 0; j < 4; ++j) {
+          if (POST) a0 = fma2(z[i].v[j], z[i].v[j], a0);
+          if (PRE == kNormLayer) {
+            a1 = add2(a1, r[i].v[j]);
+            a2 = add2(a2, h[i].v[j]);
+          }
+          if (PRE == kNormRms) {
+            a1 = fma2(r[i].v[j], r[i].v[j], a1);
+            a2 = fma2(h[i].v[j], r[i].v[j], a2);
+          }
         }
-      }
-      if constexpr (POST && PRE == kNormNone) {
-        float s1[1] = {s[0]};
-        sum(s1);
-        s[0] = s1[0];
-      } else if constexpr (PRE != kNormNone && !POST) {
-        float s2[2] = {s[1], s[2]};
-        sum(s2);
-        s[1] = s2[0];
-        s[2] = s2[1];
-      } else if constexpr (PRE != kNormNone) {
+      float s0 = a0.x + a0.y, s1 = a1.x + a1.y, s2 = a2.x + a2.y;
+      if constexpr (PRE == kNormNone) {
+        float s[1] = {s0};
         sum(s);
+        s0 = s[0];
+      } else if constexpr (!POST) {
+        float s[2] = {s1, s2};
+        sum(s);
+        s1 = s[0];
+        s2 = s[1];
+      } else {
+        float s[3] = {s0, s1, s2};
+        sum(s);
+        s0 = s[0];
+        s1 = s[1];
+        s2 = s[2];
       }
-      if (POST) rz = __frsqrt_rn(s[0] * inv_d + p.eps);
-      if (PRE == kNormLayer) {
-        mean = s[1] / D;                // divided, so that a constant row's deviations are 0
-        mh = s[2] * inv_d;
-      }
-      if (PRE == kNormRms) {
-        rstd = __frsqrt_rn(s[1] * inv_d + p.eps);
-        mhx = rstd * s[2] * inv_d;
-      }
-    }
-    if constexpr (PRE == kNormLayer) {
-      float s[2] = {0.f, 0.f};          // sum (r - mean)^2, sum h (r - mean)
+      if (POST) rz = rsqrtf(s0 * inv_d + p.eps);
+      if constexpr (PRE != kNormNone) {
+        float mh = 0.f;                 // mean h
+        if constexpr (PRE == kNormLayer) {
+          const float mean = mean_of(s1, D, inv_d);
+          mh = s2 * inv_d;
+          a1 = a2 = both(0.f);          // sum (r - mean)^2, sum h (r - mean)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (!at.valid[i]) continue;
-        const Vec8 r = St::get(rr[i]), dy = unpack8(yr[i]);
+          for (int i = 0; i < V; ++i) {
+            const float2 m = both(at.valid[i] ? -mean : 0.f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float d = r.v[j] - mean;
-          s[0] += d * d;
-          s[1] += dy.v[j] * f[i].v[j] * d;
+            for (int j = 0; j < 4; ++j) {
+              r[i].v[j] = add2(r[i].v[j], m);
+              a1 = fma2(r[i].v[j], r[i].v[j], a1);
+              a2 = fma2(h[i].v[j], r[i].v[j], a2);
+            }
+          }
+          float s[2] = {a1.x + a1.y, a2.x + a2.y};
+          sum(s);
+          s1 = s[0];
+          s2 = s[1];
+        }
+        const float rstd = rsqrtf(s1 * inv_d + p.eps), mhx = rstd * s2 * inv_d;   // mean(h xhat)
+        const float2 k0 = both(-rstd * mh), k1 = both(-rstd * mhx), k2 = both(rstd);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const Vec8 d = unpack8(dy[i]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 xh = mul2(r[i].v[j], k2);
+            g[i].v[j] = add2(g[i].v[j], fma2(k2, h[i].v[j], fma2(k1, xh, k0)));
+            acc[K - 2][i].v[j] = fma2(d.v[j], xh, acc[K - 2][i].v[j]);
+            acc[K - 1][i].v[j] = add2(acc[K - 1][i].v[j], d.v[j]);
+          }
         }
       }
-      sum(s);
-      rstd = __frsqrt_rn(s[0] * inv_d + p.eps);
-      mhx = rstd * s[1] * inv_d;
     }
-    float s[1] = {0.f};                 // sum u z
+    float2 a = both(0.f);               // sum u z
     Vec8 u[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (!at.valid[i]) continue;
-      const Vec8 r = St::get(rr[i]), dy = unpack8(yr[i]), z = unpack8(zr[i]);
-      Vec8 g = St::get(gr[i]);
+      if (at.valid[i]) St::store(p.dx, (off + 512 * i) * SP, g[i], wide);
+      const Vec8 c = kKept ? kept8(2 * i) : make_c(i);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (PRE != kNormNone) {
-          const float xh = (r.v[j] - mean) * rstd;
-          g.v[j] += rstd * (dy.v[j] * f[i].v[j] - mh - xh * mhx);
-          acc[K - 2][i][j] += dy.v[j] * xh;
-          acc[K - 1][i][j] += dy.v[j];
+      for (int j = 0; j < 4; ++j) {
+        const float2 zh = POST ? mul2(z[i].v[j], both(rz)) : z[i].v[j];
+        acc[0][i].v[j] = fma2(g[i].v[j], zh, acc[0][i].v[j]);
+        u[i].v[j] = mul2(c.v[j], g[i].v[j]);
+        if (POST) {
+          a = fma2(u[i].v[j], zh, a);
+          z[i].v[j] = zh;
         }
-        acc[0][i][j] += g.v[j] * (z.v[j] * rz);
-        u[i].v[j] = c[i].v[j] * g.v[j];
-        if (POST) s[0] += u[i].v[j] * z.v[j];
       }
-      St::store(p.dx, base + at.vec[i], g.v);
     }
-    float mu = 0.f;
+    float2 mu = both(0.f);              // -mean(u zhat)
     if constexpr (POST) {
+      float s[1] = {a.x + a.y};
       sum(s);
-      mu = rz * s[0] * inv_d;
+      mu = both(-s[0] * inv_d);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (!at.valid[i]) continue;
-      if (POST) {
-        const Vec8 z = unpack8(zr[i]);
+      if (POST)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[i].v[j] = rz * (u[i].v[j] - z.v[j] * rz * mu);
-      }
-      reinterpret_cast<uint4*>(p.dz)[base + at.vec[i]] = pack8(u[i].v);
+        for (int j = 0; j < 4; ++j) u[i].v[j] = mul2(both(rz), fma2(z[i].v[j], mu, u[i].v[j]));
+      if (at.valid[i]) *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.dz) + off + 512 * i) = pack8(u[i]);
     }
   }
 
@@ -478,9 +594,9 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float4* to = reinterpret_cast<float4*>(cols + k * p.D + 8 * at.vec[i]) + h;
-              const float* a = &acc[k][i][4 * h];
+              const float2 lo = acc[k][i].v[2 * h], hi = acc[k][i].v[2 * h + 1];
               const float4 t = g ? *to : make_float4(0, 0, 0, 0);
-              *to = make_float4(t.x + a[0], t.y + a[1], t.z + a[2], t.w + a[3]);
+              *to = make_float4(t.x + lo.x, t.y + lo.y, t.z + hi.x, t.w + hi.y);
             }
   }
   __syncthreads();
@@ -544,23 +660,32 @@ cudaError_t fwd(const ResidualParams& p, const RowPlan& plan, cudaStream_t strea
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   ProfScope prof("residual_norm_fwd", stream);
-  kernel<<<static_cast<unsigned>(p.B * plan.slabs), threads, smem, stream>>>(p, plan);
+  kernel<<<static_cast<unsigned>(p.B * plan.slabs), threads, smem, stream>>>(p, plan, reinterpret_cast<uintptr_t>(p.r) % 32 == 0);
+  return cudaGetLastError();
+}
+template <bool F32, int V, bool POST, int PRE, int WARPS>
+cudaError_t bwd_rows(const ResidualParams& p, const RowPlan& plan, cudaStream_t stream) {
+  const int K = sums_of(PRE), threads = 32 * plan.W * plan.G;
+  constexpr int SP = Stream<F32>::kParts, P = PRE == kNormNone ? SP + 1 : 2 * SP + 2;
+  const size_t cols = static_cast<size_t>(K) * p.D * sizeof(float), ring = Ring<P, V, bwd_stages<P, V, WARPS>()>::bytes(threads);
+  const size_t factors = kept_factors<WARPS>() ? static_cast<size_t>(V) * 64 * threads : 0;
+  const size_t smem = cols > ring + factors ? cols : ring + factors;
+  auto kernel = residual_norm_bwd_kernel<F32, V, POST, PRE, WARPS>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  ProfScope prof("residual_norm_bwd", stream);
+  kernel<<<static_cast<unsigned>(p.B * plan.slabs), threads, smem, stream>>>(p, plan, reinterpret_cast<uintptr_t>(p.dx) % 32 == 0);
   return cudaGetLastError();
 }
 template <bool F32, int V, bool POST, int PRE>
 cudaError_t bwd(const ResidualParams& p, const RowPlan& plan, cudaStream_t stream) {
-  const int K = sums_of(PRE), threads = 32 * plan.W * plan.G;
-  constexpr int SP = Stream<F32>::kParts, P = PRE == kNormNone ? SP + 1 : 2 * SP + 2;
-  const size_t cols = static_cast<size_t>(K) * p.D * sizeof(float), ring = Ring<P, V, bwd_stages<P, V>()>::bytes(threads);
-  const size_t smem = cols > ring ? cols : ring;
-  auto kernel = residual_norm_bwd_kernel<F32, V, POST, PRE>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  const int K = sums_of(PRE);
+  cudaError_t e;
+  if constexpr (V == 2)
+    e = plan.warps == kBwdWarps ? bwd_rows<F32, V, POST, PRE, kBwdWarps>(p, plan, stream) : bwd_rows<F32, V, POST, PRE, kMaxWarps>(p, plan, stream);
+  else
+    e = bwd_rows<F32, V, POST, PRE, kBwdWarps>(p, plan, stream);
   if (e != cudaSuccess) return e;
-  {
-    ProfScope prof("residual_norm_bwd", stream);
-    kernel<<<static_cast<unsigned>(p.B * plan.slabs), threads, smem, stream>>>(p, plan);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
   const bool weights = p.dw_post || p.dw_pre;
   if (!p.d_gate && !p.d_scale && !p.d_shift && !weights) return cudaSuccess;
   float* per_sample = weights && p.B > 1 ? p.partial + p.B * plan.slabs * K * p.D : nullptr;
@@ -591,16 +716,16 @@ cudaError_t bwd(const ResidualParams& p, const RowPlan& plan, cudaStream_t strea
 }  // namespace
 
 size_t residual_bwd_workspace(int64_t B, int64_t N, int64_t D, int pre) {
-  const RowPlan q = row_plan(B, N, D, kBwdCtas);
+  const RowPlan q = row_plan(B, N, D, kBwdCtas, kBwdWarps);
   return static_cast<size_t>(B * q.slabs * sums_of(pre) + 2 * B) * D * sizeof(float);
 }
 
 cudaError_t launch_residual_norm_fwd(const ResidualParams& p, cudaStream_t stream) {
-  const RowPlan plan = row_plan(p.B, p.N, p.D, kFwdCtas);
+  const RowPlan plan = row_plan(p.B, p.N, p.D, kFwdCtas, kMaxWarps);
   return DSV_RESIDUAL_PICK(fwd, plan.V, p, plan, stream);
 }
 cudaError_t launch_residual_norm_bwd(const ResidualParams& p, cudaStream_t stream) {
-  const RowPlan plan = row_plan(p.B, p.N, p.D, kBwdCtas);
+  const RowPlan plan = row_plan(p.B, p.N, p.D, kBwdCtas, kBwdWarps);
   return DSV_RESIDUAL_PICK(bwd, plan.V, p, plan, stream);
 }
 
