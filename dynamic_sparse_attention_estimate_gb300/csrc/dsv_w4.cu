@@ -6,56 +6,120 @@
 // multiply) takes about three instructions a weight of the 128 it can issue to its lanes: so the products run on the
 // tensor cores through mma.sync (16 x 8 x 16), whose operands come straight from the registers that the weights
 // were loaded into.  tcgen05 would want them as bf16 in shared memory, 128 rows at a time, for at most 64 columns.
-//   A value is unpacked as the bf16 number 128 + q (its four bits or-ed into 0x4300) and 128 + zero is subtracted, both
-// exact; the scale multiplies fp32 sums (forward) or the other operand (backward).  Sums are fp32, with one rounding at
-// the output.
+//   Four bits that a mask leaves at the foot of a bf16 number are q 2^-133, a subnormal one, and four bits above them 16 q 2^-133:
+// the numbers up to 255 2^-133 are evenly spaced.  One fma (which keeps subnormal numbers) makes (q - zero) / 64 of either, with
+// nothing lost and without a shift: the integer pipe, which unpacks at half the rate of the others, is what bounds these
+// kernels.  The scale multiplies fp32 sums (forward) or the other operand (backward), with 64 in it.  Sums are fp32, with one
+// rounding at the output.
+#include <type_traits>
+
 #include "dsv_block.h"
 #include "dsv_common.cuh"
 
 namespace dsv {
 namespace {
 
-constexpr uint32_t kMagic = 0x43004300u;   // bf16 128 in both halves: or-ing q into the low bits gives 128 + q
-
-DSV_DEVICE uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
-  __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<uint32_t*>(&r);
+constexpr float kUnit = 64.f;
+// -zero / 64 in both halves of a register.
+DSV_DEVICE __nv_bfloat162 zero_pair(uint32_t zero) {
+  return __float2bfloat162_rn(static_cast<int>(zero & 15u) * (-1.f / kUnit));
 }
-// Values i and i + 4 of a word's eight, less the zero point (zz: 128 + zero in both halves).
-DSV_DEVICE uint32_t unpack_pair(uint32_t word, int i, uint32_t zz) {
-  return sub_bf16x2(((word >> (4 * i)) & 0x000f000fu) | kMagic, zz);
+// (q - zero) / 64 of the halves' four bits 0 .. 3 (`high`: 4 .. 7).
+template <bool HIGH>
+DSV_DEVICE uint32_t unpack_pair(uint32_t pair, __nv_bfloat162 zero) {
+  const uint32_t bits = pair & (HIGH ? 0x00f000f0u : 0x000f000fu);
+  const __nv_bfloat162 unit = __float2bfloat162_rn(HIGH ? 0x1p123f : 0x1p127f);
+  const __nv_bfloat162 v = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&bits), unit, zero);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
-DSV_DEVICE uint32_t zero_pair(const uint8_t* zero, int64_t at) {
-  return zero ? kMagic + (zero[at] & 15u) * 0x00010001u : kMagic + 0x00080008u;
+// -zero / 64 of two bytes.
+DSV_DEVICE uint32_t zero_of2(uint32_t zeros) {
+  return pack_bf16x2(static_cast<int>(zeros & 15u) * (-1.f / kUnit), static_cast<int>(zeros >> 8 & 15u) * (-1.f / kUnit));
+}
+DSV_DEVICE uint32_t read_bytes2(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(at) : "memory");
+  return v;
 }
 
 // ---------------------------------------------------------------- forward
 // A CTA takes 16 RS rows of W; its four warps share the columns in chunks of 128 (warp w: chunks w, w + 4, ..) and add up
-// in the end.  In a chunk a lane (g = lane / 4, t = lane % 4) loads columns 32 t .. 32 t + 31 of rows g and g + 8 (16
-// bytes each): eight products of 16 columns, each with columns of all four t.  With G < 128 these are of
-// different groups, whose sums must stay apart until the scales: the 8 columns of the other operand are then 8 G / 128
-// vectors for each group, which are zero in the lanes t of other groups.
+// in the end.  A warp's next chunks are on their way into shared memory (cp.async), from where a lane (g = lane / 4,
+// t = lane % 4) takes four words (32 values) of rows g and g + 8, G / 32 of them next to each other: then the sixteen columns of a
+// product are all of one group, and its fp32 sums are scaled once a group.
 constexpr int kFwdWarps = 4;
-
+constexpr int kStages = 3;                       // chunks of a warp on their way
+// Bytes between the 64-byte rows of a chunk in shared memory, so that what a load reads at once (16 bytes of two rows, 8 of four or
+// 4 of eight, times t) is in different banks.
+template <int G>
+constexpr int fwd_pitch() {
+  return G == 128 ? 64 : G == 64 ? 96 : 80;
+}
 template <int G, int NT, int RS>
-__global__ void __launch_bounds__(32 * kFwdWarps)
-w4_fwd_kernel(W4Params p) {
-  constexpr int GP = 128 / G, VT = 8 / GP;       // groups of a chunk, vectors of a tile of eight
-  __shared__ float red[kFwdWarps][RS * 16][8 * NT + 1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int64_t f0 = static_cast<int64_t>(blockIdx.x) * (16 * RS), m0 = static_cast<int64_t>(blockIdx.y) * (VT * NT);
-  const int64_t row_bytes = p.D / 2, row_groups = p.D / G;
-  const int chunks = static_cast<int>((p.D + 127) / 128);
-  const int part = t * 32 / G;                   // group of this lane's columns in a chunk
+constexpr int fwd_smem() {
+  constexpr int ring = kStages * RS * 16 * fwd_pitch<G>() * kFwdWarps, red = kFwdWarps * RS * 16 * (8 * NT + 1) * 4;
+  return ring > red ? ring : red;
+}
+// Four, eight or sixteen bytes of shared memory.
+template <int N>
+DSV_DEVICE void read_words(uint32_t at, uint32_t* v) {
+  if constexpr (N == 1) asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v[0]) : "r"(at) : "memory");
+  if constexpr (N == 2) asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(v[0]), "=r"(v[1]) : "r"(at) : "memory");
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
+}
 
-  int64_t row[RS][2];                            // rows past the last read the last, and are not stored
+template <int G, int NT, int RS, bool ZERO>
+__global__ void __launch_bounds__(32 * kFwdWarps, NT == 1 ? 4 : NT == 2 ? 3 : 2)
+w4_fwd_kernel(W4Params p) {
+  constexpr int GP = 128 / G, WG = G / 32, kPitch = fwd_pitch<G>();   // groups of a chunk, a lane's words of a group
+  extern __shared__ __align__(16) unsigned char shared[];   // the weights on their way, then the warps' sums
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int64_t f0 = static_cast<int64_t>(blockIdx.x) * (16 * RS);
+  const int m0 = blockIdx.y * (8 * NT);
+  const int D = static_cast<int>(p.D), M = static_cast<int>(p.M), row_groups = D / G, chunks = (D + 127) / 128;
+  const int last = static_cast<int>(min(p.F - f0, static_cast<int64_t>(16 * RS))) - 1;
+
+  // Rows past the last read the last, and are not stored.  Columns past the last read the last ones: the vectors are 0 there.
+  uint32_t scale_at[RS][2];                      // element of the scales (and zero points) of the lane's rows
 #pragma unroll
   for (int i = 0; i < RS; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      row[i][h] = f0 + i * 16 + h * 8 + g;
-      if (row[i][h] >= p.F) row[i][h] = p.F - 1;
+    for (int h = 0; h < 2; ++h) scale_at[i][h] = min(i * 16 + h * 8 + g, last) * row_groups;
+  const bf16* const scales = p.scale + f0 * row_groups;
+  const uint8_t* const zeros = ZERO ? p.zero + f0 * row_groups : nullptr;
+  bf16 scale[RS][2][GP];
+  uint8_t zero[ZERO ? RS : 1][2][GP];
+  auto load_scales = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < RS; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < GP; ++q) {
+          const uint32_t at = scale_at[i][h] + min(c * GP + q, row_groups - 1);
+          scale[i][h][q] = scales[at];
+          if (ZERO) zero[i][h][q] = zeros[at];
+        }
+  };
+  // Lane l brings part l % 4 of rows l / 4, l / 4 + 8, ..
+  const uint32_t ring = smem_u32(shared) + warp * (kStages * RS * 16 * kPitch);
+  uint32_t row_at[2 * RS];
+#pragma unroll
+  for (int i = 0; i < 2 * RS; ++i) row_at[i] = min(i * 8 + g, last) * (D / 2);
+  const uint8_t* const data = p.data + f0 * (D / 2);
+  auto issue = [&](int c, int stage) {
+    if (c < chunks) {
+      const uint32_t col = min(c * 128 + t * 32, D - 32) / 2, to = ring + stage * (RS * 16 * kPitch) + g * kPitch + 16 * t;
+#pragma unroll
+      for (int i = 0; i < 2 * RS; ++i) cp_async_16(to + i * 8 * kPitch, data + (row_at[i] + col), true);
     }
+    cp_async_commit();                           // one group a chunk, so that the wait below counts chunks
+  };
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) issue(warp + s * kFwdWarps, s);
+  load_scales(warp < chunks ? warp : 0);
+
   float acc[RS][NT][4];
 #pragma unroll
   for (int i = 0; i < RS; ++i)
@@ -63,59 +127,61 @@ w4_fwd_kernel(W4Params p) {
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][n][j] = 0.f;
-
+  int stage = 0;
   for (int c = warp; c < chunks; c += kFwdWarps) {
-    const int64_t col = static_cast<int64_t>(c) * 128 + t * 32;
-    const bool inside = col < p.D;               // D is a multiple of 32
-    uint4 a[RS][2];
-    uint32_t zz[RS][2];
-    float sc[RS][2];
-    const int64_t group = min(static_cast<int64_t>(c) * GP + part, row_groups - 1);
-#pragma unroll
-    for (int i = 0; i < RS; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        a[i][h] = inside ? __ldcs(reinterpret_cast<const uint4*>(p.data + row[i][h] * row_bytes + col / 2)) : make_uint4(0, 0, 0, 0);
-        zz[i][h] = zero_pair(p.zero, row[i][h] * row_groups + group);
-        sc[i][h] = __bfloat162float(p.scale[row[i][h] * row_groups + group]);
-      }
     uint32_t b[NT][16];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int64_t m = m0 + n * VT + g % VT;
-      const bool mine = inside && g / VT == part && m < p.M;
+      const int m = m0 + n * 8 + g;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const uint4 x = mine ? __ldg(reinterpret_cast<const uint4*>(p.x + m * p.D + col) + w) : make_uint4(0, 0, 0, 0);
-        b[n][4 * w] = __byte_perm(x.x, x.z, 0x5410);       // columns 0 and 4, as unpack_pair gives them
+        const int col = c * 128 + w / WG * G + t * (8 * WG) + w % WG * 8;
+        const uint4 x = col < D && m < M ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(m) * D + col)) : make_uint4(0, 0, 0, 0);
+        b[n][4 * w] = __byte_perm(x.x, x.z, 0x5410);       // columns 0 and 4, as the halves of a word have them
         b[n][4 * w + 1] = __byte_perm(x.x, x.z, 0x7632);   // 1 and 5
         b[n][4 * w + 2] = __byte_perm(x.y, x.w, 0x5410);   // 2 and 6
         b[n][4 * w + 3] = __byte_perm(x.y, x.w, 0x7632);   // 3 and 7
       }
     }
+    cp_async_wait<kStages - 1>();
+    __syncwarp();
+    const uint32_t mine = ring + stage * (RS * 16 * kPitch) + g * kPitch + 4 * WG * t;
 #pragma unroll
     for (int i = 0; i < RS; ++i) {
-      float s[NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int q = 0; q < GP; ++q) {
+        uint32_t w0[WG], w1[WG];
+        read_words<WG>(mine + i * 16 * kPitch + q * (G / 2), w0);
+        read_words<WG>(mine + (i * 16 + 8) * kPitch + q * (G / 2), w1);
+        const __nv_bfloat162 z0 = zero_pair(ZERO ? zero[i][0][q] : 8), z1 = zero_pair(ZERO ? zero[i][1][q] : 8);
+        float s[NT][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[n][j] = 0.f;
-      const uint32_t w0[4] = {a[i][0].x, a[i][0].y, a[i][0].z, a[i][0].w}, w1[4] = {a[i][1].x, a[i][1].y, a[i][1].z, a[i][1].w};
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int w = k / 2, e = 2 * (k % 2);
-        const uint32_t frag[4] = {unpack_pair(w0[w], e, zz[i][0]), unpack_pair(w1[w], e, zz[i][1]),
-                                  unpack_pair(w0[w], e + 1, zz[i][0]), unpack_pair(w1[w], e + 1, zz[i][1])};
+          for (int j = 0; j < 4; ++j) s[n][j] = 0.f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma_bf16_16816(s[n], frag, b[n][4 * w + e], b[n][4 * w + e + 1]);
+        for (int k = 0; k < 2 * WG; ++k) {
+          const int w = k / 2, e = 2 * (k % 2);   // values e and e + 4, e + 1 and e + 5 of the word
+          const uint32_t p0 = w0[w] >> (4 * e), p1 = w1[w] >> (4 * e);
+          const uint32_t frag[4] = {unpack_pair<false>(p0, z0), unpack_pair<false>(p1, z1), unpack_pair<true>(p0, z0), unpack_pair<true>(p1, z1)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_bf16_16816(s[n], frag, b[n][4 * (q * WG + w) + e], b[n][4 * (q * WG + w) + e + 1]);
+        }
+        // sums j = 0, 1: row g; 2, 3: row g + 8; of vectors 2 t, 2 t + 1
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][n][j] += __bfloat162float(scale[i][j / 2][q]) * s[n][j];
       }
-      // sums j = 0, 1: row g; 2, 3: row g + 8; both of tile columns 2 t, 2 t + 1, which are of group 2 t / VT = part
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][n][j] += sc[i][j / 2] * s[n][j];
     }
+    if (c + kFwdWarps < chunks) load_scales(c + kFwdWarps);
+    __syncwarp();
+    issue(c + kStages * kFwdWarps, stage);       // into the stage that this chunk has left
+    stage = stage + 1 < kStages ? stage + 1 : 0;
   }
+  cp_async_wait<0>();
+  __syncthreads();
+  float(*const red)[RS * 16][8 * NT + 1] = reinterpret_cast<float(*)[RS * 16][8 * NT + 1]>(shared);
 #pragma unroll
   for (int i = 0; i < RS; ++i)
 #pragma unroll
@@ -123,62 +189,186 @@ w4_fwd_kernel(W4Params p) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) red[warp][i * 16 + g + 8 * (j / 2)][n * 8 + 2 * t + j % 2] = acc[i][n][j];
   __syncthreads();
-  for (int i = threadIdx.x; i < RS * 16 * VT * NT; i += 32 * kFwdWarps) {
+  for (int i = threadIdx.x; i < RS * 16 * 8 * NT; i += 32 * kFwdWarps) {
     const int r = i % (RS * 16), v = i / (RS * 16);
-    const int64_t f = f0 + r, m = m0 + v;
-    if (f >= p.F || m >= p.M) continue;
+    if (r > last || m0 + v >= M) continue;
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kFwdWarps; ++w)
-#pragma unroll
-      for (int q = 0; q < GP; ++q) s += red[w][r][v / VT * 8 + q * VT + v % VT];
-    if (p.bias) s += __bfloat162float(p.bias[f]);
-    p.y[m * p.F + f] = __float2bfloat16(s);
+    for (int w = 0; w < kFwdWarps; ++w) s += red[w][r][v];
+    s *= kUnit;
+    if (p.bias) s += __bfloat162float(p.bias[f0 + r]);
+    p.y[(m0 + v) * p.F + f0 + r] = __float2bfloat16(s);
   }
 }
 
 // ---------------------------------------------------------------- backward
-// dx[m, c] = sum_f (dy[m, f] scale[f, c / G]) (q[f, c] - zero): the contraction runs over the rows.  A warp takes 64 columns
-// and steps of 16 rows: a lane (g, t) loads its eight columns 8 g .. 8 g + 7 of rows 4 t .. 4 t + 3 (4 bytes each), pairs the
-// rows, and product j of four is of columns 8 g + 2 j and 8 g + 2 j + 1.  The other operand, dy times the scale, is held as
-// two bf16 numbers, the rounded value and what it left (16 bits: exact for dy in bf16, 2^-16 of the value for fp32), in
-// neighbouring columns of the tile, so that a lane's two sums of a row add up to one result.  Groups of 32: the 64 columns
-// are of two groups, and a tile holds each vector once for each.
-//   A CTA is two such column blocks by four runs of rows, whose sums it adds; the CTAs of one column block share the rows
-// of W in `splits` runs, whose partial results w4_join_kernel adds in order.
+// dx[m, c] = sum_f (dy[m, f] scale[f, c / G]) (q[f, c] - zero): the contraction runs over the rows.  A CTA takes 128 columns
+// and a run of rows in chunks of 256: two warps side by side, four below each other with 64 rows of a chunk each, the
+// next chunks on their way into shared memory.  In a step of 16 rows a lane (g, t) holds eight columns of rows t, t + 4, t + 8
+// and t + 12, pairs the rows, and product j of four is of two of its columns; the columns of a product are all of one group.
+//   The other operand, dy times the scale, is held as two bf16 numbers, the rounded value and what it left (16 bits: exact
+// for dy in bf16, 2^-16 of the value for fp32), in neighbouring columns of the tile, so that a lane's two sums of a row
+// add up to one result.  It is the same for all columns of a group, so the CTA makes it once a chunk in shared memory, in the
+// order in which the lanes take it.
+//   The CTAs of one column block share the rows of W in `splits` runs, whose partial results w4_join_kernel adds in order.
 constexpr int kBwdColWarps = 2, kBwdRowWarps = 4, kBwdWarps = kBwdColWarps * kBwdRowWarps;
-constexpr int kBwdCols = 64 * kBwdColWarps;
-constexpr int64_t kBwdWantCtas = 4 * 152;
+constexpr int kBwdCols = 64 * kBwdColWarps, kBwdSteps = 4, kBwdRows = 16 * kBwdSteps * kBwdRowWarps, kQuads = kBwdRows / 4;
+// A row of a chunk is 64 bytes; the halves of every third and fourth of four rows are exchanged, so that the four rows t and
+// the 32 bytes of a warp's columns are in different banks.
+constexpr int kBwdStage = kBwdRows * kBwdCols / 2, kBwdStages = 3;
+constexpr int64_t kBwdWantCtas = 3 * 152;
 struct W4BwdPlan {
-  int64_t col_blocks, splits, rows;     // rows of W to a CTA, a multiple of 16 kBwdRowWarps
+  int64_t col_blocks, splits, rows;     // rows of W to a CTA, a multiple of kBwdRows
 };
 W4BwdPlan w4_bwd_plan(int64_t D, int64_t F) {
   W4BwdPlan q;
-  const int64_t step = 16 * kBwdRowWarps;
   q.col_blocks = (D + kBwdCols - 1) / kBwdCols;
-  q.splits = (kBwdWantCtas + q.col_blocks - 1) / q.col_blocks;
-  const int64_t most = (F + step - 1) / step;
+  q.splits = kBwdWantCtas / q.col_blocks;
+  const int64_t most = (F + kBwdRows - 1) / kBwdRows;
   if (q.splits > most) q.splits = most;
-  q.rows = ((F + q.splits - 1) / q.splits + step - 1) / step * step;
+  if (q.splits < 1) q.splits = 1;
+  q.rows = ((F + q.splits - 1) / q.splits + kBwdRows - 1) / kBwdRows * kBwdRows;
   q.splits = (F + q.rows - 1) / q.rows;
   return q;
 }
+template <int G, int NT, bool ZERO>
+constexpr int bwd_smem() {
+  constexpr int use = kBwdStages * kBwdStage + kBwdCols / G * kQuads * (NT * 64 + (ZERO ? 8 : 0));
+  constexpr int red = kBwdRowWarps * 4 * NT * kBwdCols * 4;
+  return use > red ? use : red;
+}
 
-template <int G, int NT, bool F32>
-__global__ void __launch_bounds__(32 * kBwdWarps)
+// The rounded value of four rows' numbers and what it leaves, as bf16.  An infinite one leaves NaN, for which the maximum
+// takes -2^120, the least rest that there is: next to the infinity it is nothing.
+DSV_DEVICE uint4 split4(const float (&v)[4]) {
+  const __nv_bfloat162 least = __float2bfloat162_rn(-0x1p120f);
+  uint32_t hi[2], lo[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    hi[h] = pack_bf16x2(v[2 * h], v[2 * h + 1]);
+    const __nv_bfloat162 r = __hmax2(__floats2bfloat162_rn(v[2 * h] - bf16_lo(hi[h]), v[2 * h + 1] - bf16_hi(hi[h])), least);
+    lo[h] = *reinterpret_cast<const uint32_t*>(&r);
+  }
+  return make_uint4(hi[0], hi[1], lo[0], lo[1]);
+}
+
+// One, two or four 16-bit numbers, as one load brings them.
+template <int N>
+struct Pack {
+  using type = std::conditional_t<N == 2, unsigned short, std::conditional_t<N == 4, unsigned int, uint2>>;
+  uint32_t v[N == 8 ? 2 : 1];
+  DSV_DEVICE Pack& operator=(const type& a) {
+    if constexpr (N == 8) v[0] = a.x, v[1] = a.y;
+    else v[0] = a;
+    return *this;
+  }
+  DSV_DEVICE uint32_t get(int q) const { return v[q / 2] >> (16 * (q % 2)) & 0xffffu; }
+  DSV_DEVICE void set(int q, uint32_t a) { v[q / 2] |= a << (16 * (q % 2)); }
+};
+
+template <int G, int NT, bool ZERO>
+__global__ void __launch_bounds__(32 * kBwdWarps, NT == 1 ? 3 : NT == 2 ? 2 : 1)
 w4_bwd_kernel(W4Params p, W4BwdPlan plan) {
-  constexpr int GP = G < 64 ? 64 / G : 1, VT = 4 / GP;   // groups of a warp's columns, vectors of a tile
-  __shared__ float red[kBwdRowWarps][VT * NT][kBwdCols];
+  constexpr int CG = kBwdCols / G;               // groups of the CTA's columns
+  extern __shared__ __align__(16) unsigned char shared[];   // the stages, the other operand, the zero points; then the warps' sums
+  uint2(*const other)[NT][kQuads][8] = reinterpret_cast<uint2(*)[NT][kQuads][8]>(shared + kBwdStages * kBwdStage);   // [CG]
+  uint2(*const zeros)[kQuads] = reinterpret_cast<uint2(*)[kQuads]>(other + CG);
+  // the join kernel may be scheduled once every CTA has started; it waits for this grid before it reads
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int cw = warp % kBwdColWarps, rw = warp / kBwdColWarps;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kBwdCols + cw * 64, m0 = static_cast<int64_t>(blockIdx.z) * (VT * NT);
+  const int D = static_cast<int>(p.D), M = static_cast<int>(p.M), row_groups = D / G;
+  const int cta0 = blockIdx.x * kBwdCols, m0 = blockIdx.z * (4 * NT);
   const int64_t f_lo = blockIdx.y * plan.rows, f_hi = min(f_lo + plan.rows, p.F);
-  const int64_t row_bytes = p.D / 2, row_groups = p.D / G;
-  const bool inside = c0 + 8 * g < p.D;
-  const int64_t my_group = min((c0 + 8 * g) / G, row_groups - 1);   // of the lane's columns
-  // of the lane's place in the other operand: tile column g is (group, vector, rounded value or rest)
-  const int64_t b_group = min(c0 / G + g / (2 * VT), row_groups - 1);
-  const int b_vec = g / 2 % VT;
+  const int64_t stride = D / 2;
+
+  // The weights on their way, a chunk to a stage.  Rows past the last read the last, whose scales count as 0 in the other operand;
+  // columns past the last read the last sixteen bytes, and are not stored.
+  constexpr int kParts = kBwdCols / 32, kRowsAtOnce = 32 * kBwdWarps / kParts;
+  const uint32_t ring = smem_u32(shared);
+  const int own_part = threadIdx.x % kParts, part_row = threadIdx.x / kParts;
+  const uint32_t part_to = ring + part_row * (kBwdCols / 2) + 16 * (own_part ^ (part_row & 2));
+  const uint8_t* part_from = p.data + (f_lo + part_row) * stride + min(cta0 + 32 * own_part, D - 32) / 2;   // of the next chunk
+  auto issue = [&](int64_t f, int stage) {
+    if (f < f_hi && f + kBwdRows <= p.F) {
+#pragma unroll
+      for (int k = 0; k < kBwdRows / kRowsAtOnce; ++k)
+        cp_async_16(part_to + stage * kBwdStage + k * kRowsAtOnce * (kBwdCols / 2), part_from + k * kRowsAtOnce * stride, true);
+    } else if (f < f_hi) {
+#pragma unroll
+      for (int k = 0; k < kBwdRows / kRowsAtOnce; ++k)
+        cp_async_16(part_to + stage * kBwdStage + k * kRowsAtOnce * (kBwdCols / 2),
+                    part_from + (min(f + part_row + k * kRowsAtOnce, p.F - 1) - f - part_row) * stride, true);
+    }
+    part_from += kBwdRows * stride;
+    cp_async_commit();                           // one group a chunk, so that the wait below counts chunks
+  };
+
+  // This thread's part of the other operand: four rows of every fourth vector, for all of the CTA's groups.
+  const int own_v = threadIdx.x % 4, own_quad = threadIdx.x / 4;
+  const int own_row = own_quad / 4 * 16 + own_quad % 4;   // and the fourth, eighth and twelfth after it
+  const bool whole = D % kBwdCols == 0;          // the CTA's groups of a row are one aligned load
+  const int groups = min(CG, row_groups - cta0 / G);   // of the CTA's, those that there are
+  // scales are two chunks ahead of their use, zero points and dy one
+  using Scales = Pack<2 * CG>;
+  const uint32_t scale_step = 4 * row_groups;    // elements between the four rows
+  const bf16* scale_from = p.scale + (f_lo + own_row) * row_groups + cta0 / G;
+  auto load_scales = [&](int64_t f, Scales (&to)[4]) {
+    if (whole && f < f_hi && f + kBwdRows <= p.F) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) to[i] = __ldcs(reinterpret_cast<const typename Scales::type*>(scale_from + i * scale_step));
+    } else {
+      const int64_t left = f < f_hi ? p.F - f - own_row : 0;   // rows to the end
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        to[i] = Scales{};
+        if (4 * i < left)
+#pragma unroll
+          for (int q = 0; q < CG; ++q)
+            if (q < groups) to[i].set(q, reinterpret_cast<const uint16_t*>(scale_from + i * scale_step)[q]);
+      }
+    }
+    scale_from += kBwdRows * static_cast<int64_t>(row_groups);
+  };
+  const uint8_t* zero_from = ZERO ? p.zero + (f_lo + own_row) * row_groups + cta0 / G + min(own_v, groups - 1) : nullptr;
+  uint32_t zero = 0;                             // of four rows, a byte each: group own_v
+  float dys[NT][4];
+  const int64_t dy_at = (m0 + own_v) * p.F + own_row;
+  const int vectors = (M - m0 - own_v + 3) / 4;  // of this thread's, those that there are
+  auto load_dy = [&](int64_t f) {
+    const int64_t rest = p.F - f - own_row;
+    const int left = rest < 16 ? static_cast<int>(rest) : 16;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int64_t at = dy_at + f + 4 * n * p.F;
+      const float* const d32 = static_cast<const float*>(p.dy) + at;
+      const bf16* const d16 = static_cast<const bf16*>(p.dy) + at;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dys[n][i] = 0.f;
+      if (n >= vectors) continue;
+      if (p.dy_f32) {
+        if (left == 16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dys[n][i] = __ldg(d32 + 4 * i);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (4 * i < left) dys[n][i] = __ldg(d32 + 4 * i);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (4 * i < left) dys[n][i] = __bfloat162float(d16[4 * i]);
+      }
+    }
+    if (ZERO) {
+      zero = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * i < left) zero |= (zero_from[i * scale_step] & 15u) << (8 * i);
+      zero_from += kBwdRows * static_cast<int64_t>(row_groups);
+    }
+  };
 
   float acc[NT][4][4];
 #pragma unroll
@@ -188,74 +378,108 @@ w4_bwd_kernel(W4Params p, W4BwdPlan plan) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][j][i] = 0.f;
 
-  for (int64_t f = f_lo + rw * 16; f < f_hi; f += 16 * kBwdRowWarps) {
-    uint32_t w[4], z[4];
-    float b[NT][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t row = f + 4 * t + i;
-      const bool in = row < f_hi;
-      w[i] = in && inside ? __ldcs(reinterpret_cast<const uint32_t*>(p.data + row * row_bytes + (c0 + 8 * g) / 2)) : 0u;
-      z[i] = in && p.zero ? p.zero[row * row_groups + my_group] & 15u : 8u;
-      const float sc = in ? __bfloat162float(p.scale[row * row_groups + b_group]) : 0.f;
+  for (int s = 0; s < kBwdStages - 1; ++s) issue(f_lo + s * kBwdRows, s);
+  Scales scales[4], scales1[4];
+  load_scales(f_lo, scales);
+  load_scales(f_lo + kBwdRows, scales1);
+  load_dy(f_lo);
+  int stage = 0;
+  for (int64_t f = f_lo; f < f_hi; f += kBwdRows) {
+    cp_async_wait<kBwdStages - 2>();
+    if (f > f_lo) __syncthreads();               // every warp is done with the last chunk and its operand
+#pragma unroll
+    for (int q = 0; q < CG; ++q)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int64_t m = m0 + n * VT + b_vec;
-        float d = 0.f;
-        if (in && m < p.M)
-          d = F32 ? static_cast<const float*>(p.dy)[m * p.F + row]
-                  : __bfloat162float(static_cast<const bf16*>(p.dy)[m * p.F + row]);
-        b[n][i] = d * sc;
+        float b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = dys[n][i] * __uint_as_float(scales[i].get(q) << 16);
+        *reinterpret_cast<uint4*>(&other[q][n][own_quad][2 * own_v]) = split4(b);
+      }
+    if (ZERO && own_v < CG)
+      zeros[own_v][own_quad] = make_uint2(zero_of2(zero), zero_of2(zero >> 16));
+    __syncthreads();
+    issue(f + (kBwdStages - 1) * kBwdRows, stage ? stage - 1 : kBwdStages - 1);   // where the last chunk was
+#pragma unroll
+    for (int i = 0; i < 4; ++i) scales[i] = scales1[i];
+    load_scales(f + 2 * kBwdRows, scales1);
+    if (f + kBwdRows < f_hi) load_dy(f + kBwdRows);
+    // groups of 64 and 128: the lane's word is columns 8 g ..; of 32: two bytes each of columns 4 g .. and 32 + 4 g ..
+    const uint32_t mine = ring + stage * kBwdStage + (rw * (16 * kBwdSteps) + t) * (kBwdCols / 2) + (cw * 32 ^ (t & 2) * 16) + (G < 64 ? 2 : 4) * g;
+    stage = stage + 1 < kBwdStages ? stage + 1 : 0;
+#pragma unroll
+    for (int s = 0; s < kBwdSteps; ++s) {
+      const int quad = (rw * kBwdSteps + s) * 4 + t;
+      uint32_t now[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t at = mine + (16 * s + 4 * i) * (kBwdCols / 2);
+        if constexpr (G < 64) now[i] = read_bytes2(at) | read_bytes2(at + 16) << 16;
+        else read_words<1>(at, &now[i]);
+      }
+#pragma unroll
+      for (int q = 0; q < (G < 64 ? 2 : 1); ++q) {
+        const int group = G < 64 ? cw * 2 + q : cw * 64 / G;
+        __nv_bfloat162 z01 = zero_pair(8), z23 = z01;
+        if constexpr (ZERO) {
+          const uint2 z = zeros[group][quad];
+          z01 = *reinterpret_cast<const __nv_bfloat162*>(&z.x);
+          z23 = *reinterpret_cast<const __nv_bfloat162*>(&z.y);
+        }
+        uint2 b[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) b[n] = other[group][n][quad][g];
+#pragma unroll
+        for (int j = G < 64 ? 2 * q : 0; j < (G < 64 ? 2 * q + 2 : 4); ++j) {
+          const uint32_t pick = j * 0x0011u + (4 + j) * 0x1100u;   // byte j of either row
+          const uint32_t p01 = __byte_perm(now[0], now[1], pick), p23 = __byte_perm(now[2], now[3], pick);
+          const uint32_t frag[4] = {unpack_pair<false>(p01, z01), unpack_pair<true>(p01, z01), unpack_pair<false>(p23, z23), unpack_pair<true>(p23, z23)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_bf16_16816(acc[n][j], frag, b[n].x, b[n].y);
+        }
       }
     }
-    uint32_t other[NT][2];
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+  // sums i = 0, 1 are product j's first column, 2, 3 its second; tile columns 2 t, 2 t + 1: value and rest of vector t
+  float(*const red)[4 * NT][kBwdCols] = reinterpret_cast<float(*)[4 * NT][kBwdCols]>(shared);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t hi = pack_bf16x2(b[n][2 * h], b[n][2 * h + 1]);
-        // an infinite value leaves no rest
-        const float r0 = isinf(bf16_lo(hi)) ? 0.f : b[n][2 * h] - bf16_lo(hi), r1 = isinf(bf16_hi(hi)) ? 0.f : b[n][2 * h + 1] - bf16_hi(hi);
-        other[n][h] = g % 2 ? pack_bf16x2(r0, r1) : hi;
-      }
-    const uint32_t z01 = kMagic + z[0] + (z[1] << 16), z23 = kMagic + z[2] + (z[3] << 16);
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t pick = j * 0x0011u + (4 + j) * 0x1100u;
-      const uint32_t p01 = __byte_perm(w[0], w[1], pick), p23 = __byte_perm(w[2], w[3], pick);
-      const uint32_t frag[4] = {sub_bf16x2((p01 & 0x000f000fu) | kMagic, z01), sub_bf16x2(((p01 >> 4) & 0x000f000fu) | kMagic, z01),
-                                sub_bf16x2((p23 & 0x000f000fu) | kMagic, z23), sub_bf16x2(((p23 >> 4) & 0x000f000fu) | kMagic, z23)};
-#pragma unroll
-      for (int n = 0; n < NT; ++n) mma_bf16_16816(acc[n][j], frag, other[n][0], other[n][1]);
+      const int col = cw * 64 + (G < 64 ? j / 2 * 32 + 4 * g + j % 2 * 2 : 8 * g + 2 * j);
+      *reinterpret_cast<float2*>(&red[rw][n * 4 + t][col]) = make_float2(acc[n][j][0] + acc[n][j][1], acc[n][j][2] + acc[n][j][3]);
     }
-  }
-  // sums i = 0, 1 are column 8 g + 2 j, 2, 3 column 8 g + 2 j + 1; tile columns 2 t, 2 t + 1: value and rest of group t / VT,
-  // vector t % VT, which counts for the columns of that group
-  if (GP == 1 || (8 * g) / G == t / VT)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        red[rw][n * VT + t % VT][cw * 64 + 8 * g + 2 * j] = acc[n][j][0] + acc[n][j][1];
-        red[rw][n * VT + t % VT][cw * 64 + 8 * g + 2 * j + 1] = acc[n][j][2] + acc[n][j][3];
-      }
   __syncthreads();
-  for (int i = threadIdx.x; i < VT * NT * kBwdCols; i += 32 * kBwdWarps) {
-    const int v = i / kBwdCols, c = i % kBwdCols;
-    const int64_t m = m0 + v, col = static_cast<int64_t>(blockIdx.x) * kBwdCols + c;
-    if (m >= p.M || col >= p.D) continue;
+  for (int i = threadIdx.x; i < 4 * NT * kBwdCols; i += 32 * kBwdWarps) {
+    const int v = i / kBwdCols, col = cta0 + i % kBwdCols;
+    if (m0 + v >= M || col >= D) continue;
     float s = 0.f;
 #pragma unroll
-    for (int r = 0; r < kBwdRowWarps; ++r) s += red[r][v][c];
-    p.partial[(blockIdx.y * p.M + m) * p.D + col] = s;
+    for (int r = 0; r < kBwdRowWarps; ++r) s += red[r][v][i % kBwdCols];
+    s *= kUnit;
+    const int64_t at = static_cast<int64_t>(m0 + v) * D + col;
+    if (plan.splits == 1) p.dx[at] = __float2bfloat16(s);
+    else p.partial[blockIdx.y * (p.M * p.D) + at] = s;
   }
 }
-__global__ void __launch_bounds__(128)
+// A CTA takes 32 numbers, a warp every eighth run; the eight sums are added in order.
+__global__ void __launch_bounds__(256)
 w4_join_kernel(W4Params p, int64_t splits) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x, n = p.M * p.D;
-  if (i >= n) return;
+  __shared__ float red[8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane, n = p.M * p.D;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   float s = 0.f;
-  for (int64_t k = 0; k < splits; ++k) s += p.partial[k * n + i];
+  if (i < n)
+#pragma unroll 4
+    for (int64_t k = warp; k < splits; k += 8) s += p.partial[k * n + i];
+  red[warp][lane] = s;
+  __syncthreads();
+  if (warp || i >= n) return;
+  for (int w = 1; w < 8; ++w) s += red[w][lane];
   p.dx[i] = __float2bfloat16(s);
 }
 
@@ -299,33 +523,46 @@ w4_quantize_kernel(W4Params p) {
   }
 }
 
+template <int G, int NT, int RS, bool ZERO>
+cudaError_t fwd_zero(const W4Params& p, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((p.F + 16 * RS - 1) / (16 * RS)), static_cast<unsigned>((p.M + 8 * NT - 1) / (8 * NT)));
+  constexpr int smem = fwd_smem<G, NT, RS>();
+  auto kernel = w4_fwd_kernel<G, NT, RS, ZERO>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, 32 * kFwdWarps, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+template <int G, int NT, int RS>
+cudaError_t fwd_rows(const W4Params& p, cudaStream_t stream) {
+  return p.zero ? fwd_zero<G, NT, RS, true>(p, stream) : fwd_zero<G, NT, RS, false>(p, stream);
+}
+// Rows of a CTA: 32 share their loads of the vectors, and 16 where that would leave SMs without four CTAs.
 template <int G, int NT>
 cudaError_t fwd(const W4Params& p, cudaStream_t stream) {
-  constexpr int VT = 8 * G / 128;
-  const dim3 grid(static_cast<unsigned>((p.F + 31) / 32), static_cast<unsigned>((p.M + VT * NT - 1) / (VT * NT)));
-  w4_fwd_kernel<G, NT, 2><<<grid, 32 * kFwdWarps, 0, stream>>>(p);
-  return cudaGetLastError();
+  return p.F < 32 * 4 * 152 ? fwd_rows<G, NT, 1>(p, stream) : fwd_rows<G, NT, 2>(p, stream);
 }
 template <int G>
 cudaError_t fwd_group(const W4Params& p, cudaStream_t stream) {
-  constexpr int VT = 8 * G / 128;
-  return p.M <= VT ? fwd<G, 1>(p, stream) : p.M <= 2 * VT ? fwd<G, 2>(p, stream) : fwd<G, 4>(p, stream);
+  return p.M <= 8 ? fwd<G, 1>(p, stream) : p.M <= 16 ? fwd<G, 2>(p, stream) : fwd<G, 4>(p, stream);
+}
+template <int G, int NT, bool ZERO>
+cudaError_t bwd_zero(const W4Params& p, const W4BwdPlan& plan, cudaStream_t stream) {
+  constexpr int smem = bwd_smem<G, NT, ZERO>();
+  const dim3 grid(static_cast<unsigned>(plan.col_blocks), static_cast<unsigned>(plan.splits), static_cast<unsigned>((p.M + 4 * NT - 1) / (4 * NT)));
+  auto kernel = w4_bwd_kernel<G, NT, ZERO>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, 32 * kBwdWarps, smem, stream>>>(p, plan);
+  return cudaGetLastError();
 }
 template <int G, int NT>
 cudaError_t bwd(const W4Params& p, const W4BwdPlan& plan, cudaStream_t stream) {
-  constexpr int VT = G < 64 ? 2 : 4;
-  const dim3 grid(static_cast<unsigned>(plan.col_blocks), static_cast<unsigned>(plan.splits),
-                  static_cast<unsigned>((p.M + VT * NT - 1) / (VT * NT)));
-  if (p.dy_f32)
-    w4_bwd_kernel<G, NT, true><<<grid, 32 * kBwdWarps, 0, stream>>>(p, plan);
-  else
-    w4_bwd_kernel<G, NT, false><<<grid, 32 * kBwdWarps, 0, stream>>>(p, plan);
-  return cudaGetLastError();
+  return p.zero ? bwd_zero<G, NT, true>(p, plan, stream) : bwd_zero<G, NT, false>(p, plan, stream);
 }
 template <int G>
 cudaError_t bwd_group(const W4Params& p, const W4BwdPlan& plan, cudaStream_t stream) {
-  constexpr int VT = G < 64 ? 2 : 4;
-  return p.M <= VT ? bwd<G, 1>(p, plan, stream) : p.M <= 2 * VT ? bwd<G, 2>(p, plan, stream) : bwd<G, 4>(p, plan, stream);
+  return p.M <= 4 ? bwd<G, 1>(p, plan, stream) : p.M <= 8 ? bwd<G, 2>(p, plan, stream) : bwd<G, 4>(p, plan, stream);
 }
 
 }  // namespace
@@ -347,9 +584,18 @@ cudaError_t launch_w4_bwd(const W4Params& p, cudaStream_t stream) {
                                                                                          : bwd_group<128>(p, plan, stream);
     if (e != cudaSuccess) return e;
   }
+  if (plan.splits == 1) return cudaSuccess;
   ProfScope prof("w4_join", stream);
-  w4_join_kernel<<<static_cast<unsigned>((p.M * p.D + 127) / 128), 128, 0, stream>>>(p, plan.splits);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.M * p.D + 31) / 32));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, w4_join_kernel, p, plan.splits);
 }
 
 cudaError_t launch_w4_quantize(const W4Params& p, cudaStream_t stream) {

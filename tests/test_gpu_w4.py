@@ -64,11 +64,12 @@ def check_bwd(c, dx, dy):
 
 
 # vectors one to 64 on both sides of each tile; one group of columns and part of a chunk, several chunks to a warp; one row,
-# part of a tile of rows, more runs of rows than one
+# part of a tile of rows, more runs of rows than one, runs of several chunks
 SHAPES = [(1, 32, 1, 32), (1, 64, 5, 64), (2, 128, 16, 128), (3, 96, 33, 32), (1, 768, 4608, 64), (4, 192, 700, 64), (5, 1184, 513, 32),
           (6, 320, 65, 64), (8, 640, 129, 128), (9, 256, 100, 128), (16, 128, 257, 64), (17, 2048, 64, 64), (31, 160, 40, 32),
           (32, 512, 90, 128), (33, 64, 50, 64), (64, 384, 77, 128), (64, 96, 31, 32), (2, 8192, 24, 64), (7, 1152, 12345, 64),
-          (1, 128, 50000, 64), (4, 8192, 16, 32)]
+          (1, 128, 50000, 64), (4, 8192, 16, 32),
+          (3, 8192, 4000, 64), (9, 8192, 2600, 32), (2, 4096, 5633, 128)]
 
 
 @pytest.mark.parametrize("zeros", [False, True])
