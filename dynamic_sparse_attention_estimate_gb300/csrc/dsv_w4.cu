@@ -42,13 +42,27 @@ DSV_DEVICE uint32_t read_bytes2(uint32_t at) {
   return v;
 }
 
+// One, two or four 16-bit numbers, as one load brings them.
+template <int N>
+struct Pack {
+  using type = std::conditional_t<N == 2, unsigned short, std::conditional_t<N == 4, unsigned int, uint2>>;
+  uint32_t v[N == 8 ? 2 : 1];
+  DSV_DEVICE Pack& operator=(const type& a) {
+    if constexpr (N == 8) v[0] = a.x, v[1] = a.y;
+    else v[0] = a;
+    return *this;
+  }
+  DSV_DEVICE uint32_t get(int q) const { return v[q / 2] >> (16 * (q % 2)) & 0xffffu; }
+  DSV_DEVICE void set(int q, uint32_t a) { v[q / 2] |= a << (16 * (q % 2)); }
+};
+
 // ---------------------------------------------------------------- forward
 // A CTA takes 16 RS rows of W; its four warps share the columns in chunks of 128 (warp w: chunks w, w + 4, ..) and add up
 // in the end.  A warp's next chunks are on their way into shared memory (cp.async), from where a lane (g = lane / 4,
 // t = lane % 4) takes four words (32 values) of rows g and g + 8, G / 32 of them next to each other: then the sixteen columns of a
 // product are all of one group, and its fp32 sums are scaled once a group.
 constexpr int kFwdWarps = 4;
-constexpr int kStages = 3;                       // chunks of a warp on their way
+constexpr int kStages = 2;                       // chunks of a warp on their way
 // Bytes between the 64-byte rows of a chunk in shared memory, so that what a load reads at once (16 bytes of two rows, 8 of four or
 // 4 of eight, times t) is in different banks.
 template <int G>
@@ -69,8 +83,17 @@ DSV_DEVICE void read_words(uint32_t at, uint32_t* v) {
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
 }
 
+// A product onto zeros.
+DSV_DEVICE void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 template <int G, int NT, int RS, bool ZERO>
-__global__ void __launch_bounds__(32 * kFwdWarps, NT == 1 ? 4 : NT == 2 ? 3 : 2)
+__global__ void __launch_bounds__(32 * kFwdWarps, NT == 1 ? 5 : NT == 2 ? 4 : 2)
 w4_fwd_kernel(W4Params p) {
   constexpr int GP = 128 / G, WG = G / 32, kPitch = fwd_pitch<G>();   // groups of a chunk, a lane's words of a group
   extern __shared__ __align__(16) unsigned char shared[];   // the weights on their way, then the warps' sums
@@ -88,19 +111,26 @@ w4_fwd_kernel(W4Params p) {
     for (int h = 0; h < 2; ++h) scale_at[i][h] = min(i * 16 + h * 8 + g, last) * row_groups;
   const bf16* const scales = p.scale + f0 * row_groups;
   const uint8_t* const zeros = ZERO ? p.zero + f0 * row_groups : nullptr;
-  bf16 scale[RS][2][GP];
+  const bool whole = D % 128 == 0;               // a chunk's groups of a row are one aligned load
+  Pack<2 * GP> scale[RS][2];
   uint8_t zero[ZERO ? RS : 1][2][GP];
   auto load_scales = [&](int c) {
 #pragma unroll
     for (int i = 0; i < RS; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        if (whole) {
+          scale[i][h] = *reinterpret_cast<const typename Pack<2 * GP>::type*>(scales + (scale_at[i][h] + c * GP));
+        } else {
+          scale[i][h] = Pack<2 * GP>{};
 #pragma unroll
-        for (int q = 0; q < GP; ++q) {
-          const uint32_t at = scale_at[i][h] + min(c * GP + q, row_groups - 1);
-          scale[i][h][q] = scales[at];
-          if (ZERO) zero[i][h][q] = zeros[at];
+          for (int q = 0; q < GP; ++q)
+            scale[i][h].set(q, reinterpret_cast<const uint16_t*>(scales)[scale_at[i][h] + min(c * GP + q, row_groups - 1)]);
         }
+        if (ZERO)
+#pragma unroll
+          for (int q = 0; q < GP; ++q) zero[i][h][q] = zeros[scale_at[i][h] + min(c * GP + q, row_groups - 1)];
+      }
   };
   // Lane l brings part l % 4 of rows l / 4, l / 4 + 8, ..
   const uint32_t ring = smem_u32(shared) + warp * (kStages * RS * 16 * kPitch);
@@ -156,22 +186,22 @@ w4_fwd_kernel(W4Params p) {
         const __nv_bfloat162 z0 = zero_pair(ZERO ? zero[i][0][q] : 8), z1 = zero_pair(ZERO ? zero[i][1][q] : 8);
         float s[NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[n][j] = 0.f;
-#pragma unroll
         for (int k = 0; k < 2 * WG; ++k) {
           const int w = k / 2, e = 2 * (k % 2);   // values e and e + 4, e + 1 and e + 5 of the word
           const uint32_t p0 = w0[w] >> (4 * e), p1 = w1[w] >> (4 * e);
           const uint32_t frag[4] = {unpack_pair<false>(p0, z0), unpack_pair<false>(p1, z1), unpack_pair<true>(p0, z0), unpack_pair<true>(p1, z1)};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_bf16_16816(s[n], frag, b[n][4 * (q * WG + w) + e], b[n][4 * (q * WG + w) + e + 1]);
+          for (int n = 0; n < NT; ++n) {
+            const uint32_t b0 = b[n][4 * (q * WG + w) + e], b1 = b[n][4 * (q * WG + w) + e + 1];
+            if (k) mma_bf16_16816(s[n], frag, b0, b1);
+            else mma_first(s[n], frag, b0, b1);
+          }
         }
         // sums j = 0, 1: row g; 2, 3: row g + 8; of vectors 2 t, 2 t + 1
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][n][j] += __bfloat162float(scale[i][j / 2][q]) * s[n][j];
+          for (int j = 0; j < 4; ++j) acc[i][n][j] += __uint_as_float(scale[i][j / 2].get(q) << 16) * s[n][j];
       }
     }
     if (c + kFwdWarps < chunks) load_scales(c + kFwdWarps);
@@ -252,22 +282,8 @@ DSV_DEVICE uint4 split4(const float (&v)[4]) {
   return make_uint4(hi[0], hi[1], lo[0], lo[1]);
 }
 
-// One, two or four 16-bit numbers, as one load brings them.
-template <int N>
-struct Pack {
-  using type = std::conditional_t<N == 2, unsigned short, std::conditional_t<N == 4, unsigned int, uint2>>;
-  uint32_t v[N == 8 ? 2 : 1];
-  DSV_DEVICE Pack& operator=(const type& a) {
-    if constexpr (N == 8) v[0] = a.x, v[1] = a.y;
-    else v[0] = a;
-    return *this;
-  }
-  DSV_DEVICE uint32_t get(int q) const { return v[q / 2] >> (16 * (q % 2)) & 0xffffu; }
-  DSV_DEVICE void set(int q, uint32_t a) { v[q / 2] |= a << (16 * (q % 2)); }
-};
-
 template <int G, int NT, bool ZERO>
-__global__ void __launch_bounds__(32 * kBwdWarps, NT == 1 ? 3 : NT == 2 ? 2 : 1)
+__global__ void __launch_bounds__(32 * kBwdWarps, NT == 2 && G < 64 ? 2 : 3)
 w4_bwd_kernel(W4Params p, W4BwdPlan plan) {
   constexpr int CG = kBwdCols / G;               // groups of the CTA's columns
   extern __shared__ __align__(16) unsigned char shared[];   // the stages, the other operand, the zero points; then the warps' sums
@@ -408,7 +424,7 @@ w4_bwd_kernel(W4Params p, W4BwdPlan plan) {
     // groups of 64 and 128: the lane's word is columns 8 g ..; of 32: two bytes each of columns 4 g .. and 32 + 4 g ..
     const uint32_t mine = ring + stage * kBwdStage + (rw * (16 * kBwdSteps) + t) * (kBwdCols / 2) + (cw * 32 ^ (t & 2) * 16) + (G < 64 ? 2 : 4) * g;
     stage = stage + 1 < kBwdStages ? stage + 1 : 0;
-#pragma unroll
+#pragma unroll 2                                   // unrolled whole, the registers leave two CTAs on an SM instead of three
     for (int s = 0; s < kBwdSteps; ++s) {
       const int quad = (rw * kBwdSteps + s) * 4 + t;
       uint32_t now[4];
@@ -537,10 +553,11 @@ template <int G, int NT, int RS>
 cudaError_t fwd_rows(const W4Params& p, cudaStream_t stream) {
   return p.zero ? fwd_zero<G, NT, RS, true>(p, stream) : fwd_zero<G, NT, RS, false>(p, stream);
 }
-// Rows of a CTA: 32 share their loads of the vectors, and 16 where that would leave SMs without four CTAs.
+// Rows of a CTA: 32 share their loads of the vectors (12,288 x 2048: 5.4 us against 5.8 with 16, eight vectors 5.6 against 6.8),
+// and 16 where that would leave SMs without two CTAs.
 template <int G, int NT>
 cudaError_t fwd(const W4Params& p, cudaStream_t stream) {
-  return p.F < 32 * 4 * 152 ? fwd_rows<G, NT, 1>(p, stream) : fwd_rows<G, NT, 2>(p, stream);
+  return p.F < 32 * 2 * 152 ? fwd_rows<G, NT, 1>(p, stream) : fwd_rows<G, NT, 2>(p, stream);
 }
 template <int G>
 cudaError_t fwd_group(const W4Params& p, cudaStream_t stream) {
@@ -562,7 +579,7 @@ cudaError_t bwd(const W4Params& p, const W4BwdPlan& plan, cudaStream_t stream) {
 }
 template <int G>
 cudaError_t bwd_group(const W4Params& p, const W4BwdPlan& plan, cudaStream_t stream) {
-  return p.M <= 4 ? bwd<G, 1>(p, plan, stream) : p.M <= 8 ? bwd<G, 2>(p, plan, stream) : bwd<G, 4>(p, plan, stream);
+  return p.M <= 4 ? bwd<G, 1>(p, plan, stream) : bwd<G, 2>(p, plan, stream);   // more than eight vectors: eight at a time
 }
 
 }  // namespace
