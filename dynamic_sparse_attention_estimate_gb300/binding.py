@@ -889,8 +889,8 @@ def dsv_residual_norm_fwd(x: torch.Tensor, z: torch.Tensor, gate: Optional[torch
     return r, y
 
 
-def dsv_residual_norm_bwd_workspace(B: int, N: int, D: int, pre: str = "layer") -> int:
-    return _residual_dims(int(B), int(N), int(D), False, "none", pre, 1.0, 0.0, (int(D),) * 4)[1]
+def dsv_residual_norm_bwd_workspace(B: int, N: int, D: int, pre: str = "layer", dtype: torch.dtype = torch.bfloat16) -> int:
+    return _residual_dims(int(B), int(N), int(D), dtype is torch.float32, "none", pre, 1.0, 0.0, (int(D),) * 4)[1]
 
 
 def dsv_residual_norm_bwd(dr: Optional[torch.Tensor], dy: Optional[torch.Tensor], r: Optional[torch.Tensor], z: torch.Tensor,

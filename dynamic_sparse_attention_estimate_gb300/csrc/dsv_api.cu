@@ -1252,7 +1252,7 @@ dsv_status dsv_residual_norm_fwd(const dsv_residual_dims* dims, const void* x, c
 
 size_t dsv_residual_norm_bwd_workspace(const dsv_residual_dims* dims) {
   if (check_residual(dims) != DSV_OK) return 0;
-  return up(dsv::residual_bwd_workspace(dims->B, dims->N, dims->D, dims->pre));
+  return up(dsv::residual_bwd_workspace(dims->B, dims->N, dims->D, dims->pre, dims->stream_f32 != 0));
 }
 
 // Two outputs of B rows of D floats, `stride` apart: apart, or interleaved.

@@ -88,7 +88,7 @@ struct ResidualParams {
   float *dw_post, *dw_pre;              // [D] or null (backward)
   float* partial;                       // residual_bwd_workspace bytes (backward)
 };
-size_t residual_bwd_workspace(int64_t B, int64_t N, int64_t D, int pre);
+size_t residual_bwd_workspace(int64_t B, int64_t N, int64_t D, int pre, bool f32);
 cudaError_t launch_residual_norm_fwd(const ResidualParams& p, cudaStream_t stream);
 cudaError_t launch_residual_norm_bwd(const ResidualParams& p, cudaStream_t stream);
 

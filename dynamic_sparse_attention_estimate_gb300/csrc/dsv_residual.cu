@@ -90,8 +90,9 @@ struct RowPlan {
   int64_t slabs, rows;                  // slabs of a sample (one CTA each), rows of a slab
 };
 // Two vectors a lane where a row has more than 32: a row's sums, its scalars and its addresses cost a lane about as much as
-// eight features do, so one vector a lane was half the rate (32,768 x 2048 backward, both norms: 268 us).  About `ctas` slabs
-// over all samples, but no more than give each group of a CTA a row.
+// eight features do, so one vector a lane was half the rate (32,768 x 2048 backward, both norms: 268 us).  At most `ctas` slabs
+// over all samples (one more than there are SMs would take as long as two rounds), and no more than give each group of a CTA
+// a row.
 RowPlan row_plan(int64_t B, int64_t N, int64_t D, int64_t ctas, int warps) {
   RowPlan q;
   q.nvec = static_cast<int>(D / 8);
@@ -100,7 +101,7 @@ RowPlan row_plan(int64_t B, int64_t N, int64_t D, int64_t ctas, int warps) {
   q.warps = q.W > warps ? kMaxWarps : warps;
   q.G = q.warps / q.W;
   if (q.G > 15) q.G = 15;               // named barriers 1 .. 15
-  q.slabs = (ctas + B - 1) / B;
+  q.slabs = B < ctas ? ctas / B : 1;
   const int64_t most = (N + q.G - 1) / q.G;
   if (q.slabs > most) q.slabs = most;
   q.rows = (N + q.slabs - 1) / q.slabs;
@@ -224,6 +225,8 @@ struct Ring {
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at(stage, i, part)) : "memory");
     return v;
   }
+  // slot k of the thread's S V P
+  DSV_DEVICE void zero(int k) const { asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};\n" ::"r"(base + k * stride), "r"(0) : "memory"); }
   static __host__ __device__ size_t bytes(int threads) { return static_cast<size_t>(S) * V * P * 16 * threads; }
 };
 
@@ -351,24 +354,24 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
 // with u = alpha gate w_post g:  dz = rz (u - zhat mean(u zhat)) (no norm: dz = u).  A thread keeps the column sums
 // S = sum g zhat,  T = sum dy xhat,  U = sum dy  of its features, from which every vector's gradient follows.  The CTA's
 // sums, its row groups added in order, are one partial row.
+//   A row's passes read it from shared memory again, in bf16 as it came: held in registers in fp32 it would leave room for 12
+// warps instead of 16, and for eight where a row takes all of them (16,384 x 8192: TODO us instead of 766).
 constexpr int64_t kBwdCtas = 152;
-constexpr int kBwdWarps = 12;           // 168 registers a thread; rows of more warps take the kernel of 16 with 128
-int sums_of(int pre) { return pre == kNormNone ? 1 : 3; }
-// The factors alpha gate w_post and w_pre (1 + scale) would take 32 registers of a thread's 168: they stay in shared memory
-// (64 bytes a thread and vector), or, where 512 threads leave no room for that, are made again from the bf16 vectors.
-template <int WARPS>
+constexpr int sums_of(int pre) { return pre == kNormNone ? 1 : 3; }
+// Warps of a CTA: with an fp32 stream 12, whose two stages and factors fill shared memory, and 16 for rows that need more.
+template <bool F32>
+constexpr int bwd_warps() {
+  return F32 ? 12 : kMaxWarps;
+}
+// The factors alpha gate w_post and w_pre (1 + scale) stay in shared memory, 64 bytes a vector of a row; where rows of fp32 take 16
+// warps they are made again from the bf16 vectors.
+template <bool F32, int WARPS>
 constexpr bool kept_factors() {
-  return WARPS <= kBwdWarps;
+  return WARPS <= bwd_warps<F32>();
 }
-template <int V, int WARPS>
-constexpr int factor_bytes() {
-  return kept_factors<WARPS>() ? V * 64 * 32 * WARPS : 0;
-}
-// Stages that fit beside each other and the factors in 216 KB: parts of 16 bytes a thread and vector.
-template <int P, int V, int WARPS>
+template <int P>
 constexpr int bwd_stages() {
-  constexpr int fit = (216 * 1024 - factor_bytes<V, WARPS>()) / (P * V * 16 * 32 * WARPS);
-  return fit > 4 ? 4 : fit;
+  return P <= 3 ? 3 : 2;
 }
 
 template <bool F32, int V, bool POST, int PRE, int WARPS>
@@ -377,14 +380,20 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
   extern __shared__ __align__(16) uint4 ring_mem[];
   __shared__ __align__(16) float red[15 * kRedFloats];
   using St = Stream<F32>;
-  constexpr int SP = St::kParts, P = PRE == kNormNone ? SP + 1 : 2 * SP + 2, S = bwd_stages<P, V, WARPS>();
+  constexpr int SP = St::kParts, P = PRE == kNormNone ? SP + 1 : 2 * SP + 2, S = bwd_stages<P>();
   constexpr int K = PRE == kNormNone ? 1 : 3;
   constexpr int kDr = 0, kZ = SP, kDy = SP + 1, kR = SP + 2;    // parts of a vector
+  // the kernel of the sums may be scheduled once every CTA has started; it waits for this grid before it reads
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const Place<V> at(plan, p.N);
   RowSums sum = row_sums(plan, red, at.group, at.warp, at.lane);
   const Ring<P, V, S> ring(ring_mem);
   const float D = static_cast<float>(p.D), inv_d = 1.f / D;
 
+  // lanes past the row's end, and a dr that is not there, are zeros throughout: they add nothing to a sum
+#pragma unroll
+  for (int k = 0; k < S * V * P; ++k) ring.zero(k);
+  __syncwarp();
   const int64_t first = at.n0 + at.group, step = 16LL * plan.G * plan.nvec;
   int64_t off = ((at.b * p.N + first) * plan.nvec + at.vec[0]) * 16;
   auto issue = [&](int64_t n, int64_t o, int stage) {
@@ -423,77 +432,69 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
     for (int j = 0; j < 4; ++j) f.v[j] = mul2(w.v[j], add2(both(1.f), sc.v[j]));
     return f;
   };
-  constexpr bool kKept = kept_factors<WARPS>();
-  float4* const kept = reinterpret_cast<float4*>(reinterpret_cast<char*>(ring_mem) + Ring<P, V, S>::bytes(blockDim.x)) + threadIdx.x;
-  auto keep = [&](int slot, const Vec8& a) {
-    kept[2 * slot * blockDim.x] = make_float4(a.v[0].x, a.v[0].y, a.v[1].x, a.v[1].y);
-    kept[(2 * slot + 1) * blockDim.x] = make_float4(a.v[2].x, a.v[2].y, a.v[3].x, a.v[3].y);
+  constexpr bool kKept = kept_factors<F32, WARPS>();
+  const int row_vecs = 32 * V * plan.W;          // with those past the end
+  float4* const kept = reinterpret_cast<float4*>(reinterpret_cast<char*>(ring_mem) + Ring<P, V, S>::bytes(blockDim.x));   // [4][row_vecs]
+  auto keep = [&](int slot, int vec, const Vec8& a) {
+    kept[slot * row_vecs + vec] = make_float4(a.v[0].x, a.v[0].y, a.v[1].x, a.v[1].y);
+    kept[(slot + 1) * row_vecs + vec] = make_float4(a.v[2].x, a.v[2].y, a.v[3].x, a.v[3].y);
   };
-  auto kept8 = [&](int slot) {
-    const float4 lo = kept[2 * slot * blockDim.x], hi = kept[(2 * slot + 1) * blockDim.x];
+  auto kept8 = [&](int slot, int vec) {
+    const float4 lo = kept[slot * row_vecs + vec], hi = kept[(slot + 1) * row_vecs + vec];
     return Vec8{{make_float2(lo.x, lo.y), make_float2(lo.z, lo.w), make_float2(hi.x, hi.y), make_float2(hi.z, hi.w)}};
   };
   Vec8 acc[K][V];                       // S, T, U
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    if (kKept) {
-      keep(2 * i, make_c(i));
-      keep(2 * i + 1, make_f(i));
+    if (kKept && at.group == 0) {
+      keep(0, at.vec[i], make_c(i));
+      if (PRE != kNormNone) keep(2, at.vec[i], make_f(i));
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) acc[k][i] = all8(0.f);
   }
+  if (kKept) __syncthreads();
 
   int stage = 0;
-  // Lanes past the row's end hold zeros: they add nothing to a sum, and are not stored.
   for (int64_t n = first; n < at.n1; n += plan.G, off += step) {
     cp_async_wait<S - 2>();
     if (F32) __syncwarp();
-    Vec8 r[V], g[V], z[V], h[V];
-    uint4 dy[V];
+    issue(n + (S - 1) * plan.G, off + (S - 1) * step, stage ? stage - 1 : S - 1);   // where the last row was
+    // the row's features of vector i, and h = dy f
+    auto stream8 = [&](int i, int part) {
+      uint4 a[SP];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      r[i] = g[i] = z[i] = h[i] = all8(0.f);
-      dy[i] = make_uint4(0, 0, 0, 0);
-      if (!at.valid[i]) continue;
-      uint4 part[SP];
-      if constexpr (PRE != kNormNone) {
+      for (int k = 0; k < SP; ++k) a[k] = ring.read(stage, i, part + k);
+      return St::get(a);
+    };
+    auto bf8 = [&](int i, int part) { return unpack8(ring.read(stage, i, part)); };
+    auto h8 = [&](int i, const Vec8& dy) {
+      Vec8 f = kKept ? kept8(2, at.vec[i]) : make_f(i);
 #pragma unroll
-        for (int k = 0; k < SP; ++k) part[k] = ring.read(stage, i, kR + k);
-        r[i] = St::get(part);
-        dy[i] = ring.read(stage, i, kDy);
-        const Vec8 f = kKept ? kept8(2 * i + 1) : make_f(i), d = unpack8(dy[i]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h[i].v[j] = mul2(d.v[j], f.v[j]);
-      }
-      z[i] = unpack8(ring.read(stage, i, kZ));
-      if (p.dr) {
-#pragma unroll
-        for (int k = 0; k < SP; ++k) part[k] = ring.read(stage, i, kDr + k);
-        g[i] = St::get(part);
-      }
-    }
-    if (F32) __syncwarp();
-    issue(n + (S - 1) * plan.G, off + (S - 1) * step, stage ? stage - 1 : S - 1);   // where the last row was read from
-    stage = stage + 1 < S ? stage + 1 : 0;
+      for (int j = 0; j < 4; ++j) f.v[j] = mul2(dy.v[j], f.v[j]);
+      return f;
+    };
 
     float rz = 1.f;
+    float2 k0 = both(0.f), k1 = both(0.f), k2 = both(0.f), minus_mean[V];   // of  g = dr + k2 h + k1 xhat + k0,  xhat = k2 (r - mean)
     if constexpr (POST || PRE != kNormNone) {
       float2 a0 = both(0.f), a1 = both(0.f), a2 = both(0.f);   // sum z^2; layer: sum r, sum h; rms: sum r^2, sum h r
 #pragma unroll
-      for (int i = 0; i < V; ++i)
+      for (int i = 0; i < V; ++i) {
+        if (POST) {
+          const Vec8 z = bf8(i, kZ);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (POST) a0 = fma2(z[i].v[j], z[i].v[j], a0);
-          if (PRE == kNormLayer) {
-            a1 = add2(a1, r[i].v[j]);
-            a2 = add2(a2, h[i].v[j]);
-          }
-          if (PRE == kNormRms) {
-            a1 = fma2(r[i].v[j], r[i].v[j], a1);
-            a2 = fma2(h[i].v[j], r[i].v[j], a2);
+          for (int j = 0; j < 4; ++j) a0 = fma2(z.v[j], z.v[j], a0);
+        }
+        if constexpr (PRE != kNormNone) {
+          const Vec8 r = stream8(i, kR), h = h8(i, bf8(i, kDy));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            a1 = PRE == kNormLayer ? add2(a1, r.v[j]) : fma2(r.v[j], r.v[j], a1);
+            a2 = PRE == kNormLayer ? add2(a2, h.v[j]) : fma2(h.v[j], r.v[j], a2);
           }
         }
+      }
       float s0 = a0.x + a0.y, s1 = a1.x + a1.y, s2 = a2.x + a2.y;
       if constexpr (PRE == kNormNone) {
         float s[1] = {s0};
@@ -514,18 +515,21 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
       if (POST) rz = rsqrtf(s0 * inv_d + p.eps);
       if constexpr (PRE != kNormNone) {
         float mh = 0.f;                 // mean h
+#pragma unroll
+        for (int i = 0; i < V; ++i) minus_mean[i] = both(0.f);
         if constexpr (PRE == kNormLayer) {
           const float mean = mean_of(s1, D, inv_d);
           mh = s2 * inv_d;
           a1 = a2 = both(0.f);          // sum (r - mean)^2, sum h (r - mean)
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            const float2 m = both(at.valid[i] ? -mean : 0.f);
+            minus_mean[i] = both(at.valid[i] ? -mean : 0.f);
+            const Vec8 r = stream8(i, kR), h = h8(i, bf8(i, kDy));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              r[i].v[j] = add2(r[i].v[j], m);
-              a1 = fma2(r[i].v[j], r[i].v[j], a1);
-              a2 = fma2(h[i].v[j], r[i].v[j], a2);
+              const float2 d = add2(r.v[j], minus_mean[i]);
+              a1 = fma2(d, d, a1);
+              a2 = fma2(h.v[j], d, a2);
             }
           }
           float s[2] = {a1.x + a1.y, a2.x + a2.y};
@@ -534,35 +538,34 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
           s2 = s[1];
         }
         const float rstd = rsqrtf(s1 * inv_d + p.eps), mhx = rstd * s2 * inv_d;   // mean(h xhat)
-        const float2 k0 = both(-rstd * mh), k1 = both(-rstd * mhx), k2 = both(rstd);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const Vec8 d = unpack8(dy[i]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 xh = mul2(r[i].v[j], k2);
-            g[i].v[j] = add2(g[i].v[j], fma2(k2, h[i].v[j], fma2(k1, xh, k0)));
-            acc[K - 2][i].v[j] = fma2(d.v[j], xh, acc[K - 2][i].v[j]);
-            acc[K - 1][i].v[j] = add2(acc[K - 1][i].v[j], d.v[j]);
-          }
-        }
+        k0 = both(-rstd * mh);
+        k1 = both(-rstd * mhx);
+        k2 = both(rstd);
       }
     }
-    float2 a = both(0.f);               // sum u z
+    float2 a = both(0.f);               // sum u zhat
     Vec8 u[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (at.valid[i]) St::store(p.dx, (off + 512 * i) * SP, g[i], wide);
-      const Vec8 c = kKept ? kept8(2 * i) : make_c(i);
+      Vec8 g = stream8(i, kDr);
+      if constexpr (PRE != kNormNone) {
+        const Vec8 dy = bf8(i, kDy), h = h8(i, dy), r = stream8(i, kR);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 xh = mul2(PRE == kNormLayer ? add2(r.v[j], minus_mean[i]) : r.v[j], k2);
+          g.v[j] = add2(g.v[j], fma2(k2, h.v[j], fma2(k1, xh, k0)));
+          acc[K - 2][i].v[j] = fma2(dy.v[j], xh, acc[K - 2][i].v[j]);
+          acc[K - 1][i].v[j] = add2(acc[K - 1][i].v[j], dy.v[j]);
+        }
+      }
+      if (at.valid[i]) St::store(p.dx, (off + 512 * i) * SP, g, wide);
+      const Vec8 c = kKept ? kept8(0, at.vec[i]) : make_c(i), z = bf8(i, kZ);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 zh = POST ? mul2(z[i].v[j], both(rz)) : z[i].v[j];
-        acc[0][i].v[j] = fma2(g[i].v[j], zh, acc[0][i].v[j]);
-        u[i].v[j] = mul2(c.v[j], g[i].v[j]);
-        if (POST) {
-          a = fma2(u[i].v[j], zh, a);
-          z[i].v[j] = zh;
-        }
+        const float2 zh = POST ? mul2(z.v[j], both(rz)) : z.v[j];
+        acc[0][i].v[j] = fma2(g.v[j], zh, acc[0][i].v[j]);
+        u[i].v[j] = mul2(c.v[j], g.v[j]);
+        if (POST) a = fma2(u[i].v[j], zh, a);
       }
     }
     float2 mu = both(0.f);              // -mean(u zhat)
@@ -573,11 +576,15 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (POST)
+      if (POST) {
+        const Vec8 z = bf8(i, kZ);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[i].v[j] = mul2(both(rz), fma2(z[i].v[j], mu, u[i].v[j]));
+        for (int j = 0; j < 4; ++j) u[i].v[j] = mul2(both(rz), fma2(mul2(z.v[j], both(rz)), mu, u[i].v[j]));
+      }
       if (at.valid[i]) *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.dz) + off + 512 * i) = pack8(u[i]);
     }
+    if (F32) __syncwarp();              // before another lane brings a part of the row after the next
+    stage = stage + 1 < S ? stage + 1 : 0;
   }
 
   // the row groups' sums, added in the groups' order, where the rows were
@@ -604,36 +611,60 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
   for (int i = threadIdx.x; i < K * p.D; i += blockDim.x) out[i] = cols[i];
 }
 
-// The gradients of the vectors from the slabs' partial rows: a CTA takes 32 features of one sample, a warp every eighth
-// slab; the eight sums are added in order.  With several samples the sums S and T stay behind the partial rows for the
-// weights' gradients, which a last kernel adds over the samples.
-__global__ void __launch_bounds__(256)
-residual_vectors_kernel(ResidualParams p, int64_t slabs, int K, float* per_sample) {
-  __shared__ float red[8][3][32];
+// The gradients of the vectors from the slabs' partial rows: a CTA takes 32 features of one sample, a warp every sixteenth
+// slab, whose loads leave together; the sixteen sums are added in order.  The weights' gradients are sums over the samples too: a
+// few samples are the same CTA's in turn, more have a CTA each and leave their parts behind the partial rows, for a last kernel.
+constexpr int kSumWarps = 16;
+constexpr int64_t kSamplesInTurn = 4;
+template <int K>
+__global__ void __launch_bounds__(32 * kSumWarps)
+residual_vectors_kernel(ResidualParams p, int64_t slabs, float* per_sample) {
+  __shared__ float red[2][kSumWarps][K][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + lane, b = blockIdx.y;
-  float s[3] = {0.f, 0.f, 0.f};
-  if (d < p.D)
-    for (int64_t t = warp; t < slabs; t += 8)
-      for (int k = 0; k < K; ++k) s[k] += p.partial[((b * slabs + t) * K + k) * p.D + d];
-  for (int k = 0; k < K; ++k) red[warp][k][lane] = s[k];
-  __syncthreads();
-  if (warp || d >= p.D) return;
-  for (int k = 0; k < K; ++k) {
-    s[k] = red[0][k][lane];
-    for (int w = 1; w < 8; ++w) s[k] += red[w][k][lane];
+  const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const int64_t first = gridDim.y == p.B ? blockIdx.y : 0, last = gridDim.y == p.B ? first + 1 : p.B;
+  const bool inside = d < p.D;
+  float post = 0.f, pre = 0.f;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the partial rows
+  for (int64_t b = first; b < last; ++b) {
+    float s[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) s[k] = 0.f;
+    const float* const rows = p.partial + b * slabs * K * p.D + d;
+    for (int64_t t0 = warp; t0 < slabs; t0 += 5 * kSumWarps) {
+      float v[5][K];
+#pragma unroll
+      for (int u = 0; u < 5; ++u)
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[u][k] = inside && t0 + u * kSumWarps < slabs ? rows[((t0 + u * kSumWarps) * K + k) * p.D] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 5; ++u)
+#pragma unroll
+        for (int k = 0; k < K; ++k) s[k] += v[u][k];
+    }
+    float(*const to)[K][32] = red[b & 1];   // the last sample's are read by one warp meanwhile
+#pragma unroll
+    for (int k = 0; k < K; ++k) to[warp][k][lane] = s[k];
+    __syncthreads();
+    if (warp || !inside) continue;
+    for (int w = 1; w < kSumWarps; ++w)
+#pragma unroll
+      for (int k = 0; k < K; ++k) s[k] += to[w][k][lane];
+    const float gate = p.gate ? __bfloat162float(p.gate[b * p.gate_stride + d]) : 1.f, wz = p.w_post ? __bfloat162float(p.w_post[d]) : 1.f;
+    if (p.d_gate) p.d_gate[b * p.d_stride + d] = p.alpha * wz * s[0];
+    post += p.alpha * gate * s[0];
+    if constexpr (K > 1) {
+      const float wr = p.w_pre ? __bfloat162float(p.w_pre[d]) : 1.f;
+      const float scale = p.scale ? __bfloat162float(p.scale[b * p.scale_stride + d]) : 0.f;
+      if (p.d_scale) p.d_scale[b * p.d_stride + d] = wr * s[1];
+      if (p.d_shift) p.d_shift[b * p.d_stride + d] = s[2];
+      pre += (1.f + scale) * s[1];
+    }
   }
-  const float wz = p.post == kNormRms && p.w_post ? __bfloat162float(p.w_post[d]) : 1.f;
-  const float wr = p.w_pre ? __bfloat162float(p.w_pre[d]) : 1.f;
-  if (p.d_gate) p.d_gate[b * p.d_stride + d] = p.alpha * wz * s[0];
-  if (p.d_scale) p.d_scale[b * p.d_stride + d] = wr * s[1];
-  if (p.d_shift) p.d_shift[b * p.d_stride + d] = s[2];
-  const float gate = p.gate ? __bfloat162float(p.gate[b * p.gate_stride + d]) : 1.f;
-  const float scale = p.scale ? __bfloat162float(p.scale[b * p.scale_stride + d]) : 0.f;
-  const float post = p.alpha * gate * s[0], pre = (1.f + scale) * s[1];
+  if (warp || !inside) return;
   if (per_sample) {
-    per_sample[(2 * b) * p.D + d] = post;
-    per_sample[(2 * b + 1) * p.D + d] = pre;
+    per_sample[2 * first * p.D + d] = post;
+    per_sample[(2 * first + 1) * p.D + d] = pre;
   } else {
     if (p.dw_post) p.dw_post[d] = post;
     if (p.dw_pre) p.dw_pre[d] = pre;
@@ -644,6 +675,7 @@ residual_weights_kernel(ResidualParams p, const float* per_sample) {
   const int64_t d = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
   if (d >= p.D) return;
   float post = 0.f, pre = 0.f;
+#pragma unroll 8
   for (int64_t b = 0; b < p.B; ++b) {
     post += per_sample[(2 * b) * p.D + d];
     pre += per_sample[(2 * b + 1) * p.D + d];
@@ -667,8 +699,8 @@ template <bool F32, int V, bool POST, int PRE, int WARPS>
 cudaError_t bwd_rows(const ResidualParams& p, const RowPlan& plan, cudaStream_t stream) {
   const int K = sums_of(PRE), threads = 32 * plan.W * plan.G;
   constexpr int SP = Stream<F32>::kParts, P = PRE == kNormNone ? SP + 1 : 2 * SP + 2;
-  const size_t cols = static_cast<size_t>(K) * p.D * sizeof(float), ring = Ring<P, V, bwd_stages<P, V, WARPS>()>::bytes(threads);
-  const size_t factors = kept_factors<WARPS>() ? static_cast<size_t>(V) * 64 * threads : 0;
+  const size_t cols = static_cast<size_t>(K) * p.D * sizeof(float), ring = Ring<P, V, bwd_stages<P>()>::bytes(threads);
+  const size_t factors = kept_factors<F32, WARPS>() ? static_cast<size_t>(V) * 64 * 32 * plan.W : 0;
   const size_t smem = cols > ring + factors ? cols : ring + factors;
   auto kernel = residual_norm_bwd_kernel<F32, V, POST, PRE, WARPS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -679,21 +711,27 @@ cudaError_t bwd_rows(const ResidualParams& p, const RowPlan& plan, cudaStream_t 
 }
 template <bool F32, int V, bool POST, int PRE>
 cudaError_t bwd(const ResidualParams& p, const RowPlan& plan, cudaStream_t stream) {
-  const int K = sums_of(PRE);
-  cudaError_t e;
-  if constexpr (V == 2)
-    e = plan.warps == kBwdWarps ? bwd_rows<F32, V, POST, PRE, kBwdWarps>(p, plan, stream) : bwd_rows<F32, V, POST, PRE, kMaxWarps>(p, plan, stream);
-  else
-    e = bwd_rows<F32, V, POST, PRE, kBwdWarps>(p, plan, stream);
+  cudaError_t e = cudaSuccess;
+  constexpr int kWarps = bwd_warps<F32>();
+  if (V == 1 || plan.warps == kWarps) e = bwd_rows<F32, V, POST, PRE, kWarps>(p, plan, stream);
+  else if constexpr (V == 2) e = bwd_rows<F32, V, POST, PRE, kMaxWarps>(p, plan, stream);
   if (e != cudaSuccess) return e;
   const bool weights = p.dw_post || p.dw_pre;
   if (!p.d_gate && !p.d_scale && !p.d_shift && !weights) return cudaSuccess;
-  float* per_sample = weights && p.B > 1 ? p.partial + p.B * plan.slabs * K * p.D : nullptr;
+  const bool turns = weights && p.B <= kSamplesInTurn;   // a sample costs a turn about 1 us, another kernel 3
+  float* per_sample = weights && !turns ? p.partial + p.B * plan.slabs * sums_of(PRE) * p.D : nullptr;
   {
     ProfScope prof("residual_vectors", stream);
-    const dim3 grid(static_cast<unsigned>((p.D + 31) / 32), static_cast<unsigned>(p.B));
-    residual_vectors_kernel<<<grid, 256, 0, stream>>>(p, plan.slabs, K, per_sample);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>((p.D + 31) / 32), turns ? 1u : static_cast<unsigned>(p.B));
+    cfg.blockDim = dim3(32 * kSumWarps);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, residual_vectors_kernel<sums_of(PRE)>, p, plan.slabs, per_sample)) != cudaSuccess) return e;
   }
   if (!per_sample) return cudaSuccess;
   ProfScope prof("residual_weights", stream);
@@ -715,8 +753,8 @@ cudaError_t bwd(const ResidualParams& p, const RowPlan& plan, cudaStream_t strea
 
 }  // namespace
 
-size_t residual_bwd_workspace(int64_t B, int64_t N, int64_t D, int pre) {
-  const RowPlan q = row_plan(B, N, D, kBwdCtas, kBwdWarps);
+size_t residual_bwd_workspace(int64_t B, int64_t N, int64_t D, int pre, bool f32) {
+  const RowPlan q = row_plan(B, N, D, kBwdCtas, f32 ? bwd_warps<true>() : bwd_warps<false>());
   return static_cast<size_t>(B * q.slabs * sums_of(pre) + 2 * B) * D * sizeof(float);
 }
 
@@ -725,7 +763,7 @@ cudaError_t launch_residual_norm_fwd(const ResidualParams& p, cudaStream_t strea
   return DSV_RESIDUAL_PICK(fwd, plan.V, p, plan, stream);
 }
 cudaError_t launch_residual_norm_bwd(const ResidualParams& p, cudaStream_t stream) {
-  const RowPlan plan = row_plan(p.B, p.N, p.D, kBwdCtas, kBwdWarps);
+  const RowPlan plan = row_plan(p.B, p.N, p.D, kBwdCtas, p.f32 ? bwd_warps<true>() : bwd_warps<false>());
   return DSV_RESIDUAL_PICK(bwd, plan.V, p, plan, stream);
 }
 
