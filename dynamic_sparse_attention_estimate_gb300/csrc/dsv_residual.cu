@@ -587,88 +587,77 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
     stage = stage + 1 < S ? stage + 1 : 0;
   }
 
-  // the row groups' sums, added in the groups' order, where the rows were
+  // the row groups' sums, where the rows were, added in the groups' order
   cp_async_wait<0>();
-  float* cols = reinterpret_cast<float*>(ring_mem);   // [K][D]
-  for (int g = 0; g < plan.G; ++g) {
-    __syncthreads();
-    if (at.group == g)
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (at.valid[i])
-#pragma unroll
-          for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float4* to = reinterpret_cast<float4*>(cols + k * p.D + 8 * at.vec[i]) + h;
-              const float2 lo = acc[k][i].v[2 * h], hi = acc[k][i].v[2 * h + 1];
-              const float4 t = g ? *to : make_float4(0, 0, 0, 0);
-              *to = make_float4(t.x + lo.x, t.y + lo.y, t.z + hi.x, t.w + hi.y);
-            }
-  }
   __syncthreads();
-  float* out = p.partial + static_cast<int64_t>(blockIdx.x) * K * p.D;
-  for (int i = threadIdx.x; i < K * p.D; i += blockDim.x) out[i] = cols[i];
+  float* const cols = reinterpret_cast<float*>(ring_mem);   // [G][K][D]
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (at.valid[i])
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2 lo = acc[k][i].v[2 * h], hi = acc[k][i].v[2 * h + 1];
+          reinterpret_cast<float4*>(cols + (at.group * K + k) * p.D + 8 * at.vec[i])[h] = make_float4(lo.x, lo.y, hi.x, hi.y);
+        }
+  __syncthreads();
+  float4* const out = reinterpret_cast<float4*>(p.partial + static_cast<int64_t>(blockIdx.x) * K * p.D);
+  const int quads = K * static_cast<int>(p.D) / 4;
+  for (int i = threadIdx.x; i < quads; i += blockDim.x) {
+    float4 t = reinterpret_cast<const float4*>(cols)[i];
+    for (int g = 1; g < plan.G; ++g) {
+      const float4 a = reinterpret_cast<const float4*>(cols)[g * quads + i];
+      t = make_float4(t.x + a.x, t.y + a.y, t.z + a.z, t.w + a.w);
+    }
+    out[i] = t;
+  }
 }
 
-// The gradients of the vectors from the slabs' partial rows: a CTA takes 32 features of one sample, a warp every sixteenth
-// slab, whose loads leave together; the sixteen sums are added in order.  The weights' gradients are sums over the samples too: a
-// few samples are the same CTA's in turn, more have a CTA each and leave their parts behind the partial rows, for a last kernel.
+// The gradients of the vectors from the slabs' partial rows: a CTA takes 32 features of one of the sums S, T, U, a warp every
+// sixteenth slab, whose loads leave together; the sixteen sums are added in order.  The weights' gradients are sums over the
+// samples too: a few samples are the same CTA's in turn, more have a CTA each and leave their parts behind the partial rows, for a last
+// kernel.
 constexpr int kSumWarps = 16;
 constexpr int64_t kSamplesInTurn = 4;
-template <int K>
 __global__ void __launch_bounds__(32 * kSumWarps)
 residual_vectors_kernel(ResidualParams p, int64_t slabs, float* per_sample) {
-  __shared__ float red[2][kSumWarps][K][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float red[2][kSumWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = blockIdx.y, K = gridDim.y;
   const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  const int64_t first = gridDim.y == p.B ? blockIdx.y : 0, last = gridDim.y == p.B ? first + 1 : p.B;
+  const int64_t first = gridDim.z == p.B ? blockIdx.z : 0, last = gridDim.z == p.B ? first + 1 : p.B;
   const bool inside = d < p.D;
-  float post = 0.f, pre = 0.f;
+  float weight = 0.f;                   // the gradient of w_post (S) or w_pre (T)
   asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the partial rows
   for (int64_t b = first; b < last; ++b) {
-    float s[K];
+    const float* const rows = p.partial + (b * slabs * K + k) * p.D + d;
+    float s = 0.f;
+    for (int64_t t0 = warp; t0 < slabs; t0 += 10 * kSumWarps) {
+      float v[10];
 #pragma unroll
-    for (int k = 0; k < K; ++k) s[k] = 0.f;
-    const float* const rows = p.partial + b * slabs * K * p.D + d;
-    for (int64_t t0 = warp; t0 < slabs; t0 += 5 * kSumWarps) {
-      float v[5][K];
+      for (int u = 0; u < 10; ++u) v[u] = inside && t0 + u * kSumWarps < slabs ? rows[(t0 + u * kSumWarps) * K * p.D] : 0.f;
 #pragma unroll
-      for (int u = 0; u < 5; ++u)
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[u][k] = inside && t0 + u * kSumWarps < slabs ? rows[((t0 + u * kSumWarps) * K + k) * p.D] : 0.f;
-#pragma unroll
-      for (int u = 0; u < 5; ++u)
-#pragma unroll
-        for (int k = 0; k < K; ++k) s[k] += v[u][k];
+      for (int u = 0; u < 10; ++u) s += v[u];
     }
-    float(*const to)[K][32] = red[b & 1];   // the last sample's are read by one warp meanwhile
-#pragma unroll
-    for (int k = 0; k < K; ++k) to[warp][k][lane] = s[k];
+    red[b & 1][warp][lane] = s;         // the last sample's are read by one warp meanwhile
     __syncthreads();
     if (warp || !inside) continue;
-    for (int w = 1; w < kSumWarps; ++w)
-#pragma unroll
-      for (int k = 0; k < K; ++k) s[k] += to[w][k][lane];
-    const float gate = p.gate ? __bfloat162float(p.gate[b * p.gate_stride + d]) : 1.f, wz = p.w_post ? __bfloat162float(p.w_post[d]) : 1.f;
-    if (p.d_gate) p.d_gate[b * p.d_stride + d] = p.alpha * wz * s[0];
-    post += p.alpha * gate * s[0];
-    if constexpr (K > 1) {
-      const float wr = p.w_pre ? __bfloat162float(p.w_pre[d]) : 1.f;
-      const float scale = p.scale ? __bfloat162float(p.scale[b * p.scale_stride + d]) : 0.f;
-      if (p.d_scale) p.d_scale[b * p.d_stride + d] = wr * s[1];
-      if (p.d_shift) p.d_shift[b * p.d_stride + d] = s[2];
-      pre += (1.f + scale) * s[1];
+    for (int w = 1; w < kSumWarps; ++w) s += red[b & 1][w][lane];
+    if (k == 0) {
+      if (p.d_gate) p.d_gate[b * p.d_stride + d] = p.alpha * s * (p.w_post ? __bfloat162float(p.w_post[d]) : 1.f);
+      weight += p.alpha * s * (p.gate ? __bfloat162float(p.gate[b * p.gate_stride + d]) : 1.f);
+    } else if (k == 1) {
+      if (p.d_scale) p.d_scale[b * p.d_stride + d] = s * (p.w_pre ? __bfloat162float(p.w_pre[d]) : 1.f);
+      weight += s * (1.f + (p.scale ? __bfloat162float(p.scale[b * p.scale_stride + d]) : 0.f));
+    } else if (p.d_shift) {
+      p.d_shift[b * p.d_stride + d] = s;
     }
   }
-  if (warp || !inside) return;
-  if (per_sample) {
-    per_sample[2 * first * p.D + d] = post;
-    per_sample[(2 * first + 1) * p.D + d] = pre;
-  } else {
-    if (p.dw_post) p.dw_post[d] = post;
-    if (p.dw_pre) p.dw_pre[d] = pre;
-  }
+  if (warp || !inside || k > 1) return;
+  float* const to = per_sample ? per_sample + 2 * first * p.D : nullptr;
+  if (per_sample) to[k * p.D + d] = weight;
+  else if (k == 0 && p.dw_post) p.dw_post[d] = weight;
+  else if (k == 1 && p.dw_pre) p.dw_pre[d] = weight;
 }
 __global__ void __launch_bounds__(128)
 residual_weights_kernel(ResidualParams p, const float* per_sample) {
@@ -699,7 +688,7 @@ template <bool F32, int V, bool POST, int PRE, int WARPS>
 cudaError_t bwd_rows(const ResidualParams& p, const RowPlan& plan, cudaStream_t stream) {
   const int K = sums_of(PRE), threads = 32 * plan.W * plan.G;
   constexpr int SP = Stream<F32>::kParts, P = PRE == kNormNone ? SP + 1 : 2 * SP + 2;
-  const size_t cols = static_cast<size_t>(K) * p.D * sizeof(float), ring = Ring<P, V, bwd_stages<P>()>::bytes(threads);
+  const size_t cols = static_cast<size_t>(K) * plan.G * p.D * sizeof(float), ring = Ring<P, V, bwd_stages<P>()>::bytes(threads);
   const size_t factors = kept_factors<F32, WARPS>() ? static_cast<size_t>(V) * 64 * 32 * plan.W : 0;
   const size_t smem = cols > ring + factors ? cols : ring + factors;
   auto kernel = residual_norm_bwd_kernel<F32, V, POST, PRE, WARPS>;
@@ -726,12 +715,12 @@ cudaError_t bwd(const ResidualParams& p, const RowPlan& plan, cudaStream_t strea
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>((p.D + 31) / 32), turns ? 1u : static_cast<unsigned>(p.B));
+    cfg.gridDim = dim3(static_cast<unsigned>((p.D + 31) / 32), sums_of(PRE), turns ? 1u : static_cast<unsigned>(p.B));
     cfg.blockDim = dim3(32 * kSumWarps);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, residual_vectors_kernel<sums_of(PRE)>, p, plan.slabs, per_sample)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, residual_vectors_kernel, p, plan.slabs, per_sample)) != cudaSuccess) return e;
   }
   if (!per_sample) return cudaSuccess;
   ProfScope prof("residual_weights", stream);
