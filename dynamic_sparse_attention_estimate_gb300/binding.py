@@ -831,32 +831,36 @@ _NORMS = {"none": 0, "rms": 1, "layer": 2}
 
 
 @functools.lru_cache(maxsize=256)
-def _residual_dims(B: int, N: int, D: int, f32: bool, post: str, pre: str, alpha: float, eps: float, strides: Tuple):
-    """(dims struct, workspace bytes of the backward)."""
+def _residual_dims(B: int, N: int, D: int, f32: bool, post: str, pre: str, alpha: float, eps: float, *strides: int):
+    """(dims struct, workspace bytes of the backward); strides: of gate, scale, shift and their gradients."""
     if post not in ("none", "rms") or pre not in _NORMS:
         raise ValueError(f"post must be 'none' or 'rms' and pre 'none', 'rms' or 'layer', got {post!r} and {pre!r}")
-    dims = ResidualDims(B, N, D, _NORMS[post], _NORMS[pre], int(f32), alpha, eps, *strides)
+    dims = ResidualDims(B, N, D, _NORMS[post], _NORMS[pre], int(f32), float(alpha), float(eps), *strides)
     return dims, int(load_library().dsv_residual_norm_bwd_workspace(dims))
 
 
-def _need_stream(t: torch.Tensor, name: str):
+def _need_stream(t: torch.Tensor, name: str) -> bool:
+    """Whether the residual stream t is fp32 (else bf16)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in (torch.bfloat16, torch.float32) or t.dim() != 3 or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: need a contiguous CUDA bfloat16 or float32 [B, N, D] tensor, got {t.dtype} "
-                         f"{tuple(t.shape)} contiguous={t.is_contiguous()} device={t.device}")
+    dtype = t.dtype
+    if (dtype is torch.bfloat16 or dtype is torch.float32) and t.dim() == 3 and t.is_contiguous() and t.is_cuda:
+        return dtype is torch.float32
+    raise ValueError(f"{name}: need a contiguous CUDA bfloat16 or float32 [B, N, D] tensor, got {dtype} "
+                     f"{tuple(t.shape)} contiguous={t.is_contiguous()} device={t.device}")
 
 
-def _row_stride(t: Optional[torch.Tensor], name: str, dtype, B: int, D: int, device: int) -> int:
+def _row_stride(t: Optional[torch.Tensor], name: str, dtype, shape: Tuple[int, int], device: int) -> int:
     """The stride between samples of a [B, D] tensor with contiguous features (a part of a projection, say)."""
     if t is None:
-        return D
+        return shape[1]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype or t.shape != (B, D) or t.get_device() != device or (D > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: need a {dtype} [{B}, {D}] tensor with contiguous features on cuda:{device}, got {t.dtype} "
-                         f"{tuple(t.shape)} strides={t.stride()} device={t.device}")
-    return t.stride(0)
+    stride = t.stride()
+    if t.dtype is dtype and t.shape == shape and stride[1] == 1 and t.get_device() == device:
+        return stride[0]
+    raise ValueError(f"{name}: need a {dtype} [B, D] = {list(shape)} tensor with contiguous features on cuda:{device}, got "
+                     f"{t.dtype} {tuple(t.shape)} strides={stride} device={t.device}")
 
 
 def dsv_residual_norm_fwd(x: torch.Tensor, z: torch.Tensor, gate: Optional[torch.Tensor] = None,
@@ -868,29 +872,29 @@ def dsv_residual_norm_fwd(x: torch.Tensor, z: torch.Tensor, gate: Optional[torch
     norm times w_post) and y = norm(r) * w_pre * (1 + scale) + shift in front of the next branch (pre: "layer", "rms", or
     "none": y is None).  x, r [B, N, D] bf16 or fp32; z, y bf16; gate, scale, shift bf16 [B, D] (any stride between samples,
     e.g. parts of one projection [B, 6, D]); w_post, w_pre bf16 [D]; None: 1, 0, 0, 1, 1.  out: (r, y); r may be x itself."""
-    _need_stream(x, "x")
-    B, N, D = x.shape
-    device = x.get_device()
-    _need_on(torch.bfloat16, x.shape, device, (z, "z"))
-    _need_on(torch.bfloat16, x.shape[2:], device, (w_post, "w_post"), (w_pre, "w_pre"))
-    bf = torch.bfloat16
-    strides = (_row_stride(gate, "gate", bf, B, D, device), _row_stride(scale, "scale", bf, B, D, device),
-               _row_stride(shift, "shift", bf, B, D, device), D)
-    dims, _ = _residual_dims(B, N, D, x.dtype is torch.float32, post, pre, float(alpha), float(eps), strides)
+    f32 = _need_stream(x, "x")
+    shape, device, bf = x.shape, x.get_device(), torch.bfloat16
+    B, N, D = shape
+    vec = (B, D)
+    _need_on(bf, shape, device, (z, "z"))
+    if w_post is not None or w_pre is not None:
+        _need_on(bf, (D,), device, (w_post, "w_post"), (w_pre, "w_pre"))
+    dims = _residual_dims(B, N, D, f32, post, pre, alpha, eps, _row_stride(gate, "gate", bf, vec, device),
+                          _row_stride(scale, "scale", bf, vec, device), _row_stride(shift, "shift", bf, vec, device), D)[0]
     if out is None:
         r = torch.empty_like(x)
-        y = None if pre == "none" else torch.empty(x.shape, dtype=bf, device=x.device)
+        y = None if pre == "none" else torch.empty_like(x, dtype=bf) if f32 else torch.empty_like(x)
     else:
         r, y = out
-        _need_on(x.dtype, x.shape, device, (r, "r"))
-        _need_on(bf, x.shape, device, (y, "y"))
+        _need_on(x.dtype, shape, device, (r, "r"))
+        _need_on(bf, shape, device, (y, "y"))
     _call("dsv_residual_norm_fwd", device, dims, x.data_ptr(), _ptr(z), _ptr(gate), _ptr(w_post), _ptr(scale), _ptr(shift),
           _ptr(w_pre), _ptr(r), _ptr(y))
     return r, y
 
 
 def dsv_residual_norm_bwd_workspace(B: int, N: int, D: int, pre: str = "layer", dtype: torch.dtype = torch.bfloat16) -> int:
-    return _residual_dims(int(B), int(N), int(D), dtype is torch.float32, "none", pre, 1.0, 0.0, (int(D),) * 4)[1]
+    return _residual_dims(int(B), int(N), int(D), dtype is torch.float32, "none", pre, 1.0, 0.0, *(int(D),) * 4)[1]
 
 
 def dsv_residual_norm_bwd(dr: Optional[torch.Tensor], dy: Optional[torch.Tensor], r: Optional[torch.Tensor], z: torch.Tensor,
@@ -905,36 +909,38 @@ def dsv_residual_norm_bwd(dr: Optional[torch.Tensor], dy: Optional[torch.Tensor]
     norm behind r) and dw_post, dw_pre [D] (None where the weight is None).  out: (dx, dz), dx may be dr itself;
     d_mod: (d_gate, d_scale, d_shift) to write, e.g. parts of one [B, 6, D] gradient (None: not wanted)."""
     stream = dr if dr is not None else r
-    _need_stream(stream, "r" if dr is None else "dr")
-    shape, device, f32 = stream.shape, stream.get_device(), torch.float32
+    f32 = _need_stream(stream, "r" if dr is None else "dr")
+    shape, device, bf, full = stream.shape, stream.get_device(), torch.bfloat16, torch.float32
     B, N, D = shape
-    bf, vec = torch.bfloat16, (shape[0], shape[2])
-    _need_on(stream.dtype, shape, device, (r, "r"))
+    vec, d_stride, where = (B, D), D, stream.device
+    if r is not stream:
+        _need_on(stream.dtype, shape, device, (r, "r"))
     _need_on(bf, shape, device, (z, "z"), (dy, "dy"))
-    _need_on(bf, shape[2:], device, (w_post, "w_post"), (w_pre, "w_pre"))
+    if w_post is not None or w_pre is not None:
+        _need_on(bf, (D,), device, (w_post, "w_post"), (w_pre, "w_pre"))
     if out is None:
-        dx, dz = torch.empty_like(stream), torch.empty(shape, dtype=bf, device=stream.device)
+        dx = torch.empty_like(stream)
+        dz = torch.empty_like(stream, dtype=bf) if f32 else torch.empty_like(stream)
     else:
         dx, dz = out
         _need_on(stream.dtype, shape, device, (dx, "dx"))
         _need_on(bf, shape, device, (dz, "dz"))
-    d_stride = D
     if d_mod is None:
-        d_gate = None if gate is None else torch.empty(vec, dtype=f32, device=stream.device)
-        d_scale = None if scale is None else torch.empty(vec, dtype=f32, device=stream.device)
-        d_shift = None if pre == "none" else torch.empty(vec, dtype=f32, device=stream.device)
+        d_gate = None if gate is None else torch.empty(vec, dtype=full, device=where)
+        d_scale = None if scale is None else torch.empty(vec, dtype=full, device=where)
+        d_shift = None if pre == "none" else torch.empty(vec, dtype=full, device=where)
     else:
         d_gate, d_scale, d_shift = d_mod
-        found = {_row_stride(t, n, f32, B, D, device) for t, n in ((d_gate, "d_gate"), (d_scale, "d_scale"), (d_shift, "d_shift"))
+        found = {_row_stride(t, n, full, vec, device) for t, n in ((d_gate, "d_gate"), (d_scale, "d_scale"), (d_shift, "d_shift"))
                  if t is not None}
         if len(found) > 1 and B > 1:
             raise ValueError(f"d_mod: d_gate, d_scale and d_shift need one stride between samples, got {sorted(found)}")
         if found:
             d_stride = found.pop()
-    dw_post = None if w_post is None else torch.empty((D,), dtype=f32, device=stream.device)
-    dw_pre = None if w_pre is None else torch.empty((D,), dtype=f32, device=stream.device)
-    strides = (_row_stride(gate, "gate", bf, B, D, device), _row_stride(scale, "scale", bf, B, D, device), D, d_stride)
-    dims, nbytes = _residual_dims(B, N, D, stream.dtype is f32, post, pre, float(alpha), float(eps), strides)
+    dw_post = None if w_post is None else torch.empty((D,), dtype=full, device=where)
+    dw_pre = None if w_pre is None else torch.empty((D,), dtype=full, device=where)
+    dims, nbytes = _residual_dims(B, N, D, f32, post, pre, alpha, eps, _row_stride(gate, "gate", bf, vec, device),
+                                  _row_stride(scale, "scale", bf, vec, device), D, d_stride)
     ws, nbytes, _keep = _workspace(workspace, nbytes, stream)
     _call("dsv_residual_norm_bwd", device, dims, _ptr(dr), _ptr(dy), _ptr(r), _ptr(z), _ptr(gate), _ptr(w_post), _ptr(scale),
           _ptr(w_pre), _ptr(dx), _ptr(dz), _ptr(d_gate), _ptr(dw_post), _ptr(d_scale), _ptr(d_shift), _ptr(dw_pre), ws, nbytes)
@@ -963,16 +969,18 @@ def _w4_dims(M: int, D: int, F: int, group: int, dy_f32: bool):
 
 def _w4_args(w: W4Weight, device: int):
     """(D, F, group) after the checks of the weights."""
-    for t, n in ((w.data, "w.data"), (w.scale, "w.scale")):
+    data, scale, zero = w
+    for t, n in ((data, "w.data"), (scale, "w.scale")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{n} must be a torch.Tensor")
         if t.dim() != 2:
             raise ValueError(f"{n} needs 2 dims, got {tuple(t.shape)}")
-    F, half = w.data.shape
-    groups = w.scale.shape[1]
-    _need_on(torch.uint8, (F, half), device, (w.data, "w.data"))
-    _need_on(torch.bfloat16, (F, groups), device, (w.scale, "w.scale"))
-    _need_on(torch.uint8, (F, groups), device, (w.zero, "w.zero"))
+    F, half = data.shape
+    groups = scale.shape[1]
+    _need_on(torch.uint8, (F, half), device, (data, "w.data"))
+    _need_on(torch.bfloat16, (F, groups), device, (scale, "w.scale"))
+    if zero is not None:
+        _need_on(torch.uint8, (F, groups), device, (zero, "w.zero"))
     if not groups or (2 * half) % groups:
         raise ValueError(f"w: {2 * half} columns do not divide into {groups} groups")
     return 2 * half, F, 2 * half // groups
@@ -1008,7 +1016,8 @@ def dsv_w4_linear_fwd(x: torch.Tensor, w: W4Weight, bias: Optional[torch.Tensor]
     D, F, group = _w4_args(w, device)
     if x.shape[-1] != D:
         raise ValueError(f"x: need {D} features, got {tuple(x.shape)}")
-    _need_on(torch.bfloat16, (F,), device, (bias, "bias"))
+    if bias is not None:
+        _need_on(torch.bfloat16, (F,), device, (bias, "bias"))
     shape = (*x.shape[:-1], F)
     dims, _ = _w4_dims(x.numel() // D if D else 0, D, F, group, False)
     if out is None:

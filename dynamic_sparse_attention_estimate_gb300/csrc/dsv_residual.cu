@@ -65,8 +65,8 @@ struct Stream {
       return unpack8(a[0]);
     }
   }
-  // At a byte offset; `wide`: fp32 features at a 32-byte boundary, stored whole (in two parts they cost the L2 twice the
-  // sectors).
+  // At a byte offset; `wide`: fp32 features at a 32-byte boundary, stored whole (3 x 3,645 x 1160 forward 35 us, in two parts
+  // 37).
   static DSV_DEVICE void store(void* p, int64_t bytes, const Vec8& a, bool wide) {
     char* to = static_cast<char*>(p) + bytes;
     if constexpr (!F32) {
@@ -191,34 +191,20 @@ DSV_DEVICE RowSums row_sums(const RowPlan& plan, float* red, int group, int warp
   return RowSums{plan.W, group, warp, lane, 0, red + group * kRedFloats};
 }
 
-// A row's features on their way: S stages of P 16-byte parts for each vector of a thread in shared memory.  A part of a bf16
-// tensor is a lane's own; of an fp32 one the warp copies 512 bytes at a time, so that lane l brings half l % 2 of
-// vector 16 k + l / 2 (a lane's own two halves in two copies cost the L2 each sector twice): those are read after a
-// __syncwarp.
+// A row's features on their way: S stages of P 16-byte parts for each vector of a thread in shared memory.
 template <int P, int V, int S>
 struct Ring {
   uint32_t base, stride;                // this thread's part 0 of stage 0; bytes between parts
   DSV_DEVICE Ring(void* smem) : base(smem_u32(smem) + 16 * threadIdx.x), stride(16 * blockDim.x) {}
   DSV_DEVICE uint32_t at(int stage, int i, int part) const { return base + ((stage * V + i) * P + part) * stride; }
-  static DSV_DEVICE void copy16(uint32_t to, const void* p, int64_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(static_cast<const char*>(p) + bytes) : "memory");
-  }
-  // the lane's part of a bf16 tensor, at byte `bytes`
-  DSV_DEVICE void copy(int stage, int i, int part, const void* p, int64_t bytes, bool valid) const {
-    if (valid) copy16(at(stage, i, part), p, bytes);
-  }
-  // the lane's eight features of the stream, bf16 offset `bytes`; left: vectors from this lane's to the row's end
-  template <bool F32>
-  DSV_DEVICE void copy_stream(int stage, int i, int part, const void* p, int64_t bytes, int left, int lane) const {
-    if constexpr (!F32) {
-      copy(stage, i, part, p, bytes, left > 0);
-    } else {
+  // N parts of a tensor, from byte `bytes` on
+  template <int N>
+  DSV_DEVICE void copy(int stage, int i, int part, const void* p, int64_t bytes) const {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int ahead = 16 * k + lane / 2 - lane;   // from this lane to the vector that it brings a half of
-        if (ahead < left) copy16(at(stage, i, part + lane % 2) + 16 * ahead, p, 2 * bytes + 32 * ahead + 16 * (lane % 2));
-      }
-    }
+    for (int k = 0; k < N; ++k)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(at(stage, i, part + k)),
+                   "l"(static_cast<const char*>(p) + bytes + 16 * k)
+                   : "memory");
   }
   DSV_DEVICE uint4 read(int stage, int i, int part) const {
     uint4 v;
@@ -252,10 +238,11 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
   auto issue = [&](int64_t n, int64_t o, int stage) {
     if (n < at.n1) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        ring.template copy_stream<F32>(stage, i, 0, p.x, o + 512 * i, plan.nvec - at.vec[i], at.lane);
-        ring.copy(stage, i, SP, p.z, o + 512 * i, at.valid[i]);
-      }
+      for (int i = 0; i < V; ++i)
+        if (at.valid[i]) {
+          ring.template copy<SP>(stage, i, 0, p.x, (o + 512 * i) * SP);
+          ring.template copy<1>(stage, i, SP, p.z, o + 512 * i);
+        }
     }
     cp_async_commit();                  // one group a row, so that the wait below counts rows
   };
@@ -282,7 +269,6 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
   int stage = 0;
   for (int64_t n = first; n < at.n1; n += plan.G, off += step) {
     cp_async_wait<S - 2>();
-    if (F32) __syncwarp();
     Vec8 r[V], z[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -294,7 +280,6 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
       r[i] = St::get(x);
       z[i] = unpack8(ring.read(stage, i, SP));
     }
-    if (F32) __syncwarp();
     issue(n + (S - 1) * plan.G, off + (S - 1) * step, stage ? stage - 1 : S - 1);   // where the last row was read from
     stage = stage + 1 < S ? stage + 1 : 0;
 
@@ -393,20 +378,19 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
   // lanes past the row's end, and a dr that is not there, are zeros throughout: they add nothing to a sum
 #pragma unroll
   for (int k = 0; k < S * V * P; ++k) ring.zero(k);
-  __syncwarp();
   const int64_t first = at.n0 + at.group, step = 16LL * plan.G * plan.nvec;
   int64_t off = ((at.b * p.N + first) * plan.nvec + at.vec[0]) * 16;
   auto issue = [&](int64_t n, int64_t o, int stage) {
     if (n < at.n1) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int left = plan.nvec - at.vec[i];
+        if (!at.valid[i]) continue;
         if constexpr (PRE != kNormNone) {
-          ring.template copy_stream<F32>(stage, i, kR, p.r, o + 512 * i, left, at.lane);
-          ring.copy(stage, i, kDy, p.dy, o + 512 * i, left > 0);
+          ring.template copy<SP>(stage, i, kR, p.r, (o + 512 * i) * SP);
+          ring.template copy<1>(stage, i, kDy, p.dy, o + 512 * i);
         }
-        ring.copy(stage, i, kZ, p.z, o + 512 * i, left > 0);
-        if (p.dr) ring.template copy_stream<F32>(stage, i, kDr, p.dr, o + 512 * i, left, at.lane);
+        ring.template copy<1>(stage, i, kZ, p.z, o + 512 * i);
+        if (p.dr) ring.template copy<SP>(stage, i, kDr, p.dr, (o + 512 * i) * SP);
       }
     }
     cp_async_commit();
@@ -458,7 +442,6 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
   int stage = 0;
   for (int64_t n = first; n < at.n1; n += plan.G, off += step) {
     cp_async_wait<S - 2>();
-    if (F32) __syncwarp();
     issue(n + (S - 1) * plan.G, off + (S - 1) * step, stage ? stage - 1 : S - 1);   // where the last row was
     // the row's features of vector i, and h = dy f
     auto stream8 = [&](int i, int part) {
@@ -583,7 +566,6 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
       }
       if (at.valid[i]) *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.dz) + off + 512 * i) = pack8(u[i]);
     }
-    if (F32) __syncwarp();              // before another lane brings a part of the row after the next
     stage = stage + 1 < S ? stage + 1 : 0;
   }
 

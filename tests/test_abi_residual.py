@@ -134,4 +134,4 @@ def test_python_refuses(lib):
     with pytest.raises(TypeError, match="dr|r must"):
         pkg.dsv_residual_norm_bwd(None, x, None, x)
     with pytest.raises(ValueError, match="post must"):
-        pkg.binding._residual_dims(1, 4, 8, False, "layer", "layer", 1.0, 0.0, (8, 8, 8, 8))
+        pkg.binding._residual_dims(1, 4, 8, False, "layer", "layer", 1.0, 0.0, 8, 8, 8, 8)
