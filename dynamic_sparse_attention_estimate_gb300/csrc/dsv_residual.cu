@@ -87,7 +87,7 @@ constexpr int kMaxWarps = 16;           // of a row and of a CTA
 struct RowPlan {
   int nvec, V, W, G;                    // vectors of eight features, V to a lane, W warps to a row, G rows at a time
   int warps;                            // that a CTA may have: its kernel's registers allow no more
-  int64_t slabs, rows;                  // slabs of a sample (one CTA each), rows of a slab
+  int64_t ctas;                         // of a sample: CTA c takes rows c G, .., c G + G - 1 of every ctas G
 };
 // Two vectors a lane where a row has more than 32: a row's sums, its scalars and its addresses cost a lane about as much as
 // eight features do, so one vector a lane was half the rate (32,768 x 2048 backward, both norms: 268 us).  At most `ctas` slabs
@@ -101,11 +101,9 @@ RowPlan row_plan(int64_t B, int64_t N, int64_t D, int64_t ctas, int warps) {
   q.warps = q.W > warps ? kMaxWarps : warps;
   q.G = q.warps / q.W;
   if (q.G > 15) q.G = 15;               // named barriers 1 .. 15
-  q.slabs = B < ctas ? ctas / B : 1;
+  q.ctas = B < ctas ? ctas / B : 1;
   const int64_t most = (N + q.G - 1) / q.G;
-  if (q.slabs > most) q.slabs = most;
-  q.rows = (N + q.slabs - 1) / q.slabs;
-  q.slabs = (N + q.rows - 1) / q.rows;
+  if (q.ctas > most) q.ctas = most;
   return q;
 }
 
@@ -114,15 +112,16 @@ template <int V>
 struct Place {
   int group, warp, lane, vec[V];
   bool valid[V];
-  int64_t b, n0, n1;
+  int64_t b, first, step, end;          // sample; rows: first, first + step, .. below end
   DSV_DEVICE Place(const RowPlan& plan, int64_t N) {
     const int w = threadIdx.x >> 5;
     group = w / plan.W;
     warp = w % plan.W;
     lane = threadIdx.x & 31;
-    b = blockIdx.x / plan.slabs;
-    n0 = blockIdx.x % plan.slabs * plan.rows;
-    n1 = n0 + plan.rows < N ? n0 + plan.rows : N;
+    b = blockIdx.x / plan.ctas;
+    first = blockIdx.x % plan.ctas * plan.G + group;
+    step = plan.ctas * plan.G;
+    end = N;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       vec[i] = (warp * V + i) * 32 + lane;
@@ -233,10 +232,10 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
   const float D = static_cast<float>(p.D), inv_d = 1.f / D;
 
   // byte offset of this thread's first vector in a bf16 tensor; a vector further is 512 bytes on
-  const int64_t first = at.n0 + at.group, step = 16LL * plan.G * plan.nvec;
-  int64_t off = ((at.b * p.N + first) * plan.nvec + at.vec[0]) * 16;
+  const int64_t step = 16 * at.step * plan.nvec;
+  int64_t off = ((at.b * p.N + at.first) * plan.nvec + at.vec[0]) * 16;
   auto issue = [&](int64_t n, int64_t o, int stage) {
-    if (n < at.n1) {
+    if (n < at.end) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (at.valid[i]) {
@@ -247,7 +246,7 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
     cp_async_commit();                  // one group a row, so that the wait below counts rows
   };
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) issue(first + s * plan.G, off + s * step, s);
+  for (int s = 0; s < S - 1; ++s) issue(at.first + s * at.step, off + s * step, s);
 
   Vec8 c[V], f[V], sh[V];               // alpha gate w_post, w_pre (1 + scale), shift
 #pragma unroll
@@ -267,7 +266,7 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
   }
 
   int stage = 0;
-  for (int64_t n = first; n < at.n1; n += plan.G, off += step) {
+  for (int64_t n = at.first; n < at.end; n += at.step, off += step) {
     cp_async_wait<S - 2>();
     Vec8 r[V], z[V];
 #pragma unroll
@@ -280,7 +279,7 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
       r[i] = St::get(x);
       z[i] = unpack8(ring.read(stage, i, SP));
     }
-    issue(n + (S - 1) * plan.G, off + (S - 1) * step, stage ? stage - 1 : S - 1);   // where the last row was read from
+    issue(n + (S - 1) * at.step, off + (S - 1) * step, stage ? stage - 1 : S - 1);   // where the last row was read from
     stage = stage + 1 < S ? stage + 1 : 0;
 
     float rz = 1.f;
@@ -378,10 +377,10 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
   // lanes past the row's end, and a dr that is not there, are zeros throughout: they add nothing to a sum
 #pragma unroll
   for (int k = 0; k < S * V * P; ++k) ring.zero(k);
-  const int64_t first = at.n0 + at.group, step = 16LL * plan.G * plan.nvec;
-  int64_t off = ((at.b * p.N + first) * plan.nvec + at.vec[0]) * 16;
+  const int64_t step = 16 * at.step * plan.nvec;
+  int64_t off = ((at.b * p.N + at.first) * plan.nvec + at.vec[0]) * 16;
   auto issue = [&](int64_t n, int64_t o, int stage) {
-    if (n < at.n1) {
+    if (n < at.end) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         if (!at.valid[i]) continue;
@@ -396,7 +395,7 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
     cp_async_commit();
   };
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) issue(first + s * plan.G, off + s * step, s);
+  for (int s = 0; s < S - 1; ++s) issue(at.first + s * at.step, off + s * step, s);
 
   // the two factors of vector i
   auto make_c = [&](int i) {
@@ -440,9 +439,9 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
   if (kKept) __syncthreads();
 
   int stage = 0;
-  for (int64_t n = first; n < at.n1; n += plan.G, off += step) {
+  for (int64_t n = at.first; n < at.end; n += at.step, off += step) {
     cp_async_wait<S - 2>();
-    issue(n + (S - 1) * plan.G, off + (S - 1) * step, stage ? stage - 1 : S - 1);   // where the last row was
+    issue(n + (S - 1) * at.step, off + (S - 1) * step, stage ? stage - 1 : S - 1);   // where the last row was
     // the row's features of vector i, and h = dy f
     auto stream8 = [&](int i, int part) {
       uint4 a[SP];
@@ -663,7 +662,7 @@ cudaError_t fwd(const ResidualParams& p, const RowPlan& plan, cudaStream_t strea
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   ProfScope prof("residual_norm_fwd", stream);
-  kernel<<<static_cast<unsigned>(p.B * plan.slabs), threads, smem, stream>>>(p, plan, reinterpret_cast<uintptr_t>(p.r) % 32 == 0);
+  kernel<<<static_cast<unsigned>(p.B * plan.ctas), threads, smem, stream>>>(p, plan, reinterpret_cast<uintptr_t>(p.r) % 32 == 0);
   return cudaGetLastError();
 }
 template <bool F32, int V, bool POST, int PRE, int WARPS>
@@ -677,7 +676,7 @@ cudaError_t bwd_rows(const ResidualParams& p, const RowPlan& plan, cudaStream_t 
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   ProfScope prof("residual_norm_bwd", stream);
-  kernel<<<static_cast<unsigned>(p.B * plan.slabs), threads, smem, stream>>>(p, plan, reinterpret_cast<uintptr_t>(p.dx) % 32 == 0);
+  kernel<<<static_cast<unsigned>(p.B * plan.ctas), threads, smem, stream>>>(p, plan, reinterpret_cast<uintptr_t>(p.dx) % 32 == 0);
   return cudaGetLastError();
 }
 template <bool F32, int V, bool POST, int PRE>
@@ -690,7 +689,7 @@ cudaError_t bwd(const ResidualParams& p, const RowPlan& plan, cudaStream_t strea
   const bool weights = p.dw_post || p.dw_pre;
   if (!p.d_gate && !p.d_scale && !p.d_shift && !weights) return cudaSuccess;
   const bool turns = weights && p.B <= kSamplesInTurn;   // a sample costs a turn about 1 us, another kernel 3
-  float* per_sample = weights && !turns ? p.partial + p.B * plan.slabs * sums_of(PRE) * p.D : nullptr;
+  float* per_sample = weights && !turns ? p.partial + p.B * plan.ctas * sums_of(PRE) * p.D : nullptr;
   {
     ProfScope prof("residual_vectors", stream);
     cudaLaunchAttribute attr[1];
@@ -702,7 +701,7 @@ cudaError_t bwd(const ResidualParams& p, const RowPlan& plan, cudaStream_t strea
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, residual_vectors_kernel, p, plan.slabs, per_sample)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, residual_vectors_kernel, p, plan.ctas, per_sample)) != cudaSuccess) return e;
   }
   if (!per_sample) return cudaSuccess;
   ProfScope prof("residual_weights", stream);
@@ -726,7 +725,7 @@ cudaError_t bwd(const ResidualParams& p, const RowPlan& plan, cudaStream_t strea
 
 size_t residual_bwd_workspace(int64_t B, int64_t N, int64_t D, int pre, bool f32) {
   const RowPlan q = row_plan(B, N, D, kBwdCtas, f32 ? bwd_warps<true>() : bwd_warps<false>());
-  return static_cast<size_t>(B * q.slabs * sums_of(pre) + 2 * B) * D * sizeof(float);
+  return static_cast<size_t>(B * q.ctas * sums_of(pre) + 2 * B) * D * sizeof(float);
 }
 
 cudaError_t launch_residual_norm_fwd(const ResidualParams& p, cudaStream_t stream) {
