@@ -48,11 +48,6 @@ DSV_DEVICE uint4 pack8(const Vec8& a) {
   return make_uint4(pack_bf16x2(a.v[0].x, a.v[0].y), pack_bf16x2(a.v[1].x, a.v[1].y), pack_bf16x2(a.v[2].x, a.v[2].y),
                     pack_bf16x2(a.v[3].x, a.v[3].y));
 }
-// Eight entries of a bf16 vector, or of one that is not there.
-DSV_DEVICE Vec8 vector8(const bf16* p, int vec, float absent) {
-  return p ? unpack8(__ldg(reinterpret_cast<const uint4*>(p) + vec)) : all8(absent);
-}
-
 // Eight features of the residual stream, bf16 or fp32, in 16-byte parts.
 template <bool F32>
 struct Stream {
@@ -63,21 +58,6 @@ struct Stream {
                    make_float2(__uint_as_float(a[1].x), __uint_as_float(a[1].y)), make_float2(__uint_as_float(a[1].z), __uint_as_float(a[1].w))}};
     } else {
       return unpack8(a[0]);
-    }
-  }
-  // At a byte offset; `wide`: fp32 features at a 32-byte boundary, stored whole (3 x 3,645 x 1160 forward 35 us, in two parts
-  // 37).
-  static DSV_DEVICE void store(void* p, int64_t bytes, const Vec8& a, bool wide) {
-    char* to = static_cast<char*>(p) + bytes;
-    if constexpr (!F32) {
-      *reinterpret_cast<uint4*>(to) = pack8(a);
-    } else if (wide) {
-      asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(to), "f"(a.v[0].x), "f"(a.v[0].y), "f"(a.v[1].x),
-                   "f"(a.v[1].y), "f"(a.v[2].x), "f"(a.v[2].y), "f"(a.v[3].x), "f"(a.v[3].y)
-                   : "memory");
-    } else {
-      reinterpret_cast<float4*>(to)[0] = make_float4(a.v[0].x, a.v[0].y, a.v[1].x, a.v[1].y);
-      reinterpret_cast<float4*>(to)[1] = make_float4(a.v[2].x, a.v[2].y, a.v[3].x, a.v[3].y);
     }
   }
 };
@@ -107,25 +87,71 @@ RowPlan row_plan(int64_t B, int64_t N, int64_t D, int64_t ctas, int warps) {
   return q;
 }
 
-// This thread's place: its row group, its warp and lane in it, its vectors, its CTA's rows.
-template <int V>
+// This thread's place: its row group, its warp and lane in it, its CTA's rows, and its features.  A vector of a warp is 256 features.
+// Of a bf16 stream a lane has eight neighbours of them (16 bytes); of an fp32 one four and, 128 further, four (16 bytes each), so
+// that a warp copies and stores 512 bytes in a row there too (with eight neighbours to a lane, whose halves two instructions
+// bring, 80,000 x 1536 took 235 us forward instead of 190).
+template <bool F32, int V>
 struct Place {
-  int group, warp, lane, vec[V];
-  bool valid[V];
+  int group, warp, lane;
+  int own, span;                        // this lane's first feature, that of the warp's features that it copies of a bf16 tensor
+  bool copies[V], valid[V][2];          // whether these are in the row: vector i's copy, and half h of what the lane works on
   int64_t b, first, step, end;          // sample; rows: first, first + step, .. below end
   DSV_DEVICE Place(const RowPlan& plan, int64_t N) {
     const int w = threadIdx.x >> 5;
     group = w / plan.W;
     warp = w % plan.W;
     lane = threadIdx.x & 31;
+    own = warp * V * 256 + (F32 ? 4 : 8) * lane;
+    span = F32 ? 4 * lane : 0;
     b = blockIdx.x / plan.ctas;
     first = blockIdx.x % plan.ctas * plan.G + group;
     step = plan.ctas * plan.G;
     end = N;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      vec[i] = (warp * V + i) * 32 + lane;
-      valid[i] = vec[i] < plan.nvec;
+      copies[i] = own + span + 256 * i < 8 * plan.nvec;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) valid[i][h] = F32 ? col(i, h) < 8 * plan.nvec : copies[i];
+    }
+  }
+  static constexpr int kHalf = F32 ? 128 : 4;   // features from its first half to its second
+  DSV_DEVICE int col(int i, int h) const { return own + 256 * i + kHalf * h; }
+  DSV_DEVICE int slot(int i) const { return (warp * V + i) * 32 + lane; }
+  // those entries of a bf16 vector (zeros past its end), or of one that is not there
+  DSV_DEVICE Vec8 vector(const bf16* p, int i, float absent) const {
+    Vec8 o = all8(0.f);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (!valid[i][h]) continue;
+      o.v[2 * h] = o.v[2 * h + 1] = both(absent);
+      if (p) {
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(p + col(i, h)));
+        o.v[2 * h] = make_float2(bf16_lo(a.x), bf16_hi(a.x));
+        o.v[2 * h + 1] = make_float2(bf16_lo(a.y), bf16_hi(a.y));
+      }
+    }
+    return o;
+  }
+  // stores them to a bf16 tensor, or to the stream; `at`: the element of this lane's first feature in the row
+  DSV_DEVICE void store(bf16* p, int64_t at, int i, const Vec8& a) const {
+    const uint4 v = pack8(a);
+    bf16* const to = p + at + 256 * i;
+    if constexpr (!F32) {
+      if (copies[i]) *reinterpret_cast<uint4*>(to) = v;
+    } else {
+      if (valid[i][0]) *reinterpret_cast<uint2*>(to) = make_uint2(v.x, v.y);
+      if (valid[i][1]) *reinterpret_cast<uint2*>(to + kHalf) = make_uint2(v.z, v.w);
+    }
+  }
+  DSV_DEVICE void store_stream(void* p, int64_t at, int i, const Vec8& a) const {
+    if constexpr (!F32) {
+      store(static_cast<bf16*>(p), at, i, a);
+    } else {
+      float* const to = static_cast<float*>(p) + at + 256 * i;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (valid[i][h]) *reinterpret_cast<float4*>(to + kHalf * h) = make_float4(a.v[2 * h].x, a.v[2 * h].y, a.v[2 * h + 1].x, a.v[2 * h + 1].y);
     }
   }
 };
@@ -190,28 +216,57 @@ DSV_DEVICE RowSums row_sums(const RowPlan& plan, float* red, int group, int warp
   return RowSums{plan.W, group, warp, lane, 0, red + group * kRedFloats};
 }
 
-// A row's features on their way: S stages of P 16-byte parts for each vector of a thread in shared memory.
-template <int P, int V, int S>
+// A row's features on their way: S stages of P 16-byte parts for each vector of a thread in shared memory.  Parts of the stream
+// and, with a bf16 stream, all parts are read by the thread that copied them.  With an fp32 stream a bf16 tensor's are read by the
+// lanes that work on them, behind a __syncwarp.
+template <bool F32, int P, int V, int S>
 struct Ring {
   uint32_t base, stride;                // this thread's part 0 of stage 0; bytes between parts
-  DSV_DEVICE Ring(void* smem) : base(smem_u32(smem) + 16 * threadIdx.x), stride(16 * blockDim.x) {}
-  DSV_DEVICE uint32_t at(int stage, int i, int part) const { return base + ((stage * V + i) * P + part) * stride; }
-  // N parts of a tensor, from byte `bytes` on
-  template <int N>
-  DSV_DEVICE void copy(int stage, int i, int part, const void* p, int64_t bytes) const {
+  DSV_DEVICE Ring(void* smem) : base(smem_u32(smem) + 16 * threadIdx.x), stride(16 * blockDim.x) {
+    // lanes past the row's end, and a tensor that is not there, are zeros throughout: they add nothing to a sum
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(at(stage, i, part + k)),
-                   "l"(static_cast<const char*>(p) + bytes + 16 * k)
-                   : "memory");
+    for (int k = 0; k < S * V * P; ++k) asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};\n" ::"r"(base + k * stride), "r"(0) : "memory");
+    __syncwarp();
   }
-  DSV_DEVICE uint4 read(int stage, int i, int part) const {
+  DSV_DEVICE uint32_t at(int stage, int i, int part) const { return base + ((stage * V + i) * P + part) * stride; }
+  static DSV_DEVICE void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(from) : "memory");
+  }
+  // of a bf16 tensor, of the stream; `at`: the element of this lane's first feature in the row
+  DSV_DEVICE void copy(const Place<F32, V>& me, int stage, int i, int part, const bf16* p, int64_t from) const {
+    if (me.copies[i]) copy16(at(stage, i, part), p + from + me.span + 256 * i);
+  }
+  DSV_DEVICE void copy_stream(const Place<F32, V>& me, int stage, int i, int part, const void* p, int64_t from) const {
+    if constexpr (!F32) {
+      copy(me, stage, i, part, static_cast<const bf16*>(p), from);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (me.valid[i][h]) copy16(at(stage, i, part + h), static_cast<const float*>(p) + from + 256 * i + me.kHalf * h);
+    }
+  }
+  static DSV_DEVICE uint4 read(uint32_t a) {
     uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at(stage, i, part)) : "memory");
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
   }
-  // slot k of the thread's S V P
-  DSV_DEVICE void zero(int k) const { asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};\n" ::"r"(base + k * stride), "r"(0) : "memory"); }
+  DSV_DEVICE Vec8 bf8(const Place<F32, V>& me, int stage, int i, int part) const {
+    if constexpr (!F32) {
+      return unpack8(read(at(stage, i, part)));
+    } else {
+      uint4 v;
+      const uint32_t a = at(stage, i, part) - 8 * me.lane;   // the warp's 512 bytes: from 8 l and 256 + 8 l on
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(v.z), "=r"(v.w) : "r"(a + 256) : "memory");
+      return unpack8(v);
+    }
+  }
+  DSV_DEVICE Vec8 stream8(int stage, int i, int part) const {
+    uint4 v[Stream<F32>::kParts];
+#pragma unroll
+    for (int k = 0; k < Stream<F32>::kParts; ++k) v[k] = read(at(stage, i, part + k));
+    return Stream<F32>::get(v);
+  }
   static __host__ __device__ size_t bytes(int threads) { return static_cast<size_t>(S) * V * P * 16 * threads; }
 };
 
@@ -221,43 +276,37 @@ constexpr int64_t kFwdCtas = 152;
 
 template <bool F32, int V, bool POST, int PRE>
 __global__ void __launch_bounds__(32 * kMaxWarps, 1)
-residual_norm_fwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
+residual_norm_fwd_kernel(ResidualParams p, RowPlan plan) {
   extern __shared__ __align__(16) uint4 ring_mem[];
   __shared__ __align__(16) float red[15 * kRedFloats];
-  using St = Stream<F32>;
-  constexpr int SP = St::kParts, P = SP + 1, S = kFwdStages;
-  const Place<V> at(plan, p.N);
-  RowSums sum = row_sums(plan, red, at.group, at.warp, at.lane);
-  const Ring<P, V, S> ring(ring_mem);
+  constexpr int SP = Stream<F32>::kParts, P = SP + 1, S = kFwdStages;
+  const Place<F32, V> me(plan, p.N);
+  RowSums sum = row_sums(plan, red, me.group, me.warp, me.lane);
+  const Ring<F32, P, V, S> ring(ring_mem);
   const float D = static_cast<float>(p.D), inv_d = 1.f / D;
 
-  // byte offset of this thread's first vector in a bf16 tensor; a vector further is 512 bytes on
-  const int64_t step = 16 * at.step * plan.nvec;
-  int64_t off = ((at.b * p.N + at.first) * plan.nvec + at.vec[0]) * 16;
-  auto issue = [&](int64_t n, int64_t o, int stage) {
-    if (n < at.end) {
+  const int64_t step = me.step * p.D;   // elements between this thread's rows
+  int64_t row = (me.b * p.N + me.first) * p.D + me.own;
+  auto issue = [&](int64_t n, int64_t at, int stage) {
+    if (n < me.end) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (at.valid[i]) {
-          ring.template copy<SP>(stage, i, 0, p.x, (o + 512 * i) * SP);
-          ring.template copy<1>(stage, i, SP, p.z, o + 512 * i);
-        }
+      for (int i = 0; i < V; ++i) {
+        ring.copy_stream(me, stage, i, 0, p.x, at);
+        ring.copy(me, stage, i, SP, p.z, at);
+      }
     }
     cp_async_commit();                  // one group a row, so that the wait below counts rows
   };
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) issue(at.first + s * at.step, off + s * step, s);
+  for (int s = 0; s < S - 1; ++s) issue(me.first + s * me.step, row + s * step, s);
 
   Vec8 c[V], f[V], sh[V];               // alpha gate w_post, w_pre (1 + scale), shift
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    c[i] = f[i] = sh[i] = all8(0.f);
-    if (!at.valid[i]) continue;
-    const int vec = at.vec[i];
-    const Vec8 g = vector8(p.gate ? p.gate + at.b * p.gate_stride : nullptr, vec, 1.f);
-    const Vec8 wz = vector8(POST ? p.w_post : nullptr, vec, 1.f), wr = vector8(p.w_pre, vec, 1.f);
-    const Vec8 sc = vector8(p.scale ? p.scale + at.b * p.scale_stride : nullptr, vec, 0.f);
-    sh[i] = vector8(p.shift ? p.shift + at.b * p.shift_stride : nullptr, vec, 0.f);
+    const Vec8 g = me.vector(p.gate ? p.gate + me.b * p.gate_stride : nullptr, i, 1.f);
+    const Vec8 wz = me.vector(POST ? p.w_post : nullptr, i, 1.f), wr = me.vector(p.w_pre, i, 1.f);
+    const Vec8 sc = me.vector(p.scale ? p.scale + me.b * p.scale_stride : nullptr, i, 0.f);
+    sh[i] = me.vector(p.shift ? p.shift + me.b * p.shift_stride : nullptr, i, 0.f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       c[i].v[j] = mul2(mul2(both(p.alpha), g.v[j]), wz.v[j]);
@@ -266,20 +315,17 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
   }
 
   int stage = 0;
-  for (int64_t n = at.first; n < at.end; n += at.step, off += step) {
+  for (int64_t n = me.first; n < me.end; n += me.step, row += step) {
     cp_async_wait<S - 2>();
+    if (F32) __syncwarp();
     Vec8 r[V], z[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      r[i] = z[i] = all8(0.f);
-      if (!at.valid[i]) continue;
-      uint4 x[SP];
-#pragma unroll
-      for (int k = 0; k < SP; ++k) x[k] = ring.read(stage, i, k);
-      r[i] = St::get(x);
-      z[i] = unpack8(ring.read(stage, i, SP));
+      r[i] = ring.stream8(stage, i, 0);
+      z[i] = ring.bf8(me, stage, i, SP);
     }
-    issue(n + (S - 1) * at.step, off + (S - 1) * step, stage ? stage - 1 : S - 1);   // where the last row was read from
+    if (F32) __syncwarp();
+    issue(n + (S - 1) * me.step, row + (S - 1) * step, stage ? stage - 1 : S - 1);   // where the last row was read from
     stage = stage + 1 < S ? stage + 1 : 0;
 
     float rz = 1.f;
@@ -301,7 +347,7 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
         r[i].v[j] = fma2(c[i].v[j], POST ? mul2(z[i].v[j], both(rz)) : z[i].v[j], r[i].v[j]);
         a = PRE == kNormLayer ? add2(a, r[i].v[j]) : fma2(r[i].v[j], r[i].v[j], a);
       }
-      if (at.valid[i]) St::store(p.r, (off + 512 * i) * SP, r[i], wide);
+      me.store_stream(p.r, row, i, r[i]);
     }
     if constexpr (PRE != kNormNone) {
       float s[1] = {a.x + a.y};
@@ -311,10 +357,9 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
         a = both(0.f);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float2 m = both(at.valid[i] ? -mean : 0.f);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            r[i].v[j] = add2(r[i].v[j], m);
+            r[i].v[j] = add2(r[i].v[j], both(me.valid[i][j / 2] ? -mean : 0.f));
             a = fma2(r[i].v[j], r[i].v[j], a);
           }
         }
@@ -326,7 +371,7 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
       for (int i = 0; i < V; ++i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) r[i].v[j] = fma2(mul2(r[i].v[j], rstd), f[i].v[j], sh[i].v[j]);
-        if (at.valid[i]) *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.y) + off + 512 * i) = pack8(r[i]);
+        me.store(p.y, row, i, r[i]);
       }
     }
   }
@@ -360,64 +405,56 @@ constexpr int bwd_stages() {
 
 template <bool F32, int V, bool POST, int PRE, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, 1)
-residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
+residual_norm_bwd_kernel(ResidualParams p, RowPlan plan) {
   extern __shared__ __align__(16) uint4 ring_mem[];
   __shared__ __align__(16) float red[15 * kRedFloats];
-  using St = Stream<F32>;
-  constexpr int SP = St::kParts, P = PRE == kNormNone ? SP + 1 : 2 * SP + 2, S = bwd_stages<P>();
+  constexpr int SP = Stream<F32>::kParts, P = PRE == kNormNone ? SP + 1 : 2 * SP + 2, S = bwd_stages<P>();
   constexpr int K = PRE == kNormNone ? 1 : 3;
   constexpr int kDr = 0, kZ = SP, kDy = SP + 1, kR = SP + 2;    // parts of a vector
   // the kernel of the sums may be scheduled once every CTA has started; it waits for this grid before it reads
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  const Place<V> at(plan, p.N);
-  RowSums sum = row_sums(plan, red, at.group, at.warp, at.lane);
-  const Ring<P, V, S> ring(ring_mem);
+  const Place<F32, V> me(plan, p.N);
+  RowSums sum = row_sums(plan, red, me.group, me.warp, me.lane);
+  const Ring<F32, P, V, S> ring(ring_mem);
   const float D = static_cast<float>(p.D), inv_d = 1.f / D;
 
-  // lanes past the row's end, and a dr that is not there, are zeros throughout: they add nothing to a sum
-#pragma unroll
-  for (int k = 0; k < S * V * P; ++k) ring.zero(k);
-  const int64_t step = 16 * at.step * plan.nvec;
-  int64_t off = ((at.b * p.N + at.first) * plan.nvec + at.vec[0]) * 16;
-  auto issue = [&](int64_t n, int64_t o, int stage) {
-    if (n < at.end) {
+  const int64_t step = me.step * p.D;   // elements between this thread's rows
+  int64_t row = (me.b * p.N + me.first) * p.D + me.own;
+  auto issue = [&](int64_t n, int64_t at, int stage) {
+    if (n < me.end) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if (!at.valid[i]) continue;
         if constexpr (PRE != kNormNone) {
-          ring.template copy<SP>(stage, i, kR, p.r, (o + 512 * i) * SP);
-          ring.template copy<1>(stage, i, kDy, p.dy, o + 512 * i);
+          ring.copy_stream(me, stage, i, kR, p.r, at);
+          ring.copy(me, stage, i, kDy, p.dy, at);
         }
-        ring.template copy<1>(stage, i, kZ, p.z, o + 512 * i);
-        if (p.dr) ring.template copy<SP>(stage, i, kDr, p.dr, (o + 512 * i) * SP);
+        ring.copy(me, stage, i, kZ, p.z, at);
+        if (p.dr) ring.copy_stream(me, stage, i, kDr, p.dr, at);
       }
     }
     cp_async_commit();
   };
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) issue(at.first + s * at.step, off + s * step, s);
+  for (int s = 0; s < S - 1; ++s) issue(me.first + s * me.step, row + s * step, s);
 
   // the two factors of vector i
   auto make_c = [&](int i) {
-    Vec8 c = all8(0.f);
-    if (!at.valid[i]) return c;
-    const Vec8 g = vector8(p.gate ? p.gate + at.b * p.gate_stride : nullptr, at.vec[i], 1.f);
-    const Vec8 w = vector8(POST ? p.w_post : nullptr, at.vec[i], 1.f);
+    Vec8 c = me.vector(p.gate ? p.gate + me.b * p.gate_stride : nullptr, i, 1.f);
+    const Vec8 w = me.vector(POST ? p.w_post : nullptr, i, 1.f);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c.v[j] = mul2(mul2(both(p.alpha), g.v[j]), w.v[j]);
+    for (int j = 0; j < 4; ++j) c.v[j] = mul2(mul2(both(p.alpha), c.v[j]), w.v[j]);
     return c;
   };
   auto make_f = [&](int i) {
-    Vec8 f = all8(0.f);
-    if (!at.valid[i]) return f;
-    const Vec8 w = vector8(p.w_pre, at.vec[i], 1.f), sc = vector8(p.scale ? p.scale + at.b * p.scale_stride : nullptr, at.vec[i], 0.f);
+    Vec8 f = me.vector(p.w_pre, i, 1.f);
+    const Vec8 sc = me.vector(p.scale ? p.scale + me.b * p.scale_stride : nullptr, i, 0.f);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f.v[j] = mul2(w.v[j], add2(both(1.f), sc.v[j]));
+    for (int j = 0; j < 4; ++j) f.v[j] = mul2(f.v[j], add2(both(1.f), sc.v[j]));
     return f;
   };
   constexpr bool kKept = kept_factors<F32, WARPS>();
   const int row_vecs = 32 * V * plan.W;          // with those past the end
-  float4* const kept = reinterpret_cast<float4*>(reinterpret_cast<char*>(ring_mem) + Ring<P, V, S>::bytes(blockDim.x));   // [4][row_vecs]
+  float4* const kept = reinterpret_cast<float4*>(reinterpret_cast<char*>(ring_mem) + Ring<F32, P, V, S>::bytes(blockDim.x));   // [4][row_vecs]
   auto keep = [&](int slot, int vec, const Vec8& a) {
     kept[slot * row_vecs + vec] = make_float4(a.v[0].x, a.v[0].y, a.v[1].x, a.v[1].y);
     kept[(slot + 1) * row_vecs + vec] = make_float4(a.v[2].x, a.v[2].y, a.v[3].x, a.v[3].y);
@@ -429,9 +466,9 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
   Vec8 acc[K][V];                       // S, T, U
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    if (kKept && at.group == 0) {
-      keep(0, at.vec[i], make_c(i));
-      if (PRE != kNormNone) keep(2, at.vec[i], make_f(i));
+    if (kKept && me.group == 0) {
+      keep(0, me.slot(i), make_c(i));
+      if (PRE != kNormNone) keep(2, me.slot(i), make_f(i));
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) acc[k][i] = all8(0.f);
@@ -439,26 +476,22 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
   if (kKept) __syncthreads();
 
   int stage = 0;
-  for (int64_t n = at.first; n < at.end; n += at.step, off += step) {
+  for (int64_t n = me.first; n < me.end; n += me.step, row += step) {
     cp_async_wait<S - 2>();
-    issue(n + (S - 1) * at.step, off + (S - 1) * step, stage ? stage - 1 : S - 1);   // where the last row was
+    if (F32) __syncwarp();
+    issue(n + (S - 1) * me.step, row + (S - 1) * step, stage ? stage - 1 : S - 1);   // where the last row was
     // the row's features of vector i, and h = dy f
-    auto stream8 = [&](int i, int part) {
-      uint4 a[SP];
-#pragma unroll
-      for (int k = 0; k < SP; ++k) a[k] = ring.read(stage, i, part + k);
-      return St::get(a);
-    };
-    auto bf8 = [&](int i, int part) { return unpack8(ring.read(stage, i, part)); };
+    auto stream8 = [&](int i, int part) { return ring.stream8(stage, i, part); };
+    auto bf8 = [&](int i, int part) { return ring.bf8(me, stage, i, part); };
     auto h8 = [&](int i, const Vec8& dy) {
-      Vec8 f = kKept ? kept8(2, at.vec[i]) : make_f(i);
+      Vec8 f = kKept ? kept8(2, me.slot(i)) : make_f(i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) f.v[j] = mul2(dy.v[j], f.v[j]);
       return f;
     };
 
-    float rz = 1.f;
-    float2 k0 = both(0.f), k1 = both(0.f), k2 = both(0.f), minus_mean[V];   // of  g = dr + k2 h + k1 xhat + k0,  xhat = k2 (r - mean)
+    float rz = 1.f, mean = 0.f;
+    float2 k0 = both(0.f), k1 = both(0.f), k2 = both(0.f);   // of  g = dr + k2 h + k1 xhat + k0,  xhat = k2 (r - mean)
     if constexpr (POST || PRE != kNormNone) {
       float2 a0 = both(0.f), a1 = both(0.f), a2 = both(0.f);   // sum z^2; layer: sum r, sum h; rms: sum r^2, sum h r
 #pragma unroll
@@ -497,19 +530,16 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
       if (POST) rz = rsqrtf(s0 * inv_d + p.eps);
       if constexpr (PRE != kNormNone) {
         float mh = 0.f;                 // mean h
-#pragma unroll
-        for (int i = 0; i < V; ++i) minus_mean[i] = both(0.f);
         if constexpr (PRE == kNormLayer) {
-          const float mean = mean_of(s1, D, inv_d);
+          mean = mean_of(s1, D, inv_d);
           mh = s2 * inv_d;
           a1 = a2 = both(0.f);          // sum (r - mean)^2, sum h (r - mean)
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            minus_mean[i] = both(at.valid[i] ? -mean : 0.f);
             const Vec8 r = stream8(i, kR), h = h8(i, bf8(i, kDy));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float2 d = add2(r.v[j], minus_mean[i]);
+              const float2 d = add2(r.v[j], both(me.valid[i][j / 2] ? -mean : 0.f));
               a1 = fma2(d, d, a1);
               a2 = fma2(h.v[j], d, a2);
             }
@@ -534,14 +564,14 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
         const Vec8 dy = bf8(i, kDy), h = h8(i, dy), r = stream8(i, kR);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 xh = mul2(PRE == kNormLayer ? add2(r.v[j], minus_mean[i]) : r.v[j], k2);
+          const float2 xh = mul2(PRE == kNormLayer ? add2(r.v[j], both(-mean)) : r.v[j], k2);
           g.v[j] = add2(g.v[j], fma2(k2, h.v[j], fma2(k1, xh, k0)));
           acc[K - 2][i].v[j] = fma2(dy.v[j], xh, acc[K - 2][i].v[j]);
           acc[K - 1][i].v[j] = add2(acc[K - 1][i].v[j], dy.v[j]);
         }
       }
-      if (at.valid[i]) St::store(p.dx, (off + 512 * i) * SP, g, wide);
-      const Vec8 c = kKept ? kept8(0, at.vec[i]) : make_c(i), z = bf8(i, kZ);
+      me.store_stream(p.dx, row, i, g);
+      const Vec8 c = kKept ? kept8(0, me.slot(i)) : make_c(i), z = bf8(i, kZ);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 zh = POST ? mul2(z.v[j], both(rz)) : z.v[j];
@@ -563,8 +593,9 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) u[i].v[j] = mul2(both(rz), fma2(mul2(z.v[j], both(rz)), mu, u[i].v[j]));
       }
-      if (at.valid[i]) *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.dz) + off + 512 * i) = pack8(u[i]);
+      me.store(p.dz, row, i, u[i]);
     }
+    if (F32) __syncwarp();              // the next row's copies go where other lanes have read this one's
     stage = stage + 1 < S ? stage + 1 : 0;
   }
 
@@ -574,13 +605,13 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan, bool wide) {
   float* const cols = reinterpret_cast<float*>(ring_mem);   // [G][K][D]
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    if (at.valid[i])
 #pragma unroll
-      for (int k = 0; k < K; ++k)
+    for (int h = 0; h < 2; ++h)
+      if (me.valid[i][h])
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int k = 0; k < K; ++k) {
           const float2 lo = acc[k][i].v[2 * h], hi = acc[k][i].v[2 * h + 1];
-          reinterpret_cast<float4*>(cols + (at.group * K + k) * p.D + 8 * at.vec[i])[h] = make_float4(lo.x, lo.y, hi.x, hi.y);
+          *reinterpret_cast<float4*>(cols + (me.group * K + k) * p.D + me.col(i, h)) = make_float4(lo.x, lo.y, hi.x, hi.y);
         }
   __syncthreads();
   float4* const out = reinterpret_cast<float4*>(p.partial + static_cast<int64_t>(blockIdx.x) * K * p.D);
@@ -658,25 +689,25 @@ template <bool F32, int V, bool POST, int PRE>
 cudaError_t fwd(const ResidualParams& p, const RowPlan& plan, cudaStream_t stream) {
   auto kernel = residual_norm_fwd_kernel<F32, V, POST, PRE>;
   const int threads = 32 * plan.W * plan.G;
-  const size_t smem = Ring<Stream<F32>::kParts + 1, V, kFwdStages>::bytes(threads);
+  const size_t smem = Ring<F32, Stream<F32>::kParts + 1, V, kFwdStages>::bytes(threads);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   ProfScope prof("residual_norm_fwd", stream);
-  kernel<<<static_cast<unsigned>(p.B * plan.ctas), threads, smem, stream>>>(p, plan, reinterpret_cast<uintptr_t>(p.r) % 32 == 0);
+  kernel<<<static_cast<unsigned>(p.B * plan.ctas), threads, smem, stream>>>(p, plan);
   return cudaGetLastError();
 }
 template <bool F32, int V, bool POST, int PRE, int WARPS>
 cudaError_t bwd_rows(const ResidualParams& p, const RowPlan& plan, cudaStream_t stream) {
   const int K = sums_of(PRE), threads = 32 * plan.W * plan.G;
   constexpr int SP = Stream<F32>::kParts, P = PRE == kNormNone ? SP + 1 : 2 * SP + 2;
-  const size_t cols = static_cast<size_t>(K) * plan.G * p.D * sizeof(float), ring = Ring<P, V, bwd_stages<P>()>::bytes(threads);
+  const size_t cols = static_cast<size_t>(K) * plan.G * p.D * sizeof(float), ring = Ring<F32, P, V, bwd_stages<P>()>::bytes(threads);
   const size_t factors = kept_factors<F32, WARPS>() ? static_cast<size_t>(V) * 64 * 32 * plan.W : 0;
   const size_t smem = cols > ring + factors ? cols : ring + factors;
   auto kernel = residual_norm_bwd_kernel<F32, V, POST, PRE, WARPS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   ProfScope prof("residual_norm_bwd", stream);
-  kernel<<<static_cast<unsigned>(p.B * plan.ctas), threads, smem, stream>>>(p, plan, reinterpret_cast<uintptr_t>(p.dx) % 32 == 0);
+  kernel<<<static_cast<unsigned>(p.B * plan.ctas), threads, smem, stream>>>(p, plan);
   return cudaGetLastError();
 }
 template <bool F32, int V, bool POST, int PRE>
