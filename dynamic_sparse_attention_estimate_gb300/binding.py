@@ -636,7 +636,7 @@ def _rope_args(x: torch.Tensor, pos: Optional[torch.Tensor], rope: Optional[Rope
 
 def _call(name: str, device: int, *args):
     """One library call on this device's current stream, with the device made current for it."""
-    f = getattr(load_library(), name)
+    f = getattr(_lib or load_library(), name)
     if torch._C._cuda_getDevice() == device:
         status = f(*args, torch._C._cuda_getCurrentRawStream(device))
     else:

@@ -3,9 +3,26 @@
 // measured (the bench counts a kernel's captured DRAM traffic only for the sources it was captured on).
 #pragma once
 
+#include <atomic>
+
 #include "dsv_internal.h"
 
 namespace dsv {
+
+// Lets a kernel have `bytes` of dynamic shared memory on the current device: asked of the runtime once per kernel and device (the
+// question costs the host about 0.7 us).
+template <auto Kernel>
+cudaError_t allow_shared(int bytes) {
+  static std::atomic<uint64_t> allowed{0};   // a bit per device
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = device < 64 ? 1ull << device : 0;
+  if (allowed.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) allowed.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // Bit of the device status word: a kernel met a token position outside its axis' table.
 constexpr unsigned int kStatusBadPosition = 4u;

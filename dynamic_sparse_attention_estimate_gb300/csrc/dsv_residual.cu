@@ -64,6 +64,7 @@ struct Stream {
 
 // ---------------------------------------------------------------- how the work is laid out
 constexpr int kMaxWarps = 16;           // of a row and of a CTA
+constexpr int kMaxShared = 221 * 1024;  // dynamic shared memory of a CTA: what the sums over a row leave of 227 KB
 struct RowPlan {
   int nvec, V, W, G;                    // vectors of eight features, V to a lane, W warps to a row, G rows at a time
   int warps;                            // that a CTA may have: its kernel's registers allow no more
@@ -687,10 +688,10 @@ residual_weights_kernel(ResidualParams p, const float* per_sample) {
 
 template <bool F32, int V, bool POST, int PRE>
 cudaError_t fwd(const ResidualParams& p, const RowPlan& plan, cudaStream_t stream) {
-  auto kernel = residual_norm_fwd_kernel<F32, V, POST, PRE>;
+  constexpr auto kernel = residual_norm_fwd_kernel<F32, V, POST, PRE>;
   const int threads = 32 * plan.W * plan.G;
   const size_t smem = Ring<F32, Stream<F32>::kParts + 1, V, kFwdStages>::bytes(threads);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  const cudaError_t e = allow_shared<kernel>(kMaxShared);
   if (e != cudaSuccess) return e;
   ProfScope prof("residual_norm_fwd", stream);
   kernel<<<static_cast<unsigned>(p.B * plan.ctas), threads, smem, stream>>>(p, plan);
@@ -703,8 +704,8 @@ cudaError_t bwd_rows(const ResidualParams& p, const RowPlan& plan, cudaStream_t 
   const size_t cols = static_cast<size_t>(K) * plan.G * p.D * sizeof(float), ring = Ring<F32, P, V, bwd_stages<P>()>::bytes(threads);
   const size_t factors = kept_factors<F32, WARPS>() ? static_cast<size_t>(V) * 64 * 32 * plan.W : 0;
   const size_t smem = cols > ring + factors ? cols : ring + factors;
-  auto kernel = residual_norm_bwd_kernel<F32, V, POST, PRE, WARPS>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  constexpr auto kernel = residual_norm_bwd_kernel<F32, V, POST, PRE, WARPS>;
+  const cudaError_t e = allow_shared<kernel>(kMaxShared);
   if (e != cudaSuccess) return e;
   ProfScope prof("residual_norm_bwd", stream);
   kernel<<<static_cast<unsigned>(p.B * plan.ctas), threads, smem, stream>>>(p, plan);

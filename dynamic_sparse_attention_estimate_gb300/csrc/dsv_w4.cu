@@ -543,8 +543,8 @@ template <int G, int NT, int RS, bool ZERO>
 cudaError_t fwd_zero(const W4Params& p, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((p.F + 16 * RS - 1) / (16 * RS)), static_cast<unsigned>((p.M + 8 * NT - 1) / (8 * NT)));
   constexpr int smem = fwd_smem<G, NT, RS>();
-  auto kernel = w4_fwd_kernel<G, NT, RS, ZERO>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr auto kernel = w4_fwd_kernel<G, NT, RS, ZERO>;
+  const cudaError_t e = allow_shared<kernel>(smem);
   if (e != cudaSuccess) return e;
   kernel<<<grid, 32 * kFwdWarps, smem, stream>>>(p);
   return cudaGetLastError();
@@ -567,8 +567,8 @@ template <int G, int NT, bool ZERO>
 cudaError_t bwd_zero(const W4Params& p, const W4BwdPlan& plan, cudaStream_t stream) {
   constexpr int smem = bwd_smem<G, NT, ZERO>();
   const dim3 grid(static_cast<unsigned>(plan.col_blocks), static_cast<unsigned>(plan.splits), static_cast<unsigned>((p.M + 4 * NT - 1) / (4 * NT)));
-  auto kernel = w4_bwd_kernel<G, NT, ZERO>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr auto kernel = w4_bwd_kernel<G, NT, ZERO>;
+  const cudaError_t e = allow_shared<kernel>(smem);
   if (e != cudaSuccess) return e;
   kernel<<<grid, 32 * kBwdWarps, smem, stream>>>(p, plan);
   return cudaGetLastError();

@@ -155,9 +155,10 @@ def on_gpu(c):
 
 NORMS = [(post, pre) for post in ("none", "rms") for pre in ("none", "layer", "rms")]
 # one token and a few, one vector of features, rows of one to sixteen warps and either side of each, samples more than
-# slabs, rows more than slabs
+# CTAs, several rows in turn to a group of a CTA
 SHAPES = [(1, 1, 8), (2, 3, 24), (1, 5, 256), (3, 37, 264), (2, 77, 1024), (1, 130, 1160), (2, 9, 2048), (1, 19, 4096), (1, 7, 4104),
-          (2, 5, 8192), (1, 3000, 64), (200, 2, 128), (3, 301, 768), (1, 4, 1536), (2, 40, 5128)]
+          (2, 5, 8192), (1, 3000, 64), (200, 2, 128), (3, 301, 768), (1, 4, 1536), (2, 40, 5128),
+          (1, 3500, 1032), (2, 900, 4104)]
 
 
 @pytest.mark.parametrize("f32", [False, True])
@@ -363,6 +364,26 @@ def test_without_a_branch_it_is_adaln():
     z = dsv_adaln_fwd(g["x"], g["scale"], g["shift"])
     ref = oracle.adaln_fwd(g["x"], g["scale"], g["shift"])
     assert (np.abs(np64(y) - np64(z)) <= 2 * 2.0 ** -8 * np.abs(ref) + 1e-4).all()
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_tensors_that_start_inside_an_allocation(f32):
+    """16-byte boundaries that are none of 32."""
+    need_gpu()
+    g = on_gpu(case(2, 30, 392, f32))
+    want, dwant = fwd(g, "rms", "layer"), bwd(g, "rms", "layer")
+
+    def moved(t):
+        skip = 16 // t.element_size()
+        out = torch.empty(t.numel() + skip, dtype=t.dtype, device="cuda")[skip:].view(t.shape)
+        assert out.data_ptr() % 32 == 16
+        return out
+
+    for n in g:
+        g[n] = moved(g[n]).copy_(g[n])
+    got = fwd(g, "rms", "layer", out=tuple(moved(t) for t in want))
+    dgot = bwd(g, "rms", "layer", out=tuple(moved(t) for t in dwant[:2]), d_mod=tuple(moved(dwant[i]) for i in (2, 4, 5)))
+    assert all(torch.equal(a, b) for a, b in zip(got + dgot, want + dwant))
 
 
 def test_repeats_streams_and_a_replayed_graph():

@@ -184,6 +184,35 @@ def test_a_bad_scale_stays_in_its_weights():
     assert torch.equal(dx2[:, cols], dx[:, cols]) and torch.isnan(dx2[:, ~cols]).all()
 
 
+@pytest.mark.parametrize("G", [32, 64, 128])
+def test_tensors_that_start_inside_an_allocation(G):
+    """16-byte boundaries that are none of 32."""
+    need_gpu()
+    c = case(5, 384, 300, G, True)
+    w, x, dy = weight(c), c["x"].cuda(), c["dy"].cuda()
+    y, dx = dsv_w4_linear_fwd(x, w), dsv_w4_linear_bwd(dy, w)
+
+    def moved(t):
+        skip = 16 // t.element_size()
+        out = torch.empty(t.numel() + skip, dtype=t.dtype, device="cuda")[skip:].view(t.shape).copy_(t)
+        assert out.data_ptr() % 32 == 16
+        return out
+
+    w = W4Weight(*map(moved, w))
+    assert torch.equal(dsv_w4_linear_fwd(moved(x), w, out=moved(y)), y) and torch.equal(dsv_w4_linear_bwd(moved(dy), w, out=moved(dx)), dx)
+
+
+def test_the_smallest_numbers_keep_their_bits():
+    """Vectors of 2^-100 to 2^-60: the weights' unpacking scales them no further down."""
+    need_gpu()
+    c = case(4, 256, 70, 64, True)
+    c["x"] = (c["x"].float() * torch.tensor([2.0 ** -60, 2.0 ** -80, 2.0 ** -90, 2.0 ** -100])[:, None]).to(BF16)
+    c["dy"] = c["dy"] * torch.tensor([2.0 ** -60, 2.0 ** -80, 2.0 ** -90, 2.0 ** -100])[:, None]
+    w = weight(c)
+    check_fwd(c, dsv_w4_linear_fwd(c["x"].cuda(), w), bias=False)
+    check_bwd(c, dsv_w4_linear_bwd(c["dy"].cuda(), w), c["dy"])
+
+
 def test_shapes_of_vectors():
     need_gpu()
     c = case(6, 128, 48, 64, False)
