@@ -8,9 +8,11 @@
 // were loaded into.  tcgen05 would want them as bf16 in shared memory, 128 rows at a time, for at most 64 columns.
 //   Four bits that a mask leaves at the foot of a bf16 number are q 2^-133, a subnormal one, and four bits above them 16 q 2^-133:
 // the numbers up to 255 2^-133 are evenly spaced.  One fma (which keeps subnormal numbers) makes (q - zero) / 64 of either, with
-// nothing lost and without a shift: the integer pipe, which unpacks at half the rate of the others, is what bounds these
-// kernels.  The scale multiplies fp32 sums (forward) or the other operand (backward), with 64 in it.  Sums are fp32, with one
+// nothing lost and without a shift: the integer pipe, which unpacks at half the rate of the others, is the busiest here.  The scale multiplies fp32 sums (forward) or the other operand (backward), with 64 in it.  Sums are fp32, with one
 // rounding at the output.
+//   Forward, 294,912 x 2048 and two vectors: 63 us, 5.1 TB/s (0.77 of the copy rate); two instructions in three clocks on every
+// scheduler, of which the unpacking is half.  Backward, 98,304 x 2048 and four vectors: 32 us, 3.4 TB/s; it unpacks with one more
+// permutation a pair and makes the other operand besides.
 #include <type_traits>
 
 #include "dsv_block.h"
@@ -246,14 +248,17 @@ constexpr int kBwdCols = 64 * kBwdColWarps, kBwdSteps = 4, kBwdRows = 16 * kBwdS
 // A row of a chunk is 64 bytes; the halves of every third and fourth of four rows are exchanged, so that the four rows t and
 // the 32 bytes of a warp's columns are in different banks.
 constexpr int kBwdStage = kBwdRows * kBwdCols / 2, kBwdStages = 3;
-constexpr int64_t kBwdWantCtas = 3 * 152;
 struct W4BwdPlan {
   int64_t col_blocks, splits, rows;     // rows of W to a CTA, a multiple of kBwdRows
 };
-W4BwdPlan w4_bwd_plan(int64_t D, int64_t F) {
+// CTAs of an SM at a time: the registers of two tiles of vectors with two groups a warp leave room for two.
+constexpr int bwd_ctas(int group, int tiles) { return tiles == 2 && group < 64 ? 2 : 3; }
+// Runs so that all SMs have their CTAs at a time; passes over more than eight vectors follow one another (as many runs fewer left
+// SMs idle: 32 vectors 306 us instead of 279).
+W4BwdPlan w4_bwd_plan(int64_t M, int64_t D, int64_t F, int group) {
   W4BwdPlan q;
   q.col_blocks = (D + kBwdCols - 1) / kBwdCols;
-  q.splits = kBwdWantCtas / q.col_blocks;
+  q.splits = bwd_ctas(group, M > 4 ? 2 : 1) * 152 / q.col_blocks;
   const int64_t most = (F + kBwdRows - 1) / kBwdRows;
   if (q.splits > most) q.splits = most;
   if (q.splits < 1) q.splits = 1;
@@ -283,7 +288,7 @@ DSV_DEVICE uint4 split4(const float (&v)[4]) {
 }
 
 template <int G, int NT, bool ZERO>
-__global__ void __launch_bounds__(32 * kBwdWarps, NT == 2 && G < 64 ? 2 : 3)
+__global__ void __launch_bounds__(32 * kBwdWarps, bwd_ctas(G, NT))
 w4_bwd_kernel(W4Params p, W4BwdPlan plan) {
   constexpr int CG = kBwdCols / G;               // groups of the CTA's columns
   extern __shared__ __align__(16) unsigned char shared[];   // the stages, the other operand, the zero points; then the warps' sums
@@ -584,8 +589,8 @@ cudaError_t bwd_group(const W4Params& p, const W4BwdPlan& plan, cudaStream_t str
 
 }  // namespace
 
-size_t w4_bwd_workspace(int64_t M, int64_t D, int64_t F) {
-  return static_cast<size_t>(w4_bwd_plan(D, F).splits * M * D) * sizeof(float);
+size_t w4_bwd_workspace(int64_t M, int64_t D, int64_t F, int group) {
+  return static_cast<size_t>(w4_bwd_plan(M, D, F, group).splits * M * D) * sizeof(float);
 }
 
 cudaError_t launch_w4_fwd(const W4Params& p, cudaStream_t stream) {
@@ -594,7 +599,7 @@ cudaError_t launch_w4_fwd(const W4Params& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_w4_bwd(const W4Params& p, cudaStream_t stream) {
-  const W4BwdPlan plan = w4_bwd_plan(p.D, p.F);
+  const W4BwdPlan plan = w4_bwd_plan(p.M, p.D, p.F, p.group);
   {
     ProfScope prof("w4_linear_bwd", stream);
     const cudaError_t e = p.group == 32 ? bwd_group<32>(p, plan, stream) : p.group == 64 ? bwd_group<64>(p, plan, stream)
