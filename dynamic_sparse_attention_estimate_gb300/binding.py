@@ -975,15 +975,17 @@ def _w4_args(w: W4Weight, device: int):
             raise TypeError(f"{n} must be a torch.Tensor")
         if t.dim() != 2:
             raise ValueError(f"{n} needs 2 dims, got {tuple(t.shape)}")
-    F, half = data.shape
-    groups = scale.shape[1]
-    _need_on(torch.uint8, (F, half), device, (data, "w.data"))
-    _need_on(torch.bfloat16, (F, groups), device, (scale, "w.scale"))
+    (F, half), groups = data.shape, scale.shape[1]
+    if data.dtype is not torch.uint8 or not data.is_contiguous() or data.get_device() != device:
+        _need_on(torch.uint8, (F, half), device, (data, "w.data"))
+    if scale.dtype is not torch.bfloat16 or scale.shape[0] != F or not scale.is_contiguous() or scale.get_device() != device:
+        _need_on(torch.bfloat16, (F, groups), device, (scale, "w.scale"))
     if zero is not None:
         _need_on(torch.uint8, (F, groups), device, (zero, "w.zero"))
-    if not groups or (2 * half) % groups:
-        raise ValueError(f"w: {2 * half} columns do not divide into {groups} groups")
-    return 2 * half, F, 2 * half // groups
+    D = 2 * half
+    if not groups or D % groups:
+        raise ValueError(f"w: {D} columns do not divide into {groups} groups")
+    return D, F, D // groups
 
 
 def dsv_w4_quantize(w: torch.Tensor, group: int = 64, symmetric: bool = True) -> W4Weight:
@@ -1012,13 +1014,13 @@ def dsv_w4_linear_fwd(x: torch.Tensor, w: W4Weight, bias: Optional[torch.Tensor]
                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y [..., F] = x W^T + bias for x bf16 [..., D] of at most 64 vectors and 4-bit weights; bias bf16 [F] or None."""
     _need_vectors(x, "x", (torch.bfloat16,))
-    device = x.get_device()
+    device, shape = x.get_device(), x.shape
     D, F, group = _w4_args(w, device)
-    if x.shape[-1] != D:
-        raise ValueError(f"x: need {D} features, got {tuple(x.shape)}")
+    if shape[-1] != D:
+        raise ValueError(f"x: need {D} features, got {tuple(shape)}")
     if bias is not None:
         _need_on(torch.bfloat16, (F,), device, (bias, "bias"))
-    shape = (*x.shape[:-1], F)
+    shape = (shape[0], F) if len(shape) == 2 else (*shape[:-1], F)
     dims, _ = _w4_dims(x.numel() // D if D else 0, D, F, group, False)
     if out is None:
         out = torch.empty(shape, dtype=x.dtype, device=x.device)
@@ -1037,11 +1039,11 @@ def dsv_w4_linear_bwd(dy: torch.Tensor, w: W4Weight, out: Optional[torch.Tensor]
                       workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dx bf16 [..., D] = dy W for dy bf16 or fp32 [..., F] (the weights are frozen; a bias has the gradient dy itself)."""
     _need_vectors(dy, "dy", (torch.bfloat16, torch.float32))
-    device = dy.get_device()
+    device, shape = dy.get_device(), dy.shape
     D, F, group = _w4_args(w, device)
-    if dy.shape[-1] != F:
-        raise ValueError(f"dy: need {F} features, got {tuple(dy.shape)}")
-    shape = (*dy.shape[:-1], D)
+    if shape[-1] != F:
+        raise ValueError(f"dy: need {F} features, got {tuple(shape)}")
+    shape = (shape[0], D) if len(shape) == 2 else (*shape[:-1], D)
     dims, nbytes = _w4_dims(dy.numel() // F if F else 0, D, F, group, dy.dtype is torch.float32)
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=dy.device)
