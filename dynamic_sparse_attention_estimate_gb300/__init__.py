@@ -1,5 +1,6 @@
-"""GB300-native (sm_103a) dynamic sparse 3D attention for video DiT training (DSV), and
-the fused AdaLN (LayerNorm + modulation) operator of the same training step.
+"""GB300-native (sm_103a) dynamic sparse 3D attention for video DiT training (DSV), and the operators around it in a DiT
+block: fused AdaLN (LayerNorm + modulation), rotary positions and the qk norm, the gated feed-forward, the gated residual with
+its norms, and products of a few vectors with 4-bit weights (the modulation's projection).
 
 The compute path is a C-ABI CUDA library (``libdsv.so``, entry points declared in
 ``include/dsv.h``); :mod:`.binding` is a thin ctypes layer over it that passes

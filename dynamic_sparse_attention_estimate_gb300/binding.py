@@ -835,7 +835,7 @@ def _residual_dims(B: int, N: int, D: int, f32: bool, post: str, pre: str, alpha
     """(dims struct, workspace bytes of the backward); strides: of gate, scale, shift and their gradients."""
     if post not in ("none", "rms") or pre not in _NORMS:
         raise ValueError(f"post must be 'none' or 'rms' and pre 'none', 'rms' or 'layer', got {post!r} and {pre!r}")
-    dims = ResidualDims(B, N, D, _NORMS[post], _NORMS[pre], int(f32), float(alpha), float(eps), *strides)
+    dims = ResidualDims(B, N, D, _NORMS[post], _NORMS[pre], int(f32), alpha, eps, *strides)
     return dims, int(load_library().dsv_residual_norm_bwd_workspace(dims))
 
 
@@ -879,7 +879,7 @@ def dsv_residual_norm_fwd(x: torch.Tensor, z: torch.Tensor, gate: Optional[torch
     _need_on(bf, shape, device, (z, "z"))
     if w_post is not None or w_pre is not None:
         _need_on(bf, (D,), device, (w_post, "w_post"), (w_pre, "w_pre"))
-    dims = _residual_dims(B, N, D, f32, post, pre, alpha, eps, _row_stride(gate, "gate", bf, vec, device),
+    dims = _residual_dims(B, N, D, f32, post, pre, float(alpha), float(eps), _row_stride(gate, "gate", bf, vec, device),
                           _row_stride(scale, "scale", bf, vec, device), _row_stride(shift, "shift", bf, vec, device), D)[0]
     if out is None:
         r = torch.empty_like(x)
@@ -939,7 +939,7 @@ def dsv_residual_norm_bwd(dr: Optional[torch.Tensor], dy: Optional[torch.Tensor]
             d_stride = found.pop()
     dw_post = None if w_post is None else torch.empty((D,), dtype=full, device=where)
     dw_pre = None if w_pre is None else torch.empty((D,), dtype=full, device=where)
-    dims, nbytes = _residual_dims(B, N, D, f32, post, pre, alpha, eps, _row_stride(gate, "gate", bf, vec, device),
+    dims, nbytes = _residual_dims(B, N, D, f32, post, pre, float(alpha), float(eps), _row_stride(gate, "gate", bf, vec, device),
                                   _row_stride(scale, "scale", bf, vec, device), D, d_stride)
     ws, nbytes, _keep = _workspace(workspace, nbytes, stream)
     _call("dsv_residual_norm_bwd", device, dims, _ptr(dr), _ptr(dy), _ptr(r), _ptr(z), _ptr(gate), _ptr(w_post), _ptr(scale),

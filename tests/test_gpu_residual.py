@@ -248,6 +248,18 @@ def test_in_place(D, f32):
     assert got[0] is dr and all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_alpha_and_eps_that_are_tensors_are_read_in_every_call():
+    need_gpu()
+    g = on_gpu(case(1, 9, 64))
+    alpha, eps = torch.tensor(0.5), torch.tensor(1e-3)
+    for a, e in ((0.5, 1e-3), (2.0, 1e-3), (2.0, 10.0)):
+        alpha.fill_(a)
+        eps.fill_(e)
+        got = dsv_residual_norm_fwd(g["x"], g["z"], g["gate"], alpha=alpha, eps=eps)
+        want = dsv_residual_norm_fwd(g["x"], g["z"], g["gate"], alpha=a, eps=float(torch.tensor(e)))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def guarded(shape, dtype, pad=4096):
     numel = int(np.prod(shape))
     buf = torch.full((numel + 2 * pad,), -77.0, device="cuda").to(dtype)
