@@ -528,7 +528,8 @@ w4_quantize_kernel(W4Params p) {
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
   if (!inside) return;
-  const bf16 scale = __float2bfloat16(p.zero ? (hi - lo) / 15.f : fmaxf(-lo, hi) / 7.f);
+  // halves, which are exact, so that the range of finite weights is finite
+  const bf16 scale = __float2bfloat16(p.zero ? (0.5f * hi - 0.5f * lo) / 7.5f : fmaxf(-lo, hi) / 7.f);
   const float s = __bfloat162float(scale);
   const float zero = !p.zero ? 8.f : s > 0.f ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 0.f;
   uint32_t out = 0;

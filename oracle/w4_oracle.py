@@ -42,7 +42,7 @@ def w4_quantize(w, group, symmetric=True):
     w = _f64(w)
     g = w.reshape(w.shape[0], -1, group)
     lo, hi = np.minimum(g.min(-1), 0), np.maximum(g.max(-1), 0)
-    scale = _bf16(np.maximum(-lo, hi) / 7 if symmetric else (hi - lo).astype(np.float32) / np.float32(15))
+    scale = _bf16(np.maximum(-lo, hi) / 7 if symmetric else (hi / 2 - lo / 2).astype(np.float32) / np.float32(7.5))
     safe = np.where(scale > 0, scale, 1)
     zero = np.full(scale.shape, 8.0) if symmetric else np.where(scale > 0, np.clip(np.rint(-lo / safe), 0, 15), 0)
     q = np.clip(np.rint(g / safe[..., None]) + zero[..., None], 0, 15)

@@ -128,6 +128,21 @@ def test_quantize_is_the_oracles(F, D, G, symmetric):
     assert got.zero is None if symmetric else np.array_equal(got.zero.cpu().numpy(), zero)
 
 
+@pytest.mark.parametrize("symmetric", [True, False])
+def test_quantize_of_the_largest_weights(symmetric):
+    """A group may hold both ends of the type: its scale is finite, and every weight within half a step (and what the scale's and the
+    zero point's roundings move the ends: 15 steps of 2^-8 and half a step)."""
+    need_gpu()
+    top = torch.finfo(BF16).max
+    w = torch.linspace(-1, 1, 2 * 128, dtype=torch.float64).reshape(2, 128).mul(top).to(BF16)
+    w[0, 0], w[0, 1], w[1, 5] = top, -top, -top
+    got = dsv_w4_quantize(w.cuda(), 64, symmetric)
+    assert bool(torch.isfinite(got.scale).all())
+    values = oracle.w4_values(got.data, got.scale, got.zero)
+    step = np.repeat(np64(got.scale), 64, 1)
+    assert float((np.abs(values - np64(w)) / step).max()) <= 1.0 + 15 * 2.0 ** -8
+
+
 def guarded(shape, dtype, fill, pad=4096):
     numel = int(np.prod(shape))
     buf = torch.full((numel + 2 * pad,), fill, dtype=dtype, device="cuda")
