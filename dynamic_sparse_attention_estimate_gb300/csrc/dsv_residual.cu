@@ -73,9 +73,11 @@ struct RowPlan {
   int64_t ctas;                         // of a sample: CTA c takes rows c G, .., c G + G - 1 of every ctas G
 };
 // Two vectors a lane where a row has more than 32: a row's sums, its scalars and its addresses cost a lane about as much as
-// eight features do, so one vector a lane was half the rate (32,768 x 2048 backward, both norms: 268 us).  At most `ctas`
-// CTAs over all samples (one more than there are SMs would take as long as two rounds), and no more than give each group of one a
-// row.
+// eight features do, so one vector a lane was half the rate (32,768 x 2048 backward, both norms: 268 us).  A sample has as many
+// CTAs as fill `ctas` SMs once, or some times over where the samples do not divide them (80 samples would leave 72 of 152 idle): a
+// round costs its turns and those that a CTA's start and end are worth, and a further round has to save a twentieth (80 samples of
+// 1024 x 1152: forward 163 us in one round, 125 in three, backward 386 and 259, 200 samples 343 and 293, 770 and 564).
+constexpr int64_t kTurnsOfStart = 4;
 RowPlan row_plan(int64_t B, int64_t N, int64_t D, int64_t ctas, int warps) {
   RowPlan q;
   q.nvec = static_cast<int>(D / 8);
@@ -84,9 +86,13 @@ RowPlan row_plan(int64_t B, int64_t N, int64_t D, int64_t ctas, int warps) {
   q.warps = q.W > warps ? kMaxWarps : warps;
   q.G = q.warps / q.W;
   if (q.G > 15) q.G = 15;               // named barriers 1 .. 15
-  q.ctas = B < ctas ? ctas / B : 1;
-  const int64_t most = (N + q.G - 1) / q.G;
-  if (q.ctas > most) q.ctas = most;
+  const int64_t most = (N + q.G - 1) / q.G, rounds = (B + ctas - 1) / ctas;
+  int64_t least = -1;
+  for (int64_t r = rounds; r < rounds + 4; ++r) {
+    const int64_t c = r * ctas / B < most ? r * ctas / B : most;
+    const int64_t cost = (B * c + ctas - 1) / ctas * ((N + c * q.G - 1) / (c * q.G) + kTurnsOfStart);
+    if (least < 0 || 20 * cost < 19 * least) least = cost, q.ctas = c;
+  }
   return q;
 }
 
