@@ -636,63 +636,75 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan) {
   }
 }
 
-// The gradients of the vectors from the CTAs' partial rows: a CTA takes 32 features of one of the sums S, T, U, a warp every
-// sixteenth partial row, whose loads leave together; the sixteen sums are added in order.  The weights' gradients are sums over the
-// samples too: a few samples are the same CTA's in turn, more have a CTA each and leave their parts behind the partial rows, for a last
-// kernel.
-constexpr int kSumWarps = 16;
+// The gradients of the vectors from the CTAs' partial rows: a CTA takes 32 features of one of the sums S, T, U, a sample's `each`
+// warps every each-th partial row, ten loads leaving together; their sums are added in order.  `each` is what the sample's partial
+// rows keep busy, and the CTA's other warps take the next samples (sixteen warps to each of them: 200 samples of 64 x 1152 122 us for
+// the call instead of 63, 24 of 1024 x 1152 77 instead of 70).  The weights' gradients are sums over the samples too: a few samples are the same CTA's in turn, more leave
+// their parts behind the partial rows, for a last kernel.
+constexpr int kSumWarps = 16, kLoads = 10;
 constexpr int64_t kSamplesInTurn = 4;
 __global__ void __launch_bounds__(32 * kSumWarps)
-residual_vectors_kernel(ResidualParams p, int64_t parts, float* per_sample) {
+residual_vectors_kernel(ResidualParams p, int64_t parts, int each, int64_t samples, float* per_sample) {
   __shared__ float red[2][kSumWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = blockIdx.y, K = gridDim.y;
   const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  const int64_t first = gridDim.z == p.B ? blockIdx.z : 0, last = gridDim.z == p.B ? first + 1 : p.B;
+  const int64_t first = blockIdx.z * samples, last = min(first + samples, p.B);   // the CTA's samples
+  const int at_once = kSumWarps / each;
   const bool inside = d < p.D;
   float weight = 0.f;                   // the gradient of w_post (S) or w_pre (T)
+  int turn = 0;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the partial rows
-  for (int64_t b = first; b < last; ++b) {
+  for (int64_t b0 = first; b0 < last; b0 += at_once, turn ^= 1) {
+    const int64_t b = b0 + warp / each;
+    const bool here = inside && b < last;
     const float* const rows = p.partial + (b * parts * K + k) * p.D + d;
     float s = 0.f;
-    for (int64_t t0 = warp; t0 < parts; t0 += 10 * kSumWarps) {
-      float v[10];
+    for (int64_t t0 = warp % each; t0 < parts; t0 += kLoads * each) {
+      float v[kLoads];
 #pragma unroll
-      for (int u = 0; u < 10; ++u) v[u] = inside && t0 + u * kSumWarps < parts ? rows[(t0 + u * kSumWarps) * K * p.D] : 0.f;
+      for (int u = 0; u < kLoads; ++u) v[u] = here && t0 + u * each < parts ? rows[(t0 + u * each) * K * p.D] : 0.f;
 #pragma unroll
-      for (int u = 0; u < 10; ++u) s += v[u];
+      for (int u = 0; u < kLoads; ++u) s += v[u];
     }
-    red[b & 1][warp][lane] = s;         // the last sample's are read by one warp meanwhile
+    red[turn][warp][lane] = s;          // the last turn's are read meanwhile
     __syncthreads();
-    if (warp || !inside) continue;
-    for (int w = 1; w < kSumWarps; ++w) s += red[b & 1][w][lane];
+    if (warp % each || !here) continue;
+    for (int w = 1; w < each; ++w) s += red[turn][warp + w][lane];
+    float part = 0.f;                   // of the weight's gradient
     if (k == 0) {
       if (p.d_gate) p.d_gate[b * p.d_stride + d] = p.alpha * s * (p.w_post ? __bfloat162float(p.w_post[d]) : 1.f);
-      weight += p.alpha * s * (p.gate ? __bfloat162float(p.gate[b * p.gate_stride + d]) : 1.f);
+      part = p.alpha * s * (p.gate ? __bfloat162float(p.gate[b * p.gate_stride + d]) : 1.f);
     } else if (k == 1) {
       if (p.d_scale) p.d_scale[b * p.d_stride + d] = s * (p.w_pre ? __bfloat162float(p.w_pre[d]) : 1.f);
-      weight += s * (1.f + (p.scale ? __bfloat162float(p.scale[b * p.scale_stride + d]) : 0.f));
+      part = s * (1.f + (p.scale ? __bfloat162float(p.scale[b * p.scale_stride + d]) : 0.f));
     } else if (p.d_shift) {
       p.d_shift[b * p.d_stride + d] = s;
     }
+    if (per_sample && k < 2) per_sample[(2 * b + k) * p.D + d] = part;
+    weight += part;
   }
-  if (warp || !inside || k > 1) return;
-  float* const to = per_sample ? per_sample + 2 * first * p.D : nullptr;
-  if (per_sample) to[k * p.D + d] = weight;
-  else if (k == 0 && p.dw_post) p.dw_post[d] = weight;
-  else if (k == 1 && p.dw_pre) p.dw_pre[d] = weight;
+  // with no kernel after this one a CTA has all samples, one at a time
+  if (warp || !inside || per_sample) return;
+  if (k == 0 && p.dw_post) p.dw_post[d] = weight;
+  if (k == 1 && p.dw_pre) p.dw_pre[d] = weight;
 }
-__global__ void __launch_bounds__(128)
+// The weights' gradients from the samples' parts: 32 features of one of them to a CTA, every sixteenth sample to a warp.
+__global__ void __launch_bounds__(32 * kSumWarps)
 residual_weights_kernel(ResidualParams p, const float* per_sample) {
-  const int64_t d = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
-  if (d >= p.D) return;
-  float post = 0.f, pre = 0.f;
+  __shared__ float red[kSumWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = blockIdx.y;
+  const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  float* const out = k ? p.dw_pre : p.dw_post;
+  float s = 0.f;
+  if (d < p.D && out) {
 #pragma unroll 8
-  for (int64_t b = 0; b < p.B; ++b) {
-    post += per_sample[(2 * b) * p.D + d];
-    pre += per_sample[(2 * b + 1) * p.D + d];
+    for (int64_t b = warp; b < p.B; b += kSumWarps) s += per_sample[(2 * b + k) * p.D + d];
   }
-  if (p.dw_post) p.dw_post[d] = post;
-  if (p.dw_pre) p.dw_pre[d] = pre;
+  red[warp][lane] = s;
+  __syncthreads();
+  if (warp || d >= p.D || !out) return;
+  for (int w = 1; w < kSumWarps; ++w) s += red[w][lane];
+  out[d] = s;
 }
 
 template <bool F32, int V, bool POST, int PRE>
@@ -737,16 +749,19 @@ cudaError_t bwd(const ResidualParams& p, const RowPlan& plan, cudaStream_t strea
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>((p.D + 31) / 32), sums_of(PRE), turns ? 1u : static_cast<unsigned>(p.B));
+    int each = kSumWarps;
+    while (!turns && each > 1 && plan.ctas <= kLoads * each / 2) each /= 2;
+    const int64_t samples = turns ? p.B : kSumWarps / each;
+    cfg.gridDim = dim3(static_cast<unsigned>((p.D + 31) / 32), sums_of(PRE), static_cast<unsigned>((p.B + samples - 1) / samples));
     cfg.blockDim = dim3(32 * kSumWarps);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, residual_vectors_kernel, p, plan.ctas, per_sample)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, residual_vectors_kernel, p, plan.ctas, each, samples, per_sample)) != cudaSuccess) return e;
   }
   if (!per_sample) return cudaSuccess;
   ProfScope prof("residual_weights", stream);
-  residual_weights_kernel<<<static_cast<unsigned>((p.D + 127) / 128), 128, 0, stream>>>(p, per_sample);
+  residual_weights_kernel<<<dim3(static_cast<unsigned>((p.D + 31) / 32), 2), 32 * kSumWarps, 0, stream>>>(p, per_sample);
   return cudaGetLastError();
 }
 

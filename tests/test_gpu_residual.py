@@ -174,6 +174,26 @@ def test_both_directions_match_the_oracle(B, N, D, f32):
     assert dsv_last_device_status() == 0
 
 
+# samples that share a CTA of the vectors' sums with one to eight warps each, and that take the SMs several times over
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("B,N,D", [(80, 400, 264), (17, 130, 520), (6, 700, 128), (5, 2000, 40), (153, 3, 776), (2, 1300, 96)])
+def test_many_samples(B, N, D, f32):
+    need_gpu()
+    c = case(B, N, D, f32)
+    g = on_gpu(c)
+    for post, pre in (("rms", "layer"), ("none", "none")):
+        check_fwd(c, fwd(g, post, pre), post, pre)
+        check_bwd(c, bwd(g, post, pre), post, pre)
+    # without the weights there is no last kernel
+    c["w_pre"] = torch.ones_like(c["w_pre"])
+    g["w_pre"] = c["w_pre"].cuda()
+    with_w = bwd(g, "none", "rms")
+    without = dsv_residual_norm_bwd(g["dr"], g["dy"], g["r"], g["z"], gate=g["gate"], scale=g["scale"], **cut(g, "none", "rms")[1])
+    assert without[6] is None and torch.equal(with_w[0], without[0]) and torch.equal(with_w[1], without[1])
+    check_bwd(c, with_w, "none", "rms")
+    check_bwd(c, (*without[:6], with_w[6]), "none", "rms")
+
+
 @pytest.mark.parametrize("f32", [False, True])
 def test_vectors_that_are_not_there(f32):
     need_gpu()
