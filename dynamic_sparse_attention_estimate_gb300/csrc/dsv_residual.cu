@@ -10,7 +10,7 @@
 // Everything is fp32 from the loads on, with one rounding at each output.  The norm behind r reads r before its rounding to
 // the stream's type.
 //   Measured with the calls in a row: forward 520,192 x 2048, RMS norms, 1,376 us (6.2 TB/s, 0.93 of the copy rate), backward
-// 65,536 x 2048, RMS and layer norm, 278 us (5.8 TB/s, 0.87); simple kernels, a row loaded, summed and stored in turn, 2,681 and 670.
+// 65,536 x 2048, RMS and layer norm, 269 us (6.0 TB/s, 0.90); simple kernels, a row loaded, summed and stored in turn, 2,681 and 670.
 #include "dsv_block.h"
 #include "dsv_common.cuh"
 
@@ -395,6 +395,10 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan) {
 //   A row's passes read it from shared memory again, in bf16 as it came: held in registers in fp32 it would leave room for 12
 // warps instead of 16, and for eight where a row takes all of them (16,384 x 8192: 766 us
 // against 440 so, and 370 with rows in turn).
+//   A layer norm's deviations need the mean, which is a reduction away.  The first pass takes them from the mean p of a lane's own
+// eight features: with d = r - p and a = p - mean, sum (r - mean)^2 = sum d^2 + a (2 sum d + 8 a) and sum h (r - mean) =
+// sum h d + a sum h, with nothing large to cancel however far the row lies from 0, and no pass over the row
+// between the two reductions (65,536 x 2048, both norms, 277 to 269 us; 131,072 x 768, no branch norm, 197 to 186; 16,384 x 8192 370 to 378).
 constexpr int64_t kBwdCtas = 152;
 constexpr int sums_of(int pre) { return pre == kNormNone ? 1 : 3; }
 // Warps of a CTA: with an fp32 stream 12, whose two stages and factors fill shared memory, and 16 for rows that need more.
@@ -503,7 +507,9 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan) {
     float rz = 1.f, mean = 0.f;
     float2 k0 = both(0.f), k1 = both(0.f), k2 = both(0.f);   // of  g = dr + k2 h + k1 xhat + k0,  xhat = k2 (r - mean)
     if constexpr (POST || PRE != kNormNone) {
-      float2 a0 = both(0.f), a1 = both(0.f), a2 = both(0.f);   // sum z^2; layer: sum r, sum h; rms: sum r^2, sum h r
+      float2 a0 = both(0.f), a1 = both(0.f), a2 = both(0.f);   // sum z^2; layer: sum d^2, sum h d; rms: sum r^2, sum h r
+      float s1 = 0.f, s2 = 0.f;         // layer: sum r, sum h
+      float pivot[V], off[V], hs[V];    // layer, of each vector: the mean of its features, sum d, sum h
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         if (POST) {
@@ -513,14 +519,36 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan) {
         }
         if constexpr (PRE != kNormNone) {
           const Vec8 r = stream8(i, kR), h = h8(i, bf8(i, kDy));
+          if constexpr (PRE == kNormLayer) {
+            const float2 tr = add2(add2(r.v[0], r.v[1]), add2(r.v[2], r.v[3])), th = add2(add2(h.v[0], h.v[1]), add2(h.v[2], h.v[3]));
+            const float sr = tr.x + tr.y;
+            hs[i] = th.x + th.y;
+            s1 += sr;
+            s2 += hs[i];
+            pivot[i] = sr * (me.valid[i][1] ? 0.125f : 0.25f);
+            float2 e = both(0.f);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            a1 = PRE == kNormLayer ? add2(a1, r.v[j]) : fma2(r.v[j], r.v[j], a1);
-            a2 = PRE == kNormLayer ? add2(a2, h.v[j]) : fma2(h.v[j], r.v[j], a2);
+            for (int j = 0; j < 4; ++j) {
+              const float2 d = add2(r.v[j], both(me.valid[i][j / 2] ? -pivot[i] : 0.f));
+              e = add2(e, d);
+              a1 = fma2(d, d, a1);
+              a2 = fma2(h.v[j], d, a2);
+            }
+            off[i] = e.x + e.y;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              a1 = fma2(r.v[j], r.v[j], a1);
+              a2 = fma2(h.v[j], r.v[j], a2);
+            }
           }
         }
       }
-      float s0 = a0.x + a0.y, s1 = a1.x + a1.y, s2 = a2.x + a2.y;
+      float s0 = a0.x + a0.y;
+      if constexpr (PRE == kNormRms) {
+        s1 = a1.x + a1.y;
+        s2 = a2.x + a2.y;
+      }
       if constexpr (PRE == kNormNone) {
         float s[1] = {s0};
         sum(s);
@@ -543,18 +571,13 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan) {
         if constexpr (PRE == kNormLayer) {
           mean = mean_of(s1, D, inv_d);
           mh = s2 * inv_d;
-          a1 = a2 = both(0.f);          // sum (r - mean)^2, sum h (r - mean)
+          float s[2] = {a1.x + a1.y, a2.x + a2.y};   // sum (r - mean)^2, sum h (r - mean)
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            const Vec8 r = stream8(i, kR), h = h8(i, bf8(i, kDy));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 d = add2(r.v[j], both(me.valid[i][j / 2] ? -mean : 0.f));
-              a1 = fma2(d, d, a1);
-              a2 = fma2(h.v[j], d, a2);
-            }
+            const float a = pivot[i] - mean, n = me.valid[i][1] ? 8.f : me.valid[i][0] ? 4.f : 0.f;
+            s[0] = fmaf(a, fmaf(n, a, 2.f * off[i]), s[0]);
+            s[1] = fmaf(a, hs[i], s[1]);
           }
-          float s[2] = {a1.x + a1.y, a2.x + a2.y};
           sum(s);
           s1 = s[0];
           s2 = s[1];
