@@ -99,7 +99,7 @@ RowPlan row_plan(int64_t B, int64_t N, int64_t D, int64_t ctas, int warps) {
 // This thread's place: its row group, its warp and lane in it, its CTA's rows, and its features.  A vector of a warp is 256 features.
 // Of a bf16 stream a lane has eight neighbours of them (16 bytes); of an fp32 one four and, 128 further, four (16 bytes each), so
 // that a warp copies and stores 512 bytes in a row there too (with eight neighbours to a lane, whose halves two instructions
-// bring, 80,000 x 1536 took 235 us forward instead of 190).
+// bring, 80,000 x 1536 without norms took 241 us forward instead of 191).
 template <bool F32, int V>
 struct Place {
   int group, warp, lane;
