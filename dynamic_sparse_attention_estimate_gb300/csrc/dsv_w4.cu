@@ -11,7 +11,7 @@
 // nothing lost and without a shift: the integer pipe, which unpacks at half the rate of the others, is the busiest here.  The scale multiplies fp32 sums (forward) or the other operand (backward), with 64 in it.  Sums are fp32, with one
 // rounding at the output.
 //   Forward, 294,912 x 2048 and two vectors: 63 us, 5.1 TB/s (0.77 of the copy rate); two instructions in three clocks on every
-// scheduler, of which the unpacking is half.  Backward, 98,304 x 2048 and four vectors: 32 us, 3.4 TB/s; it unpacks with one more
+// scheduler, of which the unpacking is half.  Backward, 98,304 x 2048 and four vectors: 39 us, 2.8 TB/s; it unpacks with one more
 // permutation a pair and makes the other operand besides.
 #include <type_traits>
 
@@ -238,10 +238,12 @@ w4_fwd_kernel(W4Params p) {
 // and a run of rows in chunks of 256: two warps side by side, four below each other with 64 rows of a chunk each, the
 // next chunks on their way into shared memory.  In a step of 16 rows a lane (g, t) holds eight columns of rows t, t + 4, t + 8
 // and t + 12, pairs the rows, and product j of four is of two of its columns; the columns of a product are all of one group.
-//   The other operand, dy times the scale, is held as two bf16 numbers, the rounded value and what it left (16 bits: exact
-// for dy in bf16, 2^-16 of the value for fp32), in neighbouring columns of the tile, so that a lane's two sums of a row
-// add up to one result.  It is the same for all columns of a group, so the CTA makes it once a chunk in shared memory, in the
-// order in which the lanes take it.
+//   The other operand, dy times the scale, is held as bf16 numbers that add up to it: the rounded value and what it left, 16 bits
+// between them, which is all that a product of bf16 numbers has, in neighbouring columns of the tile, so that a lane's two sums
+// of a row add up to one result.  For dy in fp32 a third number holds the last eight bits of 24: it takes a second product,
+// onto the sums of the column of the rests (98,304 x 2048, four vectors: 39 us instead of 34 with some 17 bits, which left 18 of
+// 8192 outputs on the wrong side of their rounding; none is now).  The operand is the same for all columns of a group, so the CTA makes it once a chunk in
+// shared memory, in the order in which the lanes take it.
 //   The CTAs of one column block share the rows of W in `splits` runs, whose partial results w4_join_kernel adds in order.
 constexpr int kBwdColWarps = 2, kBwdRowWarps = 4, kBwdWarps = kBwdColWarps * kBwdRowWarps;
 constexpr int kBwdCols = 64 * kBwdColWarps, kBwdSteps = 4, kBwdRows = 16 * kBwdSteps * kBwdRowWarps, kQuads = kBwdRows / 4;
@@ -266,34 +268,41 @@ W4BwdPlan w4_bwd_plan(int64_t M, int64_t D, int64_t F, int group) {
   q.splits = (F + q.rows - 1) / q.rows;
   return q;
 }
-template <int G, int NT, bool ZERO>
+template <int G, int NT, bool ZERO, bool F32>
 constexpr int bwd_smem() {
-  constexpr int use = kBwdStages * kBwdStage + kBwdCols / G * kQuads * (NT * 64 + (ZERO ? 8 : 0));
+  constexpr int use = kBwdStages * kBwdStage + kBwdCols / G * kQuads * (NT * (F32 ? 96 : 64) + (ZERO ? 8 : 0));
   constexpr int red = kBwdRowWarps * 4 * NT * kBwdCols * 4;
   return use > red ? use : red;
 }
 
-// The rounded value of four rows' numbers and what it leaves, as bf16.  An infinite one leaves NaN, for which the maximum
-// takes -2^120, the least rest that there is: next to the infinity it is nothing.
-DSV_DEVICE uint4 split4(const float (&v)[4]) {
+// Four rows' numbers as N bf16 numbers each, every one the rounded value of what those before it leave: part k in 2 k and
+// 2 k + 1.  An infinite one leaves NaN, for which the maximum takes -2^120, the least rest that there is: next to the infinity it is
+// nothing.
+template <int N>
+DSV_DEVICE void split4(const float (&v)[4], uint32_t (&parts)[2 * N]) {
   const __nv_bfloat162 least = __float2bfloat162_rn(-0x1p120f);
-  uint32_t hi[2], lo[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    hi[h] = pack_bf16x2(v[2 * h], v[2 * h + 1]);
-    const __nv_bfloat162 r = __hmax2(__floats2bfloat162_rn(v[2 * h] - bf16_lo(hi[h]), v[2 * h + 1] - bf16_hi(hi[h])), least);
-    lo[h] = *reinterpret_cast<const uint32_t*>(&r);
+    float a = v[2 * h], b = v[2 * h + 1];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+      if (k) r = __hmax2(r, least);
+      parts[2 * k + h] = *reinterpret_cast<const uint32_t*>(&r);
+      a -= bf16_lo(parts[2 * k + h]);
+      b -= bf16_hi(parts[2 * k + h]);
+    }
   }
-  return make_uint4(hi[0], hi[1], lo[0], lo[1]);
 }
 
-template <int G, int NT, bool ZERO>
+template <int G, int NT, bool ZERO, bool F32>
 __global__ void __launch_bounds__(32 * kBwdWarps, bwd_ctas(G, NT))
 w4_bwd_kernel(W4Params p, W4BwdPlan plan) {
   constexpr int CG = kBwdCols / G;               // groups of the CTA's columns
-  extern __shared__ __align__(16) unsigned char shared[];   // the stages, the other operand, the zero points; then the warps' sums
+  extern __shared__ __align__(16) unsigned char shared[];   // the stages, the other operand and its third numbers, the zero points; then the warps' sums
   uint2(*const other)[NT][kQuads][8] = reinterpret_cast<uint2(*)[NT][kQuads][8]>(shared + kBwdStages * kBwdStage);   // [CG]
-  uint2(*const zeros)[kQuads] = reinterpret_cast<uint2(*)[kQuads]>(other + CG);
+  uint2(*const third)[NT][kQuads][4] = reinterpret_cast<uint2(*)[NT][kQuads][4]>(other + CG);                        // [CG] for dy in fp32
+  uint2(*const zeros)[kQuads] = reinterpret_cast<uint2(*)[kQuads]>(third + (F32 ? CG : 0));
   // the join kernel may be scheduled once every CTA has started; it waits for this grid before it reads
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -367,7 +376,7 @@ w4_bwd_kernel(W4Params p, W4BwdPlan plan) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) dys[n][i] = 0.f;
       if (n >= vectors) continue;
-      if (p.dy_f32) {
+      if constexpr (F32) {
         if (left == 16) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) dys[n][i] = __ldg(d32 + 4 * i);
@@ -416,7 +425,10 @@ w4_bwd_kernel(W4Params p, W4BwdPlan plan) {
         float b[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) b[i] = dys[n][i] * __uint_as_float(scales[i].get(q) << 16);
-        *reinterpret_cast<uint4*>(&other[q][n][own_quad][2 * own_v]) = split4(b);
+        uint32_t parts[F32 ? 6 : 4];
+        split4<F32 ? 3 : 2>(b, parts);
+        *reinterpret_cast<uint4*>(&other[q][n][own_quad][2 * own_v]) = make_uint4(parts[0], parts[1], parts[2], parts[3]);
+        if constexpr (F32) third[q][n][own_quad][own_v] = make_uint2(parts[4], parts[5]);
       }
     if (ZERO && own_v < CG)
       zeros[own_v][own_quad] = make_uint2(zero_of2(zero), zero_of2(zero >> 16));
@@ -448,23 +460,29 @@ w4_bwd_kernel(W4Params p, W4BwdPlan plan) {
           z01 = *reinterpret_cast<const __nv_bfloat162*>(&z.x);
           z23 = *reinterpret_cast<const __nv_bfloat162*>(&z.y);
         }
-        uint2 b[NT];
+        uint2 b[NT], b3[F32 ? NT : 1];           // the third numbers are in the columns of the rests, the odd ones
 #pragma unroll
-        for (int n = 0; n < NT; ++n) b[n] = other[group][n][quad][g];
+        for (int n = 0; n < NT; ++n) {
+          b[n] = other[group][n][quad][g];
+          if constexpr (F32) b3[n] = g & 1 ? third[group][n][quad][g / 2] : make_uint2(0, 0);
+        }
 #pragma unroll
         for (int j = G < 64 ? 2 * q : 0; j < (G < 64 ? 2 * q + 2 : 4); ++j) {
           const uint32_t pick = j * 0x0011u + (4 + j) * 0x1100u;   // byte j of either row
           const uint32_t p01 = __byte_perm(now[0], now[1], pick), p23 = __byte_perm(now[2], now[3], pick);
           const uint32_t frag[4] = {unpack_pair<false>(p01, z01), unpack_pair<true>(p01, z01), unpack_pair<false>(p23, z23), unpack_pair<true>(p23, z23)};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_bf16_16816(acc[n][j], frag, b[n].x, b[n].y);
+          for (int n = 0; n < NT; ++n) {
+            mma_bf16_16816(acc[n][j], frag, b[n].x, b[n].y);
+            if constexpr (F32) mma_bf16_16816(acc[n][j], frag, b3[n].x, b3[n].y);
+          }
         }
       }
     }
   }
   cp_async_wait<0>();
   __syncthreads();
-  // sums i = 0, 1 are product j's first column, 2, 3 its second; tile columns 2 t, 2 t + 1: value and rest of vector t
+  // sums i = 0, 1 are product j's first column, 2, 3 its second; tile columns 2 t, 2 t + 1: value and rests of vector t
   float(*const red)[4 * NT][kBwdCols] = reinterpret_cast<float(*)[4 * NT][kBwdCols]>(shared);
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -569,15 +587,19 @@ template <int G>
 cudaError_t fwd_group(const W4Params& p, cudaStream_t stream) {
   return p.M <= 8 ? fwd<G, 1>(p, stream) : p.M <= 16 ? fwd<G, 2>(p, stream) : fwd<G, 4>(p, stream);
 }
-template <int G, int NT, bool ZERO>
-cudaError_t bwd_zero(const W4Params& p, const W4BwdPlan& plan, cudaStream_t stream) {
-  constexpr int smem = bwd_smem<G, NT, ZERO>();
+template <int G, int NT, bool ZERO, bool F32>
+cudaError_t bwd_type(const W4Params& p, const W4BwdPlan& plan, cudaStream_t stream) {
+  constexpr int smem = bwd_smem<G, NT, ZERO, F32>();
   const dim3 grid(static_cast<unsigned>(plan.col_blocks), static_cast<unsigned>(plan.splits), static_cast<unsigned>((p.M + 4 * NT - 1) / (4 * NT)));
-  constexpr auto kernel = w4_bwd_kernel<G, NT, ZERO>;
+  constexpr auto kernel = w4_bwd_kernel<G, NT, ZERO, F32>;
   const cudaError_t e = allow_shared<kernel>(smem);
   if (e != cudaSuccess) return e;
   kernel<<<grid, 32 * kBwdWarps, smem, stream>>>(p, plan);
   return cudaGetLastError();
+}
+template <int G, int NT, bool ZERO>
+cudaError_t bwd_zero(const W4Params& p, const W4BwdPlan& plan, cudaStream_t stream) {
+  return p.dy_f32 ? bwd_type<G, NT, ZERO, true>(p, plan, stream) : bwd_type<G, NT, ZERO, false>(p, plan, stream);
 }
 template <int G, int NT>
 cudaError_t bwd(const W4Params& p, const W4BwdPlan& plan, cudaStream_t stream) {

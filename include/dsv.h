@@ -508,8 +508,8 @@ dsv_status dsv_residual_norm_bwd(const dsv_residual_dims* dims, const void* dr, 
  * data: uint8 [F][D / 2], q of column 2 i in the low four bits of byte i and of column 2 i + 1 in the high four;
  * scale: bf16 [F][D / group], finite; zero: uint8 [F][D / group], 0 .. 15 (its low four bits are read), or NULL: 8.
  * x, dx bf16 [M][D]; y bf16 [M][F]; bias bf16 [F] or NULL; dy [M][F], bf16 or, with dy_f32, fp32.  Contiguous.
- * Sums are fp32, with one rounding at the output.  Forward: products are exact.  Backward: dy * scale enters its products as
- * two bf16 numbers, which is exact for dy in bf16 and within 2^-16 of the value in fp32.
+ * Sums are fp32, with one rounding at the output.  Forward: products are exact.  Backward: dy * scale, rounded to fp32, enters
+ * its products as two (dy in bf16) or three (fp32) bf16 numbers that add up to it.
  * Bitwise reproducible.  Outputs must not overlap inputs.
  * Validation before any launch: 1 <= M <= 64; F >= 1; group 32, 64 or 128; D a multiple of group, D <= 2^20, F * D <= 2^40.
  */

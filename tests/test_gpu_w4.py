@@ -310,3 +310,30 @@ def test_refusals():
     with pytest.raises(DSVError, match="WORKSPACE"):
         dsv_w4_linear_bwd(dy, w, workspace=torch.zeros(8, dtype=torch.uint8, device="cuda"))
     assert dsv_last_device_status() == 0
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("M,F,G", [(1, 40, 32), (4, 300, 64), (4, 40, 32), (7, 300, 128), (8, 2000, 32), (8, 9000, 64), (13, 300, 64)])
+def test_a_gradient_in_32_bits_keeps_them(M, F, G, zeros):
+    """Pairs of rows with the same weights, a and d - a of 20 bits: what is left of them is d, which only their last bits hold.  All
+    numbers are whole multiples of a power of two, four pairs of 2^20 to a vector: every sum is below 2^23 of them and exact in fp32,
+    and so is the output, at most 4 x 3 of them."""
+    need_gpu()
+    D = 256
+    gen = torch.Generator().manual_seed(M + F + G)
+    c = case(M, D, F, G, zeros)
+    c["scale"] = torch.full((F, D // G), 0.25, dtype=BF16)
+    zero = c["zero"] if zeros else torch.full((F, D // G), 8, dtype=torch.uint8)
+    dy = torch.zeros(M, F)
+    for m in range(M):
+        for f in (2 * torch.randperm(F // 2, generator=gen)[:4]).tolist():
+            a = float(torch.randint(2 ** 19, 2 ** 20, (1,), generator=gen))
+            dy[m, f], dy[m, f + 1] = a, float(torch.randint(-3, 4, (1,), generator=gen)) - a
+    q = torch.randint(-1, 2, (F // 2, D), generator=gen).repeat_interleave(2, 0)   # the weight's difference from its zero point
+    zero[0::2] = zero[0::2].clamp(1, 14)
+    zero[1::2] = zero[0::2]
+    q = q + zero.repeat_interleave(G, 1)[:q.shape[0]]
+    c["data"] = torch.zeros(F, D // 2, dtype=torch.uint8)
+    c["data"][:q.shape[0]] = (q[:, 0::2] | q[:, 1::2] << 4).to(torch.uint8)
+    dx = dsv_w4_linear_bwd(dy.cuda(), weight(c))
+    assert np.array_equal(np64(dx), oracle.w4_linear_bwd(dy, c["data"], c["scale"], c["zero"]))
