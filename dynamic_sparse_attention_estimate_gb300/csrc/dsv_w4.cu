@@ -238,7 +238,7 @@ w4_fwd_kernel(W4Params p) {
 // and a run of rows in chunks of 256: two warps side by side, four below each other with 64 rows of a chunk each, the
 // next chunks on their way into shared memory.  In a step of 16 rows a lane (g, t) holds eight columns of rows t, t + 4, t + 8
 // and t + 12, pairs the rows, and product j of four is of two of its columns; the columns of a product are all of one group.
-//   The other operand, dy times the scale, is held as bf16 numbers that add up to it: the rounded value and what it left, 16 bits
+//   The other operand, dy times the scale, is held as bf16 numbers that add up to it: its first eight bits and the next, 16 bits
 // between them, which is all that a product of bf16 numbers has, in neighbouring columns of the tile, so that a lane's two sums
 // of a row add up to one result.  For dy in fp32 a third number holds the last eight bits of 24: it takes a second product,
 // onto the sums of the column of the rests (98,304 x 2048, four vectors: 39 us instead of 34 with some 17 bits, which left 18 of
@@ -275,9 +275,9 @@ constexpr int bwd_smem() {
   return use > red ? use : red;
 }
 
-// Four rows' numbers as N bf16 numbers each, every one the rounded value of what those before it leave: part k in 2 k and
-// 2 k + 1.  An infinite one leaves NaN, for which the maximum takes -2^120, the least rest that there is: next to the infinity it is
-// nothing.
+// Four rows' numbers as N bf16 numbers each, every one the upper half of what those before it leave (cut, not rounded: a
+// finite number stays finite however large it is, and N times eight bits are as many): part k in 2 k and 2 k + 1.  An infinite
+// one leaves NaN, for which the maximum takes -2^120, which is below every rest that there is: next to the infinity it is nothing.
 template <int N>
 DSV_DEVICE void split4(const float (&v)[4], uint32_t (&parts)[2 * N]) {
   const __nv_bfloat162 least = __float2bfloat162_rn(-0x1p120f);
@@ -286,11 +286,11 @@ DSV_DEVICE void split4(const float (&v)[4], uint32_t (&parts)[2 * N]) {
     float a = v[2 * h], b = v[2 * h + 1];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
-      if (k) r = __hmax2(r, least);
-      parts[2 * k + h] = *reinterpret_cast<const uint32_t*>(&r);
-      a -= bf16_lo(parts[2 * k + h]);
-      b -= bf16_hi(parts[2 * k + h]);
+      const uint32_t cut = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+      a -= bf16_lo(cut);
+      b -= bf16_hi(cut);
+      const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&cut), least);
+      parts[2 * k + h] = k ? *reinterpret_cast<const uint32_t*>(&r) : cut;
     }
   }
 }

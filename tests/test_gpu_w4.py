@@ -337,3 +337,20 @@ def test_a_gradient_in_32_bits_keeps_them(M, F, G, zeros):
     c["data"][:q.shape[0]] = (q[:, 0::2] | q[:, 1::2] << 4).to(torch.uint8)
     dx = dsv_w4_linear_bwd(dy.cuda(), weight(c))
     assert np.array_equal(np64(dx), oracle.w4_linear_bwd(dy, c["data"], c["scale"], c["zero"]))
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,G", [(2, 32), (2, 64), (4, 128), (9, 32), (9, 64)])
+def test_products_between_the_types_largest_numbers(M, G, dtype, sign):
+    """A gradient whose product with the scale, 1.9996 x 2^127, is finite in fp32 and rounds to infinity in bf16: times a weight of 0 it
+    is 0, times any other an output that rounds to infinity of its sign, as 64 bits have it.  The other rows are zeros."""
+    need_gpu()
+    c = case(M, 256, 70, G, True)
+    c["scale"] = torch.full((70, 256 // G), 181 * 2.0 ** 20, dtype=BF16)
+    dy = torch.zeros(M, 70, dtype=dtype)
+    dy[1, 37] = sign * 181 * 2.0 ** 93
+    exact = oracle.w4_linear_bwd(dy, c["data"], c["scale"], c["zero"])
+    assert 3.4e38 < np.abs(exact[exact != 0]).min() < 3.4028e38 and (exact[1] == 0).any()
+    dx = dsv_w4_linear_bwd(dy.cuda(), weight(c)).cpu()
+    assert torch.equal(dx, torch.from_numpy(exact).to(BF16))
