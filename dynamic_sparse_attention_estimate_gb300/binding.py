@@ -1032,6 +1032,7 @@ def dsv_w4_linear_fwd(x: torch.Tensor, w: W4Weight, bias: Optional[torch.Tensor]
 
 
 def dsv_w4_linear_bwd_workspace(M: int, D: int, F: int, group: int = 64) -> int:
+    """Bytes that are enough for dy of either type (fp32 takes as many runs of rows as bf16, or fewer)."""
     return _w4_dims(int(M), int(D), int(F), int(group), False)[1]
 
 

@@ -1375,7 +1375,7 @@ dsv_status dsv_w4_linear_fwd(const dsv_w4_dims* dims, const void* x, const uint8
 
 size_t dsv_w4_linear_bwd_workspace(const dsv_w4_dims* dims) {
   if (check_w4(dims, true) != DSV_OK) return 0;
-  return up(dsv::w4_bwd_workspace(dims->M, dims->D, dims->F, dims->group));
+  return up(dsv::w4_bwd_workspace(dims->M, dims->D, dims->F, dims->group, dims->dy_f32 != 0));
 }
 
 dsv_status dsv_w4_linear_bwd(const dsv_w4_dims* dims, const void* dy, const uint8_t* data, const void* scale,

@@ -124,7 +124,7 @@ struct W4Params {
   bf16* dx;                             // [M][D] (backward)
   float* partial;                       // w4_bwd_workspace bytes (backward)
 };
-size_t w4_bwd_workspace(int64_t M, int64_t D, int64_t F, int group);
+size_t w4_bwd_workspace(int64_t M, int64_t D, int64_t F, int group, bool dy_f32);
 cudaError_t launch_w4_quantize(const W4Params& p, cudaStream_t stream);
 cudaError_t launch_w4_fwd(const W4Params& p, cudaStream_t stream);
 cudaError_t launch_w4_bwd(const W4Params& p, cudaStream_t stream);

@@ -253,14 +253,16 @@ constexpr int kBwdStage = kBwdRows * kBwdCols / 2, kBwdStages = 3;
 struct W4BwdPlan {
   int64_t col_blocks, splits, rows;     // rows of W to a CTA, a multiple of kBwdRows
 };
-// CTAs of an SM at a time: the registers of two tiles of vectors with two groups a warp leave room for two.
-constexpr int bwd_ctas(int group, int tiles) { return tiles == 2 && group < 64 ? 2 : 3; }
+// CTAs of an SM at a time.  Two tiles of vectors, two groups a warp and a third number each take registers (and shared memory, which
+// L1 then lacks): any two of them leave room for two (98,304 x 2048, dy in fp32: eight vectors, groups of 64, 66 us with three CTAs and
+// 55 with two, four vectors, groups of 32, 60 and 52; dy in bf16, groups of 64, the other way round: 48 and 55).
+constexpr int bwd_ctas(int group, int tiles, bool f32) { return (tiles == 2) + (group < 64) + f32 > 1 ? 2 : 3; }
 // Runs so that all SMs have their CTAs at a time; passes over more than eight vectors follow one another (as many runs fewer left
 // SMs idle: 32 vectors 306 us instead of 279).
-W4BwdPlan w4_bwd_plan(int64_t M, int64_t D, int64_t F, int group) {
+W4BwdPlan w4_bwd_plan(int64_t M, int64_t D, int64_t F, int group, bool f32) {
   W4BwdPlan q;
   q.col_blocks = (D + kBwdCols - 1) / kBwdCols;
-  q.splits = bwd_ctas(group, M > 4 ? 2 : 1) * 152 / q.col_blocks;
+  q.splits = bwd_ctas(group, M > 4 ? 2 : 1, f32) * 152 / q.col_blocks;
   const int64_t most = (F + kBwdRows - 1) / kBwdRows;
   if (q.splits > most) q.splits = most;
   if (q.splits < 1) q.splits = 1;
@@ -296,7 +298,7 @@ DSV_DEVICE void split4(const float (&v)[4], uint32_t (&parts)[2 * N]) {
 }
 
 template <int G, int NT, bool ZERO, bool F32>
-__global__ void __launch_bounds__(32 * kBwdWarps, bwd_ctas(G, NT))
+__global__ void __launch_bounds__(32 * kBwdWarps, bwd_ctas(G, NT, F32))
 w4_bwd_kernel(W4Params p, W4BwdPlan plan) {
   constexpr int CG = kBwdCols / G;               // groups of the CTA's columns
   extern __shared__ __align__(16) unsigned char shared[];   // the stages, the other operand and its third numbers, the zero points; then the warps' sums
@@ -612,8 +614,8 @@ cudaError_t bwd_group(const W4Params& p, const W4BwdPlan& plan, cudaStream_t str
 
 }  // namespace
 
-size_t w4_bwd_workspace(int64_t M, int64_t D, int64_t F, int group) {
-  return static_cast<size_t>(w4_bwd_plan(M, D, F, group).splits * M * D) * sizeof(float);
+size_t w4_bwd_workspace(int64_t M, int64_t D, int64_t F, int group, bool dy_f32) {
+  return static_cast<size_t>(w4_bwd_plan(M, D, F, group, dy_f32).splits * M * D) * sizeof(float);
 }
 
 cudaError_t launch_w4_fwd(const W4Params& p, cudaStream_t stream) {
@@ -622,7 +624,7 @@ cudaError_t launch_w4_fwd(const W4Params& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_w4_bwd(const W4Params& p, cudaStream_t stream) {
-  const W4BwdPlan plan = w4_bwd_plan(p.M, p.D, p.F, p.group);
+  const W4BwdPlan plan = w4_bwd_plan(p.M, p.D, p.F, p.group, p.dy_f32);
   {
     ProfScope prof("w4_linear_bwd", stream);
     const cudaError_t e = p.group == 32 ? bwd_group<32>(p, plan, stream) : p.group == 64 ? bwd_group<64>(p, plan, stream)
