@@ -165,9 +165,13 @@ struct Place {
   }
 };
 
-// Sums over a row.  The W warps of a row meet at a barrier of their own (1 + group).
+// Sums over a row.  The W warps of a row meet at a barrier of their own (1 + group).  HALVES: of two sums over more than four warps
+// each half of the lanes adds up one (forward, both norms, 16,384 x 8192 168 us against 185, 32,768 x 4096 164 against 170; in the
+// backward 65,536 x 2048 took 259 instead of 270 and 131,072 x 768 194 instead of 187, which have four and two warps a row: how the
+// compiler places the rest; it stays as it was).
 constexpr int kSums = 3;
 constexpr int kRedFloats = 2 * kSums * kMaxWarps;   // of a row group
+template <bool HALVES>
 struct RowSums {
   int W, group, warp, lane, turn;
   float* red;                           // [2][kSums][kMaxWarps] of the group, zero from W on
@@ -201,28 +205,49 @@ struct RowSums {
     turn ^= 1;
     if (lane == 0 || (K > 1 && lane == 16) || (K > 2 && lane == 8)) buf[(lane == 16 ? 1 : lane == 8 ? 2 : 0) * kMaxWarps + warp] = v;
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * W) : "memory");
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-      const float4* p = reinterpret_cast<const float4*>(buf + i * kMaxWarps);
+    auto warps = [&](int k) {             // the warps' parts of sum k
+      const float4* p = reinterpret_cast<const float4*>(buf + k * kMaxWarps);
       float4 t = p[0];
       float2 a = add2(make_float2(t.x, t.y), make_float2(t.z, t.w));
       for (int w = 4; w < W; w += 4) {
         t = p[w / 4];
         a = add2(a, add2(make_float2(t.x, t.y), make_float2(t.z, t.w)));
       }
-      s[i] = a.x + a.y;
+      return a.x + a.y;
+    };
+    if constexpr (HALVES && K == 2) {
+      if (W > 4) {
+        const float mine = warps(lane >> 4), other = __shfl_xor_sync(kAll, mine, 16);
+        s[0] = lane & 16 ? other : mine;
+        s[1] = lane & 16 ? mine : other;
+        return;
+      }
     }
+#pragma unroll
+    for (int i = 0; i < K; ++i) s[i] = warps(i);
   }
 };
-// s / D to the last bit wherever that is a number of fp32 (so that a constant row's deviations are 0), without a division.
+// s / D to the last bit wherever that is a number of fp32, without a division.
 DSV_DEVICE float mean_of(float s, float D, float inv_d) {
   const float m = s * inv_d;
   return fmaf(fmaf(-m, D, s), inv_d, m);
 }
-DSV_DEVICE RowSums row_sums(const RowPlan& plan, float* red, int group, int warp, int lane) {
+// A layer norm's mean is only as exact as the sum over the row: rounded, it can be some last bits of the features off, which in a
+// row far from 0 with little spread is much of the spread (of a constant row of 1000.1, 768 features, it made xhat 0.06
+// instead of 0).  So the deviations d from that mean are summed too, beside their squares: their own mean is what it is off by, and
+// (sum d^2) / D - off^2 is the variance, in which nothing large cancels: off is a few roundings of the mean.
+struct Spread {
+  float off, rstd;
+};
+DSV_DEVICE Spread spread_of(float d, float dd, float D, float inv_d, float eps) {
+  const float off = mean_of(d, D, inv_d), var = fmaf(-off, off, dd * inv_d);
+  return Spread{off, rsqrtf((var < 0.f ? 0.f : var) + eps)};   // a variance that is NaN stays so
+}
+template <bool HALVES>
+DSV_DEVICE RowSums<HALVES> row_sums(const RowPlan& plan, float* red, int group, int warp, int lane) {
   for (int i = threadIdx.x; i < 15 * kRedFloats; i += blockDim.x) red[i] = 0.f;
   __syncthreads();
-  return RowSums{plan.W, group, warp, lane, 0, red + group * kRedFloats};
+  return RowSums<HALVES>{plan.W, group, warp, lane, 0, red + group * kRedFloats};
 }
 
 // A row's features on their way: S stages of P 16-byte parts for each vector of a thread in shared memory.  Parts of the stream
@@ -291,7 +316,7 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan) {
   __shared__ __align__(16) float red[15 * kRedFloats];
   constexpr int SP = Stream<F32>::kParts, P = SP + 1, S = kFwdStages;
   const Place<F32, V> me(plan, p.N);
-  RowSums sum = row_sums(plan, red, me.group, me.warp, me.lane);
+  RowSums<true> sum = row_sums<true>(plan, red, me.group, me.warp, me.lane);
   const Ring<F32, P, V, S> ring(ring_mem);
   const float D = static_cast<float>(p.D), inv_d = 1.f / D;
 
@@ -387,25 +412,35 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan) {
         s[0] = a.x + a.y;
         sum(s);
       }
+      float2 rstd, shifted = both(0.f);
       if constexpr (PRE == kNormLayer) {
         const float mean = mean_of(s[0], D, inv_d);
+        float2 e = both(0.f);
         a = both(0.f);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             r[i].v[j] = add2(r[i].v[j], both(me.valid[i][j / 2] ? -mean : 0.f));
+            e = add2(e, r[i].v[j]);
             a = fma2(r[i].v[j], r[i].v[j], a);
           }
         }
-        s[0] = a.x + a.y;
-        sum(s);
+        float s2[2] = {e.x + e.y, a.x + a.y};
+        sum(s2);
+        const Spread t = spread_of(s2[0], s2[1], D, inv_d, p.eps);
+        rstd = both(t.rstd);
+        shifted = both(-t.off * t.rstd);
+      } else {
+        rstd = both(rsqrtf(s[0] * inv_d + p.eps));
       }
-      const float2 rstd = both(rsqrtf(s[0] * inv_d + p.eps));
 #pragma unroll
       for (int i = 0; i < V; ++i) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r[i].v[j] = fma2(mul2(r[i].v[j], rstd), f[i].v[j], sh[i].v[j]);
+        for (int j = 0; j < 4; ++j) {
+          const float2 xh = PRE == kNormLayer ? fma2(r[i].v[j], rstd, shifted) : mul2(r[i].v[j], rstd);
+          r[i].v[j] = fma2(xh, f[i].v[j], sh[i].v[j]);
+        }
         me.store(p.y, row, i, r[i]);
       }
     }
@@ -425,6 +460,10 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan) {
 // eight features: with d = r - p and a = p - mean, sum (r - mean)^2 = sum d^2 + a (2 sum d + 8 a) and sum h (r - mean) =
 // sum h d + a sum h, with nothing large to cancel however far the row lies from 0, and no pass over the row
 // between the two reductions (65,536 x 2048, both norms, 277 to 269 us; 131,072 x 768, no branch norm, 197 to 186; 16,384 x 8192 370 to 378).
+//   Of an fp32 stream the second reduction also sums r - mean, whose own mean is taken off (spread_of; 80,000 x 1536, both norms, 351 us
+// instead of 366, 3 x 3,645 x 1160 60 instead of 57).  A bf16 stream needs that in the forward alone, whose rows are new in fp32:
+// its features have eight bits, so that up to 8192 of them within a factor of eight add up exactly, and of others the sum's roundings are
+// 2^-11 of the spread at most (with that sum all the same 65,536 x 2048 took 293 us).
 constexpr int64_t kBwdCtas = 152;
 constexpr int sums_of(int pre) { return pre == kNormNone ? 1 : 3; }
 // Warps of a CTA: with an fp32 stream 12, whose two stages and factors fill shared memory, and 16 for rows that need more.
@@ -450,11 +489,12 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan) {
   __shared__ __align__(16) float red[15 * kRedFloats];
   constexpr int SP = Stream<F32>::kParts, P = PRE == kNormNone ? SP + 1 : 2 * SP + 2, S = bwd_stages<P>();
   constexpr int K = PRE == kNormNone ? 1 : 3;
+  constexpr bool kCentred = F32 && PRE == kNormLayer;           // the deviations' own mean is taken off them
   constexpr int kDr = 0, kZ = SP, kDy = SP + 1, kR = SP + 2;    // parts of a vector
   // the kernel of the sums may be scheduled once every CTA has started; it waits for this grid before it reads
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const Place<F32, V> me(plan, p.N);
-  RowSums sum = row_sums(plan, red, me.group, me.warp, me.lane);
+  RowSums<false> sum = row_sums<false>(plan, red, me.group, me.warp, me.lane);
   const Ring<F32, P, V, S> ring(ring_mem);
   const float D = static_cast<float>(p.D), inv_d = 1.f / D;
 
@@ -531,7 +571,7 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan) {
     };
 
     float rz = 1.f, mean = 0.f;
-    float2 k0 = both(0.f), k1 = both(0.f), k2 = both(0.f);   // of  g = dr + k2 h + k1 xhat + k0,  xhat = k2 (r - mean)
+    float2 k0 = both(0.f), k1 = both(0.f), k2 = both(0.f), k3 = both(0.f);   // of  g = dr + k2 h + k1 xhat + k0,  xhat = k2 (r - mean) + k3
     if constexpr (POST || PRE != kNormNone) {
       float2 a0 = both(0.f), a1 = both(0.f), a2 = both(0.f);   // sum z^2; layer: sum d^2, sum h d; rms: sum r^2, sum h r
       float s1 = 0.f, s2 = 0.f;         // layer: sum r, sum h
@@ -593,22 +633,31 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan) {
       }
       if (POST) rz = rsqrtf(s0 * inv_d + p.eps);
       if constexpr (PRE != kNormNone) {
-        float mh = 0.f;                 // mean h
+        float mh = 0.f, rstd;           // mean h
         if constexpr (PRE == kNormLayer) {
           mean = mean_of(s1, D, inv_d);
           mh = s2 * inv_d;
-          float s[2] = {a1.x + a1.y, a2.x + a2.y};   // sum (r - mean)^2, sum h (r - mean)
+          float s[kCentred ? 3 : 2] = {a1.x + a1.y, a2.x + a2.y};   // sums of (r - mean)^2, h (r - mean) and r - mean
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             const float a = pivot[i] - mean, n = me.valid[i][1] ? 8.f : me.valid[i][0] ? 4.f : 0.f;
             s[0] = fmaf(a, fmaf(n, a, 2.f * off[i]), s[0]);
             s[1] = fmaf(a, hs[i], s[1]);
+            if constexpr (kCentred) s[2] += fmaf(n, a, off[i]);
           }
           sum(s);
           s1 = s[0];
-          s2 = s[1];
+          if constexpr (kCentred) {
+            const Spread t = spread_of(s[2], s1, D, inv_d, p.eps);
+            rstd = t.rstd;
+            k3 = both(-t.off * rstd);
+            s2 = fmaf(-t.off, s2, s[1]);
+          } else {
+            s2 = s[1];
+          }
         }
-        const float rstd = rsqrtf(s1 * inv_d + p.eps), mhx = rstd * s2 * inv_d;   // mean(h xhat)
+        if constexpr (!kCentred) rstd = rsqrtf(s1 * inv_d + p.eps);
+        const float mhx = rstd * s2 * inv_d;   // mean(h xhat)
         k0 = both(-rstd * mh);
         k1 = both(-rstd * mhx);
         k2 = both(rstd);
@@ -623,7 +672,7 @@ residual_norm_bwd_kernel(ResidualParams p, RowPlan plan) {
         const Vec8 dy = bf8(i, kDy), h = h8(i, dy), r = stream8(i, kR);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 xh = mul2(PRE == kNormLayer ? add2(r.v[j], both(-mean)) : r.v[j], k2);
+          const float2 d = PRE == kNormLayer ? add2(r.v[j], both(-mean)) : r.v[j], xh = kCentred ? fma2(d, k2, k3) : mul2(d, k2);
           g.v[j] = add2(g.v[j], fma2(k2, h.v[j], fma2(k1, xh, k0)));
           acc[K - 2][i].v[j] = fma2(dy.v[j], xh, acc[K - 2][i].v[j]);
           acc[K - 1][i].v[j] = add2(acc[K - 1][i].v[j], dy.v[j]);

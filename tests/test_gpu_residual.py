@@ -499,3 +499,79 @@ def test_refusals():
     with pytest.raises(ValueError, match="post must"):
         dsv_residual_norm_fwd(g["x"], g["z"], post="layer")
     assert dsv_last_device_status() == 0
+
+
+def far_terms(r):
+    """(xhat, rstd, the errors of c = r - mean r, of rstd (relative)) of a layer norm of fp32 rows r, however far from 0 they lie.  The
+    rounded mean is off by at most far = G mean|r|; the deviations d from it, |d| <= |c| + far, are off by u |d|, their own mean, which
+    is taken off them, by G mean|d|:  dc = G (mean|c| + far) + 3 u (|c| + far).  mean d^2 is off by (G + 2 u) (var + far^2) and the
+    square of d's mean by 2 far G (mean|c| + far) + 2 u far^2, so that rho = (twice G (var + far^2) + 2 far G (mean|c| + far)) /
+    (var + eps) + G covers rstd, which has half of it."""
+    c = r - mean(r)
+    far, var = G * mean(np.abs(r)), mean(c * c)
+    dc = G * (mean(np.abs(c)) + far) + 3 * U * (np.abs(c) + far)
+    rho = (2 * G * (var + far * far) + 2 * far * G * (mean(np.abs(c)) + far)) / (var + EPS) + G
+    return c / np.sqrt(var + EPS), 1 / np.sqrt(var + EPS), dc, rho
+
+
+# sums of D equal numbers that are not exact; with a spread of a few last bits; a bf16 stream whose new rows lie between its numbers
+@pytest.mark.parametrize("far,spread", [(0.1, 0.0), (10.1, 0.0), (1000.1, 0.0), (10.1, 1e-5), (1000.1, 1e-3), (-30000.7, 1e-2)])
+@pytest.mark.parametrize("D", [8, 520, 768, 1160, 1536, 5128, 7000])
+def test_rows_far_from_zero_with_little_spread(D, far, spread):
+    need_gpu()
+    B, N = 2, 9
+    c = case(B, N, D, f32=True)
+    c["x"] = (far + spread * c["x"].double()).float()
+    c["r"], c["z"] = c["x"], torch.zeros_like(c["z"])
+    xhat, rstd, dc, rho = far_terms(np64(c["x"]))
+    w, f = np.abs(np64(c["w_pre"])), ((1 + np64(c["scale"])) * np64(c["w_pre"]))[:, None]
+    dxh = rstd * dc + np.abs(xhat) * (rho + 2 * U)
+    for shift in (c["shift"], torch.zeros_like(c["shift"])):       # without it the smallest xhat shows
+        c["shift"] = shift
+        v, how = cut(c, "none", "layer")
+        y = oracle.residual_norm_fwd(c["x"], c["z"], **v, **how)[1]
+        got = fwd(on_gpu(c), "none", "layer")
+        assert torch.equal(got[0].cpu(), c["x"])
+        check("y", got[1], y, np.abs(f) * dxh + 8 * U * (np.abs(f * xhat) + np.abs(np64(shift))[:, None] + np.abs(y)) + 2.0 ** -8 * np.abs(y))
+    v.pop("shift")
+    ref, got = oracle.residual_norm_bwd(c["dr"], c["dy"], c["r"], c["z"], **v, **how), bwd(on_gpu(c), "none", "layer")
+    dy = np64(c["dy"])
+    h = dy * f
+    mh, m = mean(h), mean(h * xhat)
+    # sum h (r - mean) is sum h d less the mean of d times sum h: each is off by as much as dc
+    dmh, dm = (G + 4 * U) * mean(np.abs(h)), 2 * mean(np.abs(h) * dxh) + (G + rho + 8 * U) * mean(np.abs(h * xhat))
+    dg = rstd * (3 * U * np.abs(h) + dmh + dxh * np.abs(m) + np.abs(xhat) * dm + (np.abs(h) + np.abs(mh) + np.abs(xhat * m)) * (rho + 8 * U))
+    check("dx", got[0], ref[0], dg + 3 * U * (np.abs(np64(c["dr"])) + np.abs(ref[0])))
+    T, dT, rows = np.abs(dy * xhat), np.abs(dy) * dxh, (N + 40) * U
+    check("d_scale", got[4], ref[4], w * (dT.sum(1) + (rows + 8 * U) * T.sum(1)))
+    check("dw_pre", got[6], ref[6], (np.abs(1 + np64(c["scale"]))[:, None] * (dT + (B * rows + 8 * U) * T)).sum((0, 1)))
+
+
+@pytest.mark.parametrize("D", [520, 768, 5128])
+def test_constant_rows_between_the_streams_numbers(D):
+    """A bf16 stream of 1000 and a branch of 0.1: the new rows, whose norm is taken before their rounding, are constant in fp32."""
+    need_gpu()
+    c = case(1, 5, D)
+    c["x"], c["z"], c["gate"] = torch.full_like(c["x"], 1000.0), torch.full_like(c["z"], 0.1), torch.ones_like(c["gate"])
+    c["shift"] = torch.zeros_like(c["shift"])
+    y = np64(fwd(on_gpu(c), "none", "layer")[1])
+    f = np.abs((1 + np64(c["scale"])) * np64(c["w_pre"]))[:, None]
+    # r is 1000 and alpha gate z, rounded once: the same number in every feature
+    xhat, rstd, dc, rho = far_terms(np.full((1, 1, 1), 1000.0 + 0.75 * float(c["z"][0, 0, 0])))
+    assert (np.abs(y) <= f * rstd * dc * (1 + 2.0 ** -8) * (1 + 8 * U)).all()
+
+
+@pytest.mark.parametrize("far", [1000.0, 0.1, -30000.0])
+@pytest.mark.parametrize("D", [8, 520, 1160, 8192])
+def test_the_gradient_of_constant_rows_of_a_bf16_stream(D, far):
+    """Up to 8192 equal numbers of eight bits add up exactly in 24: xhat is 0, and with it d_scale and dw_pre, and the gradient
+    is dr + rstd (h - mean h), with rstd = eps^-1/2."""
+    need_gpu()
+    c = case(2, 7, D)
+    c["r"] = torch.full_like(c["r"], far)
+    got = bwd(on_gpu(c), "none", "layer")
+    assert not got[4].any() and not got[6].any()
+    h, dr = np64(c["dy"]) * ((1 + np64(c["scale"])) * np64(c["w_pre"]))[:, None], np64(c["dr"])
+    rstd, want = EPS ** -0.5, np64(c["dr"]) + (h - mean(h)) * EPS ** -0.5
+    bound = rstd * (3 * U * np.abs(h) + (G + 4 * U) * mean(np.abs(h)) + 16 * U * (np.abs(h) + np.abs(mean(h)))) + 2 * U * (np.abs(dr) + np.abs(want))
+    check("dx", got[0], want, bound + 2.0 ** -8 * np.abs(want))
