@@ -354,3 +354,27 @@ def test_products_between_the_types_largest_numbers(M, G, dtype, sign):
     assert 3.4e38 < np.abs(exact[exact != 0]).min() < 3.4028e38 and (exact[1] == 0).any()
     dx = dsv_w4_linear_bwd(dy.cuda(), weight(c)).cpu()
     assert torch.equal(dx, torch.from_numpy(exact).to(BF16))
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("M", [8, 12, 33])
+@pytest.mark.parametrize("D,G", [(128, 32), (160, 32), (384, 64), (320, 64), (256, 128), (640, 128)])
+def test_forward_of_many_rows(M, D, G, zeros):
+    """From 9728 rows on a CTA takes 32 of them: each group and tile of vectors, columns that fill their chunks (or end in one), and a
+    last CTA of three rows."""
+    need_gpu()
+    c = case(M, D, 9731, G, zeros)
+    check_fwd(c, dsv_w4_linear_fwd(c["x"].cuda(), weight(c), c["bias"].cuda()))
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("M", [3, 8, 11])
+@pytest.mark.parametrize("D,F,G", [(8192, 9100, 32), (8192, 9001, 64), (8192, 9300, 128), (8160, 4500, 32)])
+def test_backward_of_long_runs_of_rows(M, D, F, G, zeros):
+    """64 blocks of 128 columns leave four to seven runs of rows, of five to ten chunks of 256 rows (the last shape: three, five): each of a
+    CTA's three stages is read and filled again, with every row's gradient in the sums."""
+    need_gpu()
+    c = case(M, D, F, G, zeros)
+    w = weight(c)
+    for dy in (c["dy"], c["dy"].to(BF16)):
+        check_bwd(c, dsv_w4_linear_bwd(dy.cuda(), w), dy)
