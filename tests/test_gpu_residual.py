@@ -575,3 +575,40 @@ def test_the_gradient_of_constant_rows_of_a_bf16_stream(D, far):
     rstd, want = EPS ** -0.5, np64(c["dr"]) + (h - mean(h)) * EPS ** -0.5
     bound = rstd * (3 * U * np.abs(h) + (G + 4 * U) * mean(np.abs(h)) + 16 * U * (np.abs(h) + np.abs(mean(h)))) + 2 * U * (np.abs(dr) + np.abs(want))
     check("dx", got[0], want, bound + 2.0 ** -8 * np.abs(want))
+
+
+@pytest.mark.parametrize("N,D,norms", [(470, 6152, NORMS), (780, 8192, [("rms", "layer"), ("none", "rms")])])
+def test_long_rows_of_an_fp32_stream_in_turn(N, D, norms):
+    """Rows of 13 to 16 warps: a CTA has one at a time and three to six in turn, so that both stages are filled again and the vectors'
+    sums are of several rows."""
+    need_gpu()
+    c = case(1, N, D, f32=True)
+    g = on_gpu(c)
+    for post, pre in norms:
+        check_fwd(c, fwd(g, post, pre), post, pre)
+        check_bwd(c, bwd(g, post, pre), post, pre)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("B,N,D", [(80, 400, 264), (6, 700, 128), (5, 2000, 40), (1, 3500, 1032), (3, 900, 2048)])
+def test_vectors_gradients_by_their_own_rows(B, N, D, f32):
+    """d_gate, d_scale and d_shift are sums over the N rows of a sample: (N + 40) roundings, whatever B is.  And by their norm: N random
+    additions leave u sqrt(N / 6) times the root of the terms' squares, the terms' own errors, up to G = 40 u of each and another in
+    every row, G times it."""
+    need_gpu()
+    c = case(B, N, D, f32)
+    v, how = cut(c, "rms", "layer")
+    v.pop("shift")
+    got = bwd(on_gpu(c), "rms", "layer")
+    ref = oracle.residual_norm_bwd(c["dr"], c["dy"], c["r"], c["z"], **v, **how)
+    dy, z, w = np64(c["dy"]), np64(c["z"]), np.abs(np64(c["w_pre"]))
+    xhat, rstd, dc, rho = norm_terms(np64(c["r"]), 0 * z, "layer")
+    T, dT = dy * xhat, np.abs(dy) * (rstd * dc + np.abs(xhat) * (rho + 2 * U))
+    S = ref[0] * z / np.sqrt(mean(z * z) + EPS)
+    u, rows = 0.75 * np.abs(np64(c["w_post"])), (N + 40) * U
+    check("d_scale", got[4], ref[4], w * (dT.sum(1) + (rows + 8 * U) * np.abs(T).sum(1)))
+    check("d_shift", got[5], ref[5], rows * np.abs(dy).sum(1))
+    for name, i, terms in (("d_gate", 2, u * S), ("d_scale", 4, w * T), ("d_shift", 5, dy)):
+        err, size = np64(got[i]) - ref[i], np.sqrt((terms * terms).sum(1))
+        rel = float(np.linalg.norm(err) / np.linalg.norm(size))
+        assert rel <= (N / 6) ** 0.5 * U + G, f"{name}: {rel:.3e}"
