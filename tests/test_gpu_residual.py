@@ -612,3 +612,29 @@ def test_vectors_gradients_by_their_own_rows(B, N, D, f32):
         err, size = np64(got[i]) - ref[i], np.sqrt((terms * terms).sum(1))
         rel = float(np.linalg.norm(err) / np.linalg.norm(size))
         assert rel <= (N / 6) ** 0.5 * U + G, f"{name}: {rel:.3e}"
+
+
+@pytest.mark.parametrize("post,pre", [("none", "layer"), ("rms", "layer"), ("none", "rms")])
+@pytest.mark.parametrize("D", [264, 2048])
+def test_the_gradient_of_the_forwards_own_bf16_stream(D, post, pre):
+    """y is the norm of r before its rounding, and the backward takes r as it was stored: against the gradient at the r before its
+    rounding it is off by what 2^-8 |r| does to the row's norm (to first order; the second, of the size of rho, four times in front)."""
+    need_gpu()
+    c = case(2, 70, D)
+    g = on_gpu(c)
+    v, how = cut(c, post, pre)
+    r = oracle.residual_norm_fwd(c["x"], c["z"], **v, **how)[0]
+    v.pop("shift")
+    g["r"] = fwd(g, post, pre)[0]
+    got, ref = bwd(g, post, pre), oracle.residual_norm_bwd(c["dr"], c["dy"], r, c["z"], **v, **how)
+    dy, f, w = np64(c["dy"]), ((1 + np64(c["scale"])) * np64(c["w_pre"]))[:, None], np.abs(np64(c["w_pre"]))
+    # the stored r: half a step, of a number that fp32 has rounded before
+    xhat, rstd, dc, rho = norm_terms(r, 2.0 ** -8 * np.abs(r) + G * np.abs(r - np64(c["x"])) + 8 * U * np.abs(r), pre)
+    dxh, h, room = rstd * dc + np.abs(xhat) * (rho + 2 * U), dy * f, 1 + 4 * float(rho.max())
+    mh, m = mean(h) if pre == "layer" else 0 * rstd, mean(h * xhat)
+    dmh = (G + 4 * U) * mean(np.abs(h)) if pre == "layer" else 0
+    dm = mean(np.abs(h) * dxh) + (G + rho + 8 * U) * mean(np.abs(h * xhat))
+    dg = rstd * (3 * U * np.abs(h) + dmh + dxh * np.abs(m) + np.abs(xhat) * dm + (np.abs(h) + np.abs(mh) + np.abs(xhat * m)) * (rho + 8 * U))
+    check("dx", got[0], ref[0], room * dg + 2 * U * np.abs(np64(c["dr"])) + (2.0 ** -8 + 2 * U) * (np.abs(ref[0]) + room * dg))
+    T, dT, rows = np.abs(dy * xhat), np.abs(dy) * dxh, (70 + 40) * U
+    check("d_scale", got[4], ref[4], w * (room * dT.sum(1) + (rows + 8 * U) * (T + dT).sum(1)))
