@@ -455,11 +455,11 @@ residual_norm_fwd_kernel(ResidualParams p, RowPlan plan) {
 // sums, its row groups added in order, are one partial row.
 //   A row's passes read it from shared memory again, in bf16 as it came: held in registers in fp32 it would leave room for 12
 // warps instead of 16, and for eight where a row takes all of them (16,384 x 8192: 766 us
-// against 440 so, and 370 with rows in turn).
+// against 440 so, 370 with rows in turn then, and 379 now with the next paragraph's sums).
 //   A layer norm's deviations need the mean, which is a reduction away.  The first pass takes them from the mean p of a lane's own
 // eight features: with d = r - p and a = p - mean, sum (r - mean)^2 = sum d^2 + a (2 sum d + 8 a) and sum h (r - mean) =
 // sum h d + a sum h, with nothing large to cancel however far the row lies from 0, and no pass over the row
-// between the two reductions (65,536 x 2048, both norms, 277 to 269 us; 131,072 x 768, no branch norm, 197 to 186; 16,384 x 8192 370 to 378).
+// between the two reductions (65,536 x 2048, both norms, 277 to 269 us; 131,072 x 768, no branch norm, 197 to 186; 16,384 x 8192 370 to 379).
 //   Of an fp32 stream the second reduction also sums r - mean, whose own mean is taken off (spread_of; 80,000 x 1536, both norms, 351 us
 // instead of 366, 3 x 3,645 x 1160 60 instead of 57).  A bf16 stream needs that in the forward alone, whose rows are new in fp32:
 // its features have eight bits, so that up to 8192 of them within a factor of eight add up exactly, and of others the sum's roundings are

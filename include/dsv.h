@@ -467,7 +467,8 @@ dsv_status dsv_ffn_gated_bwd(const dsv_ffn_dims* dims, const void* dh, const voi
  * Types: z, y, dy, dz bf16; x, r, dr, dx bf16 or, with stream_f32, fp32; gate, scale, shift, w_post, w_pre bf16, each NULL
  * where it is not there (1, 0, 0, 1, 1); the vectors' gradients fp32, each NULL where not wanted.  fp32 arithmetic and
  * sums, one rounding at each output (the forward's y comes from r before its rounding).  The mean squares are fp32
- * numbers too: features beyond about 1e18 leave their row 0 or NaN, and with eps = 0 a row of zeros becomes NaN.
+ * numbers too: features beyond about 1e18 leave their row 0 or NaN, and with eps = 0 a row of zeros becomes NaN and one of
+ * features below about 1e-19 loses bits of its norm.
  * Layouts: x, z, r, y, dr, dy, dx, dz contiguous [B][N][D]; gate, scale, shift: rows of D, gate_stride, scale_stride,
  * shift_stride elements apart (multiples of 8; 0: one row for all samples), so that parts of one modulation projection
  * [B][6][D] are passed as they are; d_gate, d_scale, d_shift: rows of D, d_stride elements apart (a multiple of 4, >= D), which may
@@ -508,7 +509,8 @@ dsv_status dsv_residual_norm_bwd(const dsv_residual_dims* dims, const void* dr, 
  * data: uint8 [F][D / 2], q of column 2 i in the low four bits of byte i and of column 2 i + 1 in the high four;
  * scale: bf16 [F][D / group], finite; zero: uint8 [F][D / group], 0 .. 15 (its low four bits are read), or NULL: 8.
  * x, dx bf16 [M][D]; y bf16 [M][F]; bias bf16 [F] or NULL; dy [M][F], bf16 or, with dy_f32, fp32.  Contiguous.
- * Sums are fp32, with one rounding at the output.  Forward: products are exact.  Backward: dy * scale, rounded to fp32, enters
+ * Sums are fp32, with one rounding at the output.  Forward: products are exact, and a group's sum of
+ * x (q - zero) / 64 is taken before its scale, so that it may overflow for |x| above 2^123.  Backward: dy * scale, rounded to fp32, enters
  * its products as two (dy in bf16) or three (fp32) bf16 numbers that add up to it.
  * Bitwise reproducible.  Outputs must not overlap inputs.
  * Validation before any launch: 1 <= M <= 64; F >= 1; group 32, 64 or 128; D a multiple of group, D <= 2^20, F * D <= 2^40.
